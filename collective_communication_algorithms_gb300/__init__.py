@@ -7,18 +7,26 @@ a C ABI.  This package is its thin Python binding: the hc_* functions mirror
 the C entry points; allreduce / reduce_scatter / allgather / broadcast accept
 lists of torch tensors (one per virtual rank: CUDA tensors, or pinned host
 tensors that the kernels then read and write over the host link) and pass
-their pointers and the current CUDA stream.  PyTorch only provides device memory and streams.
+their pointers and the current CUDA stream.  training.py adds the training
+operators on either side of the collectives (embedding lookup, block-boundary
+norms, distillation loss, with gradients).  PyTorch only provides device memory and streams.
 """
 from ._binding import (ALGOS, COLLS, DTYPES, MODES, OPS, Graph, HcError, hc_allgather, hc_allreduce,
                        hc_broadcast,
                        hc_num_segments, hc_reduce_scatter, hc_schedule_stats, hc_scratch_bytes,
                        hc_segment_range, hc_step_plan, hc_version, lib, make_opts)
 from ._binding import LIB_PATH as library_path
+from .training import (bind_block_norm, bind_block_norm_grad, bind_distill, bind_distill_grad,
+                       bind_embedding, bind_embedding_grad, block_norm, block_norm_grad, distill,
+                       distill_grad, embedding, embedding_grad)
 
 __all__ = ["allreduce", "reduce_scatter", "allgather", "broadcast", "segment_range", "segments",
            "Graph", "hc_broadcast",
            "hc_allreduce", "hc_reduce_scatter", "hc_allgather", "hc_segment_range",
            "hc_num_segments", "hc_scratch_bytes", "hc_schedule_stats", "hc_step_plan",
+           "embedding", "embedding_grad", "block_norm", "block_norm_grad", "distill", "distill_grad",
+           "bind_embedding", "bind_embedding_grad", "bind_block_norm", "bind_block_norm_grad",
+           "bind_distill", "bind_distill_grad",
            "hc_version", "HcError", "make_opts", "library_path", "lib"]
 
 _TORCH_DTYPE = {"torch.int32": "int32", "torch.float32": "float32", "torch.bfloat16": "bfloat16"}

@@ -13,6 +13,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_lib", "libhc.so")
 MAX_RANKS = 64
 
+IDS = {"int32": 0, "int64": 1}
 DTYPES = {"int32": 0, "float32": 1, "bfloat16": 2}
 OPS = {"sum": 0, "prod": 1, "max": 2, "min": 3}
 ALGOS = {"ring": 0, "rhd": 1, "pipeline": 2, "hier": 3}
@@ -59,12 +60,64 @@ class hc_plan_record_t(ctypes.Structure):
                 ("out_ranks", ctypes.c_int32 * MAX_RANKS)]
 
 
+_vp, _sz, _int, _i64, _f = (ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_int64,
+                            ctypes.c_float)
+
+
+def _fields(*groups):
+    """ctypes fields from (type, "name name ...") groups, struct_size first."""
+    out = [("struct_size", _sz)]
+    for ctype, names in groups:
+        out += [(n, ctype) for n in names.split()]
+    return out
+
+
+class hc_embedding_t(ctypes.Structure):
+    _fields_ = _fields((_vp, "table ids out"), (_sz, "tokens rows dim table_stride out_stride"),
+                       (_int, "table_dtype out_dtype id_type"), (_f, "scale"), (_i64, "first_id"))
+
+
+class hc_embedding_grad_t(ctypes.Structure):
+    _fields_ = _fields((_vp, "grad_out ids grad_table scratch"),
+                       (_sz, "scratch_bytes tokens rows dim grad_out_stride grad_table_stride"),
+                       (_int, "grad_out_dtype grad_table_dtype id_type"), (_f, "scale"),
+                       (_i64, "first_id padding_id"), (_int, "accumulate"))
+
+
+class hc_block_norm_t(ctypes.Structure):
+    _fields_ = _fields((_vp, "y x post_weight gate pre_weight r z post_rstd pre_rstd"),
+                       (_sz, "tokens dim gate_rows y_stride x_stride r_stride z_stride"),
+                       (_int, "dtype weight_dtype"), (_f, "residual_scale eps"))
+
+
+class hc_block_norm_grad_t(ctypes.Structure):
+    _fields_ = _fields((_vp, "grad_r grad_z y x post_weight gate pre_weight post_rstd pre_rstd "
+                             "grad_y grad_x grad_post_weight grad_gate grad_pre_weight scratch"),
+                       (_sz, "scratch_bytes tokens dim gate_rows grad_r_stride grad_z_stride "
+                             "y_stride x_stride grad_y_stride grad_x_stride"),
+                       (_int, "dtype weight_dtype"), (_f, "residual_scale"))
+
+
+class hc_distill_t(ctypes.Structure):
+    _fields_ = _fields((_vp, "logits teacher_logits teacher_ids row_weight loss stats grad_logits"),
+                       (_sz, "tokens vocab top logits_stride teacher_stride grad_stride"),
+                       (_int, "dtype teacher_dtype id_type"), (_f, "temperature scale"))
+
+
+# the training operators and their argument structs
+OPERATORS = {"hc_embedding": hc_embedding_t, "hc_embedding_grad": hc_embedding_grad_t,
+             "hc_block_norm": hc_block_norm_t, "hc_block_norm_grad": hc_block_norm_grad_t,
+             "hc_distill": hc_distill_t, "hc_distill_grad": hc_distill_t}
+
 # every symbol include/hc.h declares
 EXPORTS = ("hc_allreduce", "hc_reduce_scatter", "hc_reduce_scatter_static_scratch",
            "hc_allgather", "hc_broadcast", "hc_segment_range", "hc_graph_create",
            "hc_graph_add_allreduce", "hc_graph_add_reduce_scatter", "hc_graph_add_allgather",
            "hc_graph_add_broadcast", "hc_graph_build",
            "hc_graph_launch", "hc_graph_info", "hc_graph_destroy",
+           "hc_embedding", "hc_embedding_grad", "hc_embedding_grad_scratch_bytes",
+           "hc_block_norm", "hc_block_norm_grad", "hc_block_norm_grad_scratch_bytes",
+           "hc_distill", "hc_distill_grad",
            "hc_num_segments", "hc_scratch_bytes", "hc_schedule_stats", "hc_step_plan",
            "hc_select_algo", "hc_device_status", "hc_test_expire_waits", "hc_last_cuda_error",
            "hc_status_string",
@@ -92,6 +145,14 @@ def lib():
         L.hc_reduce_scatter_static_scratch.restype = i32
         L.hc_allgather.argtypes = [ptrs, ptrs, i32, sz, i32, i32, ctypes.POINTER(hc_opts_t), vp]
         L.hc_allgather.restype = i32
+        for name, args in OPERATORS.items():
+            f = getattr(L, name)
+            f.argtypes = [ctypes.POINTER(args), vp]
+            f.restype = i32
+        for name in ("hc_embedding_grad", "hc_block_norm_grad"):
+            f = getattr(L, name + "_scratch_bytes")
+            f.argtypes = [ctypes.POINTER(OPERATORS[name])]
+            f.restype = sz
         L.hc_graph_create.argtypes = [ctypes.POINTER(vp)]
         L.hc_graph_create.restype = i32
         for name in ("hc_graph_add_allreduce", "hc_graph_add_reduce_scatter"):
@@ -208,13 +269,13 @@ def hc_reduce_scatter(send, recv, P, count, dtype, op, algo, opts=None, stream=0
 
 
 class BoundCall:
-    """One collective call whose arguments were converted to C types once:
+    """One call of the library whose arguments were converted to C types once:
     calling it issues the C entry point again with exactly those arguments
     (same buffers, sizes, options and stream).  For callers that repeat a
     call, e.g. once per training step, this skips the per-call argument
     conversion of the hc_* functions; the status is checked as they do."""
 
-    __slots__ = ("fn", "args", "name", "keep")
+    __slots__ = ("fn", "args", "name", "keep", "outputs")
 
     def __init__(self, name, args, keep):
         self.fn = lib()[name]  # a function object of its own, without argument conversion
@@ -346,6 +407,37 @@ def hc_select_algo(coll, P, count, dtype, mode="step", ranks_per_server=1):
                                 ctypes.byref(t)), "hc_select_algo")
     name = {v: k for k, v in ALGOS.items()}[a.value]
     return name, t.value
+
+
+def operator_args(name, **kw):
+    """The argument struct of a training operator.  Pointers are ints (0 or
+    None: NULL), dtypes and id types names or enum values."""
+    a = OPERATORS[name]()
+    a.struct_size = ctypes.sizeof(a)
+    for k, v in kw.items():
+        if k == "id_type":
+            v = _enum(IDS, v)
+        elif k.endswith("dtype"):
+            v = _enum(DTYPES, v)
+        setattr(a, k, v)
+    return a
+
+
+def hc_operator(name, args, stream=0):
+    """Calls the training operator `name` with the struct `args`."""
+    _check(getattr(lib(), name)(ctypes.byref(args), ctypes.c_void_p(int(stream)) if stream else None),
+           name)
+
+
+def hc_operator_scratch_bytes(name, args):
+    """Scratch bytes of hc_embedding_grad or hc_block_norm_grad with `args`."""
+    return getattr(lib(), name + "_scratch_bytes")(ctypes.byref(args))
+
+
+def bind_operator(name, args, keep=(), stream=0):
+    """The training operator `name` with the struct `args`, as a BoundCall."""
+    return BoundCall(name, (ctypes.byref(args), ctypes.c_void_p(int(stream)) if stream else None),
+                     (args, keep))
 
 
 def hc_device_status(clear=True):

@@ -18,7 +18,7 @@ LIB = os.path.join(OUT, "libhc.so")
 ARCHIVE = os.path.join(OUT, "libhc.a")
 SOURCES = ["hc_kernels.cu", "hc_fused_ring.cu", "hc_fused_rhd.cu", "hc_fused_pipe.cu",
            "hc_fused_hier.cu", "hc_sched.cpp", "hc_api.cpp", "hc_graph.cpp", "hc_static_scratch.cu",
-           "hc_trace.cpp"]
+           "hc_trace.cpp", "hc_ops.cpp", "hc_embedding.cu", "hc_block_norm.cu", "hc_distill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -53,6 +53,7 @@ def build(force: bool = False) -> str:
     os.makedirs(OUT, exist_ok=True)
     deps = [os.path.join(CSRC, s) for s in SOURCES]
     deps += [os.path.join(CSRC, "hc_internal.h"), os.path.join(CSRC, "hc_device.cuh"),
+             os.path.join(CSRC, "hc_ops.h"), os.path.join(CSRC, "hc_ops.cuh"),
              os.path.join(ROOT, "include", "hc.h")]
     if not force and not _stale(LIB, deps):
         return LIB

@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include "hc_internal.h"
+#include "hc_ops.h"
 
 using namespace hc;
 
@@ -75,11 +76,15 @@ bool any_overlap(std::vector<Interval>& v) {
 // The CUDA error behind the last HC_ERR_CUDA returned on this thread.
 thread_local cudaError_t g_last_cuda_error = cudaSuccess;
 
-hc_status_t cuda_status(cudaError_t e) {
+}  // namespace
+
+hc_status_t hc::cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return HC_OK;
     g_last_cuda_error = e;
     return HC_ERR_CUDA;
 }
+
+namespace {
 
 // A buffer the kernels may dereference at its own address: device or managed
 // memory, or page-locked host memory mapped at the same address (unified
@@ -96,7 +101,9 @@ hc_status_t check_device_accessible(const void* p) {
     return HC_ERR_INVALID_ARG;
 }
 
-int sm_count_of_current_device() {
+}  // namespace
+
+int hc::sm_count_of_current_device() {
     static std::atomic<int> cache[kMaxDevices];  // zero-initialised (static storage)
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
@@ -109,6 +116,8 @@ int sm_count_of_current_device() {
     if (dev >= 0 && dev < kMaxDevices) cache[dev].store(v, std::memory_order_relaxed);
     return v;
 }
+
+namespace {
 
 // ---------------------------------------------------------------- plan cache
 using PlanKey = std::tuple<int, int, int, int, int, int64_t, int, int64_t, unsigned long long,

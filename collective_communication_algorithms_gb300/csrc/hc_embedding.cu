@@ -1,0 +1,592 @@
+// hc_embedding.cu -- the embedding lookup and its gradient.
+//
+// Lookup: out[t] = scale * table[ids[t] - first], a gather of rows; every
+// byte of a token's row is read and written once.
+//
+// Gradient: grad_table[v] = scale * sum of grad_out[t] over the tokens of row
+// v.  Adding rows with atomics would make the sums depend on the order in
+// which blocks run, so the tokens are grouped by row first:
+//  - up to kEmbeddingFewTokens tokens, every block finds the tokens of its
+//    own row by comparing all ids (one launch, no scratch);
+//  - above, a stable radix sort of (row, token), then sums over groups of
+//    kEmbeddingSumChunk sorted tokens.  A row whose tokens all lie in one
+//    group is written by it; a row cut by a group's end leaves partial sums
+//    in scratch, added up in group order by a last kernel.
+#include "hc_ops.cuh"
+
+namespace hc {
+namespace {
+
+// ---------------------------------------------------------------------------
+// lookup
+// ---------------------------------------------------------------------------
+struct LookupParams {
+    const void* table;
+    const void* ids;
+    void* out;
+    int64_t tokens, rows, first, table_stride, out_stride;
+    int dim, col_blocks, tx_log2;
+    bool wide_ids;
+    float scale;
+};
+
+constexpr int kLookupThreads = 256;
+
+// A block takes 2^tx_log2 threads x N columns of (256 >> tx_log2) * U tokens.
+template <class TI, class TO, int N, int U>
+__global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const LookupParams p) {
+    const int tx = threadIdx.x & ((1 << p.tx_log2) - 1), ty = threadIdx.x >> p.tx_log2;
+    const int ny = kLookupThreads >> p.tx_log2;
+    const int64_t t0 = (int64_t)(blockIdx.x / p.col_blocks) * (ny * U) + ty;
+    const int c = ((blockIdx.x % p.col_blocks << p.tx_log2) + tx) * N;
+    grid_wait();
+    grid_release();
+    if (c >= p.dim) return;
+    const int n = p.dim - c;
+    uint64_t row[U];
+    float v[U][N];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        const int64_t t = t0 + u * ny;
+        // rows of other tables wrap to large values
+        row[u] = t < p.tokens ? (uint64_t)load_id(p.ids, t, p.wide_ids) - (uint64_t)p.first : ~0ull;
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        if (row[u] < (uint64_t)p.rows) {
+            load_n<TI, N>((const TI*)p.table + (int64_t)row[u] * p.table_stride + c, n, v[u]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i++) v[u][i] = 0.0f;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        const int64_t t = t0 + u * ny;
+        if (t >= p.tokens) break;
+#pragma unroll
+        for (int i = 0; i < N; i++) v[u][i] *= p.scale;
+        store_n<TO, N>((TO*)p.out + t * p.out_stride + c, n, v[u]);
+    }
+}
+
+template <class TI, class TO>
+cudaError_t launch_lookup(LookupParams& p, bool vec, cudaStream_t stream, int sms) {
+    constexpr int W = kVecOf<TI> > kVecOf<TO> ? kVecOf<TI> : kVecOf<TO>;
+    const int nv = (int)((p.dim + (vec ? W : 1) - 1) / (vec ? W : 1));
+    p.tx_log2 = 5;
+    while (p.tx_log2 < 8 && (1 << p.tx_log2) < nv) p.tx_log2++;
+    p.col_blocks = (nv + (1 << p.tx_log2) - 1) >> p.tx_log2;
+    const int ny = kLookupThreads >> p.tx_log2;
+    // four tokens a thread once the blocks fill the SMs several times over
+    const bool many = (p.tokens + ny - 1) / ny * p.col_blocks >= (int64_t)sms * 32;
+    const int64_t per = (int64_t)ny * (many ? 4 : 1);
+    const int64_t grid = (p.tokens + per - 1) / per * p.col_blocks;
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    const void* fn = vec ? (many ? (const void*)lookup_kernel<TI, TO, W, 4> : (const void*)lookup_kernel<TI, TO, W, 1>)
+                         : (many ? (const void*)lookup_kernel<TI, TO, 1, 4> : (const void*)lookup_kernel<TI, TO, 1, 1>);
+    void* args[] = {&p};
+    return launch_op(fn, dim3((unsigned)grid), dim3(kLookupThreads), args, 0, stream);
+}
+
+// ---------------------------------------------------------------------------
+// gradient: shared pieces
+// ---------------------------------------------------------------------------
+struct GradParams {
+    const void* grad;   // grad_out
+    const void* ids;
+    void* table;        // grad_table
+    int64_t tokens, rows, first, padding, grad_stride, table_stride;
+    int dim;
+    bool wide_ids, accumulate, has_padding;
+    float scale;
+    // sorted path
+    uint32_t *keys_in, *pos_in, *keys_out, *pos_out;
+    uint32_t *hist, *hist_next, *hist_after;  // this pass's digit counts, the next's, the one after's
+    float* part;
+    int64_t pitch, chunks, sum_chunks;
+    int chunk, shift, bits, next_shift;
+    int tiles;          // column tiles of a row
+    int64_t sum_blocks; // blocks of the sum; the others fill rows without tokens
+    int fill_rows;      // rows of one filling block
+};
+
+// Row of token t in this table, or rows when it has none (padding, another
+// rank's id).
+__device__ __forceinline__ uint32_t row_of(const GradParams& p, int64_t t) {
+    const int64_t id = load_id(p.ids, t, p.wide_ids);
+    const uint64_t r = (uint64_t)id - (uint64_t)p.first;  // ids below first wrap to large values
+    return r < (uint64_t)p.rows && !(p.has_padding && id == p.padding) ? (uint32_t)r : (uint32_t)p.rows;
+}
+
+template <class TT, int N>
+__device__ __forceinline__ void write_row(const GradParams& p, uint32_t row, int c, const float (&acc)[N]) {
+    TT* q = (TT*)p.table + (int64_t)row * p.table_stride + c;
+    const int n = p.dim - c;
+    float v[N];
+    if (p.accumulate) {
+        load_n<TT, N>(q, n, v);
+#pragma unroll
+        for (int i = 0; i < N; i++) v[i] = fmaf(acc[i], p.scale, v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i++) v[i] = acc[i] * p.scale;
+    }
+    store_n<TT, N>(q, n, v);
+}
+
+template <class TT, int N>
+__device__ __forceinline__ void zero_row(const GradParams& p, int64_t row, int tid, int threads) {
+    const float z[N] = {};
+    TT* q = (TT*)p.table + row * p.table_stride;
+    for (int c = tid * N; c < p.dim; c += threads * N) store_n<TT, N>(q + c, p.dim - c, z);
+}
+
+constexpr int kFewThreads = 128;
+constexpr int kFewWords = (int)kEmbeddingFewTokens / 32;
+constexpr int kFillRows = 32;
+
+// ---------------------------------------------------------------------------
+// gradient of a few tokens: block (token, column tile); the block of a row's
+// first token sums the row's tokens in token order, the others leave.
+// ---------------------------------------------------------------------------
+template <class TO, class TT, int N>
+__global__ void __launch_bounds__(kFewThreads) few_kernel(const GradParams p) {
+    __shared__ uint32_t same[kFewWords];
+    grid_wait();
+    grid_release();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int T = (int)p.tokens;
+    if ((int64_t)blockIdx.x >= p.sum_blocks) {  // rows without tokens
+        const int64_t v0 = ((int64_t)blockIdx.x - p.sum_blocks) * kFillRows;
+        __shared__ uint32_t touched;
+        if (threadIdx.x == 0) touched = 0;
+        __syncthreads();
+        for (int s = threadIdx.x; s < T; s += kFewThreads) {
+            const int64_t r = (int64_t)row_of(p, s) - v0;
+            if (r >= 0 && r < kFillRows) atomicOr(&touched, 1u << r);
+        }
+        __syncthreads();
+        for (int r = warp; r < kFillRows; r += kFewThreads / 32)
+            if (v0 + r < p.rows && !(touched >> r & 1)) zero_row<TT, N>(p, v0 + r, lane, 32);
+        return;
+    }
+    const int t = (int)(blockIdx.x / p.tiles);
+    const int c = ((int)(blockIdx.x % p.tiles) * kFewThreads + threadIdx.x) * N;
+    const uint32_t row = row_of(p, t);
+    if (row == (uint32_t)p.rows) return;
+    const int words = (T + 31) / 32;
+    for (int w = warp; w < words; w += kFewThreads / 32) {
+        const int s = w * 32 + lane;
+        const uint32_t m = __ballot_sync(0xFFFFFFFFu, s < T && row_of(p, s) == row);
+        if (lane == 0) same[w] = m;
+    }
+    __syncthreads();
+    for (int w = 0; w < t / 32; w++)
+        if (same[w]) return;  // an earlier token's block has the row
+    if (same[t / 32] & ((1u << (t & 31)) - 1)) return;
+    if (c >= p.dim) return;
+    float acc[N] = {};
+    const int n = p.dim - c;
+    for (int w = t / 32; w < words; w++) {
+        uint32_t m = same[w];
+        while (m) {
+            constexpr int B = 4;  // rows in flight
+            float v[B][N];
+#pragma unroll
+            for (int b = 0; b < B; b++) {
+                const int s = m ? w * 32 + __ffs(m) - 1 : -1;
+                m &= m - 1;  // 0 stays 0
+                load_n<TO, N>((const TO*)p.grad + (int64_t)(s < 0 ? 0 : s) * p.grad_stride + c, s < 0 ? 0 : n, v[b]);
+            }
+#pragma unroll
+            for (int b = 0; b < B; b++)
+#pragma unroll
+                for (int i = 0; i < N; i++) acc[i] += v[b][i];
+        }
+    }
+    write_row<TT, N>(p, row, c, acc);
+}
+
+// ---------------------------------------------------------------------------
+// stable radix sort of (row, token): a block orders `chunk` tokens.
+// ---------------------------------------------------------------------------
+constexpr int kSortThreads = 512;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kMaxBins = 512;  // digits of at most 9 bits
+
+// Digit counts of every chunk for the first pass; zeroes the next pass's.
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const GradParams p) {
+    __shared__ uint32_t count[kMaxBins];
+    grid_wait();
+    grid_release();
+    const int bins = 1 << p.bits;
+    for (int b = threadIdx.x; b < bins; b += kSortThreads) count[b] = 0;
+    __syncthreads();
+    const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
+    for (int i = threadIdx.x; i < p.chunk; i += kSortThreads)
+        if (t0 + i < p.tokens) atomicAdd(&count[row_of(p, t0 + i) & (bins - 1)], 1u);
+    __syncthreads();
+    for (int b = threadIdx.x; b < bins; b += kSortThreads) {
+        p.hist[(int64_t)blockIdx.x * bins + b] = count[b];
+        p.hist_next[(int64_t)blockIdx.x * bins + b] = 0;
+    }
+}
+
+// One pass: every token's place is (tokens of smaller digits) + (tokens of
+// its digit in earlier chunks, in earlier warps, earlier in its warp).  Also
+// counts the next pass's digits at their new places (integer adds, so their
+// order does not matter), and zeroes the counts of the pass after that.
+template <int ITEMS, bool FIRST>
+__global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(const GradParams p) {
+    __shared__ uint32_t warp_count[kSortWarps][kMaxBins];
+    __shared__ uint32_t base[kMaxBins];
+    __shared__ uint32_t scan[kSortWarps];
+    grid_wait();
+    grid_release();
+    const int bins = 1 << p.bits;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int w = 0; w < kSortWarps; w++)
+        if (tid < bins) warp_count[w][tid] = 0;
+    // digit tid: its tokens in earlier chunks, and in all
+    uint32_t before = 0, total = 0;
+    if (tid < bins) {
+        for (int64_t c = 0; c < p.chunks; c++) {
+            const uint32_t h = p.hist[c * bins + tid];
+            if (c < (int64_t)blockIdx.x) before += h;
+            total += h;
+        }
+        if (p.hist_after) p.hist_after[(int64_t)blockIdx.x * bins + tid] = 0;
+    }
+    // exclusive sum of the totals over the digits
+    uint32_t inc = total;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) scan[warp] = inc;
+    __syncthreads();
+    uint32_t off = 0;
+    for (int w = 0; w < warp; w++) off += scan[w];
+    if (tid < bins) base[tid] = off + inc - total + before;
+    // rank of every token in its warp
+    const int64_t t0 = (int64_t)blockIdx.x * p.chunk + (int64_t)warp * 32 * ITEMS + lane;
+    uint32_t key[ITEMS], pos[ITEMS], rank[ITEMS];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < ITEMS; i++) {
+        const int64_t t = t0 + i * 32;
+        const bool in = t < p.tokens;
+        key[i] = in ? (FIRST ? row_of(p, t) : p.keys_in[t]) : 0u;
+        pos[i] = in ? (FIRST ? (uint32_t)t : p.pos_in[t]) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < ITEMS; i++) {
+        const bool in = t0 + i * 32 < p.tokens;
+        const uint32_t d = in ? (key[i] >> p.shift) & (bins - 1) : (uint32_t)bins;
+        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, d);
+        const uint32_t lower = __popc(peers & ((1u << lane) - 1));
+        uint32_t seen = 0;
+        if (in) seen = warp_count[warp][d];
+        __syncwarp();
+        if (in && lower == 0) warp_count[warp][d] = seen + __popc(peers);
+        __syncwarp();
+        rank[i] = seen + lower;
+    }
+    __syncthreads();
+    if (tid < bins) {  // counts of the warps -> places of their first tokens
+        uint32_t at = base[tid];
+        for (int w = 0; w < kSortWarps; w++) {
+            const uint32_t n = warp_count[w][tid];
+            warp_count[w][tid] = at;
+            at += n;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ITEMS; i++) {
+        if (t0 + i * 32 >= p.tokens) break;
+        const uint32_t to = warp_count[warp][(key[i] >> p.shift) & (bins - 1)] + rank[i];
+        p.keys_out[to] = key[i];
+        p.pos_out[to] = pos[i];
+        if (p.hist_next)
+            atomicAdd(&p.hist_next[(int64_t)(to / (uint32_t)p.chunk) * bins + ((key[i] >> p.next_shift) & (bins - 1))], 1u);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// sums over sorted tokens: a warp takes 32 * N columns of kEmbeddingSumChunk
+// tokens; the blocks after sum_blocks zero the rows without tokens.
+// ---------------------------------------------------------------------------
+constexpr int kSumThreads = 256;
+constexpr int kSumWarps = kSumThreads / 32;
+constexpr int kRowsInFlight = 8;
+
+template <class TO, class TT, int N>
+__global__ void __launch_bounds__(kSumThreads) sum_kernel(const GradParams p) {
+    grid_wait();
+    grid_release();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t none = (uint32_t)p.rows;
+    if ((int64_t)blockIdx.x >= p.sum_blocks) {
+        // each warp: 32 rows, a lane looks one up among the sorted keys
+        const int64_t v0 = (((int64_t)blockIdx.x - p.sum_blocks) * kSumWarps + warp) * 32;
+        int64_t lo = 0, hi = p.tokens;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) / 2;
+            if (p.keys_in[mid] < (uint32_t)(v0 + lane)) lo = mid + 1;
+            else hi = mid;
+        }
+        const bool empty = v0 + lane < p.rows && (lo >= p.tokens || p.keys_in[lo] != (uint32_t)(v0 + lane));
+        uint32_t todo = __ballot_sync(0xFFFFFFFFu, empty);
+        while (todo) {
+            zero_row<TT, N>(p, v0 + __ffs(todo) - 1, lane, 32);
+            todo &= todo - 1;
+        }
+        return;
+    }
+    const int64_t item = (int64_t)blockIdx.x * kSumWarps + warp;
+    const int64_t chunk = item / p.tiles;
+    if (chunk >= p.sum_chunks) return;
+    const int c = ((int)(item % p.tiles) * 32 + lane) * N;
+    const int n = p.dim - c;
+    const int64_t s0 = chunk * kEmbeddingSumChunk;
+    const int len = (int)(p.tokens - s0 < kEmbeddingSumChunk ? p.tokens - s0 : kEmbeddingSumChunk);
+    uint32_t cur = p.keys_in[s0];
+    if (cur == none) return;  // the tokens without a row come last
+    const bool continues = s0 > 0 && p.keys_in[s0 - 1] == cur;
+    const uint32_t last = p.keys_in[s0 + len - 1];
+    const bool goes_on = s0 + len < p.tokens && p.keys_in[s0 + len] == last;
+    bool head = continues;  // the run under way began in an earlier chunk
+    float acc[N] = {};
+    for (int b = 0; b < len; b += 32) {
+        const bool in = b + lane < len;
+        const uint32_t my_key = in ? p.keys_in[s0 + b + lane] : none;
+        const uint32_t my_pos = in ? p.pos_in[s0 + b + lane] : 0u;
+        const int m = __popc(__ballot_sync(0xFFFFFFFFu, my_key != none));  // a prefix of the lanes
+        for (int j = 0; j < m; j += kRowsInFlight) {
+            float v[kRowsInFlight][N];
+#pragma unroll
+            for (int k = 0; k < kRowsInFlight; k++) {
+                const uint32_t t = __shfl_sync(0xFFFFFFFFu, my_pos, j + k);
+                load_n<TO, N>((const TO*)p.grad + (int64_t)t * p.grad_stride + c, j + k < m ? n : 0, v[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < kRowsInFlight; k++) {
+                const uint32_t key = __shfl_sync(0xFFFFFFFFu, my_key, j + k);
+                if (j + k < m && key != cur) {
+                    if (head) store_n<float, N>(p.part + chunk * 2 * p.pitch + c, n, acc);
+                    else write_row<TT, N>(p, cur, c, acc);
+                    head = false;
+                    cur = key;
+#pragma unroll
+                    for (int i = 0; i < N; i++) acc[i] = 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < N; i++) acc[i] += v[k][i];
+            }
+        }
+        if (m < 32) break;
+    }
+    if (goes_on && last != none)
+        store_n<float, N>(p.part + (chunk * 2 + (head ? 0 : 1)) * p.pitch + c, n, acc);
+    else if (head)
+        store_n<float, N>(p.part + chunk * 2 * p.pitch + c, n, acc);
+    else
+        write_row<TT, N>(p, cur, c, acc);
+}
+
+// Rows cut by the end of chunk blockIdx.x / tiles, where they begin: slot 1
+// of that chunk and slot 0 of the chunks after it.  The warps add equal parts
+// of the list, joined in order.
+constexpr int kJoinWarps = 8;
+template <class TT, int N>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const GradParams p) {
+    __shared__ float sums[kJoinWarps][32 * N];
+    grid_wait();
+    grid_release();
+    const int64_t chunk = blockIdx.x / p.tiles;
+    const int64_t s1 = (chunk + 1) * kEmbeddingSumChunk;
+    if (s1 >= p.tokens) return;
+    const uint32_t key = p.keys_in[s1];
+    if (key == (uint32_t)p.rows || p.keys_in[s1 - 1] != key) return;
+    if (chunk > 0 && p.keys_in[s1 - kEmbeddingSumChunk - 1] == key) return;  // began earlier
+    // the last chunk whose first token is of this row
+    int64_t lo = chunk + 1, hi = p.sum_chunks - 1;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi + 1) / 2;
+        if (p.keys_in[mid * kEmbeddingSumChunk] == key) lo = mid;
+        else hi = mid - 1;
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = ((int)(blockIdx.x % p.tiles) * 32 + lane) * N;
+    const int n = p.dim - c;
+    const int64_t count = lo - chunk + 1, per = (count + kJoinWarps - 1) / kJoinWarps;
+    const int64_t a = warp * per, b = a + per < count ? a + per : count;
+    float acc[N] = {};
+#pragma unroll 4
+    for (int64_t k = a; k < b; k++) {
+        float v[N];
+        load_n<float, N>(p.part + ((chunk + k) * 2 + (k == 0 ? 1 : 0)) * p.pitch + c, n, v);
+#pragma unroll
+        for (int i = 0; i < N; i++) acc[i] += v[i];
+    }
+#pragma unroll
+    for (int i = 0; i < N; i++) sums[warp][i * 32 + lane] = acc[i];
+    __syncthreads();
+    if (warp) return;
+    for (int w = 1; w < kJoinWarps && w * per < count; w++)
+#pragma unroll
+        for (int i = 0; i < N; i++) acc[i] += sums[w][i * 32 + lane];
+    write_row<TT, N>(p, key, c, acc);
+}
+
+template <class TO, class TT>
+cudaError_t launch_grad(GradParams& p, const EmbeddingScratch& sc, unsigned char* scratch, bool vec,
+                        cudaStream_t stream) {
+    constexpr int W = kVecOf<TO> > kVecOf<TT> ? kVecOf<TO> : kVecOf<TT>;
+    const int64_t nv = (p.dim + (vec ? W : 1) - 1) / (vec ? W : 1);
+    void* args[] = {&p};
+    auto grid_ok = [](int64_t g) { return g <= INT32_MAX; };
+    if (p.tokens <= (int64_t)kEmbeddingFewTokens) {
+        p.tiles = (int)((nv + kFewThreads - 1) / kFewThreads);
+        p.sum_blocks = p.tokens * p.tiles;
+        const int64_t grid = p.sum_blocks + (p.accumulate ? 0 : (p.rows + kFillRows - 1) / kFillRows);
+        if (grid == 0) return cudaSuccess;
+        if (!grid_ok(grid)) return cudaErrorInvalidValue;
+        const void* fn = vec ? (const void*)few_kernel<TO, TT, W> : (const void*)few_kernel<TO, TT, 1>;
+        return launch_op(fn, dim3((unsigned)grid), dim3(kFewThreads), args, 0, stream);
+    }
+    uint32_t *keys[2], *pos[2];
+    uint32_t* const hist = (uint32_t*)(scratch + sc.hist);
+    const size_t hist_len = (size_t)sc.chunks << sc.bits;
+    for (int i = 0; i < 2; i++) {
+        keys[i] = (uint32_t*)(scratch + sc.keys[i]);
+        pos[i] = (uint32_t*)(scratch + sc.pos[i]);
+    }
+    p.part = (float*)(scratch + sc.part);
+    p.pitch = sc.pitch;
+    p.chunk = sc.chunk;
+    p.chunks = sc.chunks;
+    p.bits = sc.bits;
+    p.sum_chunks = sc.sum_chunks;
+    p.hist = hist;
+    p.hist_next = hist + hist_len;
+    cudaError_t e = launch_op((const void*)sort_count_kernel, dim3((unsigned)p.chunks), dim3(kSortThreads), args, 0, stream);
+    if (e != cudaSuccess) return e;
+    for (int i = 0; i < sc.passes; i++) {
+        p.shift = i * sc.bits;
+        p.next_shift = p.shift + sc.bits;
+        p.keys_in = keys[(i + 1) & 1];
+        p.pos_in = pos[(i + 1) & 1];
+        p.keys_out = keys[i & 1];
+        p.pos_out = pos[i & 1];
+        p.hist = hist + (size_t)(i % 3) * hist_len;
+        p.hist_next = i + 1 < sc.passes ? hist + (size_t)((i + 1) % 3) * hist_len : nullptr;
+        p.hist_after = i + 2 < sc.passes ? hist + (size_t)((i + 2) % 3) * hist_len : nullptr;
+        const bool small = sc.chunk <= kSortThreads * 4;
+        const void* fn = i == 0 ? (small ? (const void*)sort_pass_kernel<4, true> : (const void*)sort_pass_kernel<16, true>)
+                                : (small ? (const void*)sort_pass_kernel<4, false> : (const void*)sort_pass_kernel<16, false>);
+        e = launch_op(fn, dim3((unsigned)p.chunks), dim3(kSortThreads), args, 0, stream);
+        if (e != cudaSuccess) return e;
+    }
+    p.keys_in = keys[(sc.passes - 1) & 1];
+    p.pos_in = pos[(sc.passes - 1) & 1];
+    p.tiles = (int)((nv + 31) / 32);
+    p.sum_blocks = (p.sum_chunks * p.tiles + kSumWarps - 1) / kSumWarps;
+    const int64_t fill = p.accumulate ? 0 : (p.rows + kSumThreads - 1) / kSumThreads;
+    if (!grid_ok(p.sum_blocks + fill)) return cudaErrorInvalidValue;
+    e = launch_op(vec ? (const void*)sum_kernel<TO, TT, W> : (const void*)sum_kernel<TO, TT, 1>,
+                  dim3((unsigned)(p.sum_blocks + fill)), dim3(kSumThreads), args, 0, stream);
+    if (e != cudaSuccess || p.sum_chunks < 2) return e;
+    // partial rows are 16-byte aligned, the table's may not be
+    constexpr int J = kVecOf<TT>;
+    const int64_t jv = (p.dim + (vec ? J : 1) - 1) / (vec ? J : 1);
+    p.tiles = (int)((jv + 31) / 32);
+    if (!grid_ok((p.sum_chunks - 1) * p.tiles)) return cudaErrorInvalidValue;
+    return launch_op(vec ? (const void*)join_kernel<TT, J> : (const void*)join_kernel<TT, 1>,
+                     dim3((unsigned)((p.sum_chunks - 1) * p.tiles)), dim3(kJoinWarps * 32), args, 0, stream);
+}
+
+bool aligned16(const void* p, int64_t stride, int es) {
+    return ((uintptr_t)p & 15) == 0 && (stride * es & 15) == 0;
+}
+
+}  // namespace
+
+cudaError_t launch_embedding(const hc_embedding_t& a, cudaStream_t stream, int sms) {
+    LookupParams p = {};
+    p.table = a.table;
+    p.ids = a.ids;
+    p.out = a.out;
+    p.tokens = (int64_t)a.tokens;
+    p.rows = (int64_t)a.rows;
+    p.first = a.first_id;
+    p.table_stride = (int64_t)a.table_stride;
+    p.out_stride = (int64_t)a.out_stride;
+    p.dim = (int)a.dim;
+    p.wide_ids = a.id_type == HC_ID64;
+    p.scale = a.scale;
+    const bool vec = aligned16(a.table, p.table_stride, elem_bytes(a.table_dtype)) &&
+                     aligned16(a.out, p.out_stride, elem_bytes(a.out_dtype));
+    const bool bi = a.table_dtype == HC_BFLOAT16, bo = a.out_dtype == HC_BFLOAT16;
+    if (bi) return bo ? launch_lookup<Bf16, Bf16>(p, vec, stream, sms) : launch_lookup<Bf16, float>(p, vec, stream, sms);
+    return bo ? launch_lookup<float, Bf16>(p, vec, stream, sms) : launch_lookup<float, float>(p, vec, stream, sms);
+}
+
+EmbeddingScratch embedding_scratch(int64_t tokens, int64_t rows, int64_t dim) {
+    EmbeddingScratch s = {};
+    if (tokens <= (int64_t)kEmbeddingFewTokens) return s;
+    // tokens without a row sort as `rows`, so the largest key is rows
+    int bits = 1;
+    while (bits < 32 && (rows >> bits)) bits++;
+    s.passes = (bits + 8) / 9;
+    s.bits = (bits + s.passes - 1) / s.passes;
+    s.chunk = kSortThreads * (tokens <= (1 << 18) ? 4 : 16);
+    s.chunks = (tokens + s.chunk - 1) / s.chunk;
+    s.sum_chunks = (tokens + kEmbeddingSumChunk - 1) / kEmbeddingSumChunk;
+    s.pitch = (dim + 7) / 8 * 8;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += (bytes + 255) / 256 * 256;
+        return o;
+    };
+    for (int i = 0; i < 2; i++) {
+        s.keys[i] = take((size_t)tokens * 4);
+        s.pos[i] = take((size_t)tokens * 4);
+    }
+    s.hist = take((size_t)3 * s.chunks << (s.bits + 2));
+    s.part = take((size_t)s.sum_chunks * 2 * (size_t)s.pitch * 4);
+    s.bytes = at;
+    return s;
+}
+
+cudaError_t launch_embedding_grad(const hc_embedding_grad_t& a, cudaStream_t stream, int sms) {
+    (void)sms;
+    GradParams p = {};
+    p.grad = a.grad_out;
+    p.ids = a.ids;
+    p.table = a.grad_table;
+    p.tokens = (int64_t)a.tokens;
+    p.rows = (int64_t)a.rows;
+    p.first = a.first_id;
+    p.padding = a.padding_id;
+    p.has_padding = a.padding_id >= 0;
+    p.grad_stride = (int64_t)a.grad_out_stride;
+    p.table_stride = (int64_t)a.grad_table_stride;
+    p.dim = (int)a.dim;
+    p.wide_ids = a.id_type == HC_ID64;
+    p.accumulate = a.accumulate != 0;
+    p.scale = a.scale;
+    const EmbeddingScratch sc = embedding_scratch(p.tokens, p.rows, p.dim);
+    const bool vec = aligned16(a.grad_out, p.grad_stride, elem_bytes(a.grad_out_dtype)) &&
+                     aligned16(a.grad_table, p.table_stride, elem_bytes(a.grad_table_dtype));
+    unsigned char* s = (unsigned char*)a.scratch;
+    const bool bo = a.grad_out_dtype == HC_BFLOAT16, bt = a.grad_table_dtype == HC_BFLOAT16;
+    if (bo) return bt ? launch_grad<Bf16, Bf16>(p, sc, s, vec, stream) : launch_grad<Bf16, float>(p, sc, s, vec, stream);
+    return bt ? launch_grad<float, Bf16>(p, sc, s, vec, stream) : launch_grad<float, float>(p, sc, s, vec, stream);
+}
+
+}  // namespace hc

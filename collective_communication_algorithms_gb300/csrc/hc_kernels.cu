@@ -31,6 +31,7 @@
 #include <mutex>
 
 #include "hc_device.cuh"
+#include "hc_ops.h"
 
 namespace hc {
 
@@ -428,6 +429,8 @@ void* pick_reduce_tma(hc_algo_t algo, int coll, hc_dtype_t dt, hc_op_t op, int P
     }
 }
 
+}  // namespace
+
 // Device address of hc_device_error on the current device (looked up once
 // per device).
 int* device_error_flag() {
@@ -443,6 +446,8 @@ int* device_error_flag() {
     }
     return a;
 }
+
+namespace {
 
 // Launch with programmatic stream serialization: the kernel waits for the
 // previous grid on the stream itself (griddepcontrol.wait), so its launch
@@ -468,6 +473,8 @@ cudaError_t launch_pdl(void* fn, dim3 grid, dim3 block, void** args, size_t smem
 // each pair).
 std::mutex g_kernel_attr_mu;  // guards the per-kernel caches below
 
+}  // namespace
+
 bool allow_smem(void* fn, int bytes) {
     static void* fns[512];
     static int devs[512];
@@ -488,6 +495,8 @@ bool allow_smem(void* fn, int bytes) {
     if (i < nfns) set[i] = bytes;
     return true;
 }
+
+namespace {
 
 template <int MAXI, int BATCH, hc_dtype_t DT>
 void* pick_step_op(hc_op_t op) {
@@ -652,6 +661,7 @@ cudaError_t launch_step(const Plan& plan, int P, hc_dtype_t dt, hc_op_t op,
 }
 
 void set_test_expire_waits(bool on) { g_test_expire_waits.store(on ? 1 : 0); }
+bool expiring_waits() { return g_test_expire_waits.load() != 0; }
 
 cudaError_t launch_fused(const FusedArgs& a, cudaStream_t stream, int sm_count) {
     FusedParams p;

@@ -1,0 +1,142 @@
+// hc_ops.cuh -- device-side building blocks of the training operators
+// (hc_embedding.cu, hc_block_norm.cu, hc_distill.cu): element access in
+// binary32, reductions over the threads of a row, programmatic launches.
+// Internal; not installed.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "hc_ops.h"
+
+namespace hc {
+namespace {
+
+struct Bf16 {
+    uint16_t u;
+};
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(Bf16 v) { return __uint_as_float((uint32_t)v.u << 16); }
+__device__ __forceinline__ uint32_t round_bf16x2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(Bf16* p, float v) { p->u = (uint16_t)round_bf16x2(v, 0.0f); }
+
+// A 16-byte vector of T and its elements in binary32.
+template <class T>
+constexpr int kVecOf = 16 / (int)sizeof(T);
+
+__device__ __forceinline__ void unpack(const uint4& w, float (&v)[4]) {
+    v[0] = __uint_as_float(w.x);
+    v[1] = __uint_as_float(w.y);
+    v[2] = __uint_as_float(w.z);
+    v[3] = __uint_as_float(w.w);
+}
+__device__ __forceinline__ void unpack(const uint4& w, float (&v)[8]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        v[2 * i] = __uint_as_float(u[i] << 16);
+        v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ uint4 pack(const float (&v)[4]) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                      __float_as_uint(v[3]));
+}
+__device__ __forceinline__ uint4 pack(const float (&v)[8]) {
+    return make_uint4(round_bf16x2(v[0], v[1]), round_bf16x2(v[2], v[3]), round_bf16x2(v[4], v[5]),
+                      round_bf16x2(v[6], v[7]));
+}
+
+// N consecutive elements of a row, of which the first n (any value) are in
+// range; the others read as 0 and are not written.  16-byte accesses when
+// N elements are whole vectors (the caller then guarantees the alignment)
+// and all of them are in range.
+template <class T, int N>
+__device__ __forceinline__ void load_n(const T* p, int n, float (&v)[N]) {
+    constexpr int E = kVecOf<T>;
+    if constexpr (N % E == 0) {
+        if (n >= N) {
+#pragma unroll
+            for (int i = 0; i < N / E; i++) {
+                float e[E];
+                unpack(((const uint4*)p)[i], e);
+#pragma unroll
+                for (int j = 0; j < E; j++) v[i * E + j] = e[j];
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; i++) v[i] = i < n ? to_f32(p[i]) : 0.0f;
+}
+template <class T, int N>
+__device__ __forceinline__ void store_n(T* p, int n, const float (&v)[N]) {
+    constexpr int E = kVecOf<T>;
+    if constexpr (N % E == 0) {
+        if (n >= N) {
+#pragma unroll
+            for (int i = 0; i < N / E; i++) {
+                float e[E];
+#pragma unroll
+                for (int j = 0; j < E; j++) e[j] = v[i * E + j];
+                ((uint4*)p)[i] = pack(e);
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; i++)
+        if (i < n) put(p + i, v[i]);
+}
+
+// The id of a token, whatever its width.
+__device__ __forceinline__ int64_t load_id(const void* ids, int64_t t, bool wide) {
+    return wide ? ((const int64_t*)ids)[t] : (int64_t)((const int32_t*)ids)[t];
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+
+// Programmatic dependent launch: the kernel may start while the one before it
+// on the stream drains, waits for its results before it touches memory, and
+// then lets its own dependent start.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+}  // namespace
+
+inline cudaError_t launch_op(const void* fn, dim3 grid, dim3 block, void** args, size_t smem,
+                             cudaStream_t stream, int cluster = 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+}  // namespace hc

@@ -1,0 +1,55 @@
+// hc_ops.h -- launchers of the training operators, called by hc_ops.cpp on
+// validated arguments (strides resolved, sizes in range).  Internal.
+#pragma once
+
+#include "hc_internal.h"
+
+namespace hc {
+
+cudaError_t launch_embedding(const hc_embedding_t& a, cudaStream_t stream, int sms);
+
+// Tokens up to which the gradient of the lookup needs no sort (and no
+// scratch), and the layout of its scratch above that.
+constexpr size_t kEmbeddingFewTokens = 256;
+struct EmbeddingScratch {
+    size_t keys[2], pos[2], hist, part;  // byte offsets
+    size_t bytes;
+    int chunk;            // tokens per sorting block
+    int64_t chunks;
+    int passes, bits;     // radix passes, bits of one pass's digit
+    int64_t sum_chunks;   // groups of kEmbeddingSumChunk sorted tokens
+    int64_t pitch;        // floats in one row of partial sums
+};
+constexpr int kEmbeddingSumChunk = 64;
+EmbeddingScratch embedding_scratch(int64_t tokens, int64_t rows, int64_t dim);
+cudaError_t launch_embedding_grad(const hc_embedding_grad_t& a, cudaStream_t stream, int sms);
+
+constexpr size_t kBlockNormMaxDim = 32768;
+cudaError_t launch_block_norm(const hc_block_norm_t& a, cudaStream_t stream, int sms);
+// How the rows are divided among the blocks that sum weight gradients.
+struct BlockNormPlan {
+    int64_t blocks;      // blocks (clusters) = rows of partial sums
+    int64_t unit;        // tokens (by_group 0) or groups (1) of one block
+    int64_t per_group;   // by_group 0: blocks of one group
+    int by_group;
+    int slots;           // partial sums kept by a block
+    int64_t pitch;       // floats in one row of partial sums
+    size_t bytes;
+};
+BlockNormPlan block_norm_plan(int64_t tokens, int64_t dim, int64_t gate_rows, bool gate);
+cudaError_t launch_block_norm_grad(const hc_block_norm_grad_t& a, cudaStream_t stream, int sms);
+
+constexpr size_t kDistillMaxTop = 1024;
+constexpr size_t kDistillMaxVocab = 1u << 20;
+constexpr size_t kDistillMaxRowBytes = 3u << 19;
+enum DistillMode { DISTILL_LOSS = 0, DISTILL_BOTH = 1, DISTILL_GRAD = 2 };
+cudaError_t launch_distill(const hc_distill_t& a, DistillMode mode, cudaStream_t stream, int sms);
+
+// hc_api.cpp / hc_kernels.cu
+hc_status_t cuda_status(cudaError_t e);
+int sm_count_of_current_device();
+int* device_error_flag();
+bool allow_smem(void* fn, int bytes);
+bool expiring_waits();  // hc_test_expire_waits is on
+
+}  // namespace hc

@@ -315,6 +315,201 @@ hc_status_t hc_graph_launch(hc_graph_t graph, hc_stream_t stream);
 hc_status_t hc_graph_info(hc_graph_t graph, int* collectives, int* edges, int* kernels);
 hc_status_t hc_graph_destroy(hc_graph_t graph);
 
+/*
+ * Training operators
+ * ------------------
+ * The operators of a training step on either side of its collectives: the
+ * embedding lookup, the norms and the gate at a block's boundary and the
+ * distillation loss, each with its gradient.  They leave the gradients in
+ * the caller's buffers, ready for hc_allreduce / hc_reduce_scatter.
+ *
+ * Conventions shared by these entry points (the pages have no counterpart)
+ *  - One GPU's tensors; asynchronous on `stream`, capturable into a CUDA
+ *    graph, no allocation: outputs and scratch are the caller's.  Scratch is
+ *    device memory of at least the matching *_scratch_bytes() bytes, 16-byte
+ *    aligned (HC_ERR_SCRATCH / HC_ERR_ALIGN); its contents on entry are
+ *    ignored.  Calls that may run at the same time need scratch of their own.
+ *  - Arguments come in a struct whose struct_size is its sizeof; all
+ *    validation happens before any launch.
+ *  - Matrices are row-major with unit column stride; a *_stride is the
+ *    distance between rows in elements, 0 meaning the row length.  Pointers
+ *    are aligned to their element type (HC_ERR_ALIGN otherwise); 16-byte
+ *    aligned pointers and row pitches take the wide-access kernels.
+ *  - Values are HC_FLOAT32 or HC_BFLOAT16 (HC_ERR_UNSUPPORTED otherwise).
+ *    Arithmetic and sums are binary32, and every output is rounded once.
+ *  - Sums over tokens run in an order fixed by the sizes, so a call repeated
+ *    on the same inputs gives the same bits.
+ *  - An output may not overlap an input or another output, except exactly in
+ *    place (same pointer and stride) where an entry point says so
+ *    (HC_ERR_INVALID_ARG).  Rows of strided matrices may interleave.
+ *  - tokens == 0 launches nothing, except that the gradients summed over
+ *    tokens are then written as zeros.
+ */
+typedef enum { HC_ID32 = 0, HC_ID64 = 1 } hc_id_t;
+
+/*
+ * Embedding lookup: out[t] = scale * table[ids[t] - first_id], or a zero row
+ * when ids[t] - first_id is not in [0, rows).  The table is then one rank's
+ * share of a vocabulary split by rows: a sum hc_allreduce of the ranks'
+ * outputs is the whole lookup (one rank contributes each row, all others
+ * zeros).  Negative ids (padding) give zero rows.
+ */
+typedef struct {
+    size_t struct_size;
+    const void* table;  /* rows x dim */
+    const void* ids;    /* tokens */
+    void* out;          /* tokens x dim */
+    size_t tokens, rows, dim;
+    size_t table_stride, out_stride;
+    hc_dtype_t table_dtype, out_dtype;
+    hc_id_t id_type;
+    float scale;
+    int64_t first_id;   /* id of the table's row 0 */
+} hc_embedding_t;
+hc_status_t hc_embedding(const hc_embedding_t* args, hc_stream_t stream);
+
+/*
+ * Gradient of the lookup: grad_table[v] = scale * sum of grad_out[t] over
+ * the tokens with ids[t] - first_id == v, in token order within fixed groups
+ * of tokens.  Tokens whose id is padding_id, or not in this table, have no
+ * part (their rows of grad_out are not read).
+ *  accumulate : 0: every row of grad_table is written, rows without tokens
+ *               as zeros; 1: the sums are added to what grad_table holds (in
+ *               binary32, rounded once), and only rows with tokens are touched.
+ *  tokens, rows at most 2^31 - 1, dim at most 2^24 (HC_ERR_UNSUPPORTED), as
+ *  for the lookup.
+ */
+typedef struct {
+    size_t struct_size;
+    const void* grad_out;  /* tokens x dim */
+    const void* ids;       /* tokens */
+    void* grad_table;      /* rows x dim */
+    void* scratch;
+    size_t scratch_bytes;
+    size_t tokens, rows, dim;
+    size_t grad_out_stride, grad_table_stride;
+    hc_dtype_t grad_out_dtype, grad_table_dtype;
+    hc_id_t id_type;
+    float scale;
+    int64_t first_id;
+    int64_t padding_id;    /* negative: none */
+    int accumulate;
+} hc_embedding_grad_t;
+hc_status_t hc_embedding_grad(const hc_embedding_grad_t* args, hc_stream_t stream);
+/* Scratch bytes of hc_embedding_grad (its pointers are not looked at); 0 for
+ * sizes that it refuses, and for calls that need none. */
+size_t hc_embedding_grad_scratch_bytes(const hc_embedding_grad_t* args);
+
+/*
+ * Block boundary: the norm after a block, the block's gate, the scaled
+ * residual and the norm before the next block, in one pass.
+ *   post_rstd = 1 / sqrt(mean(y^2) + eps)
+ *   r = residual_scale * x + gate[t / (tokens / gate_rows)] * (y * post_rstd * post_weight)
+ *   pre_rstd = 1 / sqrt(mean(r^2) + eps)
+ *   z = r * pre_rstd * pre_weight
+ * per row t, with r kept unrounded for its norm.  The gate has one row for
+ * each run of tokens / gate_rows tokens (one for all, one for each sequence,
+ * one for each token).  A NULL weight or gate stands for ones.
+ *  z, pre_rstd : NULL: not computed (the last block's boundary).
+ *  post_rstd   : NULL: not kept.  hc_block_norm_grad reads both.
+ *  r, z        : either may be exactly x or y in place.
+ *  dim         : 1 to 32768 (HC_ERR_UNSUPPORTED above).
+ */
+typedef struct {
+    size_t struct_size;
+    const void* y;            /* tokens x dim: the block's output */
+    const void* x;            /* tokens x dim: the residual stream */
+    const void* post_weight;  /* dim */
+    const void* gate;         /* gate_rows x dim, contiguous */
+    const void* pre_weight;   /* dim */
+    void* r;                  /* tokens x dim */
+    void* z;                  /* tokens x dim */
+    float* post_rstd;         /* tokens */
+    float* pre_rstd;          /* tokens */
+    size_t tokens, dim, gate_rows;
+    size_t y_stride, x_stride, r_stride, z_stride;
+    hc_dtype_t dtype;         /* y, x, r, z */
+    hc_dtype_t weight_dtype;  /* post_weight, gate, pre_weight */
+    float residual_scale, eps;
+} hc_block_norm_t;
+hc_status_t hc_block_norm(const hc_block_norm_t* args, hc_stream_t stream);
+
+/*
+ * Gradient of the block boundary, from the gradients of r (by its later
+ * uses) and z, the forward inputs and the kept post_rstd and pre_rstd.
+ *  grad_r, grad_z : NULL stands for zeros (not both; without grad_z,
+ *                   pre_rstd, pre_weight and grad_pre_weight are not used).
+ *  grad_y, grad_x : may be exactly any of grad_r, grad_z, y, x in place.
+ *  grad_post_weight, grad_gate, grad_pre_weight : in weight_dtype,
+ *                   contiguous; NULL: not computed.
+ */
+typedef struct {
+    size_t struct_size;
+    const void* grad_r;       /* tokens x dim */
+    const void* grad_z;       /* tokens x dim */
+    const void* y;
+    const void* x;
+    const void* post_weight;
+    const void* gate;
+    const void* pre_weight;
+    const float* post_rstd;
+    const float* pre_rstd;
+    void* grad_y;             /* tokens x dim */
+    void* grad_x;             /* tokens x dim */
+    void* grad_post_weight;   /* dim */
+    void* grad_gate;          /* gate_rows x dim */
+    void* grad_pre_weight;    /* dim */
+    void* scratch;
+    size_t scratch_bytes;
+    size_t tokens, dim, gate_rows;
+    size_t grad_r_stride, grad_z_stride, y_stride, x_stride, grad_y_stride, grad_x_stride;
+    hc_dtype_t dtype;
+    hc_dtype_t weight_dtype;
+    float residual_scale;
+} hc_block_norm_grad_t;
+hc_status_t hc_block_norm_grad(const hc_block_norm_grad_t* args, hc_stream_t stream);
+/* Scratch bytes of hc_block_norm_grad (its pointers are not looked at); 0
+ * for sizes that it refuses. */
+size_t hc_block_norm_grad_scratch_bytes(const hc_block_norm_grad_t* args);
+
+/*
+ * Distillation from a teacher's top logits.  Per row, with p the softmax of
+ * teacher_logits / temperature over the row's entries, q that of logits /
+ * temperature over the vocabulary, and w = scale * row_weight[t]:
+ *   loss[t] = w * temperature^2 * sum_k p_k (log p_k - log q[id_k])
+ *   grad_logits[t][j] = w * temperature * (q[j] - sum of p_k with id_k == j)
+ * An entry whose id is not in [0, vocab) (a row with fewer than `top`
+ * entries) or whose teacher logit is -inf has no part; entries with the same
+ * id add up.  A row with w == 0 or without entries has loss 0, stats 0 and
+ * gradient 0 whatever its logits hold (they are not read).  Logits of -inf
+ * (masked columns) have q = 0.
+ *  stats       : [t] = (largest logit, sum of exp((logit - largest) /
+ *                temperature)), what hc_distill_grad needs; NULL: not kept.
+ *  grad_logits : NULL: the loss alone.  May be exactly logits in place.
+ *  top         : 1 to 1024; vocab at most 2^20 elements and 1.5 MiB a row
+ *                (HC_ERR_UNSUPPORTED).
+ * hc_distill_grad writes grad_logits alone, from stats (loss is not used):
+ * the backward pass of a loss whose row_weight is only known then.
+ */
+typedef struct {
+    size_t struct_size;
+    const void* logits;          /* tokens x vocab */
+    const void* teacher_logits;  /* tokens x top */
+    const void* teacher_ids;     /* tokens x top */
+    const float* row_weight;     /* tokens; NULL stands for ones */
+    float* loss;                 /* tokens */
+    float* stats;                /* tokens x 2 */
+    void* grad_logits;           /* tokens x vocab */
+    size_t tokens, vocab, top;
+    size_t logits_stride, teacher_stride, grad_stride;  /* teacher_stride: both teacher matrices */
+    hc_dtype_t dtype;            /* logits, grad_logits */
+    hc_dtype_t teacher_dtype;
+    hc_id_t id_type;
+    float temperature, scale;
+} hc_distill_t;
+hc_status_t hc_distill(const hc_distill_t* args, hc_stream_t stream);
+hc_status_t hc_distill_grad(const hc_distill_t* args, hc_stream_t stream);
+
 /* Segment k's element range (see the layout rule above).  k < S, where
  * S = hc_num_segments(algo, coll, P). */
 hc_status_t hc_segment_range(hc_algo_t algo, hc_coll_t coll, int P, size_t count,
