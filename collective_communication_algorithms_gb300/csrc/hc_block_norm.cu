@@ -1,67 +1,150 @@
 // hc_block_norm.cu -- the norm after a block, its gate, the scaled residual
 // and the norm before the next block, and their gradient.
 //
-// A row stays in the registers of its threads from its loads to its stores:
-// forward, y and x are read once and r and z written once, with two row sums
-// between (y^2, then r^2, which needs the first); backward, grad_r, grad_z, y
-// and x are read once and grad_x and grad_y written once, again with two row
-// sums.  Rows longer than one block holds are split over a cluster, whose
-// blocks exchange their sums through distributed shared memory.
+// A row stays on chip from its loads to its stores: forward, y and x are read
+// once and r and z written once, with two row sums between (y^2, then r^2,
+// which needs the first); backward, grad_r, grad_z, y and x are read once and
+// grad_x and grad_y written once, again with two row sums.  What bounds both
+// is the memory, so the kernels are built to keep loads in flight while rows
+// wait for their sums:
+//  - rows of up to 512 (gradient: 256) columns: a power of two of lanes of one warp has a row
+//    (8 or 16 columns a lane); the sums are shuffles and many warps hide the loads;
+//  - longer rows: a group of threads (as many columns each) works through its rows
+//    while bulk copies bring the next ones into a ring of shared-memory
+//    stages; a stage is free again after the row's first sum, when every
+//    thread holds its columns in registers;
+//  - rows longer than a block's threads hold are split over a cluster, whose
+//    blocks exchange their sums through distributed shared memory.
+//
+// Rows that do not start on 16-byte boundaries take the same kernels with one
+// element per access, neighbouring threads on neighbouring columns.
 //
 // Weight gradients: sums over tokens of dz * rhat (pre) and A = D * yhat,
 // from which the others follow: d gate = post_weight * sum A over the gate's
 // tokens, d post_weight = sum gate * A.  A block sums its own run of tokens in
 // registers and leaves partial sums in scratch; a second kernel adds them in
 // a fixed order.
+#include <algorithm>
+
 #include "hc_ops.cuh"
 
 namespace hc {
 namespace {
 
-constexpr int kMaxCluster = 8;
-constexpr int kNormThreads = 1024;
-constexpr int kNormGradThreads = 512;  // up to 128 registers a thread
+// Columns of a thread: the forward pass holds two rows' values and the
+// weights, the gradient four rows' and up to three sums.
+constexpr int kCols = 16, kGradCols = 8;
+constexpr int kNormThreads = 512;  // of a block at most: up to 128 registers a thread
+constexpr int kStages = 4;         // rows in flight of a group of threads at most
+constexpr int kMaxGroups = 8;      // groups of threads (rows) of a block at most
 
-// Cluster-wide barrier (every thread of every block of the cluster).
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ unsigned cluster_rank() {
-    unsigned r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void store_remote(float* local, unsigned rank, float v) {
-    const unsigned a = (unsigned)__cvta_generic_to_shared(local);
-    asm volatile(
-        "{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, %1;\n st.shared::cluster.f32 [r], %2;\n}\n" ::"r"(a),
-        "r"(rank), "f"(v)
-        : "memory");
-}
+// What the bulk copies of a row need of a matrix.
+struct Operand {
+    const void* base;
+    int64_t stride;
+};
 
-// Sum of v over the blockDim.x threads of a row (and the blocks of the
-// cluster), in a fixed order.  Calls alternate between two slots of shared
-// memory: a call's slot is written again only after the barrier of the call
-// between, which every thread reaches after its reads.
+// Shape of a launch: tx threads (or lanes) have a row, ty rows a block.
+struct Layout2 {
+    int tx, ty, cs;     // cs: blocks of a cluster
+    int stages;         // 0: rows in a warp, loaded directly
+    int slot;           // bytes of one row (slice) of one operand in a stage
+    int* err;
+    unsigned long long wait_ns;
+    int hold;           // wait-expiry test mode
+};
+
+// The ring of one group of threads: OPS operands a stage.
+template <class T, int OPS>
+struct Ring {
+    unsigned char* data;
+    uint64_t* full;
+    const Layout2& lay;
+    int64_t tokens;
+    int first, cols;  // this block's slice of the columns
+    bool ok = true;
+
+    __device__ __forceinline__ static int shift_of(const T* p) { return (int)(((uintptr_t)p & 15) / sizeof(T)); }
+    __device__ __forceinline__ unsigned char* slot(int stage, int op) const {
+        return data + (size_t)(stage * OPS + op) * lay.slot;
+    }
+    // Thread 0 of the group: bring token t into a stage.  The copies take the
+    // whole 16-byte vectors that hold the slice, with neighbouring elements of
+    // the matrix; only before its first and after its last element there may
+    // be nothing, so those two vectors are filled element by element.
+    __device__ void load(int stage, int64_t t, const Operand (&op)[OPS]) const {
+        unsigned bytes = 0;
+        int lo[OPS], hi[OPS];
+#pragma unroll
+        for (int o = 0; o < OPS; o++) {
+            lo[o] = hi[o] = 0;
+            if (!op[o].base) continue;
+            const T* p = (const T*)op[o].base + t * op[o].stride + first;
+            const int shift = shift_of(p), end = shift + cols;
+            hi[o] = (end * (int)sizeof(T) + 15) / 16;
+            T* q = (T*)slot(stage, o);
+            if (shift && t == 0 && first == 0) {
+                lo[o] = 1;
+                for (int i = shift; i < kVecOf<T> && i < end; i++) q[i] = p[i - shift];
+            }
+            if (end % kVecOf<T> && t == tokens - 1) {
+                hi[o]--;
+                for (int i = max(hi[o] * kVecOf<T>, shift); i < end; i++) q[i] = p[i - shift];
+            }
+            if (hi[o] > lo[o]) bytes += (unsigned)(hi[o] - lo[o]) * 16;
+        }
+        mbar_arrive_expect_tx(&full[stage], bytes);
+#pragma unroll
+        for (int o = 0; o < OPS; o++) {
+            if (hi[o] <= lo[o]) continue;
+            const uintptr_t p = (uintptr_t)((const T*)op[o].base + t * op[o].stride + first) & ~(uintptr_t)15;
+            bulk_g2s(slot(stage, o) + lo[o] * 16, p + (uintptr_t)lo[o] * 16, (unsigned)(hi[o] - lo[o]) * 16, &full[stage]);
+        }
+    }
+    // Wait for row k of the group.  After a wait that gave up the thread goes
+    // on without waiting (its outputs are undefined) to the end of its rows.
+    __device__ __forceinline__ void wait(int k, bool leader) {
+        if (!ok) return;
+        const int stage = k % lay.stages;
+        if (mbar_wait_quick(&full[stage], (unsigned)(k / lay.stages) & 1, k == 0 ? lay.wait_ns : kWaitLimitNs)) return;
+        ok = false;
+        mbar_expired(&full[stage], lay.err, k == 0 ? lay.hold : 0, leader);
+    }
+    // Thread 0, after a wait gave up at row k0 .. : let the copies of the
+    // rows up to `issued` land before the block leaves.
+    __device__ void drain(int issued) const {
+        for (int k = max(0, issued - lay.stages); k < issued; k++)
+            mbar_wait_bounded(&full[k % lay.stages], (unsigned)(k / lay.stages) & 1, kWaitLimitNs);
+    }
+};
+
+// Sum of v over the threads of a row (and the blocks of the cluster), in a
+// fixed order.  Calls alternate between two slots of shared memory: a call's
+// slot is written again only after the barrier of the call between, which
+// every thread reaches after its reads.
+template <bool RING>
 struct RowSum {
-    float (*warp)[32];         // [2][row * warps + warp]
-    float (*rank)[kMaxCluster];  // [2][rank], clusters have one row a block
-    int cs;
-    int slot;
+    float (*warp)[32];           // [2][group * warps + warp]
+    float (*rank)[kMaxCluster];  // [2][rank], clusters have one group a block
+    int tx, ty, cs;              // threads of a row, this row's number
+    int slot = 0;
     __device__ __forceinline__ float operator()(float v) {
+        if (!RING) {
+            for (int o = tx >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+            return v;
+        }
         slot ^= 1;
         v = warp_sum(v);
-        const int warps = blockDim.x >> 5;
-        if (warps > 1) {
-            const int w = threadIdx.x >> 5;
-            if ((threadIdx.x & 31) == 0) warp[slot][threadIdx.y * warps + w] = v;
-            __syncthreads();
-            v = 0.0f;
-            for (int i = 0; i < warps; i++) v += warp[slot][threadIdx.y * warps + i];
-        }
+        const int warps = tx >> 5, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) warp[slot][ty * warps + w] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(ty + 1), "r"(tx) : "memory");
+        v = warp_sum(lane < warps ? warp[slot][ty * warps + lane] : 0.0f);
         if (cs > 1) {
-            if (threadIdx.x < (unsigned)cs) store_remote(&rank[slot][cluster_rank()], threadIdx.x, v);
-            cluster_sync();
+            unsigned me;
+            asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(me));
+            if (threadIdx.x < (unsigned)cs) store_remote(&rank[slot][me], threadIdx.x, v);
+            cluster_arrive();
+            cluster_wait();
             v = 0.0f;
             for (int i = 0; i < cs; i++) v += rank[slot][i];
         }
@@ -69,258 +152,354 @@ struct RowSum {
     }
 };
 
-struct NormParams {
-    const void *y, *x, *post_weight, *gate, *pre_weight;
-    void *r, *z;
-    float *post_rstd, *pre_rstd;
-    int64_t tokens, per_gate, y_stride, x_stride, r_stride, z_stride;
-    int dim, cs;
-    bool bf16_weights;
-    float residual_scale, eps;
+// A thread's columns: vectors v of N neighbouring ones, tx * N apart.
+template <class T, int N, int C>
+struct Columns {
+    static constexpr int V = C / N;
+    int tid, tx, first, dim;  // first column of the block's slice
+    __device__ __forceinline__ int local(int v) const { return (v * tx + tid) * N; }
+    __device__ __forceinline__ int at(int v) const { return first + local(v); }
+    __device__ __forceinline__ int in(int v) const { return dim - at(v); }  // columns left
+
+    __device__ __forceinline__ void load(const T* row, bool live, float (&x)[C]) const {
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            float e[N];
+            load_n<T, N>(row + at(v), live ? in(v) : 0, e);
+#pragma unroll
+            for (int i = 0; i < N; i++) x[v * N + i] = e[i];
+        }
+    }
+    // from a ring's slot, whose element `shift` is column `first`
+    __device__ __forceinline__ void load(const unsigned char* slot, int shift, float (&x)[C]) const {
+        load((const T*)slot + shift - first, true, x);
+    }
+    __device__ __forceinline__ void store(T* row, bool live, const float (&x)[C]) const {
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            float e[N];
+#pragma unroll
+            for (int i = 0; i < N; i++) e[i] = x[v * N + i];
+            store_n<T, N>(row + at(v), live ? in(v) : 0, e);
+        }
+    }
+    // a weight vector (ones where there is none)
+    __device__ __forceinline__ void weight(const void* w, bool bf16, int64_t row, float (&x)[C]) const {
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            float e[N];
+            if (!w) {
+#pragma unroll
+                for (int i = 0; i < N; i++) e[i] = 1.0f;
+            } else if (bf16) {
+                load_n<Bf16, N>((const Bf16*)w + row * dim + at(v), in(v), e);
+            } else {
+                load_n<float, N>((const float*)w + row * dim + at(v), in(v), e);
+            }
+#pragma unroll
+            for (int i = 0; i < N; i++) x[v * N + i] = e[i];
+        }
+    }
 };
 
-// N elements of a weight vector (ones where there is none).
-template <int N>
-__device__ __forceinline__ void load_weight(const void* w, bool bf16, int64_t at, int n, float (&v)[N]) {
-    if (!w) {
-#pragma unroll
-        for (int i = 0; i < N; i++) v[i] = 1.0f;
-    } else if (bf16) {
-        load_n<Bf16, N>((const Bf16*)w + at, n, v);
-    } else {
-        load_n<float, N>((const float*)w + at, n, v);
-    }
-}
+struct NormParams {
+    Operand in[2];  // y, x
+    const void *post_weight, *gate, *pre_weight;
+    void *r, *z;
+    float *post_rstd, *pre_rstd;
+    int64_t tokens, r_stride, z_stride;
+    unsigned per_gate;
+    int dim;
+    bool bf16_weights;
+    float residual_scale, eps;
+    Layout2 lay;
+};
 
-// blockDim = (threads of a row, rows of a block); a thread holds V vectors of
-// N columns, blockDim.x * N columns apart.
-template <class T, int N, int V>
+// blockDim = (tx, ty) for a ring, (tx * ty) for rows in warps.
+template <class T, int N, bool RING>
 __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p) {
+    extern __shared__ __align__(16) unsigned char dyn[];
+    __shared__ uint64_t full[kMaxGroups][kStages];
     __shared__ float warp_sums[2][32];
     __shared__ float rank_sums[2][kMaxCluster];
-    RowSum row_sum{warp_sums, rank_sums, p.cs, 0};
-    const int64_t t = (int64_t)(blockIdx.x / p.cs) * blockDim.y + threadIdx.y;
-    const int c0 = ((int)(blockIdx.x % p.cs) * blockDim.x * V + threadIdx.x) * N;
-    const int step = blockDim.x * N;
-    const bool live = t < p.tokens;
-    if (p.cs > 1) cluster_sync();  // every block of the cluster runs
+    const Layout2& L = p.lay;
+    const int tid = RING ? threadIdx.x : threadIdx.x % L.tx;
+    const int ty = RING ? threadIdx.y : threadIdx.x / L.tx;
+    const int rank = RING ? blockIdx.x % L.cs : 0;
+    const Columns<T, N, kCols> col{tid, L.tx, rank * L.tx * kCols, p.dim};
+    RowSum<RING> row_sum{warp_sums, rank_sums, L.tx, ty, L.cs};
+    const int64_t start = (int64_t)(blockIdx.x / L.cs) * L.ty + ty;
+    const int64_t step = (int64_t)(gridDim.x / L.cs) * L.ty;
+    Ring<T, 2> ring{dyn + (size_t)ty * L.stages * 2 * L.slot, full[ty], L, p.tokens, col.first,
+                    min(L.tx * kCols, p.dim - col.first)};
+    if (RING) {
+        if (tid == 0) {
+            for (int i = 0; i < L.stages; i++) mbar_init(&full[ty][i], 1 + (i == 0 ? L.hold : 0));
+            mbar_init_fence();
+        }
+        if (L.cs > 1) cluster_arrive();
+        __syncthreads();
+        if (L.cs > 1) cluster_wait();  // every block of the cluster runs
+    }
     grid_wait();
     grid_release();
-    float y[V][N], x[V][N];
-    float s = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; v++) {
-        const int c = c0 + v * step, n = live ? p.dim - c : 0;
-        load_n<T, N>((const T*)p.y + t * p.y_stride + c, n, y[v]);
-        load_n<T, N>((const T*)p.x + t * p.x_stride + c, n, x[v]);
-    }
-#pragma unroll
-    for (int v = 0; v < V; v++)
-#pragma unroll
-        for (int i = 0; i < N; i++) s = fmaf(y[v][i], y[v][i], s);
-    const float post = rsqrtf(row_sum(s) / (float)p.dim + p.eps);
-    const int64_t g = live ? t / p.per_gate : 0;
-    s = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; v++) {
-        const int c = c0 + v * step, n = live ? p.dim - c : 0;
-        float w[N], gt[N];
-        load_weight<N>(p.post_weight, p.bf16_weights, c, n, w);
-        load_weight<N>(p.gate, p.bf16_weights, g * p.dim + c, n, gt);
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            x[v][i] = fmaf(p.residual_scale, x[v][i], gt[i] * (y[v][i] * post * w[i]));
-            s = fmaf(x[v][i], x[v][i], s);
+    int issued = 0;
+    if (RING && tid == 0)
+        for (; issued < L.stages && start + issued * step < p.tokens; issued++) ring.load(issued, start + issued * step, p.in);
+    int k = 0;
+    for (int64_t t = start;; t += step, k++) {
+        // rows in warps: every lane takes part in the shuffles of its one row
+        const bool live = t < p.tokens;
+        if (RING ? !live : k > 0) break;
+        const T* yrow = (const T*)p.in[0].base + t * p.in[0].stride;
+        const T* xrow = (const T*)p.in[1].base + t * p.in[1].stride;
+        float y[kCols], x[kCols], w[kCols], gt[kCols];
+        const int64_t g = live ? (unsigned)t / p.per_gate : 0;
+        if (RING) {
+            col.weight(p.post_weight, p.bf16_weights, 0, w);  // while the row is on its way
+            col.weight(p.gate, p.bf16_weights, g, gt);
+            ring.wait(k, tid == 0);
+            const int stage = k % L.stages;
+            col.load(ring.slot(stage, 0), ring.shift_of(yrow + col.first), y);
+            col.load(ring.slot(stage, 1), ring.shift_of(xrow + col.first), x);
+        } else {
+            col.load(yrow, live, y);
+            col.load(xrow, live, x);
+            col.weight(p.post_weight, p.bf16_weights, 0, w);
+            col.weight(p.gate, p.bf16_weights, g, gt);
         }
-        store_n<T, N>((T*)p.r + t * p.r_stride + c, n, x[v]);
-    }
-    const bool first = threadIdx.x == 0 && blockIdx.x % p.cs == 0 && live;
-    if (first && p.post_rstd) p.post_rstd[t] = post;
-    if (!p.z) return;
-    const float pre = rsqrtf(row_sum(s) / (float)p.dim + p.eps);
-    if (first && p.pre_rstd) p.pre_rstd[t] = pre;
+        float s = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; v++) {
-        const int c = c0 + v * step, n = live ? p.dim - c : 0;
-        float w[N];
-        load_weight<N>(p.pre_weight, p.bf16_weights, c, n, w);
+        for (int i = 0; i < kCols; i++) s = fmaf(y[i], y[i], s);
+        const float post = rsqrtf(row_sum(s) / (float)p.dim + p.eps);
+        if (RING && tid == 0 && ring.ok && start + issued * step < p.tokens) {
+            ring.load(issued % L.stages, start + issued * step, p.in);
+            issued++;
+        }
+        s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < N; i++) x[v][i] *= pre * w[i];
-        store_n<T, N>((T*)p.z + t * p.z_stride + c, n, x[v]);
+        for (int i = 0; i < kCols; i++) {
+            x[i] = fmaf(p.residual_scale, x[i], gt[i] * (y[i] * post * w[i]));
+            s = fmaf(x[i], x[i], s);
+        }
+        col.store((T*)p.r + t * p.r_stride, live, x);
+        const bool first = tid == 0 && rank == 0 && live;
+        if (first && p.post_rstd) p.post_rstd[t] = post;
+        if (!p.z) continue;
+        col.weight(p.pre_weight, p.bf16_weights, 0, w);
+        const float pre = rsqrtf(row_sum(s) / (float)p.dim + p.eps);
+        if (first && p.pre_rstd) p.pre_rstd[t] = pre;
+#pragma unroll
+        for (int i = 0; i < kCols; i++) x[i] *= pre * w[i];
+        col.store((T*)p.z + t * p.z_stride, live, x);
     }
+    if (RING && tid == 0 && !ring.ok) ring.drain(issued);
 }
 
 // ---------------------------------------------------------------------------
 // gradient
 // ---------------------------------------------------------------------------
 struct NormGradParams {
-    const void *grad_r, *grad_z, *y, *x, *post_weight, *gate, *pre_weight;
+    Operand in[4];  // grad_r, grad_z, y, x
+    const void *post_weight, *gate, *pre_weight;
     const float *post_rstd, *pre_rstd;
     void *grad_y, *grad_x, *grad_post_weight, *grad_gate, *grad_pre_weight;
     float* part;         // [block][slot][pitch]: gate * A, dz * rhat, A
-    int64_t tokens, gates, per_gate;
-    int64_t grad_r_stride, grad_z_stride, y_stride, x_stride, grad_y_stride, grad_x_stride;
-    int64_t blocks, unit, per_group, pitch, jobs;
-    int dim, cs, slots;
+    int64_t tokens, gates;
+    int64_t grad_y_stride, grad_x_stride;
+    int64_t blocks, per_group, pitch, jobs;
+    unsigned per_gate, unit;
+    int dim, slots;
     bool bf16_weights;
     float residual_scale;
+    Layout2 lay;
 };
 
 // Add the rows' sums of a block into row 0's, in row order, and store them.
-template <int N>
-__device__ __forceinline__ void store_part(float* joined, float* part, int c, int n, float (&acc)[N]) {
-    if (blockDim.y > 1) {
-        float* mine = joined + (threadIdx.y * blockDim.x + threadIdx.x) * N;
+template <class T, int N, int C>
+__device__ __forceinline__ void store_part(const Columns<T, N, C>& col, int ty, int rows, float* joined, float* part,
+                                           float (&acc)[C]) {
+    if (rows > 1) {
+        float* mine = joined + ty * col.tx + col.tid;
+        const int pitch = rows * col.tx;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < N; i++) mine[i] = acc[i];
+        for (int i = 0; i < C; i++) mine[i * pitch] = acc[i];
         __syncthreads();
-        if (threadIdx.y) return;
-        for (unsigned r = 1; r < blockDim.y; r++)
+        if (ty) return;
+        for (int r = 1; r < rows; r++)
 #pragma unroll
-            for (int i = 0; i < N; i++) acc[i] += joined[(r * blockDim.x + threadIdx.x) * N + i];
+            for (int i = 0; i < C; i++) acc[i] += mine[i * pitch + r * col.tx];
     }
-    store_n<float, N>(part + c, n, acc);
+#pragma unroll
+    for (int v = 0; v < Columns<T, N, C>::V; v++) {
+        float e[N];
+#pragma unroll
+        for (int i = 0; i < N; i++) e[i] = acc[v * N + i];
+        store_n<float, N>(part + col.at(v), col.in(v), e);
+    }
 }
 
 // GROUPS false: the block's run of `unit` tokens lies in one gate row, its
-// rows are dealt to the blockDim.y rows of threads.  true: the block has
+// tokens are dealt to the block's rows of threads.  true: the block has
 // `unit` whole gate rows, dealt to the rows of threads.
-template <class T, int N, int V, bool GROUPS>
-__global__ void __launch_bounds__(kNormGradThreads) norm_grad_kernel(const NormGradParams p) {
-    extern __shared__ float joined[];
+template <class T, int N, bool RING, bool GROUPS>
+__global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradParams p) {
+    constexpr int C = kGradCols;
+    extern __shared__ __align__(16) unsigned char dyn[];
+    __shared__ uint64_t full[kMaxGroups][kStages];
     __shared__ float warp_sums[2][32];
     __shared__ float rank_sums[2][kMaxCluster];
-    RowSum row_sum{warp_sums, rank_sums, p.cs, 0};
-    const int64_t block = blockIdx.x / p.cs;
-    const int c0 = ((int)(blockIdx.x % p.cs) * blockDim.x * V + threadIdx.x) * N;
-    const int step = blockDim.x * N;
-    if (p.cs > 1) cluster_sync();
-    grid_wait();
-    grid_release();
-    float a[V][N] = {}, ga[V][N] = {}, pre_acc[V][N] = {};
-    // tokens [begin + k * stride, k < count) of this row of threads; a barrier
-    // in every step, so the count is the block's
-    int64_t gate_row, begin, end, count, stride, groups = 1;
+    const Layout2& L = p.lay;
+    const int tid = RING ? threadIdx.x : threadIdx.x % L.tx;
+    const int ty = RING ? threadIdx.y : threadIdx.x / L.tx;
+    const int rank = RING ? blockIdx.x % L.cs : 0;
+    const int64_t block = blockIdx.x / L.cs;
+    const Columns<T, N, C> col{tid, L.tx, rank * L.tx * C, p.dim};
+    RowSum<RING> row_sum{warp_sums, rank_sums, L.tx, ty, L.cs};
+    Ring<T, 4> ring{dyn + (size_t)ty * L.stages * 4 * L.slot, full[ty], L, p.tokens, col.first,
+                    min(L.tx * C, p.dim - col.first)};
+    // this row of threads has `count` tokens; steps: what the warp goes
+    // through together (rows in warps)
+    unsigned count, steps;
+    int64_t gate_row, base;
     if (GROUPS) {
-        gate_row = block * p.unit + threadIdx.y;
-        groups = (p.unit + blockDim.y - 1) / blockDim.y;
+        const int64_t first = block * p.unit;
+        const unsigned have = (unsigned)min((int64_t)p.unit, p.gates - first);
+        count = ((unsigned)ty < have ? (have - ty - 1) / L.ty + 1 : 0u) * p.per_gate;
+        steps = (p.unit + L.ty - 1) / L.ty * p.per_gate;
+        gate_row = first + ty;
+        base = 0;
     } else {
         gate_row = block / p.per_group;
+        const unsigned lo = (unsigned)(block % p.per_group) * p.unit;
+        const unsigned have = min(p.unit, p.per_gate - lo);
+        count = (unsigned)ty < have ? (have - ty - 1) / L.ty + 1 : 0u;
+        steps = (p.unit + L.ty - 1) / L.ty;
+        base = gate_row * p.per_gate + lo + ty;
     }
-    for (int64_t k = 0; k < groups; k++) {
-        if (GROUPS) {
-            const bool has = k * blockDim.y + threadIdx.y < p.unit && gate_row < p.gates;
-            begin = gate_row * p.per_gate;
-            end = has ? begin + p.per_gate : begin;
-            stride = 1;
-            count = p.per_gate;
-        } else {
-            const int64_t lo = gate_row * p.per_gate + block % p.per_group * p.unit;
-            const int64_t hi = (gate_row + 1) * p.per_gate;
-            end = lo + p.unit < hi ? lo + p.unit : hi;
-            begin = lo + threadIdx.y;
-            stride = blockDim.y;
-            count = (end - lo + stride - 1) / stride;
+    auto token = [&](unsigned k) -> int64_t {
+        if (!GROUPS) return base + (int64_t)k * L.ty;
+        const unsigned j = k / p.per_gate;
+        return (block * p.unit + ty + (int64_t)j * L.ty) * p.per_gate + (k - j * p.per_gate);
+    };
+    if (RING) {
+        if (tid == 0) {
+            for (int i = 0; i < L.stages; i++) mbar_init(&full[ty][i], 1 + (i == 0 ? L.hold : 0));
+            mbar_init_fence();
         }
-        for (int64_t step_k = 0; step_k < count; step_k++) {
-            const int64_t t = begin + step_k * stride;
-            const bool live = t < end;
-            float gr[V][N], gz[V][N], y[V][N], x[V][N];
+        if (L.cs > 1) cluster_arrive();
+        __syncthreads();
+        if (L.cs > 1) cluster_wait();
+        steps = count;
+    }
+    grid_wait();
+    grid_release();
+    unsigned issued = 0;
+    if (RING && tid == 0)
+        for (; issued < (unsigned)L.stages && issued < count; issued++) ring.load(issued, token(issued), p.in);
+    float a[C] = {}, ga[C] = {}, pre_acc[C] = {};
+    unsigned in_gate = 0;  // tokens of the gate row done
+    for (unsigned k = 0; k < steps; k++) {
+        const bool live = k < count;
+        const int64_t t = live ? token(k) : 0;
+        float w[C], d0[C], y[C], rh[C];
+        const float post = live ? p.post_rstd[t] : 0.0f;
+        const float pre = live && p.in[1].base ? p.pre_rstd[t] : 0.0f;
+        // y -> yhat; x -> rhat; h = gz * pre_weight; d0 = gr + pre * h
+        float s = 0.0f;
+        {
+            float gt[C], gz[C];
+            if (RING) ring.wait((int)k, tid == 0);
+            auto load = [&](int o, float (&v)[C]) {
+                const T* row = (const T*)p.in[o].base + t * p.in[o].stride;
+                if (!p.in[o].base) {
 #pragma unroll
-            for (int v = 0; v < V; v++) {
-                const int c = c0 + v * step, n = live ? p.dim - c : 0;
-                load_n<T, N>((const T*)p.grad_r + t * p.grad_r_stride + c, p.grad_r ? n : 0, gr[v]);
-                load_n<T, N>((const T*)p.grad_z + t * p.grad_z_stride + c, p.grad_z ? n : 0, gz[v]);
-                load_n<T, N>((const T*)p.y + t * p.y_stride + c, n, y[v]);
-                load_n<T, N>((const T*)p.x + t * p.x_stride + c, n, x[v]);
-            }
-            const float post = live ? p.post_rstd[t] : 0.0f;
-            const float pre = live && p.grad_z ? p.pre_rstd[t] : 0.0f;
-            // y -> yhat; x -> rhat; gz -> h = gz * pre_weight after its use
-            float s = 0.0f;
-#pragma unroll
-            for (int v = 0; v < V; v++) {
-                const int c = c0 + v * step, n = live ? p.dim - c : 0;
-                float w[N], gt[N], pw[N];
-                load_weight<N>(p.post_weight, p.bf16_weights, c, n, w);
-                load_weight<N>(p.gate, p.bf16_weights, gate_row * p.dim + c, n, gt);
-                load_weight<N>(p.pre_weight, p.bf16_weights, c, n, pw);
-#pragma unroll
-                for (int i = 0; i < N; i++) {
-                    y[v][i] *= post;
-                    x[v][i] = fmaf(p.residual_scale, x[v][i], gt[i] * (y[v][i] * w[i])) * pre;
-                    pre_acc[v][i] = fmaf(gz[v][i], x[v][i], pre_acc[v][i]);
-                    gz[v][i] *= pw[i];
-                    s = fmaf(gz[v][i], x[v][i], s);
+                    for (int i = 0; i < C; i++) v[i] = 0.0f;
+                } else if (RING) {
+                    col.load(ring.slot((int)(k % L.stages), o), ring.shift_of(row + col.first), v);
+                } else {
+                    col.load(row, live, v);
                 }
+            };
+            load(0, d0);
+            load(1, gz);
+            load(2, y);
+            load(3, rh);
+            col.weight(p.post_weight, p.bf16_weights, 0, w);
+            col.weight(p.gate, p.bf16_weights, live ? gate_row : 0, gt);
+#pragma unroll
+            for (int i = 0; i < C; i++) {
+                y[i] *= post;
+                w[i] *= gt[i];
+                rh[i] = fmaf(p.residual_scale, rh[i], w[i] * y[i]) * pre;
+                pre_acc[i] = fmaf(gz[i], rh[i], pre_acc[i]);
             }
-            const float m1 = p.grad_z ? row_sum(s) / (float)p.dim : 0.0f;
-            s = 0.0f;
+            col.weight(p.pre_weight, p.bf16_weights, 0, gt);
 #pragma unroll
-            for (int v = 0; v < V; v++) {
-                const int c = c0 + v * step, n = live ? p.dim - c : 0;
-                float w[N], gt[N], out[N];
-                load_weight<N>(p.post_weight, p.bf16_weights, c, n, w);
-                load_weight<N>(p.gate, p.bf16_weights, gate_row * p.dim + c, n, gt);
-#pragma unroll
-                for (int i = 0; i < N; i++) {
-                    const float d = fmaf(pre, fmaf(-x[v][i], m1, gz[v][i]), gr[v][i]);
-                    a[v][i] = fmaf(d, y[v][i], a[v][i]);
-                    out[i] = p.residual_scale * d;
-                    gr[v][i] = d * gt[i] * w[i];
-                    s = fmaf(gr[v][i], y[v][i], s);
-                }
-                store_n<T, N>((T*)p.grad_x + t * p.grad_x_stride + c, n, out);
-            }
-            const float m2 = row_sum(s) / (float)p.dim;
-#pragma unroll
-            for (int v = 0; v < V; v++) {
-                const int c = c0 + v * step, n = live ? p.dim - c : 0;
-#pragma unroll
-                for (int i = 0; i < N; i++) gr[v][i] = post * fmaf(-y[v][i], m2, gr[v][i]);
-                store_n<T, N>((T*)p.grad_y + t * p.grad_y_stride + c, n, gr[v]);
+            for (int i = 0; i < C; i++) {
+                const float h = gz[i] * gt[i];
+                s = fmaf(h, rh[i], s);
+                d0[i] = fmaf(pre, h, d0[i]);
             }
         }
-        // A of this gate row is complete (GROUPS), or of the block's run
-#pragma unroll
-        for (int v = 0; v < V; v++) {
-            const int c = c0 + v * step, n = p.dim - c;
-            const bool has = !GROUPS || end > begin;
-            float gt[N];
-            load_weight<N>(p.gate, p.bf16_weights, gate_row * p.dim + c, has ? n : 0, gt);
-#pragma unroll
-            for (int i = 0; i < N; i++) ga[v][i] = has ? fmaf(gt[i], a[v][i], ga[v][i]) : ga[v][i];
-            if (GROUPS) {
-                if (p.grad_gate && has) {
-                    float w[N];
-                    load_weight<N>(p.post_weight, p.bf16_weights, c, n, w);
-#pragma unroll
-                    for (int i = 0; i < N; i++) w[i] *= a[v][i];
-                    if (p.bf16_weights) store_n<Bf16, N>((Bf16*)p.grad_gate + gate_row * p.dim + c, n, w);
-                    else store_n<float, N>((float*)p.grad_gate + gate_row * p.dim + c, n, w);
-                }
-#pragma unroll
-                for (int i = 0; i < N; i++) a[v][i] = 0.0f;
-            }
+        const float m1 = pre * (row_sum(s) / (float)p.dim);
+        if (RING && tid == 0 && ring.ok && issued < count) {
+            ring.load((int)(issued % L.stages), token(issued), p.in);
+            issued++;
         }
-        if (GROUPS) gate_row += blockDim.y;
+        // d = gr + pre (h - rhat mean(h rhat)), k = d * gate * post_weight
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < C; i++) {
+            const float d = fmaf(-m1, rh[i], d0[i]);
+            const float ay = d * y[i];
+            a[i] += ay;
+            rh[i] = p.residual_scale * d;
+            d0[i] = d * w[i];
+            s = fmaf(w[i], ay, s);
+        }
+        col.store((T*)p.grad_x + t * p.grad_x_stride, live, rh);
+        const float m2 = row_sum(s) / (float)p.dim;
+#pragma unroll
+        for (int i = 0; i < C; i++) d0[i] = post * fmaf(-m2, y[i], d0[i]);
+        col.store((T*)p.grad_y + t * p.grad_y_stride, live, d0);
+        if (GROUPS && ++in_gate == p.per_gate) {  // A of this gate row is complete
+            in_gate = 0;
+            col.weight(p.gate, p.bf16_weights, live ? gate_row : 0, w);
+#pragma unroll
+            for (int i = 0; i < C; i++) ga[i] = fmaf(w[i], a[i], ga[i]);
+            if (p.grad_gate && live) {
+                col.weight(p.post_weight, p.bf16_weights, 0, w);
+#pragma unroll
+                for (int i = 0; i < C; i++) w[i] *= a[i];
+                if (p.bf16_weights) Columns<Bf16, N, C>{tid, L.tx, col.first, p.dim}.store((Bf16*)p.grad_gate + gate_row * p.dim, true, w);
+                else Columns<float, N, C>{tid, L.tx, col.first, p.dim}.store((float*)p.grad_gate + gate_row * p.dim, true, w);
+            }
+#pragma unroll
+            for (int i = 0; i < C; i++) a[i] = 0.0f;
+            gate_row += L.ty;
+        }
+    }
+    if (RING && tid == 0 && !ring.ok) ring.drain((int)issued);
+    if (!GROUPS) {
+        float gt[C];
+        col.weight(p.gate, p.bf16_weights, gate_row, gt);
+#pragma unroll
+        for (int i = 0; i < C; i++) ga[i] = gt[i] * a[i];
     }
     float* part = p.part + block * p.slots * p.pitch;
-#pragma unroll
-    for (int v = 0; v < V; v++) {
-        const int c = c0 + v * step, n = p.dim - c;
-        store_part<N>(joined, part, c, n, ga[v]);
-        store_part<N>(joined, part + p.pitch, c, n, pre_acc[v]);
-        if (!GROUPS) store_part<N>(joined, part + 2 * p.pitch, c, n, a[v]);
-    }
+    float* joined = (float*)dyn;  // every row has left the ring
+    store_part(col, ty, L.ty, joined, part, ga);
+    store_part(col, ty, L.ty, joined, part + p.pitch, pre_acc);
+    if (!GROUPS) store_part(col, ty, L.ty, joined, part + 2 * p.pitch, a);
 }
 
-// Sums of the partial rows: blockIdx.y 0: post weight, 1: pre weight, 2 + g:
-// gate row g.  The warps add equal parts of the list, joined in order.
+// Sums of the partial rows: job 0: post weight, 1: pre weight, 2 + g: gate
+// row g.  The warps add equal parts of the list, joined in order.
 constexpr int kSumWarps = 16;
 __global__ void __launch_bounds__(kSumWarps * 32) norm_sum_kernel(const NormGradParams p) {
-    __shared__ float4 sums[kSumWarps][32];
+    __shared__ float sums[kSumWarps][32];
     grid_wait();
     grid_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -329,123 +508,124 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_sum_kernel(const NormGrad
         if (!out) continue;
         const int64_t g = job - 2;
         const int64_t first = job < 2 ? 0 : g * p.per_group, count = job < 2 ? p.blocks : p.per_group;
-        const int c = (blockIdx.x * 32 + lane) * 4;  // the pitch is a multiple of 4 columns
+        const int c = blockIdx.x * 32 + lane;
         const float* src = p.part + (first * p.slots + (job < 2 ? job : 2)) * p.pitch + c;
         const int64_t per = (count + kSumWarps - 1) / kSumWarps;
         const int64_t a = warp * per, b = a + per < count ? a + per : count;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float acc = 0.0f;
         if (c < p.dim) {
-#pragma unroll 4
-            for (int64_t k = a; k < b; k++) {
-                const float4 v = *(const float4*)(src + k * p.slots * p.pitch);
-                acc.x += v.x;
-                acc.y += v.y;
-                acc.z += v.z;
-                acc.w += v.w;
-            }
+#pragma unroll 8
+            for (int64_t k = a; k < b; k++) acc += src[k * p.slots * p.pitch];
         }
         __syncthreads();  // the last job's sums have been read
         sums[warp][lane] = acc;
         __syncthreads();
         if (warp || c >= p.dim) continue;
-        for (int w = 1; w < kSumWarps && w * per < count; w++) {
-            const float4 v = sums[w][lane];
-            acc.x += v.x;
-            acc.y += v.y;
-            acc.z += v.z;
-            acc.w += v.w;
-        }
-        float v[4] = {acc.x, acc.y, acc.z, acc.w};
-        const int n = p.dim - c < 4 ? p.dim - c : 4;
+        for (int w = 1; w < kSumWarps && w * per < count; w++) acc += sums[w][lane];
+        if (job >= 2 && p.post_weight)
+            acc *= p.bf16_weights ? to_f32(((const Bf16*)p.post_weight)[c]) : ((const float*)p.post_weight)[c];
         const int64_t at = (job < 2 ? 0 : g * p.dim) + c;
-        for (int i = 0; i < n; i++) {
-            if (job >= 2 && p.post_weight)
-                v[i] *= p.bf16_weights ? to_f32(((const Bf16*)p.post_weight)[c + i]) : ((const float*)p.post_weight)[c + i];
-            if (p.bf16_weights) put((Bf16*)out + at + i, v[i]);
-            else put((float*)out + at + i, v[i]);
-        }
+        if (p.bf16_weights) put((Bf16*)out + at, acc);
+        else put((float*)out + at, acc);
     }
 }
 
-// Threads of a row, rows of a block and blocks of a cluster for `dim` columns
-// held C to a thread.
-struct Shape {
-    int tx, ty, cs;
-};
-Shape row_shape(int64_t dim, int C, int most_threads, int64_t rows) {
-    Shape s;
-    const int64_t threads = (dim + C - 1) / C;
-    s.cs = 1;
-    while (threads > (int64_t)most_threads * s.cs) s.cs *= 2;
-    const int64_t per = (threads + s.cs - 1) / s.cs;
-    s.tx = (int)((per + 31) / 32 * 32);
-    s.ty = 1;
-    while (s.cs == 1 && s.tx * s.ty < 128 && s.ty < rows) s.ty *= 2;
-    return s;
+// Launch shape for rows of `dim` columns of es bytes, `ops` operands loaded.
+constexpr int kStageBytes = 200 << 10;  // of an SM's blocks together
+Layout2 row_layout(int64_t dim, int es, int ops, bool vec, int per_thread, int block_threads) {
+    Layout2 L = {};
+    const int64_t threads = (dim + per_thread - 1) / per_thread;
+    L.cs = 1;
+    if (threads <= 32) {
+        L.tx = 1;
+        while (L.tx < threads) L.tx *= 2;
+        L.ty = 256 / L.tx;
+        return L;
+    }
+    while (threads > (int64_t)kNormThreads * L.cs) L.cs *= 2;
+    L.tx = (int)(((threads + L.cs - 1) / L.cs + 31) / 32 * 32);
+    L.ty = L.cs > 1 ? 1 : std::max(1, std::min(kMaxGroups, block_threads / L.tx));
+    const int64_t cols = std::min<int64_t>(dim, (int64_t)L.tx * per_thread);
+    L.slot = (int)((cols * es + (vec ? 0 : 16) + 15) / 16 * 16);
+    const int64_t share = (int64_t)kStageBytes / (kNormThreads / (L.tx * L.ty));
+    L.stages = (int)std::min<int64_t>(kStages, share / ((int64_t)L.slot * ops * L.ty));
+    return L;
 }
 
 template <class T>
-bool wide(const void* p, int64_t stride) {
-    return ((uintptr_t)p & 15) == 0 && (stride * (int64_t)sizeof(T) & 15) == 0;
+bool wide(const void* p, int64_t stride, int64_t dim) {
+    return ((uintptr_t)p & 15) == 0 && (stride * (int64_t)sizeof(T) & 15) == 0 && (dim * (int64_t)sizeof(T) & 15) == 0;
 }
-bool wide_weight(const void* w, bool bf16, int64_t stride) {
-    return bf16 ? wide<Bf16>(w, stride) : wide<float>(w, stride);
+bool wide_weight(const void* w, bool bf16, int64_t dim) {
+    return !w || (bf16 ? wide<Bf16>(w, dim, dim) : wide<float>(w, dim, dim));
+}
+
+// Fills the parts of the layout that depend on the device, and launches.
+cudaError_t launch_rows(const void* fn, Layout2* L, int ops, int64_t grid, void** args, size_t least_smem, cudaStream_t stream) {
+    L->err = device_error_flag();
+    if (!L->err) return cudaErrorInvalidValue;
+    L->hold = expiring_waits() ? 1 : 0;
+    L->wait_ns = L->hold ? kTestWaitLimitNs : kWaitLimitNs;
+    if (grid * L->cs > INT32_MAX) return cudaErrorInvalidValue;
+    const size_t smem = std::max(least_smem, (size_t)L->slot * ops * L->stages * L->ty);
+    if (!allow_smem((void*)fn, (int)smem)) return cudaErrorInvalidValue;
+    const dim3 block = L->stages ? dim3(L->tx, L->ty) : dim3(L->tx * L->ty);
+    return launch_op(fn, dim3((unsigned)(grid * L->cs)), block, args, smem, stream, L->cs);
 }
 
 template <class T>
-cudaError_t run_norm(NormParams& p, cudaStream_t stream) {
+cudaError_t run_norm(NormParams& p, cudaStream_t stream, int sms) {
     constexpr int E = kVecOf<T>;
-    const bool vec = wide<T>(p.y, p.y_stride) && wide<T>(p.x, p.x_stride) && wide<T>(p.r, p.r_stride) &&
-                     (!p.z || wide<T>(p.z, p.z_stride)) && wide_weight(p.post_weight, p.bf16_weights, 0) &&
-                     wide_weight(p.gate, p.bf16_weights, p.dim) && wide_weight(p.pre_weight, p.bf16_weights, 0);
-    const Shape s = row_shape(p.dim, 8, kNormThreads, p.tokens);
-    p.cs = s.cs;
-    const int64_t grid = (p.tokens + s.ty - 1) / s.ty * s.cs;
-    if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    const void* fn = vec ? (const void*)norm_kernel<T, E, 8 / E> : (const void*)norm_kernel<T, 1, 8>;
+    const bool vec = wide<T>(p.in[0].base, p.in[0].stride, p.dim) && wide<T>(p.in[1].base, p.in[1].stride, p.dim) &&
+                     wide<T>(p.r, p.r_stride, p.dim) && (!p.z || wide<T>(p.z, p.z_stride, p.dim)) &&
+                     wide_weight(p.post_weight, p.bf16_weights, p.dim) && wide_weight(p.gate, p.bf16_weights, p.dim) &&
+                     wide_weight(p.pre_weight, p.bf16_weights, p.dim);
+    p.lay = row_layout(p.dim, sizeof(T), 2, vec, kCols, kNormThreads / 2);
+    const bool ring = p.lay.stages > 0;
+    int64_t grid = (p.tokens + p.lay.ty - 1) / p.lay.ty;
+    if (ring) grid = std::min<int64_t>(grid, std::max(1, sms * (kNormThreads / (p.lay.tx * p.lay.ty)) / p.lay.cs));
+    const void* fn = vec ? (ring ? (const void*)norm_kernel<T, E, true> : (const void*)norm_kernel<T, E, false>)
+                         : (ring ? (const void*)norm_kernel<T, 1, true> : (const void*)norm_kernel<T, 1, false>);
     void* args[] = {&p};
-    return launch_op(fn, dim3((unsigned)grid), dim3(s.tx, s.ty), args, 0, stream, s.cs);
+    return launch_rows(fn, &p.lay, 2, grid, args, 0, stream);
 }
 
 template <class T>
 cudaError_t run_norm_grad(NormGradParams& p, bool by_group, cudaStream_t stream) {
     constexpr int E = kVecOf<T>;
-    const bool vec = (!p.grad_r || wide<T>(p.grad_r, p.grad_r_stride)) &&
-                     (!p.grad_z || wide<T>(p.grad_z, p.grad_z_stride)) && wide<T>(p.y, p.y_stride) &&
-                     wide<T>(p.x, p.x_stride) && wide<T>(p.grad_y, p.grad_y_stride) &&
-                     wide<T>(p.grad_x, p.grad_x_stride) && wide_weight(p.post_weight, p.bf16_weights, 0) &&
-                     wide_weight(p.gate, p.bf16_weights, p.dim) && wide_weight(p.pre_weight, p.bf16_weights, 0) &&
-                     wide_weight(p.grad_gate, p.bf16_weights, p.dim);
-    const Shape s = row_shape(p.dim, 8, kNormGradThreads, p.unit);
-    p.cs = s.cs;
-    const void* fn = vec ? (by_group ? (const void*)norm_grad_kernel<T, E, 8 / E, true>
-                                     : (const void*)norm_grad_kernel<T, E, 8 / E, false>)
-                         : (by_group ? (const void*)norm_grad_kernel<T, 1, 8, true>
-                                     : (const void*)norm_grad_kernel<T, 1, 8, false>);
+    bool vec = wide<T>(p.grad_y, p.grad_y_stride, p.dim) && wide<T>(p.grad_x, p.grad_x_stride, p.dim) &&
+               wide_weight(p.post_weight, p.bf16_weights, p.dim) && wide_weight(p.gate, p.bf16_weights, p.dim) &&
+               wide_weight(p.pre_weight, p.bf16_weights, p.dim) && wide_weight(p.grad_gate, p.bf16_weights, p.dim);
+    for (const Operand& o : p.in) vec = vec && (!o.base || wide<T>(o.base, o.stride, p.dim));
+    p.lay = row_layout(p.dim, sizeof(T), 4, vec, kGradCols, kNormThreads);
+    const bool ring = p.lay.stages > 0;
+    const void* fn;
+    if (vec) fn = ring ? (by_group ? (const void*)norm_grad_kernel<T, E, true, true> : (const void*)norm_grad_kernel<T, E, true, false>)
+                       : (by_group ? (const void*)norm_grad_kernel<T, E, false, true> : (const void*)norm_grad_kernel<T, E, false, false>);
+    else fn = ring ? (by_group ? (const void*)norm_grad_kernel<T, 1, true, true> : (const void*)norm_grad_kernel<T, 1, true, false>)
+                   : (by_group ? (const void*)norm_grad_kernel<T, 1, false, true> : (const void*)norm_grad_kernel<T, 1, false, false>);
     void* args[] = {&p};
     if (p.blocks > 0) {
-        if (p.blocks * s.cs > INT32_MAX) return cudaErrorInvalidValue;
-        const size_t smem = s.ty > 1 ? (size_t)s.tx * s.ty * E * sizeof(float) : 0;
-        const cudaError_t e = launch_op(fn, dim3((unsigned)(p.blocks * s.cs)), dim3(s.tx, s.ty), args, smem, stream, s.cs);
+        const size_t joined = p.lay.ty > 1 ? (size_t)p.lay.tx * p.lay.ty * kGradCols * sizeof(float) : 0;
+        const cudaError_t e = launch_rows(fn, &p.lay, 4, p.blocks, args, joined, stream);
         if (e != cudaSuccess) return e;
     }
     // gate rows by_group blocks have not written; without tokens all are zeros
     p.jobs = 2 + (p.grad_gate && (!by_group || p.blocks == 0) ? p.gates : 0);
     if (!p.grad_post_weight && !p.grad_pre_weight && p.jobs == 2) return cudaSuccess;
     return launch_op((const void*)norm_sum_kernel,
-                     dim3((unsigned)((p.dim + 127) / 128), (unsigned)(p.jobs < 65535 ? p.jobs : 65535)),
+                     dim3((unsigned)((p.dim + 31) / 32), (unsigned)(p.jobs < 65535 ? p.jobs : 65535)),
                      dim3(kSumWarps * 32), args, 0, stream);
 }
 
-constexpr int64_t kGradBlocks = 304;  // partial sums aimed at
+constexpr int64_t kGradBlocks = 152;  // partial sums aimed at
 
 }  // namespace
 
 cudaError_t launch_block_norm(const hc_block_norm_t& a, cudaStream_t stream, int sms) {
-    (void)sms;
     NormParams p = {};
-    p.y = a.y;
-    p.x = a.x;
+    p.in[0] = {a.y, (int64_t)a.y_stride};
+    p.in[1] = {a.x, (int64_t)a.x_stride};
     p.post_weight = a.post_weight;
     p.gate = a.gate;
     p.pre_weight = a.pre_weight;
@@ -454,16 +634,14 @@ cudaError_t launch_block_norm(const hc_block_norm_t& a, cudaStream_t stream, int
     p.post_rstd = a.post_rstd;
     p.pre_rstd = a.pre_rstd;
     p.tokens = (int64_t)a.tokens;
-    p.per_gate = a.gate ? p.tokens / (int64_t)a.gate_rows : p.tokens;
-    p.y_stride = (int64_t)a.y_stride;
-    p.x_stride = (int64_t)a.x_stride;
+    p.per_gate = (unsigned)(a.gate ? a.tokens / a.gate_rows : a.tokens);
     p.r_stride = (int64_t)a.r_stride;
     p.z_stride = (int64_t)a.z_stride;
     p.dim = (int)a.dim;
     p.bf16_weights = a.weight_dtype == HC_BFLOAT16;
     p.residual_scale = a.residual_scale;
     p.eps = a.eps;
-    return a.dtype == HC_BFLOAT16 ? run_norm<Bf16>(p, stream) : run_norm<float>(p, stream);
+    return a.dtype == HC_BFLOAT16 ? run_norm<Bf16>(p, stream, sms) : run_norm<float>(p, stream, sms);
 }
 
 BlockNormPlan block_norm_plan(int64_t tokens, int64_t dim, int64_t gate_rows, bool gate) {
@@ -494,10 +672,10 @@ cudaError_t launch_block_norm_grad(const hc_block_norm_grad_t& a, cudaStream_t s
     (void)sms;
     const BlockNormPlan q = block_norm_plan((int64_t)a.tokens, (int64_t)a.dim, (int64_t)a.gate_rows, a.gate != nullptr);
     NormGradParams p = {};
-    p.grad_r = a.grad_r;
-    p.grad_z = a.grad_z;
-    p.y = a.y;
-    p.x = a.x;
+    p.in[0] = {a.grad_r, (int64_t)a.grad_r_stride};
+    p.in[1] = {a.grad_z, (int64_t)a.grad_z_stride};
+    p.in[2] = {a.y, (int64_t)a.y_stride};
+    p.in[3] = {a.x, (int64_t)a.x_stride};
     p.post_weight = a.post_weight;
     p.gate = a.gate;
     p.pre_weight = a.pre_weight;
@@ -511,15 +689,11 @@ cudaError_t launch_block_norm_grad(const hc_block_norm_grad_t& a, cudaStream_t s
     p.part = (float*)a.scratch;
     p.tokens = (int64_t)a.tokens;
     p.gates = a.gate ? (int64_t)a.gate_rows : 1;
-    p.per_gate = p.tokens / p.gates;
-    p.grad_r_stride = (int64_t)a.grad_r_stride;
-    p.grad_z_stride = (int64_t)a.grad_z_stride;
-    p.y_stride = (int64_t)a.y_stride;
-    p.x_stride = (int64_t)a.x_stride;
+    p.per_gate = (unsigned)(p.tokens / p.gates);
     p.grad_y_stride = (int64_t)a.grad_y_stride;
     p.grad_x_stride = (int64_t)a.grad_x_stride;
     p.blocks = q.blocks;
-    p.unit = q.unit;
+    p.unit = (unsigned)q.unit;
     p.per_group = q.per_group;
     p.pitch = q.pitch;
     p.slots = q.slots;

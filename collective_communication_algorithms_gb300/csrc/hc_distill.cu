@@ -17,8 +17,6 @@
 // foreign elements set to -inf.
 #include "hc_ops.cuh"
 
-#include "hc_device.cuh"
-
 namespace hc {
 namespace {
 
@@ -59,16 +57,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void store_remote(float* local, unsigned rank, float v) {
-    asm volatile(
-        "{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, %1;\n st.shared::cluster.f32 [r], %2;\n}\n" ::"r"(
-            smem_addr(local)),
-        "r"(rank), "f"(v)
-        : "memory");
-}
-
 // Joins the lanes' (maximum, sum of 2^((x - maximum) c)) of a warp.
 __device__ __forceinline__ void warp_join(float& m, float& l, float c) {
     const float mx = warp_max(m);
@@ -204,8 +192,7 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillParams p
     if (tid == 0) {
         for (int i = 0; i < kPieces; i++) mbar_init(&sh.full[i], 1 + (i == 0 ? p.hold : 0));
         sh.failed = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_init_fence();
     }
     __syncthreads();
     grid_wait();
@@ -270,7 +257,7 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillParams p
     if (tid == 32 && whi < hi && !(hi - 1 == lo && lo < wlo)) take(buf[hi - 1 - lo]);
     bool ok = true;
     for (int i = 0; i < pieces && ok; i++) {
-        if (!mbar_wait_bounded(&sh.full[i], 0, i == 0 ? p.wait_ns : kWaitLimitNs)) {
+        if (!mbar_wait_quick(&sh.full[i], 0, i == 0 ? p.wait_ns : kWaitLimitNs)) {
             mbar_expired(&sh.full[i], p.err, i == 0 ? p.hold : 0, tid == 0);
             ok = false;
             break;

@@ -6,6 +6,7 @@
 
 #include <cuda_runtime.h>
 
+#include "hc_device.cuh"
 #include "hc_ops.h"
 
 namespace hc {
@@ -17,13 +18,8 @@ struct Bf16 {
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(Bf16 v) { return __uint_as_float((uint32_t)v.u << 16); }
-__device__ __forceinline__ uint32_t round_bf16x2(float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(Bf16* p, float v) { p->u = (uint16_t)round_bf16x2(v, 0.0f); }
+__device__ __forceinline__ void put(Bf16* p, float v) { p->u = (uint16_t)pack_bf16x2(v, 0.0f); }
 
 // A 16-byte vector of T and its elements in binary32.
 template <class T>
@@ -48,8 +44,8 @@ __device__ __forceinline__ uint4 pack(const float (&v)[4]) {
                       __float_as_uint(v[3]));
 }
 __device__ __forceinline__ uint4 pack(const float (&v)[8]) {
-    return make_uint4(round_bf16x2(v[0], v[1]), round_bf16x2(v[2], v[3]), round_bf16x2(v[4], v[5]),
-                      round_bf16x2(v[6], v[7]));
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7]));
 }
 
 // N consecutive elements of a row, of which the first n (any value) are in
@@ -108,6 +104,31 @@ __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
     return v;
+}
+
+// ---------------------------------------------------------------------------
+// clusters
+// ---------------------------------------------------------------------------
+constexpr int kMaxCluster = 8;
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Write to the same shared-memory variable of another block of the cluster.
+__device__ __forceinline__ void store_remote(float* local, unsigned rank, float v) {
+    asm volatile(
+        "{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, %1;\n st.shared::cluster.f32 [r], %2;\n}\n" ::"r"(
+            smem_addr(local)),
+        "r"(rank), "f"(v)
+        : "memory");
+}
+
+// Makes freshly initialised barriers visible to the bulk copies.
+__device__ __forceinline__ void mbar_init_fence() {
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// mbar_wait_bounded without reading the clock when the phase is over.
+__device__ __forceinline__ bool mbar_wait_quick(uint64_t* m, unsigned parity, unsigned long long limit_ns) {
+    return mbar_try_wait(m, parity) || mbar_wait_bounded(m, parity, limit_ns);
 }
 
 // Programmatic dependent launch: the kernel may start while the one before it
