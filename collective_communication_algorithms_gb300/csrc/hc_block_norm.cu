@@ -54,8 +54,10 @@ struct Layout2 {
     int hold;           // wait-expiry test mode
 };
 
-// The ring of one group of threads: OPS operands a stage.
-template <class T, int OPS>
+// The ring of one group of threads: OPS operands a stage, operand o brought by
+// lane o of the group's first warp (so that a row's copies are set up side by
+// side).  ALIGNED: every row and slice starts and ends on 16 bytes.
+template <class T, int OPS, bool ALIGNED>
 struct Ring {
     unsigned char* data;
     uint64_t* full;
@@ -64,54 +66,57 @@ struct Ring {
     int first, cols;  // this block's slice of the columns
     bool ok = true;
 
-    __device__ __forceinline__ static int shift_of(const T* p) { return (int)(((uintptr_t)p & 15) / sizeof(T)); }
+    __device__ __forceinline__ static int shift_of(const T* p) {
+        return ALIGNED ? 0 : (int)(((uintptr_t)p & 15) / sizeof(T));
+    }
     __device__ __forceinline__ unsigned char* slot(int stage, int op) const {
-        return data + (size_t)(stage * OPS + op) * lay.slot;
+        return data + (stage * OPS + op) * lay.slot;
     }
-    // Thread 0 of the group: bring token t into a stage.  The copies take the
-    // whole 16-byte vectors that hold the slice, with neighbouring elements of
-    // the matrix; only before its first and after its last element there may
-    // be nothing, so those two vectors are filled element by element.
-    __device__ void load(int stage, int64_t t, const Operand (&op)[OPS]) const {
-        unsigned bytes = 0;
-        int lo[OPS], hi[OPS];
-#pragma unroll
-        for (int o = 0; o < OPS; o++) {
-            lo[o] = hi[o] = 0;
-            if (!op[o].base) continue;
-            const T* p = (const T*)op[o].base + t * op[o].stride + first;
-            const int shift = shift_of(p), end = shift + cols;
-            hi[o] = (end * (int)sizeof(T) + 15) / 16;
-            T* q = (T*)slot(stage, o);
-            if (shift && t == 0 && first == 0) {
-                lo[o] = 1;
-                for (int i = shift; i < kVecOf<T> && i < end; i++) q[i] = p[i - shift];
-            }
-            if (end % kVecOf<T> && t == tokens - 1) {
-                hi[o]--;
-                for (int i = max(hi[o] * kVecOf<T>, shift); i < end; i++) q[i] = p[i - shift];
-            }
-            if (hi[o] > lo[o]) bytes += (unsigned)(hi[o] - lo[o]) * 16;
+    // One thread of the group, before the block's first barrier.
+    __device__ void init() const {
+        for (int i = 0; i < lay.stages; i++) mbar_init(&full[i], OPS + (i == 0 ? lay.hold : 0));
+        mbar_init_fence();
+    }
+    // Lane o: bring token t's row of its operand into a stage.  The copy takes
+    // the whole 16-byte vectors that hold the slice, with neighbouring elements
+    // of the matrix; only before its first and after its last element there
+    // may be nothing, so those two vectors are filled element by element.
+    __device__ __forceinline__ void load(int stage, int64_t t, int o, const Operand& op) const {
+        if (!op.base) {
+            mbar_arrive(&full[stage]);
+            return;
         }
+        const T* p = (const T*)op.base + t * op.stride + first;
+        unsigned char* to = slot(stage, o);
+        if (ALIGNED) {
+            mbar_arrive_expect_tx(&full[stage], (unsigned)cols * (unsigned)sizeof(T));
+            bulk_g2s(to, (uintptr_t)p, (unsigned)cols * (unsigned)sizeof(T), &full[stage]);
+            return;
+        }
+        const int shift = shift_of(p), end = shift + cols;
+        int lo = 0, hi = (end * (int)sizeof(T) + 15) / 16;
+        T* q = (T*)to;
+        if (shift && t == 0 && first == 0) {
+            lo = 1;
+            for (int i = shift; i < kVecOf<T> && i < end; i++) q[i] = p[i - shift];
+        }
+        if (end % kVecOf<T> && t == tokens - 1) {
+            hi--;
+            for (int i = max(hi * kVecOf<T>, shift); i < end; i++) q[i] = p[i - shift];
+        }
+        const unsigned bytes = hi > lo ? (unsigned)(hi - lo) * 16 : 0u;
         mbar_arrive_expect_tx(&full[stage], bytes);
-#pragma unroll
-        for (int o = 0; o < OPS; o++) {
-            if (hi[o] <= lo[o]) continue;
-            const uintptr_t p = (uintptr_t)((const T*)op[o].base + t * op[o].stride + first) & ~(uintptr_t)15;
-            bulk_g2s(slot(stage, o) + lo[o] * 16, p + (uintptr_t)lo[o] * 16, (unsigned)(hi[o] - lo[o]) * 16, &full[stage]);
-        }
+        if (bytes) bulk_g2s(to + lo * 16, ((uintptr_t)p & ~(uintptr_t)15) + (uintptr_t)lo * 16, bytes, &full[stage]);
     }
-    // Wait for row k of the group.  After a wait that gave up the thread goes
-    // on without waiting (its outputs are undefined) to the end of its rows.
-    __device__ __forceinline__ void wait(int k, bool leader) {
-        if (!ok) return;
-        const int stage = k % lay.stages;
-        if (mbar_wait_quick(&full[stage], (unsigned)(k / lay.stages) & 1, k == 0 ? lay.wait_ns : kWaitLimitNs)) return;
+    // Wait for the k-th row.  After a wait that gave up the thread goes on
+    // without waiting (its outputs are undefined) to the end of its rows.
+    __device__ __forceinline__ void wait(int stage, unsigned phase, bool first_row, bool leader) {
+        if (!ok || mbar_wait_quick(&full[stage], phase & 1, first_row ? lay.wait_ns : kWaitLimitNs)) return;
         ok = false;
-        mbar_expired(&full[stage], lay.err, k == 0 ? lay.hold : 0, leader);
+        mbar_expired(&full[stage], lay.err, first_row ? lay.hold : 0, leader);
     }
-    // Thread 0, after a wait gave up at row k0 .. : let the copies of the
-    // rows up to `issued` land before the block leaves.
+    // After a wait gave up: let the copies of the first `issued` rows land
+    // before the block leaves.
     __device__ void drain(int issued) const {
         for (int k = max(0, issued - lay.stages); k < issued; k++)
             mbar_wait_bounded(&full[k % lay.stages], (unsigned)(k / lay.stages) & 1, kWaitLimitNs);
@@ -122,12 +127,18 @@ struct Ring {
 // fixed order.  Calls alternate between two slots of shared memory: a call's
 // slot is written again only after the barrier of the call between, which
 // every thread reaches after its reads.
+constexpr int kRowWarps = kNormThreads / 32;
 template <bool RING>
 struct RowSum {
-    float (*warp)[32];           // [2][group * warps + warp]
-    float (*rank)[kMaxCluster];  // [2][rank], clusters have one group a block
-    int tx, ty, cs;              // threads of a row, this row's number
+    float (*warp)[kMaxGroups * 4 + kRowWarps];  // [2][group * padded warps + warp], unused ones 0
+    float (*rank)[kMaxCluster];                 // [2][rank], clusters have one group a block
+    int tx, ty, cs;                             // threads of a row, this row's number
     int slot = 0;
+    __device__ __forceinline__ int padded() const { return ((tx >> 5) + 3) & ~3; }
+    // All threads of the block, before its first barrier.
+    __device__ __forceinline__ void init(int thread, int threads) const {
+        for (int i = thread; i < kMaxGroups * 4 + kRowWarps; i += threads) warp[0][i] = warp[1][i] = 0.0f;
+    }
     __device__ __forceinline__ float operator()(float v) {
         if (!RING) {
             for (int o = tx >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
@@ -135,10 +146,15 @@ struct RowSum {
         }
         slot ^= 1;
         v = warp_sum(v);
-        const int warps = tx >> 5, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        if (lane == 0) warp[slot][ty * warps + w] = v;
+        const int n = padded();
+        float* const mine = &warp[slot][ty * n];
+        if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = v;
         asm volatile("bar.sync %0, %1;" ::"r"(ty + 1), "r"(tx) : "memory");
-        v = warp_sum(lane < warps ? warp[slot][ty * warps + lane] : 0.0f);
+        v = 0.0f;
+        for (int i = 0; i < n; i += 4) {
+            const float4 f = *(const float4*)(mine + i);
+            v += (f.x + f.y) + (f.z + f.w);
+        }
         if (cs > 1) {
             unsigned me;
             asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(me));
@@ -152,7 +168,9 @@ struct RowSum {
     }
 };
 
-// A thread's columns: vectors v of N neighbouring ones, tx * N apart.
+// A thread's columns: vectors v of N neighbouring ones, tx * N apart.  N is 1,
+// or dim is a multiple of N and every row aligned, so that a vector lies in
+// the row as a whole or not at all.
 template <class T, int N, int C>
 struct Columns {
     static constexpr int V = C / N;
@@ -165,7 +183,7 @@ struct Columns {
 #pragma unroll
         for (int v = 0; v < V; v++) {
             float e[N];
-            load_n<T, N>(row + at(v), live ? in(v) : 0, e);
+            load_whole<T, N>(row + at(v), live && in(v) > 0, e);
 #pragma unroll
             for (int i = 0; i < N; i++) x[v * N + i] = e[i];
         }
@@ -180,7 +198,7 @@ struct Columns {
             float e[N];
 #pragma unroll
             for (int i = 0; i < N; i++) e[i] = x[v * N + i];
-            store_n<T, N>(row + at(v), live ? in(v) : 0, e);
+            store_whole<T, N>(row + at(v), live && in(v) > 0, e);
         }
     }
     // a weight vector (ones where there is none)
@@ -192,9 +210,9 @@ struct Columns {
 #pragma unroll
                 for (int i = 0; i < N; i++) e[i] = 1.0f;
             } else if (bf16) {
-                load_n<Bf16, N>((const Bf16*)w + row * dim + at(v), in(v), e);
+                load_whole<Bf16, N>((const Bf16*)w + row * dim + at(v), in(v) > 0, e);
             } else {
-                load_n<float, N>((const float*)w + row * dim + at(v), in(v), e);
+                load_whole<float, N>((const float*)w + row * dim + at(v), in(v) > 0, e);
             }
 #pragma unroll
             for (int i = 0; i < N; i++) x[v * N + i] = e[i];
@@ -220,7 +238,7 @@ template <class T, int N, bool RING>
 __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p) {
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ uint64_t full[kMaxGroups][kStages];
-    __shared__ float warp_sums[2][32];
+    __shared__ __align__(16) float warp_sums[2][kMaxGroups * 4 + kRowWarps];
     __shared__ float rank_sums[2][kMaxCluster];
     const Layout2& L = p.lay;
     const int tid = RING ? threadIdx.x : threadIdx.x % L.tx;
@@ -230,68 +248,84 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p) 
     RowSum<RING> row_sum{warp_sums, rank_sums, L.tx, ty, L.cs};
     const int64_t start = (int64_t)(blockIdx.x / L.cs) * L.ty + ty;
     const int64_t step = (int64_t)(gridDim.x / L.cs) * L.ty;
-    Ring<T, 2> ring{dyn + (size_t)ty * L.stages * 2 * L.slot, full[ty], L, p.tokens, col.first,
-                    min(L.tx * kCols, p.dim - col.first)};
+    Ring<T, 2, (N > 1)> ring{dyn + (size_t)ty * L.stages * 2 * L.slot, full[ty], L, p.tokens, col.first,
+                             min(L.tx * kCols, p.dim - col.first)};
     if (RING) {
-        if (tid == 0) {
-            for (int i = 0; i < L.stages; i++) mbar_init(&full[ty][i], 1 + (i == 0 ? L.hold : 0));
-            mbar_init_fence();
-        }
+        if (tid == 0) ring.init();
+        row_sum.init(threadIdx.y * L.tx + tid, L.tx * L.ty);
         if (L.cs > 1) cluster_arrive();
         __syncthreads();
         if (L.cs > 1) cluster_wait();  // every block of the cluster runs
     }
     grid_wait();
     grid_release();
+    int64_t next = start;  // token of the next row to bring
     int issued = 0;
-    if (RING && tid == 0)
-        for (; issued < L.stages && start + issued * step < p.tokens; issued++) ring.load(issued, start + issued * step, p.in);
-    int k = 0;
-    for (int64_t t = start;; t += step, k++) {
+    if (RING && tid < 2)
+        for (; issued < L.stages && next < p.tokens; issued++, next += step) ring.load(issued, next, tid, p.in[tid]);
+    const float inv_dim = 1.0f / (float)p.dim;
+    float wg[kCols], pw[kCols];  // post_weight * gate, pre_weight
+    int64_t gate_end = -1;       // of the tokens that wg is for
+    col.weight(p.pre_weight, p.bf16_weights, 0, pw);
+    int stage = 0;
+    unsigned phase = 0;
+    for (int64_t t = start;; t += step) {
         // rows in warps: every lane takes part in the shuffles of its one row
         const bool live = t < p.tokens;
-        if (RING ? !live : k > 0) break;
+        if (RING && !live) break;
+        float y[kCols], x[kCols];
         const T* yrow = (const T*)p.in[0].base + t * p.in[0].stride;
         const T* xrow = (const T*)p.in[1].base + t * p.in[1].stride;
-        float y[kCols], x[kCols], w[kCols], gt[kCols];
-        const int64_t g = live ? (unsigned)t / p.per_gate : 0;
-        if (RING) {
-            col.weight(p.post_weight, p.bf16_weights, 0, w);  // while the row is on its way
-            col.weight(p.gate, p.bf16_weights, g, gt);
-            ring.wait(k, tid == 0);
-            const int stage = k % L.stages;
-            col.load(ring.slot(stage, 0), ring.shift_of(yrow + col.first), y);
-            col.load(ring.slot(stage, 1), ring.shift_of(xrow + col.first), x);
-        } else {
+        if (!RING) {
             col.load(yrow, live, y);
             col.load(xrow, live, x);
-            col.weight(p.post_weight, p.bf16_weights, 0, w);
+        }
+        if (t >= gate_end) {
+            const int64_t g = live ? (unsigned)t / p.per_gate : 0;
+            gate_end = (g + 1) * p.per_gate;
+            float gt[kCols];
+            col.weight(p.post_weight, p.bf16_weights, 0, wg);
             col.weight(p.gate, p.bf16_weights, g, gt);
+#pragma unroll
+            for (int i = 0; i < kCols; i++) wg[i] *= gt[i];
+        }
+        if (RING) {
+            ring.wait(stage, phase, t == start, tid == 0);
+            col.load(ring.slot(stage, 0), ring.shift_of(yrow + col.first), y);
+            col.load(ring.slot(stage, 1), ring.shift_of(xrow + col.first), x);
         }
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < kCols; i++) s = fmaf(y[i], y[i], s);
-        const float post = rsqrtf(row_sum(s) / (float)p.dim + p.eps);
-        if (RING && tid == 0 && ring.ok && start + issued * step < p.tokens) {
-            ring.load(issued % L.stages, start + issued * step, p.in);
-            issued++;
+        const float post = rsqrtf(fmaf(row_sum(s), inv_dim, p.eps));
+        if (RING) {
+            if (tid < 2 && ring.ok && next < p.tokens) {
+                ring.load(stage, next, tid, p.in[tid]);
+                issued++;
+                next += step;
+            }
+            if (++stage == L.stages) {
+                stage = 0;
+                phase++;
+            }
         }
         s = 0.0f;
 #pragma unroll
         for (int i = 0; i < kCols; i++) {
-            x[i] = fmaf(p.residual_scale, x[i], gt[i] * (y[i] * post * w[i]));
+            x[i] = fmaf(wg[i], y[i] * post, p.residual_scale * x[i]);
             s = fmaf(x[i], x[i], s);
         }
         col.store((T*)p.r + t * p.r_stride, live, x);
         const bool first = tid == 0 && rank == 0 && live;
         if (first && p.post_rstd) p.post_rstd[t] = post;
-        if (!p.z) continue;
-        col.weight(p.pre_weight, p.bf16_weights, 0, w);
-        const float pre = rsqrtf(row_sum(s) / (float)p.dim + p.eps);
-        if (first && p.pre_rstd) p.pre_rstd[t] = pre;
+        if (p.z) {
+            const float pre = rsqrtf(fmaf(row_sum(s), inv_dim, p.eps));
+            if (first && p.pre_rstd) p.pre_rstd[t] = pre;
 #pragma unroll
-        for (int i = 0; i < kCols; i++) x[i] *= pre * w[i];
-        col.store((T*)p.z + t * p.z_stride, live, x);
+            for (int i = 0; i < kCols; i++) x[i] *= pre * pw[i];
+            col.store((T*)p.z + t * p.z_stride, live, x);
+        }
+        if (!RING) break;
     }
     if (RING && tid == 0 && !ring.ok) ring.drain(issued);
 }
@@ -348,7 +382,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
     constexpr int C = kGradCols;
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ uint64_t full[kMaxGroups][kStages];
-    __shared__ float warp_sums[2][32];
+    __shared__ __align__(16) float warp_sums[2][kMaxGroups * 4 + kRowWarps];
     __shared__ float rank_sums[2][kMaxCluster];
     const Layout2& L = p.lay;
     const int tid = RING ? threadIdx.x : threadIdx.x % L.tx;
@@ -357,8 +391,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
     const int64_t block = blockIdx.x / L.cs;
     const Columns<T, N, C> col{tid, L.tx, rank * L.tx * C, p.dim};
     RowSum<RING> row_sum{warp_sums, rank_sums, L.tx, ty, L.cs};
-    Ring<T, 4> ring{dyn + (size_t)ty * L.stages * 4 * L.slot, full[ty], L, p.tokens, col.first,
-                    min(L.tx * C, p.dim - col.first)};
+    Ring<T, 4, (N > 1)> ring{dyn + (size_t)ty * L.stages * 4 * L.slot, full[ty], L, p.tokens, col.first,
+                             min(L.tx * C, p.dim - col.first)};
     // this row of threads has `count` tokens; steps: what the warp goes
     // through together (rows in warps)
     unsigned count, steps;
@@ -378,16 +412,27 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
         steps = (p.unit + L.ty - 1) / L.ty;
         base = gate_row * p.per_gate + lo + ty;
     }
-    auto token = [&](unsigned k) -> int64_t {
-        if (!GROUPS) return base + (int64_t)k * L.ty;
-        const unsigned j = k / p.per_gate;
-        return (block * p.unit + ty + (int64_t)j * L.ty) * p.per_gate + (k - j * p.per_gate);
+    // the tokens in order: the one to do, and (lanes that bring rows) the next
+    // one to bring
+    struct Walk {
+        int64_t t, gate;
+        unsigned in_gate;
     };
-    if (RING) {
-        if (tid == 0) {
-            for (int i = 0; i < L.stages; i++) mbar_init(&full[ty][i], 1 + (i == 0 ? L.hold : 0));
-            mbar_init_fence();
+    auto advance = [&](Walk& w) {
+        if (!GROUPS) {
+            w.t += L.ty;
+        } else if (++w.in_gate == p.per_gate) {
+            w.in_gate = 0;
+            w.gate += L.ty;
+            w.t = w.gate * p.per_gate;
+        } else {
+            w.t++;
         }
+    };
+    Walk now{GROUPS ? gate_row * p.per_gate : base, gate_row, 0};
+    if (RING) {
+        if (tid == 0) ring.init();
+        row_sum.init(threadIdx.y * L.tx + tid, L.tx * L.ty);
         if (L.cs > 1) cluster_arrive();
         __syncthreads();
         if (L.cs > 1) cluster_wait();
@@ -395,93 +440,112 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
     }
     grid_wait();
     grid_release();
+    Walk next = now;
     unsigned issued = 0;
-    if (RING && tid == 0)
-        for (; issued < (unsigned)L.stages && issued < count; issued++) ring.load(issued, token(issued), p.in);
+    if (RING && tid < 4)
+        for (; issued < (unsigned)L.stages && issued < count; issued++) {
+            ring.load(issued, next.t, tid, p.in[tid]);
+            advance(next);
+        }
+    const float inv_dim = 1.0f / (float)p.dim;
     float a[C] = {}, ga[C] = {}, pre_acc[C] = {};
-    unsigned in_gate = 0;  // tokens of the gate row done
+    float wg[C], pw[C];  // post_weight * gate, pre_weight
+    auto load_gate = [&](int64_t g) {
+        float gt[C];
+        col.weight(p.post_weight, p.bf16_weights, 0, wg);
+        col.weight(p.gate, p.bf16_weights, g, gt);
+#pragma unroll
+        for (int i = 0; i < C; i++) wg[i] *= gt[i];
+    };
+    col.weight(p.pre_weight, p.bf16_weights, 0, pw);
+    if (count) load_gate(now.gate);
+    int stage = 0;
+    unsigned phase = 0;
     for (unsigned k = 0; k < steps; k++) {
         const bool live = k < count;
-        const int64_t t = live ? token(k) : 0;
-        float w[C], d0[C], y[C], rh[C];
+        const int64_t t = now.t;
+        float d0[C] = {}, y[C] = {}, rh[C] = {};
         const float post = live ? p.post_rstd[t] : 0.0f;
         const float pre = live && p.in[1].base ? p.pre_rstd[t] : 0.0f;
         // y -> yhat; x -> rhat; h = gz * pre_weight; d0 = gr + pre * h
         float s = 0.0f;
-        {
-            float gt[C], gz[C];
-            if (RING) ring.wait((int)k, tid == 0);
+        if (RING || live) {
+            float gz[C];
+            if (RING) ring.wait(stage, phase, k == 0, tid == 0);
             auto load = [&](int o, float (&v)[C]) {
                 const T* row = (const T*)p.in[o].base + t * p.in[o].stride;
                 if (!p.in[o].base) {
 #pragma unroll
                     for (int i = 0; i < C; i++) v[i] = 0.0f;
                 } else if (RING) {
-                    col.load(ring.slot((int)(k % L.stages), o), ring.shift_of(row + col.first), v);
+                    col.load(ring.slot(stage, o), ring.shift_of(row + col.first), v);
                 } else {
-                    col.load(row, live, v);
+                    col.load(row, true, v);
                 }
             };
             load(0, d0);
             load(1, gz);
             load(2, y);
             load(3, rh);
-            col.weight(p.post_weight, p.bf16_weights, 0, w);
-            col.weight(p.gate, p.bf16_weights, live ? gate_row : 0, gt);
 #pragma unroll
             for (int i = 0; i < C; i++) {
                 y[i] *= post;
-                w[i] *= gt[i];
-                rh[i] = fmaf(p.residual_scale, rh[i], w[i] * y[i]) * pre;
+                rh[i] = fmaf(wg[i], y[i], p.residual_scale * rh[i]) * pre;
                 pre_acc[i] = fmaf(gz[i], rh[i], pre_acc[i]);
-            }
-            col.weight(p.pre_weight, p.bf16_weights, 0, gt);
-#pragma unroll
-            for (int i = 0; i < C; i++) {
-                const float h = gz[i] * gt[i];
+                const float h = gz[i] * pw[i];
                 s = fmaf(h, rh[i], s);
                 d0[i] = fmaf(pre, h, d0[i]);
             }
         }
-        const float m1 = pre * (row_sum(s) / (float)p.dim);
-        if (RING && tid == 0 && ring.ok && issued < count) {
-            ring.load((int)(issued % L.stages), token(issued), p.in);
-            issued++;
+        const float m1 = pre * (row_sum(s) * inv_dim);
+        if (RING) {
+            if (tid < 4 && ring.ok && issued < count) {
+                ring.load(stage, next.t, tid, p.in[tid]);
+                issued++;
+                advance(next);
+            }
+            if (++stage == L.stages) {
+                stage = 0;
+                phase++;
+            }
         }
         // d = gr + pre (h - rhat mean(h rhat)), k = d * gate * post_weight
         s = 0.0f;
+        if (RING || live) {
 #pragma unroll
-        for (int i = 0; i < C; i++) {
-            const float d = fmaf(-m1, rh[i], d0[i]);
-            const float ay = d * y[i];
-            a[i] += ay;
-            rh[i] = p.residual_scale * d;
-            d0[i] = d * w[i];
-            s = fmaf(w[i], ay, s);
+            for (int i = 0; i < C; i++) {
+                const float d = fmaf(-m1, rh[i], d0[i]);
+                a[i] = fmaf(d, y[i], a[i]);
+                rh[i] = p.residual_scale * d;
+                d0[i] = d * wg[i];
+                s = fmaf(d0[i], y[i], s);
+            }
         }
         col.store((T*)p.grad_x + t * p.grad_x_stride, live, rh);
-        const float m2 = row_sum(s) / (float)p.dim;
+        const float m2 = row_sum(s) * inv_dim;
 #pragma unroll
         for (int i = 0; i < C; i++) d0[i] = post * fmaf(-m2, y[i], d0[i]);
         col.store((T*)p.grad_y + t * p.grad_y_stride, live, d0);
-        if (GROUPS && ++in_gate == p.per_gate) {  // A of this gate row is complete
-            in_gate = 0;
-            col.weight(p.gate, p.bf16_weights, live ? gate_row : 0, w);
+        if (GROUPS && now.in_gate + 1 == p.per_gate) {  // A of this gate row is complete
+            float w[C];
+            col.weight(p.gate, p.bf16_weights, live ? now.gate : 0, w);
 #pragma unroll
-            for (int i = 0; i < C; i++) ga[i] = fmaf(w[i], a[i], ga[i]);
+            for (int i = 0; i < C; i++) ga[i] = RING || live ? fmaf(w[i], a[i], ga[i]) : ga[i];
             if (p.grad_gate && live) {
                 col.weight(p.post_weight, p.bf16_weights, 0, w);
 #pragma unroll
                 for (int i = 0; i < C; i++) w[i] *= a[i];
-                if (p.bf16_weights) Columns<Bf16, N, C>{tid, L.tx, col.first, p.dim}.store((Bf16*)p.grad_gate + gate_row * p.dim, true, w);
-                else Columns<float, N, C>{tid, L.tx, col.first, p.dim}.store((float*)p.grad_gate + gate_row * p.dim, true, w);
+                if (p.bf16_weights) Columns<Bf16, N, C>{tid, L.tx, col.first, p.dim}.store((Bf16*)p.grad_gate + now.gate * p.dim, true, w);
+                else Columns<float, N, C>{tid, L.tx, col.first, p.dim}.store((float*)p.grad_gate + now.gate * p.dim, true, w);
             }
 #pragma unroll
             for (int i = 0; i < C; i++) a[i] = 0.0f;
-            gate_row += L.ty;
+            if (k + 1 < count) load_gate(now.gate + L.ty);
         }
+        advance(now);
     }
     if (RING && tid == 0 && !ring.ok) ring.drain((int)issued);
+    __syncthreads();  // every row has left the ring, whose memory the sums reuse
     if (!GROUPS) {
         float gt[C];
         col.weight(p.gate, p.bf16_weights, gate_row, gt);
@@ -489,7 +553,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
         for (int i = 0; i < C; i++) ga[i] = gt[i] * a[i];
     }
     float* part = p.part + block * p.slots * p.pitch;
-    float* joined = (float*)dyn;  // every row has left the ring
+    float* joined = (float*)dyn;
     store_part(col, ty, L.ty, joined, part, ga);
     store_part(col, ty, L.ty, joined, part + p.pitch, pre_acc);
     if (!GROUPS) store_part(col, ty, L.ty, joined, part + 2 * p.pitch, a);

@@ -90,6 +90,40 @@ __device__ __forceinline__ void store_n(T* p, int n, const float (&v)[N]) {
         if (i < n) put(p + i, v[i]);
 }
 
+// N consecutive elements that are in range as a whole or not at all.
+template <class T, int N>
+__device__ __forceinline__ void load_whole(const T* p, bool in, float (&v)[N]) {
+    constexpr int E = kVecOf<T>;
+    if (!in) {
+#pragma unroll
+        for (int i = 0; i < N; i++) v[i] = 0.0f;
+    } else if constexpr (N % E == 0) {
+        load_n<T, N>(p, N, v);
+    } else if constexpr (N == 4 && E == 8) {  // half a vector of bf16
+        const uint2 u = *(const uint2*)p;
+        v[0] = __uint_as_float(u.x << 16);
+        v[1] = __uint_as_float(u.x & 0xFFFF0000u);
+        v[2] = __uint_as_float(u.y << 16);
+        v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i++) v[i] = to_f32(p[i]);
+    }
+}
+template <class T, int N>
+__device__ __forceinline__ void store_whole(T* p, bool in, const float (&v)[N]) {
+    constexpr int E = kVecOf<T>;
+    if (!in) return;
+    if constexpr (N % E == 0) {
+        store_n<T, N>(p, N, v);
+    } else if constexpr (N == 4 && E == 8) {
+        *(uint2*)p = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i++) put(p + i, v[i]);
+    }
+}
+
 // The id of a token, whatever its width.
 __device__ __forceinline__ int64_t load_id(const void* ids, int64_t t, bool wide) {
     return wide ? ((const int64_t*)ids)[t] : (int64_t)((const int32_t*)ids)[t];
