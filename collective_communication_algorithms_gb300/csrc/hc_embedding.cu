@@ -8,10 +8,14 @@
 // which blocks run, so the tokens are grouped by row first:
 //  - up to kEmbeddingFewTokens tokens, every block finds the tokens of its
 //    own row by comparing all ids (one launch, no scratch);
-//  - above, a stable radix sort of (row, token), then sums over groups of
-//    kEmbeddingSumChunk sorted tokens.  A row whose tokens all lie in one
-//    group is written by it; a row cut by a group's end leaves partial sums
-//    in scratch, added up in group order by a last kernel.
+//  - above, a stable radix sort of (row, token), in the shared memory of one
+//    cluster while it holds the tokens, else in passes over global memory;
+//    then sums over groups of sorted tokens.  A row whose tokens all lie in
+//    one group is written by it; a row cut by a group's end leaves partial
+//    sums in scratch and its place on a list, and a last kernel adds up the
+//    listed rows' partial sums in group order.
+#include <algorithm>
+
 #include "hc_ops.cuh"
 
 namespace hc {
@@ -104,11 +108,11 @@ struct GradParams {
     uint32_t *keys_in, *pos_in, *keys_out, *pos_out;
     uint32_t *hist, *hist_next, *hist_after;  // this pass's digit counts, the next's, the one after's
     float* part;
+    uint32_t* cut;      // [0]: rows cut by a group's end, then the groups they begin in
     int64_t pitch, chunks, sum_chunks;
-    int chunk, shift, bits, next_shift;
+    int chunk, shift, bits, next_shift, passes, sum_chunk;
     int tiles;          // column tiles of a row
-    int64_t sum_blocks; // blocks of the sum; the others fill rows without tokens
-    int fill_rows;      // rows of one filling block
+    int64_t sum_blocks, fill_blocks;  // sums; zeros for rows without tokens
 };
 
 // Row of token t in this table, or rows when it has none (padding, another
@@ -209,18 +213,138 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const GradParams p) {
 }
 
 // ---------------------------------------------------------------------------
-// stable radix sort of (row, token): a block orders `chunk` tokens.
+// stable radix sort of (row, token) in the shared memory of one cluster: block
+// r holds places [r * chunk, (r + 1) * chunk).  In every pass a warp takes a
+// run of its block's tokens; a token's new place is (tokens of smaller
+// digits) + (tokens of its digit in earlier blocks, in earlier warps, earlier
+// in its warp).  The last pass writes to global memory.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxBins = 512;  // digits of at most 9 bits
+constexpr int64_t kClusterSortTokens = kMaxCluster * 8192;
 
+struct ClusterSort {
+    uint32_t warp_at[kSortWarps][kMaxBins];     // tokens of a warp, then the place of its next one
+    uint32_t counts[kMaxCluster][kMaxBins];     // tokens of every block of the cluster
+    uint32_t scan[kSortWarps];
+};
+
+__device__ __forceinline__ unsigned remote_addr(const void* local, unsigned rank) {
+    unsigned a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(local)), "r"(rank));
+    return a;
+}
+
+__global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(const GradParams p) {
+    extern __shared__ __align__(16) unsigned char dyn[];
+    ClusterSort& sh = *(ClusterSort*)dyn;
+    uint2* const buf = (uint2*)(dyn + sizeof(ClusterSort));  // two of chunk places
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const unsigned rank = blockIdx.x, blocks = gridDim.x;
+    const int bins = 1 << p.bits;
+    const int64_t place0 = (int64_t)rank * p.chunk;
+    const int have = (int)max((int64_t)0, min((int64_t)p.chunk, p.tokens - place0));
+    const int per_warp = p.chunk / kSortWarps;  // a multiple of 32
+    const int begin = warp * per_warp, end = min(begin + per_warp, have);
+    if (blocks > 1) cluster_arrive();
+    grid_wait();
+    grid_release();
+    if (rank == 0 && tid == 0) p.cut[0] = 0;
+    if (blocks > 1) cluster_wait();  // every block runs
+    for (int pass = 0; pass < p.passes; pass++) {
+        const int shift = pass * p.bits;
+        const bool last = pass + 1 == p.passes;
+        const uint2* from = buf + (size_t)((pass + 1) & 1) * p.chunk;
+        const unsigned to = smem_addr(buf + (size_t)(pass & 1) * p.chunk);
+        auto take = [&](int i) {
+            return pass ? from[i] : make_uint2(row_of(p, place0 + i), (uint32_t)(place0 + i));
+        };
+        for (int w = 0; w < kSortWarps; w++)
+            if (tid < bins) sh.warp_at[w][tid] = 0;
+        __syncthreads();
+        for (int i = begin + lane; i < end; i += 32) atomicAdd(&sh.warp_at[warp][(take(i).x >> shift) & (bins - 1)], 1u);
+        __syncthreads();
+        if (tid < bins) {
+            uint32_t n = 0;
+            for (int w = 0; w < kSortWarps; w++) n += sh.warp_at[w][tid];
+            for (unsigned r = 0; r < blocks; r++)
+                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote_addr(&sh.counts[rank][tid], r)), "r"(n) : "memory");
+        }
+        if (blocks > 1) {
+            cluster_arrive();
+            cluster_wait();
+        } else {
+            __syncthreads();
+        }
+        uint32_t before = 0, total = 0;
+        if (tid < bins)
+            for (unsigned r = 0; r < blocks; r++) {
+                const uint32_t n = sh.counts[r][tid];
+                if (r < rank) before += n;
+                total += n;
+            }
+        uint32_t inc = total;  // inclusive sum over the digits
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+            if (lane >= o) inc += u;
+        }
+        if (lane == 31) sh.scan[warp] = inc;
+        __syncthreads();
+        if (tid < bins) {
+            uint32_t at = inc - total + before;
+            for (int w = 0; w < warp; w++) at += sh.scan[w];
+            for (int w = 0; w < kSortWarps; w++) {
+                const uint32_t n = sh.warp_at[w][tid];
+                sh.warp_at[w][tid] = at;
+                at += n;
+            }
+        }
+        __syncthreads();
+        for (int b = begin; b < end; b += 32) {
+            const bool in = b + lane < end;
+            const uint2 e = in ? take(b + lane) : make_uint2(0u, 0u);
+            const uint32_t d = in ? (e.x >> shift) & (bins - 1) : (uint32_t)bins;
+            const uint32_t peers = __match_any_sync(0xFFFFFFFFu, d);
+            const uint32_t lower = __popc(peers & ((1u << lane) - 1));
+            const uint32_t at = in ? sh.warp_at[warp][d] : 0u;
+            __syncwarp();
+            if (in && lower == 0) sh.warp_at[warp][d] = at + __popc(peers);
+            __syncwarp();
+            if (!in) continue;
+            const uint32_t place = at + lower;
+            if (last) {
+                p.keys_out[place] = e.x;
+                p.pos_out[place] = e.y;
+            } else {
+                const unsigned r = place / (unsigned)p.chunk, o = place - r * (unsigned)p.chunk;
+                unsigned a;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(to + o * 8), "r"(r));
+                asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(e.x), "r"(e.y) : "memory");
+            }
+        }
+        if (!last) {
+            if (blocks > 1) {
+                cluster_arrive();
+                cluster_wait();
+            } else {
+                __syncthreads();
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the same sort in passes over global memory: a block orders `chunk` tokens.
+// ---------------------------------------------------------------------------
 // Digit counts of every chunk for the first pass; zeroes the next pass's.
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const GradParams p) {
     __shared__ uint32_t count[kMaxBins];
     grid_wait();
     grid_release();
     const int bins = 1 << p.bits;
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.cut[0] = 0;
     for (int b = threadIdx.x; b < bins; b += kSortThreads) count[b] = 0;
     __syncthreads();
     const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
@@ -316,22 +440,62 @@ __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(const GradParam
 }
 
 // ---------------------------------------------------------------------------
-// sums over sorted tokens: a warp takes 32 * N columns of kEmbeddingSumChunk
-// tokens; the blocks after sum_blocks zero the rows without tokens.
+// sums over sorted tokens: a warp takes 256 columns of sum_chunk tokens, of
+// which kRowsInFlight (and the table's rows that they end, when adding to
+// them) are on their way at a time, as they lie in memory.
 // ---------------------------------------------------------------------------
 constexpr int kSumThreads = 256;
 constexpr int kSumWarps = kSumThreads / 32;
-constexpr int kRowsInFlight = 8;
+constexpr int kLaneCols = 8;       // columns of a lane
+constexpr int kRowsInFlight = 4;
 
-template <class TO, class TT, int N>
+// A lane's columns of a row of T: neighbouring ones (VEC), or 32 apart.
+template <class T, bool VEC>
+struct Lane {
+    union {
+        uint4 vec[kLaneCols * sizeof(T) / 16];
+        T e[kLaneCols];
+    };
+    // n: columns of the row from the lane's first
+    __device__ __forceinline__ void load(const T* row, int c, int n) {
+        if (VEC && n >= kLaneCols) {
+#pragma unroll
+            for (int i = 0; i < (int)(kLaneCols * sizeof(T) / 16); i++) vec[i] = ((const uint4*)(row + c))[i];
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kLaneCols; i++) {
+            const int o = VEC ? i : 32 * i;
+            if (o < n) e[i] = row[c + o];
+        }
+    }
+    __device__ __forceinline__ float get(int i) const { return to_f32(e[i]); }
+};
+template <class T, bool VEC>
+__device__ __forceinline__ void store_lane(T* row, int c, int n, const float (&v)[kLaneCols]) {
+    if constexpr (VEC) {
+        store_n<T, kLaneCols>(row + c, n, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kLaneCols; i++)
+            if (32 * i < n) put(row + c + 32 * i, v[i]);
+    }
+}
+
+template <class TO, class TT, bool VEC>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const GradParams p) {
     grid_wait();
     grid_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t none = (uint32_t)p.rows;
-    if ((int64_t)blockIdx.x >= p.sum_blocks) {
+    // sums and fills alternate as their numbers allow, so that the fills'
+    // writes overlap the sums' waits for their rows
+    const int64_t b = blockIdx.x, both = 2 * min(p.sum_blocks, p.fill_blocks);
+    const bool fill = b < both ? b & 1 : p.fill_blocks > p.sum_blocks;
+    const int64_t index = b < both ? b >> 1 : b - both / 2;
+    if (fill) {
         // each warp: 32 rows, a lane looks one up among the sorted keys
-        const int64_t v0 = (((int64_t)blockIdx.x - p.sum_blocks) * kSumWarps + warp) * 32;
+        const int64_t v0 = (index * kSumWarps + warp) * 32;
         int64_t lo = 0, hi = p.tokens;
         while (lo < hi) {
             const int64_t mid = (lo + hi) / 2;
@@ -341,110 +505,127 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const GradParams p) {
         const bool empty = v0 + lane < p.rows && (lo >= p.tokens || p.keys_in[lo] != (uint32_t)(v0 + lane));
         uint32_t todo = __ballot_sync(0xFFFFFFFFu, empty);
         while (todo) {
-            zero_row<TT, N>(p, v0 + __ffs(todo) - 1, lane, 32);
+            zero_row<TT, VEC ? kLaneCols : 1>(p, v0 + __ffs(todo) - 1, lane, 32);
             todo &= todo - 1;
         }
         return;
     }
-    const int64_t item = (int64_t)blockIdx.x * kSumWarps + warp;
+    const int64_t item = index * kSumWarps + warp;
     const int64_t chunk = item / p.tiles;
     if (chunk >= p.sum_chunks) return;
-    const int c = ((int)(item % p.tiles) * 32 + lane) * N;
+    const int tile = (int)(item % p.tiles);
+    const int c = tile * 32 * kLaneCols + (VEC ? lane * kLaneCols : lane);
     const int n = p.dim - c;
-    const int64_t s0 = chunk * kEmbeddingSumChunk;
-    const int len = (int)(p.tokens - s0 < kEmbeddingSumChunk ? p.tokens - s0 : kEmbeddingSumChunk);
-    uint32_t cur = p.keys_in[s0];
-    if (cur == none) return;  // the tokens without a row come last
-    const bool continues = s0 > 0 && p.keys_in[s0 - 1] == cur;
-    const uint32_t last = p.keys_in[s0 + len - 1];
-    const bool goes_on = s0 + len < p.tokens && p.keys_in[s0 + len] == last;
-    bool head = continues;  // the run under way began in an earlier chunk
-    float acc[N] = {};
-    for (int b = 0; b < len; b += 32) {
-        const bool in = b + lane < len;
-        const uint32_t my_key = in ? p.keys_in[s0 + b + lane] : none;
-        const uint32_t my_pos = in ? p.pos_in[s0 + b + lane] : 0u;
-        const int m = __popc(__ballot_sync(0xFFFFFFFFu, my_key != none));  // a prefix of the lanes
-        for (int j = 0; j < m; j += kRowsInFlight) {
-            float v[kRowsInFlight][N];
+    const int64_t s0 = chunk * p.sum_chunk;
+    const int len = (int)min((int64_t)p.sum_chunk, p.tokens - s0);
+    const uint32_t key = lane < len ? p.keys_in[s0 + lane] : none;
+    const uint32_t pos = lane < len ? p.pos_in[s0 + lane] : 0u;
+    const uint32_t prev = s0 > 0 ? p.keys_in[s0 - 1] : none;
+    const uint32_t next = s0 + len < p.tokens ? p.keys_in[s0 + len] : none;
+    const int m = __popc(__ballot_sync(0xFFFFFFFFu, key != none));  // a prefix: tokens without a row come last
+    if (m == 0) return;
+    const uint32_t first = __shfl_sync(0xFFFFFFFFu, key, 0), last = __shfl_sync(0xFFFFFFFFu, key, m - 1);
+    const uint32_t after = __shfl_down_sync(0xFFFFFFFFu, key, 1);
+    // a row's last token here; of a row that goes on after these tokens, that
+    // began before them
+    const bool ends = lane < m && (lane == m - 1 || after != key);
+    const bool goes_on = ends && key == last && next == last;
+    const bool began = ends && key == first && prev == first;
+    const uint32_t end_mask = __ballot_sync(0xFFFFFFFFu, ends);
+    const uint32_t head_mask = __ballot_sync(0xFFFFFFFFu, began);
+    const uint32_t tail_mask = __ballot_sync(0xFFFFFFFFu, goes_on && !began);
+    const uint32_t old_mask = p.accumulate ? end_mask & ~(head_mask | tail_mask) : 0u;
+    if (tail_mask && tile == 0 && lane == 0) p.cut[1 + atomicAdd(p.cut, 1u)] = (uint32_t)chunk;
+    float acc[kLaneCols] = {};
+    for (int j = 0; j < m; j += kRowsInFlight) {
+        Lane<TO, VEC> v[kRowsInFlight];
+        Lane<TT, VEC> old[kRowsInFlight];
 #pragma unroll
-            for (int k = 0; k < kRowsInFlight; k++) {
-                const uint32_t t = __shfl_sync(0xFFFFFFFFu, my_pos, j + k);
-                load_n<TO, N>((const TO*)p.grad + (int64_t)t * p.grad_stride + c, j + k < m ? n : 0, v[k]);
-            }
-#pragma unroll
-            for (int k = 0; k < kRowsInFlight; k++) {
-                const uint32_t key = __shfl_sync(0xFFFFFFFFu, my_key, j + k);
-                if (j + k < m && key != cur) {
-                    if (head) store_n<float, N>(p.part + chunk * 2 * p.pitch + c, n, acc);
-                    else write_row<TT, N>(p, cur, c, acc);
-                    head = false;
-                    cur = key;
-#pragma unroll
-                    for (int i = 0; i < N; i++) acc[i] = 0.0f;
-                }
-#pragma unroll
-                for (int i = 0; i < N; i++) acc[i] += v[k][i];
-            }
+        for (int k = 0; k < kRowsInFlight; k++) {
+            const uint32_t t = __shfl_sync(0xFFFFFFFFu, pos, j + k), r = __shfl_sync(0xFFFFFFFFu, key, j + k);
+            if (j + k < m) v[k].load((const TO*)p.grad + (int64_t)t * p.grad_stride, c, n);
+            if (old_mask >> (j + k) & 1) old[k].load((const TT*)p.table + (int64_t)r * p.table_stride, c, n);
         }
-        if (m < 32) break;
+#pragma unroll
+        for (int k = 0; k < kRowsInFlight; k++) {
+            const uint32_t bit = 1u << (j + k);
+            const uint32_t r = __shfl_sync(0xFFFFFFFFu, key, j + k);
+            if (j + k < m)
+#pragma unroll
+                for (int i = 0; i < kLaneCols; i++) acc[i] += v[k].get(i);
+            if (!(end_mask & bit)) continue;
+            if ((head_mask | tail_mask) & bit) {
+                store_lane<float, VEC>(p.part + (chunk * 2 + (tail_mask & bit ? 1 : 0)) * p.pitch, c, n, acc);
+            } else {
+                if (old_mask & bit) {
+#pragma unroll
+                    for (int i = 0; i < kLaneCols; i++) acc[i] = fmaf(acc[i], p.scale, old[k].get(i));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kLaneCols; i++) acc[i] *= p.scale;
+                }
+                store_lane<TT, VEC>((TT*)p.table + (int64_t)r * p.table_stride, c, n, acc);
+            }
+#pragma unroll
+            for (int i = 0; i < kLaneCols; i++) acc[i] = 0.0f;
+        }
     }
-    if (goes_on && last != none)
-        store_n<float, N>(p.part + (chunk * 2 + (head ? 0 : 1)) * p.pitch + c, n, acc);
-    else if (head)
-        store_n<float, N>(p.part + chunk * 2 * p.pitch + c, n, acc);
-    else
-        write_row<TT, N>(p, cur, c, acc);
 }
 
-// Rows cut by the end of chunk blockIdx.x / tiles, where they begin: slot 1
-// of that chunk and slot 0 of the chunks after it.  The warps add equal parts
-// of the list, joined in order.
+// The rows on the list: slot 1 of the group where a row begins and slot 0 of
+// the groups after it.  The warps of a block add equal parts of a row's
+// partial sums, joined in order.
 constexpr int kJoinWarps = 8;
 template <class TT, int N>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const GradParams p) {
     __shared__ float sums[kJoinWarps][32 * N];
     grid_wait();
     grid_release();
-    const int64_t chunk = blockIdx.x / p.tiles;
-    const int64_t s1 = (chunk + 1) * kEmbeddingSumChunk;
-    if (s1 >= p.tokens) return;
-    const uint32_t key = p.keys_in[s1];
-    if (key == (uint32_t)p.rows || p.keys_in[s1 - 1] != key) return;
-    if (chunk > 0 && p.keys_in[s1 - kEmbeddingSumChunk - 1] == key) return;  // began earlier
-    // the last chunk whose first token is of this row
-    int64_t lo = chunk + 1, hi = p.sum_chunks - 1;
-    while (lo < hi) {
-        const int64_t mid = (lo + hi + 1) / 2;
-        if (p.keys_in[mid * kEmbeddingSumChunk] == key) lo = mid;
-        else hi = mid - 1;
-    }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = ((int)(blockIdx.x % p.tiles) * 32 + lane) * N;
-    const int n = p.dim - c;
-    const int64_t count = lo - chunk + 1, per = (count + kJoinWarps - 1) / kJoinWarps;
-    const int64_t a = warp * per, b = a + per < count ? a + per : count;
-    float acc[N] = {};
+    const int64_t items = (int64_t)p.cut[0] * p.tiles;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int64_t chunk = p.cut[1 + item / p.tiles];
+        const uint32_t key = p.keys_in[(chunk + 1) * p.sum_chunk];
+        // the last group whose first token is of this row: doubling, then halving
+        int64_t lo = chunk + 1, hi = chunk + 2, step = 1;
+        while (hi < p.sum_chunks && p.keys_in[hi * p.sum_chunk] == key) {
+            lo = hi;
+            step *= 2;
+            hi += step;
+        }
+        hi = min(hi, p.sum_chunks);
+        while (hi - lo > 1) {
+            const int64_t mid = (lo + hi) / 2;
+            if (p.keys_in[mid * p.sum_chunk] == key) lo = mid;
+            else hi = mid;
+        }
+        const int c = ((int)(item % p.tiles) * 32 + lane) * N;
+        const int n = p.dim - c;
+        const int64_t count = lo - chunk + 1, per = (count + kJoinWarps - 1) / kJoinWarps;
+        const int64_t a = warp * per, b = min(a + per, count);
+        float acc[N] = {};
 #pragma unroll 4
-    for (int64_t k = a; k < b; k++) {
-        float v[N];
-        load_n<float, N>(p.part + ((chunk + k) * 2 + (k == 0 ? 1 : 0)) * p.pitch + c, n, v);
+        for (int64_t k = a; k < b; k++) {
+            float v[N];
+            load_n<float, N>(p.part + ((chunk + k) * 2 + (k == 0 ? 1 : 0)) * p.pitch + c, n, v);
 #pragma unroll
-        for (int i = 0; i < N; i++) acc[i] += v[i];
+            for (int i = 0; i < N; i++) acc[i] += v[i];
+        }
+        __syncthreads();  // the last row's sums have been read
+#pragma unroll
+        for (int i = 0; i < N; i++) sums[warp][i * 32 + lane] = acc[i];
+        __syncthreads();
+        if (warp) continue;
+        for (int w = 1; w < kJoinWarps && w * per < count; w++)
+#pragma unroll
+            for (int i = 0; i < N; i++) acc[i] += sums[w][i * 32 + lane];
+        write_row<TT, N>(p, key, c, acc);
     }
-#pragma unroll
-    for (int i = 0; i < N; i++) sums[warp][i * 32 + lane] = acc[i];
-    __syncthreads();
-    if (warp) return;
-    for (int w = 1; w < kJoinWarps && w * per < count; w++)
-#pragma unroll
-        for (int i = 0; i < N; i++) acc[i] += sums[w][i * 32 + lane];
-    write_row<TT, N>(p, key, c, acc);
 }
 
 template <class TO, class TT>
 cudaError_t launch_grad(GradParams& p, const EmbeddingScratch& sc, unsigned char* scratch, bool vec,
-                        cudaStream_t stream) {
+                        cudaStream_t stream, int sms) {
     constexpr int W = kVecOf<TO> > kVecOf<TT> ? kVecOf<TO> : kVecOf<TT>;
     const int64_t nv = (p.dim + (vec ? W : 1) - 1) / (vec ? W : 1);
     void* args[] = {&p};
@@ -459,54 +640,69 @@ cudaError_t launch_grad(GradParams& p, const EmbeddingScratch& sc, unsigned char
         return launch_op(fn, dim3((unsigned)grid), dim3(kFewThreads), args, 0, stream);
     }
     uint32_t *keys[2], *pos[2];
-    uint32_t* const hist = (uint32_t*)(scratch + sc.hist);
-    const size_t hist_len = (size_t)sc.chunks << sc.bits;
     for (int i = 0; i < 2; i++) {
         keys[i] = (uint32_t*)(scratch + sc.keys[i]);
         pos[i] = (uint32_t*)(scratch + sc.pos[i]);
     }
     p.part = (float*)(scratch + sc.part);
+    p.cut = (uint32_t*)(scratch + sc.cut);
     p.pitch = sc.pitch;
     p.chunk = sc.chunk;
     p.chunks = sc.chunks;
     p.bits = sc.bits;
+    p.passes = sc.passes;
+    p.sum_chunk = sc.sum_chunk;
     p.sum_chunks = sc.sum_chunks;
-    p.hist = hist;
-    p.hist_next = hist + hist_len;
-    cudaError_t e = launch_op((const void*)sort_count_kernel, dim3((unsigned)p.chunks), dim3(kSortThreads), args, 0, stream);
-    if (e != cudaSuccess) return e;
-    for (int i = 0; i < sc.passes; i++) {
-        p.shift = i * sc.bits;
-        p.next_shift = p.shift + sc.bits;
-        p.keys_in = keys[(i + 1) & 1];
-        p.pos_in = pos[(i + 1) & 1];
-        p.keys_out = keys[i & 1];
-        p.pos_out = pos[i & 1];
-        p.hist = hist + (size_t)(i % 3) * hist_len;
-        p.hist_next = i + 1 < sc.passes ? hist + (size_t)((i + 1) % 3) * hist_len : nullptr;
-        p.hist_after = i + 2 < sc.passes ? hist + (size_t)((i + 2) % 3) * hist_len : nullptr;
-        const bool small = sc.chunk <= kSortThreads * 4;
-        const void* fn = i == 0 ? (small ? (const void*)sort_pass_kernel<4, true> : (const void*)sort_pass_kernel<16, true>)
-                                : (small ? (const void*)sort_pass_kernel<4, false> : (const void*)sort_pass_kernel<16, false>);
-        e = launch_op(fn, dim3((unsigned)p.chunks), dim3(kSortThreads), args, 0, stream);
+    cudaError_t e;
+    if (sc.cluster) {
+        p.keys_out = keys[0];
+        p.pos_out = pos[0];
+        const int smem = (int)sizeof(ClusterSort) + sc.chunk * 8 * (sc.passes > 2 ? 2 : 1);
+        if (!allow_smem((void*)cluster_sort_kernel, smem)) return cudaErrorInvalidValue;
+        e = launch_op((const void*)cluster_sort_kernel, dim3((unsigned)sc.cluster), dim3(kSortThreads), args, (size_t)smem, stream, sc.cluster);
         if (e != cudaSuccess) return e;
+        p.keys_in = keys[0];
+        p.pos_in = pos[0];
+    } else {
+        uint32_t* const hist = (uint32_t*)(scratch + sc.hist);
+        const size_t hist_len = (size_t)sc.chunks << sc.bits;
+        p.hist = hist;
+        p.hist_next = hist + hist_len;
+        e = launch_op((const void*)sort_count_kernel, dim3((unsigned)p.chunks), dim3(kSortThreads), args, 0, stream);
+        if (e != cudaSuccess) return e;
+        for (int i = 0; i < sc.passes; i++) {
+            p.shift = i * sc.bits;
+            p.next_shift = p.shift + sc.bits;
+            p.keys_in = keys[(i + 1) & 1];
+            p.pos_in = pos[(i + 1) & 1];
+            p.keys_out = keys[i & 1];
+            p.pos_out = pos[i & 1];
+            p.hist = hist + (size_t)(i % 3) * hist_len;
+            p.hist_next = i + 1 < sc.passes ? hist + (size_t)((i + 1) % 3) * hist_len : nullptr;
+            p.hist_after = i + 2 < sc.passes ? hist + (size_t)((i + 2) % 3) * hist_len : nullptr;
+            const bool small = sc.chunk <= kSortThreads * 4;
+            const void* fn = i == 0 ? (small ? (const void*)sort_pass_kernel<4, true> : (const void*)sort_pass_kernel<16, true>)
+                                    : (small ? (const void*)sort_pass_kernel<4, false> : (const void*)sort_pass_kernel<16, false>);
+            e = launch_op(fn, dim3((unsigned)p.chunks), dim3(kSortThreads), args, 0, stream);
+            if (e != cudaSuccess) return e;
+        }
+        p.keys_in = keys[(sc.passes - 1) & 1];
+        p.pos_in = pos[(sc.passes - 1) & 1];
     }
-    p.keys_in = keys[(sc.passes - 1) & 1];
-    p.pos_in = pos[(sc.passes - 1) & 1];
-    p.tiles = (int)((nv + 31) / 32);
+    p.tiles = (p.dim + 32 * kLaneCols - 1) / (32 * kLaneCols);
     p.sum_blocks = (p.sum_chunks * p.tiles + kSumWarps - 1) / kSumWarps;
-    const int64_t fill = p.accumulate ? 0 : (p.rows + kSumThreads - 1) / kSumThreads;
-    if (!grid_ok(p.sum_blocks + fill)) return cudaErrorInvalidValue;
-    e = launch_op(vec ? (const void*)sum_kernel<TO, TT, W> : (const void*)sum_kernel<TO, TT, 1>,
-                  dim3((unsigned)(p.sum_blocks + fill)), dim3(kSumThreads), args, 0, stream);
+    p.fill_blocks = p.accumulate ? 0 : (p.rows + kSumThreads - 1) / kSumThreads;
+    if (!grid_ok(p.sum_blocks + p.fill_blocks)) return cudaErrorInvalidValue;
+    e = launch_op(vec ? (const void*)sum_kernel<TO, TT, true> : (const void*)sum_kernel<TO, TT, false>,
+                  dim3((unsigned)(p.sum_blocks + p.fill_blocks)), dim3(kSumThreads), args, 0, stream);
     if (e != cudaSuccess || p.sum_chunks < 2) return e;
     // partial rows are 16-byte aligned, the table's may not be
     constexpr int J = kVecOf<TT>;
     const int64_t jv = (p.dim + (vec ? J : 1) - 1) / (vec ? J : 1);
     p.tiles = (int)((jv + 31) / 32);
-    if (!grid_ok((p.sum_chunks - 1) * p.tiles)) return cudaErrorInvalidValue;
-    return launch_op(vec ? (const void*)join_kernel<TT, J> : (const void*)join_kernel<TT, 1>,
-                     dim3((unsigned)((p.sum_chunks - 1) * p.tiles)), dim3(kJoinWarps * 32), args, 0, stream);
+    const int64_t grid = std::min<int64_t>((p.sum_chunks - 1) * p.tiles, (int64_t)sms * 8);
+    return launch_op(vec ? (const void*)join_kernel<TT, J> : (const void*)join_kernel<TT, 1>, dim3((unsigned)grid),
+                     dim3(kJoinWarps * 32), args, 0, stream);
 }
 
 bool aligned16(const void* p, int64_t stride, int es) {
@@ -543,9 +739,21 @@ EmbeddingScratch embedding_scratch(int64_t tokens, int64_t rows, int64_t dim) {
     while (bits < 32 && (rows >> bits)) bits++;
     s.passes = (bits + 8) / 9;
     s.bits = (bits + s.passes - 1) / s.passes;
-    s.chunk = kSortThreads * (tokens <= (1 << 18) ? 4 : 16);
+    if (tokens <= kClusterSortTokens) {
+        // at least 2048 tokens a block
+        s.cluster = 1;
+        while (s.cluster < kMaxCluster && tokens > 2048 * s.cluster) s.cluster *= 2;
+        const int64_t per = (tokens + s.cluster - 1) / s.cluster;
+        s.chunk = (int)((per + kSortThreads - 1) / kSortThreads * kSortThreads);
+    } else {
+        s.chunk = kSortThreads * (tokens <= (1 << 18) ? 4 : 16);
+    }
     s.chunks = (tokens + s.chunk - 1) / s.chunk;
-    s.sum_chunks = (tokens + kEmbeddingSumChunk - 1) / kEmbeddingSumChunk;
+    // groups of 8 to 32 tokens (a lane each), about 2400 warps' worth
+    s.sum_chunk = 32;
+    const int64_t tiles = (dim + 32 * kLaneCols - 1) / (32 * kLaneCols);
+    while (s.sum_chunk > 8 && tokens * tiles < 2400 * s.sum_chunk) s.sum_chunk /= 2;
+    s.sum_chunks = (tokens + s.sum_chunk - 1) / s.sum_chunk;
     s.pitch = (dim + 7) / 8 * 8;
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -553,18 +761,18 @@ EmbeddingScratch embedding_scratch(int64_t tokens, int64_t rows, int64_t dim) {
         at += (bytes + 255) / 256 * 256;
         return o;
     };
-    for (int i = 0; i < 2; i++) {
+    for (int i = 0; i < (s.cluster ? 1 : 2); i++) {
         s.keys[i] = take((size_t)tokens * 4);
         s.pos[i] = take((size_t)tokens * 4);
     }
-    s.hist = take((size_t)3 * s.chunks << (s.bits + 2));
+    if (!s.cluster) s.hist = take((size_t)3 * s.chunks << (s.bits + 2));
+    s.cut = take(((size_t)s.sum_chunks + 1) * 4);
     s.part = take((size_t)s.sum_chunks * 2 * (size_t)s.pitch * 4);
     s.bytes = at;
     return s;
 }
 
 cudaError_t launch_embedding_grad(const hc_embedding_grad_t& a, cudaStream_t stream, int sms) {
-    (void)sms;
     GradParams p = {};
     p.grad = a.grad_out;
     p.ids = a.ids;
@@ -585,8 +793,8 @@ cudaError_t launch_embedding_grad(const hc_embedding_grad_t& a, cudaStream_t str
                      aligned16(a.grad_table, p.table_stride, elem_bytes(a.grad_table_dtype));
     unsigned char* s = (unsigned char*)a.scratch;
     const bool bo = a.grad_out_dtype == HC_BFLOAT16, bt = a.grad_table_dtype == HC_BFLOAT16;
-    if (bo) return bt ? launch_grad<Bf16, Bf16>(p, sc, s, vec, stream) : launch_grad<Bf16, float>(p, sc, s, vec, stream);
-    return bt ? launch_grad<float, Bf16>(p, sc, s, vec, stream) : launch_grad<float, float>(p, sc, s, vec, stream);
+    if (bo) return bt ? launch_grad<Bf16, Bf16>(p, sc, s, vec, stream, sms) : launch_grad<Bf16, float>(p, sc, s, vec, stream, sms);
+    return bt ? launch_grad<float, Bf16>(p, sc, s, vec, stream, sms) : launch_grad<float, float>(p, sc, s, vec, stream, sms);
 }
 
 }  // namespace hc

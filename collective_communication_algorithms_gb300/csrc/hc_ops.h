@@ -12,15 +12,16 @@ cudaError_t launch_embedding(const hc_embedding_t& a, cudaStream_t stream, int s
 // scratch), and the layout of its scratch above that.
 constexpr size_t kEmbeddingFewTokens = 256;
 struct EmbeddingScratch {
-    size_t keys[2], pos[2], hist, part;  // byte offsets
+    size_t keys[2], pos[2], hist, cut, part;  // byte offsets
     size_t bytes;
+    int cluster;          // blocks of the one-cluster sort; 0: passes over global memory
     int chunk;            // tokens per sorting block
     int64_t chunks;
     int passes, bits;     // radix passes, bits of one pass's digit
-    int64_t sum_chunks;   // groups of kEmbeddingSumChunk sorted tokens
+    int sum_chunk;        // sorted tokens summed by one warp
+    int64_t sum_chunks;   // groups of them
     int64_t pitch;        // floats in one row of partial sums
 };
-constexpr int kEmbeddingSumChunk = 64;
 EmbeddingScratch embedding_scratch(int64_t tokens, int64_t rows, int64_t dim);
 cudaError_t launch_embedding_grad(const hc_embedding_grad_t& a, cudaStream_t stream, int sms);
 
