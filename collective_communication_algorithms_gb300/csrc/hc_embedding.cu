@@ -46,7 +46,6 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const LookupPara
     grid_wait();
     grid_release();
     if (c >= p.dim) return;
-    const int n = p.dim - c;
     uint64_t row[U];
     float v[U][N];
 #pragma unroll
@@ -57,12 +56,7 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const LookupPara
     }
 #pragma unroll
     for (int u = 0; u < U; u++) {
-        if (row[u] < (uint64_t)p.rows) {
-            load_n<TI, N>((const TI*)p.table + (int64_t)row[u] * p.table_stride + c, n, v[u]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; i++) v[u][i] = 0.0f;
-        }
+        load_whole<TI, N>((const TI*)p.table + (int64_t)row[u] * p.table_stride + c, row[u] < (uint64_t)p.rows, v[u]);
     }
 #pragma unroll
     for (int u = 0; u < U; u++) {
@@ -70,13 +64,13 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const LookupPara
         if (t >= p.tokens) break;
 #pragma unroll
         for (int i = 0; i < N; i++) v[u][i] *= p.scale;
-        store_n<TO, N>((TO*)p.out + t * p.out_stride + c, n, v[u]);
+        store_whole<TO, N>((TO*)p.out + t * p.out_stride + c, true, v[u]);
     }
 }
 
 template <class TI, class TO>
 cudaError_t launch_lookup(LookupParams& p, bool vec, cudaStream_t stream, int sms) {
-    constexpr int W = kVecOf<TI> > kVecOf<TO> ? kVecOf<TI> : kVecOf<TO>;
+    constexpr int W = std::max(kVecOf<TI>, kVecOf<TO>);
     const int nv = (int)((p.dim + (vec ? W : 1) - 1) / (vec ? W : 1));
     p.tx_log2 = 5;
     while (p.tx_log2 < 8 && (1 << p.tx_log2) < nv) p.tx_log2++;
@@ -108,11 +102,12 @@ struct GradParams {
     uint32_t *keys_in, *pos_in, *keys_out, *pos_out;
     uint32_t *hist, *hist_next, *hist_after;  // this pass's digit counts, the next's, the one after's
     float* part;
+    unsigned char* touched;  // rows with tokens (NULL when adding to the table)
     uint32_t* cut;      // [0]: rows cut by a group's end, then the groups they begin in
     int64_t pitch, chunks, sum_chunks;
     int chunk, shift, bits, next_shift, passes, sum_chunk;
     int tiles;          // column tiles of a row
-    int64_t sum_blocks, fill_blocks;  // sums; zeros for rows without tokens
+    int64_t sum_blocks;  // few tokens: the blocks after them write the rows without tokens
 };
 
 // Row of token t in this table, or rows when it has none (padding, another
@@ -191,17 +186,16 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const GradParams p) {
     if (same[t / 32] & ((1u << (t & 31)) - 1)) return;
     if (c >= p.dim) return;
     float acc[N] = {};
-    const int n = p.dim - c;
     for (int w = t / 32; w < words; w++) {
         uint32_t m = same[w];
         while (m) {
-            constexpr int B = 4;  // rows in flight
+            constexpr int B = 8;  // rows in flight
             float v[B][N];
 #pragma unroll
             for (int b = 0; b < B; b++) {
                 const int s = m ? w * 32 + __ffs(m) - 1 : -1;
                 m &= m - 1;  // 0 stays 0
-                load_n<TO, N>((const TO*)p.grad + (int64_t)(s < 0 ? 0 : s) * p.grad_stride + c, s < 0 ? 0 : n, v[b]);
+                load_whole<TO, N>((const TO*)p.grad + (int64_t)s * p.grad_stride + c, s >= 0, v[b]);
             }
 #pragma unroll
             for (int b = 0; b < B; b++)
@@ -222,7 +216,7 @@ __global__ void __launch_bounds__(kFewThreads) few_kernel(const GradParams p) {
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxBins = 512;  // digits of at most 9 bits
-constexpr int64_t kClusterSortTokens = kMaxCluster * 8192;
+constexpr int64_t kClusterSortTokens = kMaxCluster * 4096;
 
 struct ClusterSort {
     uint32_t warp_at[kSortWarps][kMaxBins];     // tokens of a warp, then the place of its next one
@@ -247,15 +241,24 @@ __global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(const GradPa
     const int have = (int)max((int64_t)0, min((int64_t)p.chunk, p.tokens - place0));
     const int per_warp = p.chunk / kSortWarps;  // a multiple of 32
     const int begin = warp * per_warp, end = min(begin + per_warp, have);
-    if (blocks > 1) cluster_arrive();
     grid_wait();
     grid_release();
     if (rank == 0 && tid == 0) p.cut[0] = 0;
+    if (p.touched)
+        for (int64_t v = rank * kSortThreads + tid; v < (p.rows + 15) / 16; v += (int64_t)blocks * kSortThreads)
+            ((uint4*)p.touched)[v] = make_uint4(0, 0, 0, 0);
+    if (blocks > 1) cluster_arrive();
     // the first pass reads the second buffer
 #pragma unroll 8
     for (int i = tid; i < have; i += kSortThreads)
         buf[p.chunk + i] = make_uint2(row_of(p, place0 + i), (uint32_t)(place0 + i));
-    if (blocks > 1) cluster_wait();  // every block runs
+    if (blocks > 1) cluster_wait();  // every block runs, every flag is clear
+    else __syncthreads();
+    if (p.touched)
+        for (int i = tid; i < have; i += kSortThreads) {
+            const uint32_t row = buf[p.chunk + i].x;
+            if (row < (uint32_t)p.rows) p.touched[row] = 1;
+        }
     for (int pass = 0; pass < p.passes; pass++) {
         const int shift = pass * p.bits;
         const bool last = pass + 1 == p.passes;
@@ -346,6 +349,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const GradPara
     grid_release();
     const int bins = 1 << p.bits;
     if (blockIdx.x == 0 && threadIdx.x == 0) p.cut[0] = 0;
+    if (p.touched)
+        for (int64_t v = (int64_t)blockIdx.x * kSortThreads + threadIdx.x; v < (p.rows + 15) / 16; v += (int64_t)gridDim.x * kSortThreads)
+            ((uint4*)p.touched)[v] = make_uint4(0, 0, 0, 0);
     for (int b = threadIdx.x; b < bins; b += kSortThreads) count[b] = 0;
     __syncthreads();
     const int64_t t0 = (int64_t)blockIdx.x * p.chunk;
@@ -405,6 +411,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(const GradParam
         const bool in = t < p.tokens;
         key[i] = in ? (FIRST ? row_of(p, t) : p.keys_in[t]) : 0u;
         pos[i] = in ? (FIRST ? (uint32_t)t : p.pos_in[t]) : 0u;
+        if (FIRST && p.touched && in && key[i] < (uint32_t)p.rows) p.touched[key[i]] = 1;
     }
 #pragma unroll
     for (int i = 0; i < ITEMS; i++) {
@@ -442,135 +449,151 @@ __global__ void __launch_bounds__(kSortThreads) sort_pass_kernel(const GradParam
 
 // ---------------------------------------------------------------------------
 // sums over sorted tokens: a warp takes 256 columns of sum_chunk tokens, of
-// which kRowsInFlight (and the table's rows that they end, when adding to
+// which eight (or four, and the table's rows that they end, when adding to
 // them) are on their way at a time, as they lie in memory.
 // ---------------------------------------------------------------------------
 constexpr int kSumThreads = 256;
 constexpr int kSumWarps = kSumThreads / 32;
 constexpr int kLaneCols = 8;       // columns of a lane
-constexpr int kRowsInFlight = 4;
 
-// A lane's columns of a row of T: neighbouring ones (VEC), or 32 apart.
-template <class T, bool VEC>
+// A lane's columns of a row of T: vectors of W neighbouring ones, 32 W apart
+// (so that a warp's accesses are contiguous).
+template <class T, int W>
 struct Lane {
+    static constexpr int kVecs = kLaneCols / W, kBytes = W * (int)sizeof(T);
     union {
-        uint4 vec[kLaneCols * sizeof(T) / 16];
+        uint4 v16[kLaneCols * sizeof(T) / 16];
+        uint2 v8[kLaneCols * sizeof(T) / 8];
         T e[kLaneCols];
     };
-    // n: columns of the row from the lane's first
-    __device__ __forceinline__ void load(const T* row, int c, int n) {
-        if (VEC && n >= kLaneCols) {
+    // n: columns of the row from the lane's first, whole vectors of them (a
+    // branch for parts of vectors kept the rows' loads from overlapping: 250 us
+    // instead of 150 for 65536 tokens of 2048 columns)
+    __device__ __forceinline__ void load(const T* p, int n) {
 #pragma unroll
-            for (int i = 0; i < (int)(kLaneCols * sizeof(T) / 16); i++) vec[i] = ((const uint4*)(row + c))[i];
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < kLaneCols; i++) {
-            const int o = VEC ? i : 32 * i;
-            if (o < n) e[i] = row[c + o];
+        for (int v = 0; v < kVecs; v++) {
+            const int o = v * 32 * W;
+            if (o >= n) continue;
+            if constexpr (kBytes == 16) v16[v] = *(const uint4*)(p + o);
+            else if constexpr (kBytes == 8) v8[v] = *(const uint2*)(p + o);
+            else e[v] = p[o];
         }
     }
     __device__ __forceinline__ float get(int i) const { return to_f32(e[i]); }
 };
-template <class T, bool VEC>
-__device__ __forceinline__ void store_lane(T* row, int c, int n, const float (&v)[kLaneCols]) {
-    if constexpr (VEC) {
-        store_n<T, kLaneCols>(row + c, n, v);
-    } else {
+template <class T, int W>
+__device__ __forceinline__ void store_lane(T* p, int n, const float (&x)[kLaneCols]) {
 #pragma unroll
-        for (int i = 0; i < kLaneCols; i++)
-            if (32 * i < n) put(row + c + 32 * i, v[i]);
+    for (int v = 0; v < kLaneCols / W; v++) {
+        float e[W];
+#pragma unroll
+        for (int i = 0; i < W; i++) e[i] = x[v * W + i];
+        store_whole<T, W>(p + v * 32 * W, v * 32 * W < n, e);
     }
 }
 
-template <class TO, class TT, bool VEC>
+template <class TO, class TT, int W, bool ACC>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const GradParams p) {
+    constexpr int kRowsInFlight = ACC ? 4 : 8;
     grid_wait();
     grid_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t none = (uint32_t)p.rows;
-    // sums and fills alternate as their numbers allow, so that the fills'
-    // writes overlap the sums' waits for their rows (fills spread evenly to the
-    // end took 315 us instead of 265 for 65536 tokens of 2048 fp32 columns)
-    const int64_t b = blockIdx.x, both = 2 * min(p.sum_blocks, p.fill_blocks);
-    const bool fill = b < both ? b & 1 : p.fill_blocks > p.sum_blocks;
-    const int64_t index = b < both ? b >> 1 : b - both / 2;
-    if (fill) {
-        // each warp: 32 rows, a lane looks one up among the sorted keys
-        const int64_t v0 = (index * kSumWarps + warp) * 32;
-        int64_t lo = 0, hi = p.tokens;
-        while (lo < hi) {
-            const int64_t mid = (lo + hi) / 2;
-            if (p.keys_in[mid] < (uint32_t)(v0 + lane)) lo = mid + 1;
-            else hi = mid;
+    const int64_t item = (int64_t)blockIdx.x * kSumWarps + warp;
+    constexpr int kZeroBytes = 4096;
+    __shared__ __align__(16) unsigned char zeros[ACC || W == 1 ? 16 : kZeroBytes];
+    struct Leave {  // the copies out of `zeros` read it before the block leaves
+        __device__ __forceinline__ ~Leave() {
+            if (!ACC && W > 1) bulk_wait_read_all();
         }
-        const bool empty = v0 + lane < p.rows && (lo >= p.tokens || p.keys_in[lo] != (uint32_t)(v0 + lane));
-        uint32_t todo = __ballot_sync(0xFFFFFFFFu, empty);
-        while (todo) {
-            zero_row<TT, VEC ? kLaneCols : 1>(p, v0 + __ffs(todo) - 1, lane, 32);
-            todo &= todo - 1;
-        }
-        return;
+    } leave;
+    if (!ACC && W > 1) {
+        for (int i = threadIdx.x; i < kZeroBytes / 16; i += kSumThreads) ((uint4*)zeros)[i] = make_uint4(0, 0, 0, 0);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();
     }
-    const int64_t item = index * kSumWarps + warp;
+    if (!ACC) {
+        // every warp zeroes an equal share of the rows without tokens, by bulk
+        // copies where rows are aligned, which queue apart from the loads
+        // below
+        const int64_t warps = (int64_t)gridDim.x * kSumWarps, share = (p.rows + warps - 1) / warps;
+        const int64_t v1 = min((item + 1) * share, p.rows);
+        for (int64_t v0 = item * share; v0 < v1; v0 += 32) {
+            const int64_t v = v0 + lane;
+            const bool empty = v < v1 && !p.touched[v];
+            if (W > 1) {
+                if (empty) {
+                    const uintptr_t q = (uintptr_t)((TT*)p.table + v * p.table_stride);
+                    const int bytes = p.dim * (int)sizeof(TT);
+                    for (int o = 0; o < bytes; o += kZeroBytes) bulk_s2g(q + o, zeros, (unsigned)min(kZeroBytes, bytes - o));
+                }
+            } else {
+                uint32_t todo = __ballot_sync(0xFFFFFFFFu, empty);
+                while (todo) {
+                    zero_row<TT, 1>(p, v0 + __ffs(todo) - 1, lane, 32);
+                    todo &= todo - 1;
+                }
+            }
+        }
+        bulk_commit();
+    }
     const int64_t chunk = item / p.tiles;
     if (chunk >= p.sum_chunks) return;
     const int tile = (int)(item % p.tiles);
-    const int c = tile * 32 * kLaneCols + (VEC ? lane * kLaneCols : lane);
+    const int c = tile * 32 * kLaneCols + lane * W;
     const int n = p.dim - c;
-    const int64_t s0 = chunk * p.sum_chunk;
-    const int len = (int)min((int64_t)p.sum_chunk, p.tokens - s0);
-    const uint32_t key = lane < len ? p.keys_in[s0 + lane] : none;
-    const uint32_t pos = lane < len ? p.pos_in[s0 + lane] : 0u;
-    const uint32_t prev = s0 > 0 ? p.keys_in[s0 - 1] : none;
-    const uint32_t next = s0 + len < p.tokens ? p.keys_in[s0 + len] : none;
-    const int m = __popc(__ballot_sync(0xFFFFFFFFu, key != none));  // a prefix: tokens without a row come last
-    if (m == 0) return;
-    const uint32_t first = __shfl_sync(0xFFFFFFFFu, key, 0), last = __shfl_sync(0xFFFFFFFFu, key, m - 1);
-    const uint32_t after = __shfl_down_sync(0xFFFFFFFFu, key, 1);
-    // a row's last token here; of a row that goes on after these tokens, that
-    // began before them
-    const bool ends = lane < m && (lane == m - 1 || after != key);
-    const bool goes_on = ends && key == last && next == last;
-    const bool began = ends && key == first && prev == first;
-    const uint32_t end_mask = __ballot_sync(0xFFFFFFFFu, ends);
-    const uint32_t head_mask = __ballot_sync(0xFFFFFFFFu, began);
-    const uint32_t tail_mask = __ballot_sync(0xFFFFFFFFu, goes_on && !began);
-    const uint32_t old_mask = p.accumulate ? end_mask & ~(head_mask | tail_mask) : 0u;
-    if (tail_mask && tile == 0 && lane == 0) p.cut[1 + atomicAdd(p.cut, 1u)] = (uint32_t)chunk;
+    const int64_t s0 = chunk * p.sum_chunk, s1 = min(s0 + p.sum_chunk, p.tokens);
+    // whether the row under way began before s0
+    bool head = s0 > 0 && p.keys_in[s0 - 1] == p.keys_in[s0];
     float acc[kLaneCols] = {};
-    for (int j = 0; j < m; j += kRowsInFlight) {
-        Lane<TO, VEC> v[kRowsInFlight];
-        Lane<TT, VEC> old[kRowsInFlight];
+    for (int64_t b = s0; b < s1; b += 32) {
+        const int64_t s = b + lane;
+        const uint32_t key = s < s1 ? p.keys_in[s] : none;
+        const uint32_t pos = s < s1 ? p.pos_in[s] : 0u;
+        const uint32_t next = s + 1 < p.tokens ? p.keys_in[s + 1] : none;
+        const int m = __popc(__ballot_sync(0xFFFFFFFFu, key != none));  // a prefix: tokens without a row come last
+        // a row's last token, or the group's; of a row that goes on after it
+        const uint32_t end_mask = __ballot_sync(0xFFFFFFFFu, lane < m && (next != key || s + 1 == s1));
+        const uint32_t on_mask = __ballot_sync(0xFFFFFFFFu, lane < m && next == key && s + 1 == s1);
+        // written to the table, not to a partial sum
+        const uint32_t whole_mask = end_mask & ~on_mask & ~(head ? end_mask & (0u - end_mask) : 0u);
+        for (int j = 0; j < m; j += kRowsInFlight) {
+            Lane<TO, W> v[kRowsInFlight];
+            Lane<TT, W> old[kRowsInFlight];
 #pragma unroll
-        for (int k = 0; k < kRowsInFlight; k++) {
-            const uint32_t t = __shfl_sync(0xFFFFFFFFu, pos, j + k), r = __shfl_sync(0xFFFFFFFFu, key, j + k);
-            if (j + k < m) v[k].load((const TO*)p.grad + (int64_t)t * p.grad_stride, c, n);
-            if (old_mask >> (j + k) & 1) old[k].load((const TT*)p.table + (int64_t)r * p.table_stride, c, n);
-        }
-#pragma unroll
-        for (int k = 0; k < kRowsInFlight; k++) {
-            const uint32_t bit = 1u << (j + k);
-            const uint32_t r = __shfl_sync(0xFFFFFFFFu, key, j + k);
-            if (j + k < m)
-#pragma unroll
-                for (int i = 0; i < kLaneCols; i++) acc[i] += v[k].get(i);
-            if (!(end_mask & bit)) continue;
-            if ((head_mask | tail_mask) & bit) {
-                store_lane<float, VEC>(p.part + (chunk * 2 + (tail_mask & bit ? 1 : 0)) * p.pitch, c, n, acc);
-            } else {
-                if (old_mask & bit) {
-#pragma unroll
-                    for (int i = 0; i < kLaneCols; i++) acc[i] = fmaf(acc[i], p.scale, old[k].get(i));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kLaneCols; i++) acc[i] *= p.scale;
-                }
-                store_lane<TT, VEC>((TT*)p.table + (int64_t)r * p.table_stride, c, n, acc);
+            for (int k = 0; k < kRowsInFlight; k++) {
+                const uint32_t t = __shfl_sync(0xFFFFFFFFu, pos, j + k), r = __shfl_sync(0xFFFFFFFFu, key, j + k);
+                if (j + k < m) v[k].load((const TO*)p.grad + (int64_t)t * p.grad_stride + c, n);
+                if (ACC && (whole_mask >> (j + k) & 1)) old[k].load((const TT*)p.table + (int64_t)r * p.table_stride + c, n);
             }
 #pragma unroll
-            for (int i = 0; i < kLaneCols; i++) acc[i] = 0.0f;
+            for (int k = 0; k < kRowsInFlight; k++) {
+                const uint32_t bit = 1u << (j + k);
+                const uint32_t r = __shfl_sync(0xFFFFFFFFu, key, j + k);
+                if (j + k < m)
+#pragma unroll
+                    for (int i = 0; i < kLaneCols; i++) acc[i] += v[k].get(i);
+                if (!(end_mask & bit)) continue;
+                if (whole_mask & bit) {
+                    if (ACC) {
+#pragma unroll
+                        for (int i = 0; i < kLaneCols; i++) acc[i] = fmaf(acc[i], p.scale, old[k].get(i));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kLaneCols; i++) acc[i] *= p.scale;
+                    }
+                    store_lane<TT, W>((TT*)p.table + (int64_t)r * p.table_stride + c, n, acc);
+                } else {
+                    const bool tail = (on_mask & bit) && !head;
+                    store_lane<float, W>(p.part + (chunk * 2 + (tail ? 1 : 0)) * p.pitch + c, n, acc);
+                    if (tail && tile == 0 && lane == 0) p.cut[1 + atomicAdd(p.cut, 1u)] = (uint32_t)chunk;
+                }
+                head = false;
+#pragma unroll
+                for (int i = 0; i < kLaneCols; i++) acc[i] = 0.0f;
+            }
         }
+        if (m < 32) break;
     }
 }
 
@@ -656,7 +679,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const GradParams 
 template <class TO, class TT>
 cudaError_t launch_grad(GradParams& p, const EmbeddingScratch& sc, unsigned char* scratch, bool vec,
                         cudaStream_t stream, int sms) {
-    constexpr int W = kVecOf<TO> > kVecOf<TT> ? kVecOf<TO> : kVecOf<TT>;
+    constexpr int W = std::min(kVecOf<TO>, kVecOf<TT>);
     const int64_t nv = (p.dim + (vec ? W : 1) - 1) / (vec ? W : 1);
     void* args[] = {&p};
     auto grid_ok = [](int64_t g) { return g <= INT32_MAX; };
@@ -676,6 +699,7 @@ cudaError_t launch_grad(GradParams& p, const EmbeddingScratch& sc, unsigned char
     }
     p.part = (float*)(scratch + sc.part);
     p.cut = (uint32_t*)(scratch + sc.cut);
+    p.touched = p.accumulate ? nullptr : scratch + sc.touched;
     p.pitch = sc.pitch;
     p.chunk = sc.chunk;
     p.chunks = sc.chunks;
@@ -721,13 +745,15 @@ cudaError_t launch_grad(GradParams& p, const EmbeddingScratch& sc, unsigned char
     }
     p.tiles = (p.dim + 32 * kLaneCols - 1) / (32 * kLaneCols);
     p.sum_blocks = (p.sum_chunks * p.tiles + kSumWarps - 1) / kSumWarps;
-    p.fill_blocks = p.accumulate ? 0 : (p.rows + kSumThreads - 1) / kSumThreads;
-    if (!grid_ok(p.sum_blocks + p.fill_blocks)) return cudaErrorInvalidValue;
-    e = launch_op(vec ? (const void*)sum_kernel<TO, TT, true> : (const void*)sum_kernel<TO, TT, false>,
-                  dim3((unsigned)(p.sum_blocks + p.fill_blocks)), dim3(kSumThreads), args, 0, stream);
+    // enough warps for the rows without tokens, too
+    const int64_t sum_grid = std::max<int64_t>(p.sum_blocks, p.accumulate ? 1 : std::min<int64_t>((p.rows + kSumWarps - 1) / kSumWarps, 4 * sms));
+    if (!grid_ok(sum_grid)) return cudaErrorInvalidValue;
+    const void* fn = p.accumulate ? (vec ? (const void*)sum_kernel<TO, TT, W, true> : (const void*)sum_kernel<TO, TT, 1, true>)
+                                  : (vec ? (const void*)sum_kernel<TO, TT, W, false> : (const void*)sum_kernel<TO, TT, 1, false>);
+    e = launch_op(fn, dim3((unsigned)sum_grid), dim3(kSumThreads), args, 0, stream);
     if (e != cudaSuccess || p.sum_chunks < 2) return e;
     // partial rows are 16-byte aligned, the table's may not be
-    constexpr int J = kVecOf<TT>;
+    constexpr int J = 4;
     const int64_t jv = (p.dim + (vec ? J : 1) - 1) / (vec ? J : 1);
     p.tiles = (int)((jv + 31) / 32);
     const int64_t grid = std::min<int64_t>((p.sum_chunks + kJoinWarps - 2) / kJoinWarps * p.tiles, (int64_t)sms * 8);
@@ -735,8 +761,9 @@ cudaError_t launch_grad(GradParams& p, const EmbeddingScratch& sc, unsigned char
                      dim3(kJoinWarps * 32), args, 0, stream);
 }
 
-bool aligned16(const void* p, int64_t stride, int es) {
-    return ((uintptr_t)p & 15) == 0 && (stride * es & 15) == 0;
+// Rows that take accesses of W elements: on 16-byte boundaries, whole vectors.
+bool aligned16(const void* p, int64_t stride, int dim, int es) {
+    return ((uintptr_t)p & 15) == 0 && (stride * es & 15) == 0 && dim % 8 == 0;
 }
 
 }  // namespace
@@ -754,8 +781,8 @@ cudaError_t launch_embedding(const hc_embedding_t& a, cudaStream_t stream, int s
     p.dim = (int)a.dim;
     p.wide_ids = a.id_type == HC_ID64;
     p.scale = a.scale;
-    const bool vec = aligned16(a.table, p.table_stride, elem_bytes(a.table_dtype)) &&
-                     aligned16(a.out, p.out_stride, elem_bytes(a.out_dtype));
+    const bool vec = aligned16(a.table, p.table_stride, p.dim, elem_bytes(a.table_dtype)) &&
+                     aligned16(a.out, p.out_stride, p.dim, elem_bytes(a.out_dtype));
     const bool bi = a.table_dtype == HC_BFLOAT16, bo = a.out_dtype == HC_BFLOAT16;
     if (bi) return bo ? launch_lookup<Bf16, Bf16>(p, vec, stream, sms) : launch_lookup<Bf16, float>(p, vec, stream, sms);
     return bo ? launch_lookup<float, Bf16>(p, vec, stream, sms) : launch_lookup<float, float>(p, vec, stream, sms);
@@ -779,10 +806,10 @@ EmbeddingScratch embedding_scratch(int64_t tokens, int64_t rows, int64_t dim) {
         s.chunk = kSortThreads * (tokens <= (1 << 18) ? 4 : 16);
     }
     s.chunks = (tokens + s.chunk - 1) / s.chunk;
-    // groups of 8 to 32 tokens (a lane each), about 2400 warps' worth
-    s.sum_chunk = 32;
+    // groups of 8 to 128 tokens, at least a round of the warps that the SMs hold (24 each)
+    s.sum_chunk = 128;
     const int64_t tiles = (dim + 32 * kLaneCols - 1) / (32 * kLaneCols);
-    while (s.sum_chunk > 8 && tokens * tiles < 2400 * s.sum_chunk) s.sum_chunk /= 2;
+    while (s.sum_chunk > 8 && tokens * tiles < 24 * 152 * s.sum_chunk) s.sum_chunk /= 2;
     s.sum_chunks = (tokens + s.sum_chunk - 1) / s.sum_chunk;
     s.pitch = (dim + 7) / 8 * 8;
     size_t at = 0;
@@ -797,6 +824,7 @@ EmbeddingScratch embedding_scratch(int64_t tokens, int64_t rows, int64_t dim) {
     }
     if (!s.cluster) s.hist = take((size_t)3 * s.chunks << (s.bits + 2));
     s.cut = take(((size_t)s.sum_chunks + 1) * 4);
+    s.touched = take((size_t)rows);
     s.part = take((size_t)s.sum_chunks * 2 * (size_t)s.pitch * 4);
     s.bytes = at;
     return s;
@@ -819,8 +847,8 @@ cudaError_t launch_embedding_grad(const hc_embedding_grad_t& a, cudaStream_t str
     p.accumulate = a.accumulate != 0;
     p.scale = a.scale;
     const EmbeddingScratch sc = embedding_scratch(p.tokens, p.rows, p.dim);
-    const bool vec = aligned16(a.grad_out, p.grad_stride, elem_bytes(a.grad_out_dtype)) &&
-                     aligned16(a.grad_table, p.table_stride, elem_bytes(a.grad_table_dtype));
+    const bool vec = aligned16(a.grad_out, p.grad_stride, p.dim, elem_bytes(a.grad_out_dtype)) &&
+                     aligned16(a.grad_table, p.table_stride, p.dim, elem_bytes(a.grad_table_dtype));
     unsigned char* s = (unsigned char*)a.scratch;
     const bool bo = a.grad_out_dtype == HC_BFLOAT16, bt = a.grad_table_dtype == HC_BFLOAT16;
     if (bo) return bt ? launch_grad<Bf16, Bf16>(p, sc, s, vec, stream, sms) : launch_grad<Bf16, float>(p, sc, s, vec, stream, sms);

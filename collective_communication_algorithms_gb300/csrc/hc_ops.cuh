@@ -35,8 +35,8 @@ __device__ __forceinline__ void unpack(const uint4& w, float (&v)[8]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        v[2 * i] = __uint_as_float(u[i] << 16);
-        v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        v[2 * i] = bf_lo(u[i]);
+        v[2 * i + 1] = bf_hi(u[i]);
     }
 }
 __device__ __forceinline__ uint4 pack(const float (&v)[4]) {
@@ -49,9 +49,9 @@ __device__ __forceinline__ uint4 pack(const float (&v)[8]) {
 }
 
 // N consecutive elements of a row, of which the first n (any value) are in
-// range; the others read as 0 and are not written.  16-byte accesses when
-// N elements are whole vectors (the caller then guarantees the alignment)
-// and all of them are in range.
+// range; the others read as 0 and are not written.  Accesses of 8 or 16 bytes
+// when N > 1 elements make them (the caller then guarantees 16-byte aligned
+// rows and N-element aligned places) and all N are in range.
 template <class T, int N>
 __device__ __forceinline__ void load_n(const T* p, int n, float (&v)[N]) {
     constexpr int E = kVecOf<T>;
@@ -64,6 +64,15 @@ __device__ __forceinline__ void load_n(const T* p, int n, float (&v)[N]) {
 #pragma unroll
                 for (int j = 0; j < E; j++) v[i * E + j] = e[j];
             }
+            return;
+        }
+    } else if constexpr (2 * N == E && sizeof(T) == 2) {  // half a vector of bf16
+        if (n >= N) {
+            const uint2 u = *(const uint2*)p;
+            v[0] = bf_lo(u.x);
+            v[1] = bf_hi(u.x);
+            v[2] = bf_lo(u.y);
+            v[3] = bf_hi(u.y);
             return;
         }
     }
@@ -84,6 +93,11 @@ __device__ __forceinline__ void store_n(T* p, int n, const float (&v)[N]) {
             }
             return;
         }
+    } else if constexpr (2 * N == E && sizeof(T) == 2) {
+        if (n >= N) {
+            *(uint2*)p = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+            return;
+        }
     }
 #pragma unroll
     for (int i = 0; i < N; i++)
@@ -93,35 +107,16 @@ __device__ __forceinline__ void store_n(T* p, int n, const float (&v)[N]) {
 // N consecutive elements that are in range as a whole or not at all.
 template <class T, int N>
 __device__ __forceinline__ void load_whole(const T* p, bool in, float (&v)[N]) {
-    constexpr int E = kVecOf<T>;
-    if (!in) {
-#pragma unroll
-        for (int i = 0; i < N; i++) v[i] = 0.0f;
-    } else if constexpr (N % E == 0) {
+    if (in) {
         load_n<T, N>(p, N, v);
-    } else if constexpr (N == 4 && E == 8) {  // half a vector of bf16
-        const uint2 u = *(const uint2*)p;
-        v[0] = __uint_as_float(u.x << 16);
-        v[1] = __uint_as_float(u.x & 0xFFFF0000u);
-        v[2] = __uint_as_float(u.y << 16);
-        v[3] = __uint_as_float(u.y & 0xFFFF0000u);
     } else {
 #pragma unroll
-        for (int i = 0; i < N; i++) v[i] = to_f32(p[i]);
+        for (int i = 0; i < N; i++) v[i] = 0.0f;
     }
 }
 template <class T, int N>
 __device__ __forceinline__ void store_whole(T* p, bool in, const float (&v)[N]) {
-    constexpr int E = kVecOf<T>;
-    if (!in) return;
-    if constexpr (N % E == 0) {
-        store_n<T, N>(p, N, v);
-    } else if constexpr (N == 4 && E == 8) {
-        *(uint2*)p = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; i++) put(p + i, v[i]);
-    }
+    if (in) store_n<T, N>(p, N, v);
 }
 
 // The id of a token, whatever its width.

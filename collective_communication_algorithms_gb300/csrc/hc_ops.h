@@ -10,9 +10,9 @@ cudaError_t launch_embedding(const hc_embedding_t& a, cudaStream_t stream, int s
 
 // Tokens up to which the gradient of the lookup needs no sort (and no
 // scratch), and the layout of its scratch above that.
-constexpr size_t kEmbeddingFewTokens = 256;
+constexpr size_t kEmbeddingFewTokens = 512;
 struct EmbeddingScratch {
-    size_t keys[2], pos[2], hist, cut, part;  // byte offsets
+    size_t keys[2], pos[2], hist, cut, touched, part;  // byte offsets
     size_t bytes;
     int cluster;          // blocks of the one-cluster sort; 0: passes over global memory
     int chunk;            // tokens per sorting block
