@@ -9,7 +9,10 @@
 // that it is read once and its gradient written once.  Bulk copies bring a
 // block's share in; the threads reduce each piece as it lands, rescaling
 // their running sums when their maximum grows; the blocks exchange (m, l)
-// through distributed shared memory and write the gradient.
+// through distributed shared memory and write the gradient.  A warp of its own
+// starts the copies and works on the teacher's entries meanwhile: their
+// probabilities, the loss, and the gradient where they point, which it stores
+// over the others' when those are done.
 //
 // Rows need not start on 16-byte boundaries: a share is a run of aligned
 // 16-byte vectors of memory, the vectors that also hold a neighbouring row's
@@ -20,8 +23,9 @@
 namespace hc {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;               // that go through the logits
 constexpr int kWarps = kThreads / 32;
+constexpr int kBlock = kThreads + 32;       // and the teacher's warp
 constexpr int kPieces = 16;  // bulk copies (and barriers) of a share at most
 
 struct DistillParams {
@@ -41,12 +45,13 @@ struct DistillParams {
     int* err;
     unsigned long long wait_ns;
     int hold;
+    bool in_place;    // the gradient replaces the logits
 };
 
 struct Shared {
     uint64_t full[kPieces];
     float warp_m[kWarps], warp_l[kWarps];
-    float rank_m[8], rank_l[8];
+    float rank_m[kMaxCluster], rank_l[kMaxCluster];
     int failed;
     int entries;     // of the row, valid ones
     float t_top, t_log;  // teacher: largest logit, log of its sum
@@ -57,6 +62,74 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Pairs of binary32 numbers, one instruction for both.
+struct Pair {
+    unsigned long long v;
+    __device__ __forceinline__ Pair() {}
+    __device__ __forceinline__ Pair(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+    __device__ __forceinline__ void get(float& lo, float& hi) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+};
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Pair exp2_pair(Pair a) {
+    float lo, hi;
+    a.get(lo, hi);
+    return Pair(exp2_fast(lo), exp2_fast(hi));
+}
+// A 16-byte vector as pairs, and its largest element (NaN left out).
+__device__ __forceinline__ void pairs_of(const uint4& u, Pair (&v)[2]) {
+    v[0] = Pair(__uint_as_float(u.x), __uint_as_float(u.y));
+    v[1] = Pair(__uint_as_float(u.z), __uint_as_float(u.w));
+}
+__device__ __forceinline__ void pairs_of(const uint4& u, Pair (&v)[4]) {
+    v[0] = Pair(bf_lo(u.x), bf_hi(u.x));
+    v[1] = Pair(bf_lo(u.y), bf_hi(u.y));
+    v[2] = Pair(bf_lo(u.z), bf_hi(u.z));
+    v[3] = Pair(bf_lo(u.w), bf_hi(u.w));
+}
+__device__ __forceinline__ uint4 pack_pairs(const Pair (&v)[2]) {
+    float a, b, c, d;
+    v[0].get(a, b);
+    v[1].get(c, d);
+    return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+}
+__device__ __forceinline__ uint4 pack_pairs(const Pair (&v)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        float a, b;
+        v[i].get(a, b);
+        w[i] = pack_bf16x2(a, b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <class T>
+__device__ __forceinline__ float largest(const uint4& u) {
+    if (sizeof(T) == 2) {
+        const uint32_t m = max_bf16x2(max_bf16x2(u.x, u.y), max_bf16x2(u.z, u.w));
+        return fmaxf(bf_lo(m), bf_hi(m));
+    }
+    return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+}
+// Waits of the threads that go through the logits, and of the teacher's warp
+// for them.
+__device__ __forceinline__ void logits_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+__device__ __forceinline__ void stored_arrive() { asm volatile("bar.arrive 2, %0;" ::"n"(kBlock) : "memory"); }
+__device__ __forceinline__ void stored_wait() { asm volatile("bar.sync 2, %0;" ::"n"(kBlock) : "memory"); }
+
 // Joins the lanes' (maximum, sum of 2^((x - maximum) c)) of a warp.
 __device__ __forceinline__ void warp_join(float& m, float& l, float c) {
     const float mx = warp_max(m);
@@ -153,38 +226,82 @@ __device__ __forceinline__ void store_grad(const Window<T>& w, T* row, bool same
 template <class T>
 __device__ __forceinline__ void zero_grad(const Window<T>& w, T* row, bool same, int lo, int hi) {
     const float z[kVecOf<T>] = {};
-    for (int i = lo + threadIdx.x; i < hi; i += kThreads) store_grad<T>(w, row, same, i, z);
+    for (int i = lo + threadIdx.x; i < hi; i += kBlock) store_grad<T>(w, row, same, i, z);
 }
 
-// Gradient of the entries this block's vectors [lo, hi) hold, over what the
-// block has stored: g * (q - sum of the p with the same id).  x_of(k): the
-// logit of entry k.
+__host__ __device__ inline int bucket_count(int top) {
+    int n = 64;
+    while (n < 4 * top) n *= 2;
+    return n;
+}
+
+// The teacher's warp: gradient of the entries that this block's vectors [lo,
+// hi) hold, g * (q - sum of the p with the same id), kept in prob's place until
+// the other threads have stored theirs.  x_of(k): the logit of entry k.
 template <class T, class X>
 __device__ __forceinline__ void entry_grads(const DistillParams& p, const Window<T>& w, T* row, int lo, int hi,
-                                            const int* ids, const float* prob, float m, float l_inv, float c, float g,
-                                            X x_of) {
-    for (int k = threadIdx.x; k < p.top; k += kThreads) {
-        const int id = ids[k];
-        if (id < 0) continue;
-        const int i = (w.shift + id) / kVecOf<T>;
+                                            const int* ids, const float* prob, float* value, int* buckets, float m,
+                                            float l_inv, float c, float g, X x_of) {
+    const int lane = threadIdx.x & 31, mask = bucket_count(p.top) - 1;
+    // entries by a hash of their id: only one that shares its bucket can have
+    // a twin, and looks for it among all
+    auto bucket = [&](int id) { return (int)((unsigned)id * 2654435761u >> 16) & mask; };
+    for (int i = lane; i <= mask; i += 32) buckets[i] = 0;
+    __syncwarp();
+    for (int k = lane; k < p.top; k += 32)
+        if (ids[k] >= 0) atomicAdd(&buckets[bucket(ids[k])], 1);
+    __syncwarp();
+    for (int k = lane; k < p.top; k += 32) {
+        const int id = ids[k], i = id < 0 ? -1 : (w.shift + id) / kVecOf<T>;
         if (i < lo || i >= hi) continue;
-        float sum = 0.0f;
-        for (int o = 0; o < p.top; o++) sum += ids[o] == id ? prob[o] : 0.0f;
-        put(row + id, g * (exp2_fast((x_of(k) - m) * c) * l_inv - sum));
+        float sum = prob[k];
+        if (buckets[bucket(id)] > 1) {
+            sum = 0.0f;
+            for (int o = 0; o < p.top; o++) sum += ids[o] == id ? prob[o] : 0.0f;
+        }
+        value[k] = g * (exp2_fast((x_of(k) - m) * c) * l_inv - sum);
+    }
+    stored_wait();
+    for (int k = lane; k < p.top; k += 32) {
+        const int id = ids[k], i = id < 0 ? -1 : (w.shift + id) / kVecOf<T>;
+        if (i >= lo && i < hi) put(row + id, value[k]);
+    }
+}
+
+// Gradient of the other columns: 2^((x - m) c) * gl.
+template <class T>
+__device__ __forceinline__ uint4 column_grads(const uint4& u, Pair minus_m, Pair c, Pair gl) {
+    Pair v[kVecOf<T> / 2];
+    pairs_of(u, v);
+#pragma unroll
+    for (int j = 0; j < kVecOf<T> / 2; j++) v[j] = exp2_pair((v[j] + minus_m) * c) * gl;
+    return pack_pairs(v);
+}
+template <class T>
+__device__ __forceinline__ void store_vector(const Window<T>& w, T* row, bool same, int i, const uint4& u) {
+    if (same) {
+        *(uint4*)(row + (i * kVecOf<T> - w.shift)) = u;
+    } else {
+        float v[kVecOf<T>];
+        unpack(u, v);
+#pragma unroll
+        for (int j = 0; j < kVecOf<T>; j++) put(row + (i * kVecOf<T> - w.shift) + j, v[j]);
     }
 }
 
 // MODE 0: the loss, 1: the loss and the gradient (DISTILL_LOSS, DISTILL_BOTH).
 template <class T, int MODE>
-__global__ void __launch_bounds__(kThreads) distill_kernel(const DistillParams p) {
+__global__ void __launch_bounds__(kBlock, 3) distill_kernel(const DistillParams p) {
     constexpr int E = kVecOf<T>;
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ Shared sh;
     uint4* const buf = (uint4*)dyn;
     int* const ids = (int*)(buf + p.share);
     float* const prob = (float*)(ids + p.top);
-    float* const named = prob + p.top;  // block 0: the logits the teacher names
+    float* const named = prob + p.top;  // block 0: the logits the teacher names; then entries' gradients
+    int* const buckets = (int*)(named + p.top);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool teacher = warp == kWarps;
     const unsigned rank = blockIdx.x % p.cs;
     const int64_t t = blockIdx.x / p.cs;
     const float c = 1.4426950408889634f / p.temperature;
@@ -198,9 +315,10 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillParams p
     grid_wait();
     grid_release();
     const float wt = p.scale * (p.weight ? p.weight[t] : 1.0f);
-    const Window<T> w((const T*)p.logits + t * p.logits_stride, p.vocab);
+    const T* const row = (const T*)p.logits + t * p.logits_stride;
+    const Window<T> w(row, p.vocab);
     T* const grow = (T*)p.grad + t * p.grad_stride;
-    const bool same = (((uintptr_t)grow ^ (uintptr_t)((const T*)p.logits + t * p.logits_stride)) & 15) == 0;
+    const bool same = (((uintptr_t)grow ^ (uintptr_t)row) & 15) == 0;
     const int lo = min((int)rank * p.share, w.count), hi = min(lo + p.share, w.count);
     if (wt == 0.0f) {  // the same in every block of the cluster
         if (p.cs > 1) cluster_wait();
@@ -214,85 +332,93 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillParams p
     // whole vectors of the share by bulk copies, the edges by hand
     const int wlo = max(lo, w.whole_lo()), whi = max(wlo, min(hi, w.whole_hi()));
     const int pieces = (whi - wlo + p.piece - 1) / p.piece;
-    if (tid == 0) {
-        for (int i = 0; i < pieces; i++) {
-            const int a = wlo + i * p.piece, n = min(p.piece, whi - a);
-            mbar_arrive_expect_tx(&sh.full[i], (unsigned)n * 16);
-            bulk_g2s(buf + (a - lo), w.base + (uintptr_t)a * 16, (unsigned)n * 16, &sh.full[i]);
+    float m = -INFINITY, l = 0.0f;
+    if (teacher) {
+        if (lane < pieces) {  // kPieces <= 32
+            const int a = wlo + lane * p.piece, n = min(p.piece, whi - a);
+            mbar_arrive_expect_tx(&sh.full[lane], (unsigned)n * 16);
+            bulk_g2s(buf + (a - lo), w.base + (uintptr_t)a * 16, (unsigned)n * 16, &sh.full[lane]);
         }
-    }
-    if (tid >= 32 && tid < 64) {
-        const int i = tid == 32 ? lo : tid == 33 ? hi - 1 : -1;
-        if (i >= lo && i < hi && (i < wlo || i >= whi)) {
-            float v[E];
-            edge_vector<T>(w, i, v);
-            buf[i - lo] = pack(v);
-        }
-    }
-    if (warp == 0) {
+        __syncwarp();
         teacher_softmax(p, t, c, ids, prob, sh);
         __syncwarp();
         if (rank == 0)
-            for (int k = lane; k < p.top; k += 32)
-                named[k] = ids[k] >= 0 ? to_f32(((const T*)p.logits + t * p.logits_stride)[ids[k]]) : 0.0f;
-    }
-    __syncthreads();
-    // running maximum and sum of this thread's vectors
-    float m = -INFINITY, l = 0.0f;
-    auto take = [&](const uint4& u) {
-        float v[E];
-        unpack(u, v);
-        float mx = v[0];
+            for (int k = lane; k < p.top; k += 32) named[k] = ids[k] >= 0 ? to_f32(row[ids[k]]) : 0.0f;
+    } else {
+        // running maximum and sum of this thread's vectors
+        Pair sum(0.0f, 0.0f);
+        const Pair cc(c, c);
+        auto take = [&](const uint4& u) {
+            const float mx = largest<T>(u);
+            if (mx > m) {
+                const float f = exp2_fast((m - mx) * c);  // 0 at first
+                sum = sum * Pair(f, f);
+                m = mx;
+            }
+            const float ref = m == -INFINITY ? 0.0f : -m;
+            const Pair minus(ref, ref);
+            Pair v[E / 2];
+            pairs_of(u, v);
 #pragma unroll
-        for (int j = 1; j < E; j++) mx = fmaxf(mx, v[j]);
-        if (mx > m) {
-            l *= exp2_fast((m - mx) * c);  // 0 * 2^-inf at first
-            m = mx;
+            for (int j = 0; j < E / 2; j++) sum = sum + exp2_pair((v[j] + minus) * cc);
+        };
+        const int edge = tid == 0 && lo < wlo ? lo : tid == 32 && whi < hi && !(hi - 1 == lo && lo < wlo) ? hi - 1 : -1;
+        if (edge >= 0) {
+            float v[E];
+            edge_vector<T>(w, edge, v);
+            buf[edge - lo] = pack(v);
+            take(buf[edge - lo]);
         }
-        const float ref = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-        for (int j = 0; j < E; j++) l += exp2_fast((v[j] - ref) * c);
-    };
-    if (tid == 0 && lo < wlo) take(buf[0]);
-    if (tid == 32 && whi < hi && !(hi - 1 == lo && lo < wlo)) take(buf[hi - 1 - lo]);
-    bool ok = true;
-    for (int i = 0; i < pieces && ok; i++) {
-        if (!mbar_wait_quick(&sh.full[i], 0, i == 0 ? p.wait_ns : kWaitLimitNs)) {
-            mbar_expired(&sh.full[i], p.err, i == 0 ? p.hold : 0, tid == 0);
-            ok = false;
-            break;
+        bool ok = true;
+        for (int i = 0; i < pieces; i++) {
+            if (!mbar_wait_quick(&sh.full[i], 0, i == 0 ? p.wait_ns : kWaitLimitNs)) {
+                mbar_expired(&sh.full[i], p.err, i == 0 ? p.hold : 0, tid == 0);
+                ok = false;
+                break;
+            }
+            const int a = wlo + i * p.piece - lo, b = min(a + p.piece, whi - lo);
+            for (int j = a + tid; j < b; j += kThreads) take(buf[j]);
         }
-        const int a = wlo + i * p.piece - lo, b = min(a + p.piece, whi - lo);
-        for (int j = a + tid; j < b; j += kThreads) take(buf[j]);
-    }
-    if (!ok) {
-        for (int i = 0; i < pieces; i++) mbar_wait_bounded(&sh.full[i], 0, kWaitLimitNs);
-        sh.failed = 1;
-    }
-    warp_join(m, l, c);
-    if (lane == 0) {
-        sh.warp_m[warp] = m;
-        sh.warp_l[warp] = l;
-    }
-    __syncthreads();
-    m = lane < kWarps ? sh.warp_m[lane] : -INFINITY;
-    l = lane < kWarps ? sh.warp_l[lane] : 0.0f;
-    warp_join(m, l, c);
-    if (p.cs > 1) {
-        cluster_wait();  // every block of the cluster has started
-        if (tid < p.cs) {
-            store_remote(&sh.rank_m[rank], tid, m);
-            store_remote(&sh.rank_l[rank], tid, l);
+        if (!ok) {
+            for (int i = 0; i < pieces; i++) mbar_wait_bounded(&sh.full[i], 0, kWaitLimitNs);
+            sh.failed = 1;
         }
-        cluster_arrive();
-        cluster_wait();
-        m = lane < p.cs ? sh.rank_m[lane] : -INFINITY;
-        l = lane < p.cs ? sh.rank_l[lane] : 0.0f;
+        float l2;
+        sum.get(l, l2);
+        l += l2;
+        warp_join(m, l, c);
+        if (lane == 0) {
+            sh.warp_m[warp] = m;
+            sh.warp_l[warp] = l;
+        }
+        logits_sync();
+        m = lane < kWarps ? sh.warp_m[lane] : -INFINITY;
+        l = lane < kWarps ? sh.warp_l[lane] : 0.0f;
         warp_join(m, l, c);
     }
+    // the row's (m, l), and the teacher's entries, to every thread
+    if (p.cs > 1) cluster_wait();  // every block of the cluster has started
+    if (tid < p.cs) {
+        if (p.cs > 1) {
+            store_remote(&sh.rank_m[rank], tid, m);
+            store_remote(&sh.rank_l[rank], tid, l);
+        } else {
+            sh.rank_m[0] = m;
+            sh.rank_l[0] = l;
+        }
+    }
+    if (p.cs > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
     if (sh.failed) return;
+    m = lane < p.cs ? sh.rank_m[lane] : -INFINITY;
+    l = lane < p.cs ? sh.rank_l[lane] : 0.0f;
+    warp_join(m, l, c);
     const bool empty = sh.entries == 0;
-    if (rank == 0 && warp == 0) {
+    if (rank == 0 && teacher) {
         float sum = 0.0f;
         const float log_l = logf(l), inv_t = 1.0f / p.temperature;
         for (int k = lane; k < p.top; k += 32) {
@@ -317,28 +443,34 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillParams p
         return;
     }
     const float g = wt * p.temperature, l_inv = 1.0f / l, gl = g * l_inv;
-    for (int i = lo + tid; i < hi; i += kThreads) {
-        float v[E];
-        unpack(buf[i - lo], v);
-#pragma unroll
-        for (int j = 0; j < E; j++) v[j] = exp2_fast((v[j] - m) * c) * gl;
-        store_grad<T>(w, grow, same, i, v);
+    if (teacher) {
+        __syncwarp();
+        entry_grads<T>(p, w, grow, lo, hi, ids, prob, named, buckets, m, l_inv, c, g, [&](int k) {
+            return to_f32(((const T*)(buf))[w.shift + ids[k] - lo * E]);
+        });
+        return;
     }
-    __syncthreads();
-    entry_grads<T>(p, w, grow, lo, hi, ids, prob, m, l_inv, c, g, [&](int k) {
-        return to_f32(((const T*)(buf))[w.shift + ids[k] - lo * E]);
-    });
+    const Pair minus(-m, -m), cc(c, c), gg(gl, gl);
+    for (int i = wlo + tid; i < whi; i += kThreads) store_vector<T>(w, grow, same, i, column_grads<T>(buf[i - lo], minus, cc, gg));
+    const int edge = tid == 0 && lo < wlo ? lo : tid == 32 && whi < hi && !(hi - 1 == lo && lo < wlo) ? hi - 1 : -1;
+    if (edge >= 0) {
+        float v[E];
+        unpack(column_grads<T>(buf[edge - lo], minus, cc, gg), v);
+        store_grad<T>(w, grow, same, edge, v);
+    }
+    stored_arrive();
 }
 
 // The gradient alone, from stats: blocks of `share` vectors, independent.
 template <class T>
-__global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillParams p) {
+__global__ void __launch_bounds__(kBlock, 2) distill_grad_kernel(const DistillParams p) {
     constexpr int E = kVecOf<T>;
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ Shared sh;
     int* const ids = (int*)dyn;
     float* const prob = (float*)(ids + p.top);
     float* const named = prob + p.top;
+    int* const buckets = (int*)(named + p.top);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t t = blockIdx.x / p.cs;
     const float c = 1.4426950408889634f / p.temperature;
@@ -350,51 +482,58 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillPar
     T* const grow = (T*)p.grad + t * p.grad_stride;
     const bool same = (((uintptr_t)grow ^ (uintptr_t)row) & 15) == 0;
     const int lo = min((int)(blockIdx.x % p.cs) * p.share, w.count), hi = min(lo + p.share, w.count);
-    if (wt == 0.0f) {
+    // stats of 0 mark a row without weight or entries
+    const float m = p.stats[2 * t], l = p.stats[2 * t + 1];
+    if (wt == 0.0f || (m == 0.0f && l == 0.0f)) {
         zero_grad<T>(w, grow, same, lo, hi);
         return;
     }
-    if (warp == 0) {
+    const float l_inv = 1.0f / l, g = wt * p.temperature, gl = g * l_inv;
+    if (warp == kWarps) {
         teacher_softmax(p, t, c, ids, prob, sh);
         __syncwarp();
-        // in place, only this block's own elements are still as they were
         for (int k = lane; k < p.top; k += 32) {
             const int i = ids[k] >= 0 ? (w.shift + ids[k]) / E : -1;
             named[k] = i >= lo && i < hi ? to_f32(row[ids[k]]) : 0.0f;
         }
-    }
-    __syncthreads();
-    if (sh.entries == 0) {
-        zero_grad<T>(w, grow, same, lo, hi);
+        if (p.in_place) __syncthreads();
+        else __syncwarp();
+        entry_grads<T>(p, w, grow, lo, hi, ids, prob, named, buckets, m, l_inv, c, g, [&](int k) { return named[k]; });
         return;
     }
-    const float m = p.stats[2 * t], l_inv = 1.0f / p.stats[2 * t + 1];
-    const float g = wt * p.temperature, gl = g * l_inv;
+    const int wlo = max(lo, w.whole_lo()), whi = max(wlo, min(hi, w.whole_hi()));
+    const int edge = tid == 0 && lo < wlo ? lo : tid == 32 && whi < hi && !(hi - 1 == lo && lo < wlo) ? hi - 1 : -1;
+    float ev[E];
+    if (edge >= 0) edge_vector<T>(w, edge, ev);
+    const Pair minus(-m, -m), cc(c, c), gg(gl, gl);
     constexpr int B = 4;  // vectors in flight
-    for (int i0 = lo + tid; i0 < hi; i0 += B * kThreads) {
-        float v[B][E];
+    for (int i0 = wlo; i0 < whi; i0 += B * kThreads) {
+        uint4 v[B];
 #pragma unroll
         for (int b = 0; b < B; b++) {
-            const int i = i0 + b * kThreads;
-            if (i >= hi) break;
-            if (w.whole(i)) unpack(*(const uint4*)(w.base + (uintptr_t)i * 16), v[b]);
-            else edge_vector<T>(w, i, v[b]);
+            const int i = i0 + tid + b * kThreads;
+            if (i < whi) v[b] = *(const uint4*)(w.base + (uintptr_t)i * 16);
         }
+        // in place, the teacher's warp reads its logits before they are replaced
+        if (p.in_place && i0 == wlo) __syncthreads();
 #pragma unroll
         for (int b = 0; b < B; b++) {
-            const int i = i0 + b * kThreads;
-            if (i >= hi) break;
-#pragma unroll
-            for (int j = 0; j < E; j++) v[b][j] = exp2_fast((v[b][j] - m) * c) * gl;
-            store_grad<T>(w, grow, same, i, v[b]);
+            const int i = i0 + tid + b * kThreads;
+            if (i < whi) store_vector<T>(w, grow, same, i, column_grads<T>(v[b], minus, cc, gg));
         }
     }
-    __syncthreads();
-    entry_grads<T>(p, w, grow, lo, hi, ids, prob, m, l_inv, c, g, [&](int k) { return named[k]; });
+    if (p.in_place && wlo >= whi) __syncthreads();
+    if (edge >= 0) {
+        float v[E];
+        unpack(column_grads<T>(pack(ev), minus, cc, gg), v);
+        store_grad<T>(w, grow, same, edge, v);
+    }
+    stored_arrive();
 }
 
-// Shared memory of a block's share: three blocks fit an SM.
-constexpr int kShareBytes = 64 << 10;
+// A block's share of a row: three blocks fit an SM (and 128 KB or 256 KB rows
+// of any alignment are two or four shares).
+constexpr int kShareBytes = 65 << 10;
 constexpr int kMaxShareBytes = 200 << 10;
 
 }  // namespace
@@ -418,21 +557,22 @@ cudaError_t launch_distill(const hc_distill_t& a, DistillMode mode, cudaStream_t
     p.bf16_teacher = a.teacher_dtype == HC_BFLOAT16;
     p.temperature = a.temperature;
     p.scale = a.scale;
+    p.in_place = a.grad_logits == a.logits;
     const bool bf = a.dtype == HC_BFLOAT16;
     const int E = bf ? 8 : 4;
     const int vecs = (p.vocab + 2 * E - 2) / E;  // of a row at any alignment
     void* args[] = {&p};
-    const int entry_bytes = p.top * 12;
+    const int entry_bytes = p.top * 12 + bucket_count(p.top) * 4;
     if (mode == DISTILL_GRAD) {
         p.share = 4 * kThreads;
         p.cs = (vecs + p.share - 1) / p.share;
         const int64_t grid = p.tokens * p.cs;
         if (grid > INT32_MAX) return cudaErrorInvalidValue;
         const void* fn = bf ? (const void*)distill_grad_kernel<Bf16> : (const void*)distill_grad_kernel<float>;
-        return launch_op(fn, dim3((unsigned)grid), dim3(kThreads), args, (size_t)entry_bytes, stream);
+        return launch_op(fn, dim3((unsigned)grid), dim3(kBlock), args, (size_t)entry_bytes, stream);
     }
     p.cs = 1;
-    while (p.cs < 8 && ((int64_t)vecs * 16 > (int64_t)kShareBytes * p.cs ||
+    while (p.cs < kMaxCluster && ((int64_t)vecs * 16 > (int64_t)kShareBytes * p.cs ||
                         (p.tokens * p.cs < sms && vecs / p.cs > kThreads)))
         p.cs *= 2;
     p.share = (vecs + p.cs - 1) / p.cs;
@@ -450,7 +590,7 @@ cudaError_t launch_distill(const hc_distill_t& a, DistillMode mode, cudaStream_t
     if (!allow_smem((void*)fn, smem)) return cudaErrorInvalidValue;
     const int64_t grid = p.tokens * p.cs;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    return launch_op(fn, dim3((unsigned)grid), dim3(kThreads), args, (size_t)smem, stream, p.cs);
+    return launch_op(fn, dim3((unsigned)grid), dim3(kBlock), args, (size_t)smem, stream, p.cs);
 }
 
 }  // namespace hc

@@ -488,8 +488,10 @@ size_t hc_block_norm_grad_scratch_bytes(const hc_block_norm_grad_t* args);
  *  grad_logits : NULL: the loss alone.  May be exactly logits in place.
  *  top         : 1 to 1024; vocab at most 2^20 elements and 1.5 MiB a row
  *                (HC_ERR_UNSUPPORTED).
- * hc_distill_grad writes grad_logits alone, from stats (loss is not used):
- * the backward pass of a loss whose row_weight is only known then.
+ * hc_distill_grad writes grad_logits alone, from the stats that hc_distill
+ * kept of the same logits and teacher (loss is not used): the backward pass of
+ * a loss whose row_weight is only known then.  A row whose stats are 0 has
+ * gradient 0.
  */
 typedef struct {
     size_t struct_size;
