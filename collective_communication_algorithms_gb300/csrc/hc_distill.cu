@@ -18,6 +18,8 @@
 // 16-byte vectors of memory, the vectors that also hold a neighbouring row's
 // elements (or lie past the matrix) are fetched element by element, the
 // foreign elements set to -inf.
+#include <algorithm>
+
 #include "hc_ops.cuh"
 
 namespace hc {
@@ -46,6 +48,7 @@ struct DistillParams {
     unsigned long long wait_ns;
     int hold;
     bool in_place;    // the gradient replaces the logits
+    int64_t ahead;    // rows that the resident blocks hold
 };
 
 struct Shared {
@@ -123,6 +126,9 @@ __device__ __forceinline__ float largest(const uint4& u) {
         return fmaxf(bf_lo(m), bf_hi(m));
     }
     return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+}
+__device__ __forceinline__ void bulk_prefetch_l2(uintptr_t p, unsigned bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 // Waits of the threads that go through the logits, and of the teacher's warp
 // for them.
@@ -306,15 +312,15 @@ __global__ void __launch_bounds__(kBlock, 3) distill_kernel(const DistillParams 
     const int64_t t = blockIdx.x / p.cs;
     const float c = 1.4426950408889634f / p.temperature;
     if (p.cs > 1) cluster_arrive();
+    grid_wait();
+    grid_release();
+    const float wt = p.scale * (p.weight ? p.weight[t] : 1.0f);
     if (tid == 0) {
         for (int i = 0; i < kPieces; i++) mbar_init(&sh.full[i], 1 + (i == 0 ? p.hold : 0));
         sh.failed = 0;
         mbar_init_fence();
     }
     __syncthreads();
-    grid_wait();
-    grid_release();
-    const float wt = p.scale * (p.weight ? p.weight[t] : 1.0f);
     const T* const row = (const T*)p.logits + t * p.logits_stride;
     const Window<T> w(row, p.vocab);
     T* const grow = (T*)p.grad + t * p.grad_stride;
@@ -338,6 +344,16 @@ __global__ void __launch_bounds__(kBlock, 3) distill_kernel(const DistillParams 
             const int a = wlo + lane * p.piece, n = min(p.piece, whi - a);
             mbar_arrive_expect_tx(&sh.full[lane], (unsigned)n * 16);
             bulk_g2s(buf + (a - lo), w.base + (uintptr_t)a * 16, (unsigned)n * 16, &sh.full[lane]);
+        }
+        // the share of the row that takes this block's place comes into L2
+        // meanwhile: what shared memory holds is too little to keep the memory
+        // busy while blocks wait for each other
+        const int64_t then = t + p.ahead;
+        if (p.ahead && then < p.tokens && lane < kPieces && (!p.weight || p.weight[then] != 0.0f)) {
+            const Window<T> next((const T*)p.logits + then * p.logits_stride, p.vocab);
+            const int b = min((int)(rank + 1) * p.share, next.whole_hi());
+            const int a = max((int)rank * p.share, next.whole_lo()) + lane * p.piece, n = min(p.piece, b - a);
+            if (n > 0) bulk_prefetch_l2(next.base + (uintptr_t)a * 16, (unsigned)n * 16);
         }
         __syncwarp();
         teacher_softmax(p, t, c, ids, prob, sh);
@@ -590,6 +606,7 @@ cudaError_t launch_distill(const hc_distill_t& a, DistillMode mode, cudaStream_t
     if (!allow_smem((void*)fn, smem)) return cudaErrorInvalidValue;
     const int64_t grid = p.tokens * p.cs;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    p.ahead = (int64_t)sms * std::max(1, std::min(3, (224 << 10) / smem)) / p.cs;
     return launch_op(fn, dim3((unsigned)grid), dim3(kBlock), args, (size_t)smem, stream, p.cs);
 }
 
