@@ -29,6 +29,7 @@ constexpr int kThreads = 256;               // that go through the logits
 constexpr int kWarps = kThreads / 32;
 constexpr int kBlock = kThreads + 32;       // and the teacher's warp
 constexpr int kPieces = 16;  // bulk copies (and barriers) of a share at most
+constexpr int kUnroll = 4;   // vectors that a thread takes at a time
 
 struct DistillParams {
     const void* logits;
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kBlock, 3) distill_kernel(const DistillParams 
     const unsigned rank = blockIdx.x % p.cs;
     const int64_t t = blockIdx.x / p.cs;
     const float c = 1.4426950408889634f / p.temperature;
-    if (p.cs > 1) cluster_arrive();
+    if (p.cs > 1) cluster_arrive_relaxed();
     grid_wait();
     grid_release();
     const float wt = p.scale * (p.weight ? p.weight[t] : 1.0f);
@@ -364,8 +365,15 @@ __global__ void __launch_bounds__(kBlock, 3) distill_kernel(const DistillParams 
         // running maximum and sum of this thread's vectors
         Pair sum(0.0f, 0.0f);
         const Pair cc(c, c);
-        auto take = [&](const uint4& u) {
-            const float mx = largest<T>(u);
+        auto take = [&](const uint4* u, int n, int step) {  // n vectors, `step` apart; kUnroll or fewer
+            uint4 x[kUnroll];
+            float mx = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kUnroll; k++)
+                if (k < n) {
+                    x[k] = u[k * step];
+                    mx = fmaxf(mx, largest<T>(x[k]));
+                }
             if (mx > m) {
                 const float f = exp2_fast((m - mx) * c);  // 0 at first
                 sum = sum * Pair(f, f);
@@ -373,17 +381,21 @@ __global__ void __launch_bounds__(kBlock, 3) distill_kernel(const DistillParams 
             }
             const float ref = m == -INFINITY ? 0.0f : -m;
             const Pair minus(ref, ref);
-            Pair v[E / 2];
-            pairs_of(u, v);
 #pragma unroll
-            for (int j = 0; j < E / 2; j++) sum = sum + exp2_pair((v[j] + minus) * cc);
+            for (int k = 0; k < kUnroll; k++)
+                if (k < n) {
+                    Pair v[E / 2];
+                    pairs_of(x[k], v);
+#pragma unroll
+                    for (int j = 0; j < E / 2; j++) sum = sum + exp2_pair((v[j] + minus) * cc);
+                }
         };
         const int edge = tid == 0 && lo < wlo ? lo : tid == 32 && whi < hi && !(hi - 1 == lo && lo < wlo) ? hi - 1 : -1;
         if (edge >= 0) {
             float v[E];
             edge_vector<T>(w, edge, v);
             buf[edge - lo] = pack(v);
-            take(buf[edge - lo]);
+            take(buf + (edge - lo), 1, 0);
         }
         bool ok = true;
         for (int i = 0; i < pieces; i++) {
@@ -393,11 +405,16 @@ __global__ void __launch_bounds__(kBlock, 3) distill_kernel(const DistillParams 
                 break;
             }
             const int a = wlo + i * p.piece - lo, b = min(a + p.piece, whi - lo);
-            for (int j = a + tid; j < b; j += kThreads) take(buf[j]);
+            for (int j = a + tid; j < b; j += kUnroll * kThreads) {
+                const int n = (b - j + kThreads - 1) / kThreads;
+                if (n >= kUnroll) take(buf + j, kUnroll, kThreads);
+                else take(buf + j, n, kThreads);
+            }
         }
         if (!ok) {
             for (int i = 0; i < pieces; i++) mbar_wait_bounded(&sh.full[i], 0, kWaitLimitNs);
             sh.failed = 1;
+            __threadfence_block();
         }
         float l2;
         sum.get(l, l2);
@@ -424,7 +441,10 @@ __global__ void __launch_bounds__(kBlock, 3) distill_kernel(const DistillParams 
         }
     }
     if (p.cs > 1) {
-        cluster_arrive();
+        // only these two warps have something for others (a releasing arrival
+        // waits for what its warp has under way)
+        if (warp == 0 || teacher) cluster_arrive();
+        else cluster_arrive_relaxed();
         cluster_wait();
     } else {
         __syncthreads();
@@ -467,6 +487,7 @@ __global__ void __launch_bounds__(kBlock, 3) distill_kernel(const DistillParams 
         return;
     }
     const Pair minus(-m, -m), cc(c, c), gg(gl, gl);
+#pragma unroll 4
     for (int i = wlo + tid; i < whi; i += kThreads) store_vector<T>(w, grow, same, i, column_grads<T>(buf[i - lo], minus, cc, gg));
     const int edge = tid == 0 && lo < wlo ? lo : tid == 32 && whi < hi && !(hi - 1 == lo && lo < wlo) ? hi - 1 : -1;
     if (edge >= 0) {
@@ -594,7 +615,7 @@ cudaError_t launch_distill(const hc_distill_t& a, DistillMode mode, cudaStream_t
     p.share = (vecs + p.cs - 1) / p.cs;
     if (p.share * 16 > kMaxShareBytes) return cudaErrorInvalidValue;
     p.piece = (p.share + kPieces - 1) / kPieces;
-    if (p.piece < kThreads) p.piece = kThreads;
+    if (p.piece < kUnroll * kThreads) p.piece = kUnroll * kThreads;
     p.err = device_error_flag();
     if (!p.err) return cudaErrorInvalidValue;
     p.hold = expiring_waits() ? 1 : 0;

@@ -140,6 +140,7 @@ __device__ __forceinline__ float warp_max(float v) {
 // ---------------------------------------------------------------------------
 constexpr int kMaxCluster = 8;
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Write to the same shared-memory variable of another block of the cluster.
 __device__ __forceinline__ void store_remote(float* local, unsigned rank, float v) {
