@@ -25,9 +25,10 @@
 namespace hc {
 namespace {
 
-constexpr int kThreads = 256;               // that go through the logits
+constexpr int kThreads = 128;               // that go through the logits
 constexpr int kWarps = kThreads / 32;
 constexpr int kBlock = kThreads + 32;       // and the teacher's warp
+constexpr int kResident = 6;                // blocks of an SM
 constexpr int kPieces = 16;  // bulk copies (and barriers) of a share at most
 constexpr int kUnroll = 4;   // vectors that a thread takes at a time
 
@@ -81,6 +82,11 @@ __device__ __forceinline__ Pair operator+(Pair a, Pair b) {
 __device__ __forceinline__ Pair operator*(Pair a, Pair b) {
     Pair r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Pair fma_pair(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
     return r;
 }
 __device__ __forceinline__ Pair exp2_pair(Pair a) {
@@ -275,13 +281,16 @@ __device__ __forceinline__ void entry_grads(const DistillParams& p, const Window
     }
 }
 
-// Gradient of the other columns: 2^((x - m) c) * gl.
+// Gradient of the other columns: 2^((x - m) c) * gl.  What is rounded to bf16
+// takes the exponent as x c - m c: m c is off by half a unit of binary32, the
+// result by about 1e-6 of itself, far below a bf16 rounding.
 template <class T>
-__device__ __forceinline__ uint4 column_grads(const uint4& u, Pair minus_m, Pair c, Pair gl) {
+__device__ __forceinline__ uint4 column_grads(const uint4& u, Pair minus_m, Pair minus_mc, Pair c, Pair gl) {
     Pair v[kVecOf<T> / 2];
     pairs_of(u, v);
 #pragma unroll
-    for (int j = 0; j < kVecOf<T> / 2; j++) v[j] = exp2_pair((v[j] + minus_m) * c) * gl;
+    for (int j = 0; j < kVecOf<T> / 2; j++)
+        v[j] = exp2_pair(sizeof(T) == 2 ? fma_pair(v[j], c, minus_mc) : (v[j] + minus_m) * c) * gl;
     return pack_pairs(v);
 }
 template <class T>
@@ -298,7 +307,7 @@ __device__ __forceinline__ void store_vector(const Window<T>& w, T* row, bool sa
 
 // MODE 0: the loss, 1: the loss and the gradient (DISTILL_LOSS, DISTILL_BOTH).
 template <class T, int MODE>
-__global__ void __launch_bounds__(kBlock, 3) distill_kernel(const DistillParams p) {
+__global__ void __launch_bounds__(kBlock, kResident) distill_kernel(const DistillParams p) {
     constexpr int E = kVecOf<T>;
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ Shared sh;
@@ -486,13 +495,13 @@ __global__ void __launch_bounds__(kBlock, 3) distill_kernel(const DistillParams 
         });
         return;
     }
-    const Pair minus(-m, -m), cc(c, c), gg(gl, gl);
+    const Pair minus(-m, -m), minus_c(-m * c, -m * c), cc(c, c), gg(gl, gl);
 #pragma unroll 4
-    for (int i = wlo + tid; i < whi; i += kThreads) store_vector<T>(w, grow, same, i, column_grads<T>(buf[i - lo], minus, cc, gg));
+    for (int i = wlo + tid; i < whi; i += kThreads) store_vector<T>(w, grow, same, i, column_grads<T>(buf[i - lo], minus, minus_c, cc, gg));
     const int edge = tid == 0 && lo < wlo ? lo : tid == 32 && whi < hi && !(hi - 1 == lo && lo < wlo) ? hi - 1 : -1;
     if (edge >= 0) {
         float v[E];
-        unpack(column_grads<T>(buf[edge - lo], minus, cc, gg), v);
+        unpack(column_grads<T>(buf[edge - lo], minus, minus_c, cc, gg), v);
         store_grad<T>(w, grow, same, edge, v);
     }
     stored_arrive();
@@ -542,7 +551,7 @@ __global__ void __launch_bounds__(kBlock, 2) distill_grad_kernel(const DistillPa
     const int edge = tid == 0 && lo < wlo ? lo : tid == 32 && whi < hi && !(hi - 1 == lo && lo < wlo) ? hi - 1 : -1;
     float ev[E];
     if (edge >= 0) edge_vector<T>(w, edge, ev);
-    const Pair minus(-m, -m), cc(c, c), gg(gl, gl);
+    const Pair minus(-m, -m), minus_c(-m * c, -m * c), cc(c, c), gg(gl, gl);
     constexpr int B = 4;  // vectors in flight
     for (int i0 = wlo; i0 < whi; i0 += B * kThreads) {
         uint4 v[B];
@@ -556,21 +565,21 @@ __global__ void __launch_bounds__(kBlock, 2) distill_grad_kernel(const DistillPa
 #pragma unroll
         for (int b = 0; b < B; b++) {
             const int i = i0 + tid + b * kThreads;
-            if (i < whi) store_vector<T>(w, grow, same, i, column_grads<T>(v[b], minus, cc, gg));
+            if (i < whi) store_vector<T>(w, grow, same, i, column_grads<T>(v[b], minus, minus_c, cc, gg));
         }
     }
     if (p.in_place && wlo >= whi) __syncthreads();
     if (edge >= 0) {
         float v[E];
-        unpack(column_grads<T>(pack(ev), minus, cc, gg), v);
+        unpack(column_grads<T>(pack(ev), minus, minus_c, cc, gg), v);
         store_grad<T>(w, grow, same, edge, v);
     }
     stored_arrive();
 }
 
-// A block's share of a row: three blocks fit an SM (and 128 KB or 256 KB rows
-// of any alignment are two or four shares).
-constexpr int kShareBytes = 65 << 10;
+// A block's share of a row: six blocks fit an SM (and 128 KB or 256 KB rows of
+// any alignment are four or eight shares).
+constexpr int kShareBytes = 33 << 10;
 constexpr int kMaxShareBytes = 200 << 10;
 
 }  // namespace
@@ -627,7 +636,7 @@ cudaError_t launch_distill(const hc_distill_t& a, DistillMode mode, cudaStream_t
     if (!allow_smem((void*)fn, smem)) return cudaErrorInvalidValue;
     const int64_t grid = p.tokens * p.cs;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    p.ahead = (int64_t)sms * std::max(1, std::min(3, (224 << 10) / smem)) / p.cs;
+    p.ahead = (int64_t)sms * std::max(1, std::min(kResident, (224 << 10) / smem)) / p.cs;
     return launch_op(fn, dim3((unsigned)grid), dim3(kBlock), args, (size_t)smem, stream, p.cs);
 }
 
