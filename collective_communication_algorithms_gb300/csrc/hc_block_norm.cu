@@ -168,57 +168,64 @@ struct RowSum {
     }
 };
 
-// A thread's columns: vectors v of N neighbouring ones, tx * N apart.  N is 1,
-// or dim is a multiple of N and every row aligned, so that a vector lies in
-// the row as a whole or not at all.
-template <class T, int N, int C>
+// A thread's columns, in pairs: vectors v of N neighbouring ones, tx * N apart.
+// N is 1, or dim is a multiple of N and every row aligned, so that a vector
+// lies in the row as a whole or not at all.  FULL: every vector lies in it.
+template <class T, int N, int C, bool FULL>
 struct Columns {
     static constexpr int V = C / N;
     int tid, tx, first, dim;  // first column of the block's slice
     __device__ __forceinline__ int local(int v) const { return (v * tx + tid) * N; }
     __device__ __forceinline__ int at(int v) const { return first + local(v); }
-    __device__ __forceinline__ int in(int v) const { return dim - at(v); }  // columns left
+    __device__ __forceinline__ bool in(int v) const { return FULL || at(v) < dim; }
 
-    __device__ __forceinline__ void load(const T* row, bool live, float (&x)[C]) const {
+    template <class S>
+    __device__ __forceinline__ void get(const S* row, bool live, Pair (&x)[C / 2]) const {
+        float f[C];
 #pragma unroll
         for (int v = 0; v < V; v++) {
             float e[N];
-            load_whole<T, N>(row + at(v), live && in(v) > 0, e);
+            load_whole<S, N>(row + at(v), live && in(v), e);
 #pragma unroll
-            for (int i = 0; i < N; i++) x[v * N + i] = e[i];
+            for (int i = 0; i < N; i++) f[v * N + i] = e[i];
         }
+#pragma unroll
+        for (int i = 0; i < C / 2; i++) x[i] = Pair(f[2 * i], f[2 * i + 1]);
     }
+    __device__ __forceinline__ void load(const T* row, bool live, Pair (&x)[C / 2]) const { get<T>(row, live, x); }
     // from a ring's slot, whose element `shift` is column `first`
-    __device__ __forceinline__ void load(const unsigned char* slot, int shift, float (&x)[C]) const {
-        load((const T*)slot + shift - first, true, x);
+    __device__ __forceinline__ void load(const unsigned char* slot, int shift, Pair (&x)[C / 2]) const {
+        get<T>((const T*)slot + shift - first, true, x);
     }
-    __device__ __forceinline__ void store(T* row, bool live, const float (&x)[C]) const {
+    __device__ __forceinline__ void store(T* row, bool live, const Pair (&x)[C / 2]) const {
+        float f[C];
+#pragma unroll
+        for (int i = 0; i < C / 2; i++) x[i].get(f[2 * i], f[2 * i + 1]);
 #pragma unroll
         for (int v = 0; v < V; v++) {
             float e[N];
 #pragma unroll
-            for (int i = 0; i < N; i++) e[i] = x[v * N + i];
-            store_whole<T, N>(row + at(v), live && in(v) > 0, e);
+            for (int i = 0; i < N; i++) e[i] = f[v * N + i];
+            store_whole<T, N>(row + at(v), live && in(v), e);
         }
     }
     // a weight vector (ones where there is none)
-    __device__ __forceinline__ void weight(const void* w, bool bf16, int64_t row, float (&x)[C]) const {
+    __device__ __forceinline__ void weight(const void* w, bool bf16, int64_t row, Pair (&x)[C / 2]) const {
+        if (!w) {
 #pragma unroll
-        for (int v = 0; v < V; v++) {
-            float e[N];
-            if (!w) {
-#pragma unroll
-                for (int i = 0; i < N; i++) e[i] = 1.0f;
-            } else if (bf16) {
-                load_whole<Bf16, N>((const Bf16*)w + row * dim + at(v), in(v) > 0, e);
-            } else {
-                load_whole<float, N>((const float*)w + row * dim + at(v), in(v) > 0, e);
-            }
-#pragma unroll
-            for (int i = 0; i < N; i++) x[v * N + i] = e[i];
+            for (int i = 0; i < C / 2; i++) x[i] = Pair(1.0f, 1.0f);
+        } else if (bf16) {
+            get<Bf16>((const Bf16*)w + row * dim, true, x);
+        } else {
+            get<float>((const float*)w + row * dim, true, x);
         }
     }
 };
+__device__ __forceinline__ float both(Pair a) {
+    float lo, hi;
+    a.get(lo, hi);
+    return lo + hi;
+}
 
 struct NormParams {
     Operand in[2];  // y, x
@@ -234,7 +241,7 @@ struct NormParams {
 };
 
 // blockDim = (tx, ty) for a ring, (tx * ty) for rows in warps.
-template <class T, int N, bool RING>
+template <class T, int N, bool RING, bool FULL>
 __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p) {
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ uint64_t full[kMaxGroups][kStages];
@@ -244,7 +251,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p) 
     const int tid = RING ? threadIdx.x : threadIdx.x % L.tx;
     const int ty = RING ? threadIdx.y : threadIdx.x / L.tx;
     const int rank = RING ? blockIdx.x % L.cs : 0;
-    const Columns<T, N, kCols> col{tid, L.tx, rank * L.tx * kCols, p.dim};
+    constexpr int H = kCols / 2;
+    const Columns<T, N, kCols, FULL> col{tid, L.tx, rank * L.tx * kCols, p.dim};
     RowSum<RING> row_sum{warp_sums, rank_sums, L.tx, ty, L.cs};
     const int64_t start = (int64_t)(blockIdx.x / L.cs) * L.ty + ty;
     const int64_t step = (int64_t)(gridDim.x / L.cs) * L.ty;
@@ -264,7 +272,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p) 
     if (RING && tid < 2)
         for (; issued < L.stages && next < p.tokens; issued++, next += step) ring.load(issued, next, tid, p.in[tid]);
     const float inv_dim = 1.0f / (float)p.dim;
-    float wg[kCols], pw[kCols];  // post_weight * gate, pre_weight
+    const Pair scale(p.residual_scale, p.residual_scale);
+    Pair wg[H], pw[H];  // post_weight * gate, pre_weight
     int64_t gate_end = -1;       // of the tokens that wg is for
     col.weight(p.pre_weight, p.bf16_weights, 0, pw);
     int stage = 0;
@@ -273,7 +282,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p) 
         // rows in warps: every lane takes part in the shuffles of its one row
         const bool live = t < p.tokens;
         if (RING && !live) break;
-        float y[kCols], x[kCols];
+        Pair y[H], x[H];
         const T* yrow = (const T*)p.in[0].base + t * p.in[0].stride;
         const T* xrow = (const T*)p.in[1].base + t * p.in[1].stride;
         if (!RING) {
@@ -283,21 +292,22 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p) 
         if (t >= gate_end) {
             const int64_t g = live ? (unsigned)t / p.per_gate : 0;
             gate_end = (g + 1) * p.per_gate;
-            float gt[kCols];
+            Pair gt[H];
             col.weight(p.post_weight, p.bf16_weights, 0, wg);
             col.weight(p.gate, p.bf16_weights, g, gt);
 #pragma unroll
-            for (int i = 0; i < kCols; i++) wg[i] *= gt[i];
+            for (int i = 0; i < H; i++) wg[i] = wg[i] * gt[i];
         }
         if (RING) {
             ring.wait(stage, phase, t == start, tid == 0);
             col.load(ring.slot(stage, 0), ring.shift_of(yrow + col.first), y);
             col.load(ring.slot(stage, 1), ring.shift_of(xrow + col.first), x);
         }
-        float s = 0.0f;
+        Pair s(0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < kCols; i++) s = fmaf(y[i], y[i], s);
-        const float post = rsqrtf(fmaf(row_sum(s), inv_dim, p.eps));
+        for (int i = 0; i < H; i++) s = fma_pair(y[i], y[i], s);
+        const float post = rsqrtf(fmaf(row_sum(both(s)), inv_dim, p.eps));
+        const Pair post2(post, post);
         if (RING) {
             if (tid < 2 && ring.ok && next < p.tokens) {
                 ring.load(stage, next, tid, p.in[tid]);
@@ -309,20 +319,21 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p) 
                 phase++;
             }
         }
-        s = 0.0f;
+        s = Pair(0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < kCols; i++) {
-            x[i] = fmaf(wg[i], y[i] * post, p.residual_scale * x[i]);
-            s = fmaf(x[i], x[i], s);
+        for (int i = 0; i < H; i++) {
+            x[i] = fma_pair(wg[i], y[i] * post2, scale * x[i]);
+            s = fma_pair(x[i], x[i], s);
         }
         col.store((T*)p.r + t * p.r_stride, live, x);
         const bool first = tid == 0 && rank == 0 && live;
         if (first && p.post_rstd) p.post_rstd[t] = post;
         if (p.z) {
-            const float pre = rsqrtf(fmaf(row_sum(s), inv_dim, p.eps));
+            const float pre = rsqrtf(fmaf(row_sum(both(s)), inv_dim, p.eps));
             if (first && p.pre_rstd) p.pre_rstd[t] = pre;
+            const Pair pre2(pre, pre);
 #pragma unroll
-            for (int i = 0; i < kCols; i++) x[i] *= pre * pw[i];
+            for (int i = 0; i < H; i++) x[i] = x[i] * (pre2 * pw[i]);
             col.store((T*)p.z + t * p.z_stride, live, x);
         }
         if (!RING) break;
@@ -350,9 +361,12 @@ struct NormGradParams {
 };
 
 // Add the rows' sums of a block into row 0's, in row order, and store them.
-template <class T, int N, int C>
-__device__ __forceinline__ void store_part(const Columns<T, N, C>& col, int ty, int rows, float* joined, float* part,
-                                           float (&acc)[C]) {
+template <class T, int N, int C, bool FULL>
+__device__ __forceinline__ void store_part(const Columns<T, N, C, FULL>& col, int ty, int rows, float* joined, float* part,
+                                           const Pair (&sums)[C / 2]) {
+    float acc[C];
+#pragma unroll
+    for (int i = 0; i < C / 2; i++) sums[i].get(acc[2 * i], acc[2 * i + 1]);
     if (rows > 1) {
         float* mine = joined + ty * col.tx + col.tid;
         const int pitch = rows * col.tx;
@@ -366,20 +380,20 @@ __device__ __forceinline__ void store_part(const Columns<T, N, C>& col, int ty, 
             for (int i = 0; i < C; i++) acc[i] += mine[i * pitch + r * col.tx];
     }
 #pragma unroll
-    for (int v = 0; v < Columns<T, N, C>::V; v++) {
+    for (int v = 0; v < C / N; v++) {
         float e[N];
 #pragma unroll
         for (int i = 0; i < N; i++) e[i] = acc[v * N + i];
-        store_n<float, N>(part + col.at(v), col.in(v), e);
+        store_whole<float, N>(part + col.at(v), col.in(v), e);
     }
 }
 
 // GROUPS false: the block's run of `unit` tokens lies in one gate row, its
 // tokens are dealt to the block's rows of threads.  true: the block has
 // `unit` whole gate rows, dealt to the rows of threads.
-template <class T, int N, bool RING, bool GROUPS>
+template <class T, int N, bool RING, bool GROUPS, bool FULL>
 __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradParams p) {
-    constexpr int C = kGradCols;
+    constexpr int C = kGradCols, H = C / 2;
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ uint64_t full[kMaxGroups][kStages];
     __shared__ __align__(16) float warp_sums[2][kMaxGroups * 4 + kRowWarps];
@@ -389,7 +403,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
     const int ty = RING ? threadIdx.y : threadIdx.x / L.tx;
     const int rank = RING ? blockIdx.x % L.cs : 0;
     const int64_t block = blockIdx.x / L.cs;
-    const Columns<T, N, C> col{tid, L.tx, rank * L.tx * C, p.dim};
+    const Columns<T, N, C, FULL> col{tid, L.tx, rank * L.tx * C, p.dim};
     RowSum<RING> row_sum{warp_sums, rank_sums, L.tx, ty, L.cs};
     Ring<T, 4, (N > 1)> ring{dyn + (size_t)ty * L.stages * 4 * L.slot, full[ty], L, p.tokens, col.first,
                              min(L.tx * C, p.dim - col.first)};
@@ -448,14 +462,17 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
             advance(next);
         }
     const float inv_dim = 1.0f / (float)p.dim;
-    float a[C] = {}, ga[C] = {}, pre_acc[C] = {};
-    float wg[C], pw[C];  // post_weight * gate, pre_weight
+    const Pair zero(0.0f, 0.0f), scale(p.residual_scale, p.residual_scale);
+    Pair a[H], ga[H], pre_acc[H];
+#pragma unroll
+    for (int i = 0; i < H; i++) a[i] = ga[i] = pre_acc[i] = zero;
+    Pair wg[H], pw[H];  // post_weight * gate, pre_weight
     auto load_gate = [&](int64_t g) {
-        float gt[C];
+        Pair gt[H];
         col.weight(p.post_weight, p.bf16_weights, 0, wg);
         col.weight(p.gate, p.bf16_weights, g, gt);
 #pragma unroll
-        for (int i = 0; i < C; i++) wg[i] *= gt[i];
+        for (int i = 0; i < H; i++) wg[i] = wg[i] * gt[i];
     };
     col.weight(p.pre_weight, p.bf16_weights, 0, pw);
     if (count) load_gate(now.gate);
@@ -464,19 +481,22 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
     for (unsigned k = 0; k < steps; k++) {
         const bool live = k < count;
         const int64_t t = now.t;
-        float d0[C] = {}, y[C] = {}, rh[C] = {};
+        Pair d0[H], y[H], rh[H];
+#pragma unroll
+        for (int i = 0; i < H; i++) d0[i] = y[i] = rh[i] = zero;
         const float post = live ? p.post_rstd[t] : 0.0f;
         const float pre = live && p.in[1].base ? p.pre_rstd[t] : 0.0f;
         // y -> yhat; x -> rhat; h = gz * pre_weight; d0 = gr + pre * h
-        float s = 0.0f;
+        const Pair post2(post, post), pre2(pre, pre);
+        Pair s = zero;
         if (RING || live) {
-            float gz[C];
+            Pair gz[H];
             if (RING) ring.wait(stage, phase, k == 0, tid == 0);
-            auto load = [&](int o, float (&v)[C]) {
+            auto load = [&](int o, Pair (&v)[H]) {
                 const T* row = (const T*)p.in[o].base + t * p.in[o].stride;
                 if (!p.in[o].base) {
 #pragma unroll
-                    for (int i = 0; i < C; i++) v[i] = 0.0f;
+                    for (int i = 0; i < H; i++) v[i] = zero;
                 } else if (RING) {
                     col.load(ring.slot(stage, o), ring.shift_of(row + col.first), v);
                 } else {
@@ -488,16 +508,16 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
             load(2, y);
             load(3, rh);
 #pragma unroll
-            for (int i = 0; i < C; i++) {
-                y[i] *= post;
-                rh[i] = fmaf(wg[i], y[i], p.residual_scale * rh[i]) * pre;
-                pre_acc[i] = fmaf(gz[i], rh[i], pre_acc[i]);
-                const float h = gz[i] * pw[i];
-                s = fmaf(h, rh[i], s);
-                d0[i] = fmaf(pre, h, d0[i]);
+            for (int i = 0; i < H; i++) {
+                y[i] = y[i] * post2;
+                rh[i] = fma_pair(wg[i], y[i], scale * rh[i]) * pre2;
+                pre_acc[i] = fma_pair(gz[i], rh[i], pre_acc[i]);
+                const Pair h = gz[i] * pw[i];
+                s = fma_pair(h, rh[i], s);
+                d0[i] = fma_pair(pre2, h, d0[i]);
             }
         }
-        const float m1 = pre * (row_sum(s) * inv_dim);
+        const float m1 = -pre * (row_sum(both(s)) * inv_dim);
         if (RING) {
             if (tid < 4 && ring.ok && issued < count) {
                 ring.load(stage, next.t, tid, p.in[tid]);
@@ -510,36 +530,40 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
             }
         }
         // d = gr + pre (h - rhat mean(h rhat)), k = d * gate * post_weight
-        s = 0.0f;
+        s = zero;
+        const Pair m12(m1, m1);
         if (RING || live) {
 #pragma unroll
-            for (int i = 0; i < C; i++) {
-                const float d = fmaf(-m1, rh[i], d0[i]);
-                a[i] = fmaf(d, y[i], a[i]);
-                rh[i] = p.residual_scale * d;
+            for (int i = 0; i < H; i++) {
+                const Pair d = fma_pair(m12, rh[i], d0[i]);
+                a[i] = fma_pair(d, y[i], a[i]);
+                rh[i] = scale * d;
                 d0[i] = d * wg[i];
-                s = fmaf(d0[i], y[i], s);
+                s = fma_pair(d0[i], y[i], s);
             }
         }
         col.store((T*)p.grad_x + t * p.grad_x_stride, live, rh);
-        const float m2 = row_sum(s) * inv_dim;
+        const float m2 = -row_sum(both(s)) * inv_dim;
+        const Pair m22(m2, m2);
 #pragma unroll
-        for (int i = 0; i < C; i++) d0[i] = post * fmaf(-m2, y[i], d0[i]);
+        for (int i = 0; i < H; i++) d0[i] = post2 * fma_pair(m22, y[i], d0[i]);
         col.store((T*)p.grad_y + t * p.grad_y_stride, live, d0);
         if (GROUPS && now.in_gate + 1 == p.per_gate) {  // A of this gate row is complete
-            float w[C];
+            Pair w[H];
             col.weight(p.gate, p.bf16_weights, live ? now.gate : 0, w);
+            if (RING || live) {
 #pragma unroll
-            for (int i = 0; i < C; i++) ga[i] = RING || live ? fmaf(w[i], a[i], ga[i]) : ga[i];
+                for (int i = 0; i < H; i++) ga[i] = fma_pair(w[i], a[i], ga[i]);
+            }
             if (p.grad_gate && live) {
                 col.weight(p.post_weight, p.bf16_weights, 0, w);
 #pragma unroll
-                for (int i = 0; i < C; i++) w[i] *= a[i];
-                if (p.bf16_weights) Columns<Bf16, N, C>{tid, L.tx, col.first, p.dim}.store((Bf16*)p.grad_gate + now.gate * p.dim, true, w);
-                else Columns<float, N, C>{tid, L.tx, col.first, p.dim}.store((float*)p.grad_gate + now.gate * p.dim, true, w);
+                for (int i = 0; i < H; i++) w[i] = w[i] * a[i];
+                if (p.bf16_weights) Columns<Bf16, N, C, FULL>{tid, L.tx, col.first, p.dim}.store((Bf16*)p.grad_gate + now.gate * p.dim, true, w);
+                else Columns<float, N, C, FULL>{tid, L.tx, col.first, p.dim}.store((float*)p.grad_gate + now.gate * p.dim, true, w);
             }
 #pragma unroll
-            for (int i = 0; i < C; i++) a[i] = 0.0f;
+            for (int i = 0; i < H; i++) a[i] = zero;
             if (k + 1 < count) load_gate(now.gate + L.ty);
         }
         advance(now);
@@ -547,10 +571,10 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
     if (RING && tid == 0 && !ring.ok) ring.drain((int)issued);
     __syncthreads();  // every row has left the ring, whose memory the sums reuse
     if (!GROUPS) {
-        float gt[C];
+        Pair gt[H];
         col.weight(p.gate, p.bf16_weights, gate_row, gt);
 #pragma unroll
-        for (int i = 0; i < C; i++) ga[i] = gt[i] * a[i];
+        for (int i = 0; i < H; i++) ga[i] = gt[i] * a[i];
     }
     float* part = p.part + block * p.slots * p.pitch;
     float* joined = (float*)dyn;
@@ -648,10 +672,17 @@ cudaError_t run_norm(NormParams& p, cudaStream_t stream, int sms) {
     const bool ring = p.lay.stages > 0;
     int64_t grid = (p.tokens + p.lay.ty - 1) / p.lay.ty;
     if (ring) grid = std::min<int64_t>(grid, std::max(1, sms * (kNormThreads / (p.lay.tx * p.lay.ty)) / p.lay.cs));
-    const void* fn = vec ? (ring ? (const void*)norm_kernel<T, E, true> : (const void*)norm_kernel<T, E, false>)
-                         : (ring ? (const void*)norm_kernel<T, 1, true> : (const void*)norm_kernel<T, 1, false>);
+    const bool full = (int64_t)p.lay.tx * p.lay.cs * kCols == p.dim;
+    const void* fn = vec ? (ring ? (full ? (const void*)norm_kernel<T, E, true, true> : (const void*)norm_kernel<T, E, true, false>)
+                                 : (const void*)norm_kernel<T, E, false, false>)
+                         : (ring ? (const void*)norm_kernel<T, 1, true, false> : (const void*)norm_kernel<T, 1, false, false>);
     void* args[] = {&p};
     return launch_rows(fn, &p.lay, 2, grid, args, 0, stream);
+}
+
+template <class T, int N, bool RING, bool FULL>
+const void* pick_grad(bool by_group) {
+    return by_group ? (const void*)norm_grad_kernel<T, N, RING, true, FULL> : (const void*)norm_grad_kernel<T, N, RING, false, FULL>;
 }
 
 template <class T>
@@ -663,11 +694,10 @@ cudaError_t run_norm_grad(NormGradParams& p, bool by_group, cudaStream_t stream)
     for (const Operand& o : p.in) vec = vec && (!o.base || wide<T>(o.base, o.stride, p.dim));
     p.lay = row_layout(p.dim, sizeof(T), 4, vec, kGradCols, kNormThreads);
     const bool ring = p.lay.stages > 0;
-    const void* fn;
-    if (vec) fn = ring ? (by_group ? (const void*)norm_grad_kernel<T, E, true, true> : (const void*)norm_grad_kernel<T, E, true, false>)
-                       : (by_group ? (const void*)norm_grad_kernel<T, E, false, true> : (const void*)norm_grad_kernel<T, E, false, false>);
-    else fn = ring ? (by_group ? (const void*)norm_grad_kernel<T, 1, true, true> : (const void*)norm_grad_kernel<T, 1, true, false>)
-                   : (by_group ? (const void*)norm_grad_kernel<T, 1, false, true> : (const void*)norm_grad_kernel<T, 1, false, false>);
+    const bool full = (int64_t)p.lay.tx * p.lay.cs * kGradCols == p.dim;
+    const void* fn = vec ? (ring ? (full ? pick_grad<T, E, true, true>(by_group) : pick_grad<T, E, true, false>(by_group))
+                                 : pick_grad<T, E, false, false>(by_group))
+                         : (ring ? pick_grad<T, 1, true, false>(by_group) : pick_grad<T, 1, false, false>(by_group));
     void* args[] = {&p};
     if (p.blocks > 0) {
         const size_t joined = p.lay.ty > 1 ? (size_t)p.lay.tx * p.lay.ty * kGradCols * sizeof(float) : 0;
