@@ -31,9 +31,12 @@
 namespace hc {
 namespace {
 
-// Columns of a thread: the forward pass holds two rows' values and the
-// weights, the gradient four rows' and up to three sums.
-constexpr int kCols = 16, kGradCols = 8;
+// Columns of a thread.  More of them share the row sums' shuffles and barriers
+// (16384 x 4096 bf16, gradient: 176 us with 8, 145 with 16), as far as the
+// registers go: the gradient holds three rows' values and two sums, with 16
+// columns the weights stay in shared memory, and with a sum more, for gate rows
+// that end within a block, 8 columns are what fits.
+constexpr int kCols = 16, kGradCols = 16, kGradFewCols = 8;
 constexpr int kNormThreads = 512;  // of a block at most: up to 128 registers a thread
 constexpr int kStages = 4;         // rows in flight of a group of threads at most
 constexpr int kMaxGroups = 8;      // groups of threads (rows) of a block at most
@@ -49,6 +52,7 @@ struct Layout2 {
     int tx, ty, cs;     // cs: blocks of a cluster
     int stages;         // 0: rows in a warp, loaded directly
     int slot;           // bytes of one row (slice) of one operand in a stage
+    int weights;        // bytes of weights kept after the stages
     int* err;
     unsigned long long wait_ns;
     int hold;           // wait-expiry test mode
@@ -82,7 +86,7 @@ struct Ring {
     // of the matrix; only before its first and after its last element there
     // may be nothing, so those two vectors are filled element by element.
     __device__ __forceinline__ void load(int stage, int64_t t, int o, const Operand& op) const {
-        if (!op.base) {
+        if (!op.base || !cols) {  // the last block of a cluster may have no columns
             mbar_arrive(&full[stage]);
             return;
         }
@@ -257,7 +261,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p) 
     const int64_t start = (int64_t)(blockIdx.x / L.cs) * L.ty + ty;
     const int64_t step = (int64_t)(gridDim.x / L.cs) * L.ty;
     Ring<T, 2, (N > 1)> ring{dyn + (size_t)ty * L.stages * 2 * L.slot, full[ty], L, p.tokens, col.first,
-                             min(L.tx * kCols, p.dim - col.first)};
+                             max(0, min(L.tx * kCols, p.dim - col.first))};
     if (RING) {
         if (tid == 0) ring.init();
         row_sum.init(threadIdx.y * L.tx + tid, L.tx * L.ty);
@@ -391,9 +395,10 @@ __device__ __forceinline__ void store_part(const Columns<T, N, C, FULL>& col, in
 // GROUPS false: the block's run of `unit` tokens lies in one gate row, its
 // tokens are dealt to the block's rows of threads.  true: the block has
 // `unit` whole gate rows, dealt to the rows of threads.
-template <class T, int N, bool RING, bool GROUPS, bool FULL>
+template <class T, int N, bool RING, bool GROUPS, bool FULL, int C>
 __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradParams p) {
-    constexpr int C = kGradCols, H = C / 2;
+    constexpr int H = C / 2;
+    constexpr bool SHARED_WEIGHTS = C == kGradCols;
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ uint64_t full[kMaxGroups][kStages];
     __shared__ __align__(16) float warp_sums[2][kMaxGroups * 4 + kRowWarps];
@@ -406,7 +411,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
     const Columns<T, N, C, FULL> col{tid, L.tx, rank * L.tx * C, p.dim};
     RowSum<RING> row_sum{warp_sums, rank_sums, L.tx, ty, L.cs};
     Ring<T, 4, (N > 1)> ring{dyn + (size_t)ty * L.stages * 4 * L.slot, full[ty], L, p.tokens, col.first,
-                             min(L.tx * C, p.dim - col.first)};
+                             max(0, min(L.tx * C, p.dim - col.first))};
     // this row of threads has `count` tokens; steps: what the warp goes
     // through together (rows in warps)
     unsigned count, steps;
@@ -466,16 +471,48 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
     Pair a[H], ga[H], pre_acc[H];
 #pragma unroll
     for (int i = 0; i < H; i++) a[i] = ga[i] = pre_acc[i] = zero;
-    Pair wg[H], pw[H];  // post_weight * gate, pre_weight
+    // post_weight * gate and pre_weight: in registers, or a pair of columns
+    // each in shared memory (one copy a block: its tokens share the gate)
+    Pair wg_[SHARED_WEIGHTS ? 1 : H], pw_[SHARED_WEIGHTS ? 1 : H];
+    float4* const shared_weights = (float4*)(dyn + (size_t)L.ty * L.stages * 4 * L.slot) + tid;
     auto load_gate = [&](int64_t g) {
-        Pair gt[H];
+        Pair wg[H], gt[H];
         col.weight(p.post_weight, p.bf16_weights, 0, wg);
         col.weight(p.gate, p.bf16_weights, g, gt);
 #pragma unroll
-        for (int i = 0; i < H; i++) wg[i] = wg[i] * gt[i];
+        for (int i = 0; i < H; i++) {
+            wg[i] = wg[i] * gt[i];
+            if constexpr (!SHARED_WEIGHTS) wg_[i] = wg[i];
+        }
+        if constexpr (SHARED_WEIGHTS) {
+            Pair pw[H];
+            col.weight(p.pre_weight, p.bf16_weights, 0, pw);
+#pragma unroll
+            for (int i = 0; i < H; i++) {
+                float4 f;
+                wg[i].get(f.x, f.y);
+                pw[i].get(f.z, f.w);
+                if (ty == 0) shared_weights[i * L.tx] = f;
+            }
+        }
     };
-    col.weight(p.pre_weight, p.bf16_weights, 0, pw);
-    if (count) load_gate(now.gate);
+    auto weights = [&](int i, Pair& wg, Pair& pw) {
+        if constexpr (SHARED_WEIGHTS) {
+            const float4 f = shared_weights[i * L.tx];
+            wg = Pair(f.x, f.y);
+            pw = Pair(f.z, f.w);
+        } else {
+            wg = wg_[i];
+            pw = pw_[i];
+        }
+    };
+    if constexpr (SHARED_WEIGHTS) {
+        load_gate(now.gate);
+        __syncthreads();
+    } else {
+        col.weight(p.pre_weight, p.bf16_weights, 0, pw_);
+        if (count) load_gate(now.gate);
+    }
     int stage = 0;
     unsigned phase = 0;
     for (unsigned k = 0; k < steps; k++) {
@@ -509,10 +546,12 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
             load(3, rh);
 #pragma unroll
             for (int i = 0; i < H; i++) {
+                Pair wg, pw;
+                weights(i, wg, pw);
                 y[i] = y[i] * post2;
-                rh[i] = fma_pair(wg[i], y[i], scale * rh[i]) * pre2;
+                rh[i] = fma_pair(wg, y[i], scale * rh[i]) * pre2;
                 pre_acc[i] = fma_pair(gz[i], rh[i], pre_acc[i]);
-                const Pair h = gz[i] * pw[i];
+                const Pair h = gz[i] * pw;
                 s = fma_pair(h, rh[i], s);
                 d0[i] = fma_pair(pre2, h, d0[i]);
             }
@@ -535,10 +574,12 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
         if (RING || live) {
 #pragma unroll
             for (int i = 0; i < H; i++) {
+                Pair wg, pw;
+                weights(i, wg, pw);
                 const Pair d = fma_pair(m12, rh[i], d0[i]);
                 a[i] = fma_pair(d, y[i], a[i]);
                 rh[i] = scale * d;
-                d0[i] = d * wg[i];
+                d0[i] = d * wg;
                 s = fma_pair(d0[i], y[i], s);
             }
         }
@@ -586,8 +627,9 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
 // Sums of the partial rows: job 0: post weight, 1: pre weight, 2 + g: gate
 // row g.  The warps add equal parts of the list, joined in order.
 constexpr int kSumWarps = 16;
+template <int L>  // columns of a lane
 __global__ void __launch_bounds__(kSumWarps * 32) norm_sum_kernel(const NormGradParams p) {
-    __shared__ float sums[kSumWarps][32];
+    __shared__ float sums[kSumWarps][32 * L];
     grid_wait();
     grid_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -596,47 +638,62 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_sum_kernel(const NormGrad
         if (!out) continue;
         const int64_t g = job - 2;
         const int64_t first = job < 2 ? 0 : g * p.per_group, count = job < 2 ? p.blocks : p.per_group;
-        const int c = blockIdx.x * 32 + lane;
+        const int c = (blockIdx.x * 32 + lane) * L;
         const float* src = p.part + (first * p.slots + (job < 2 ? job : 2)) * p.pitch + c;
         const int64_t per = (count + kSumWarps - 1) / kSumWarps;
         const int64_t a = warp * per, b = a + per < count ? a + per : count;
-        float acc = 0.0f;
-        if (c < p.dim) {
+        float acc[L] = {};
+        if (c < p.pitch) {  // the pitch is a multiple of L
 #pragma unroll 8
-            for (int64_t k = a; k < b; k++) acc += src[k * p.slots * p.pitch];
+            for (int64_t k = a; k < b; k++) {
+                float v[L];
+                load_n<float, L>(src + k * p.slots * p.pitch, L, v);
+#pragma unroll
+                for (int i = 0; i < L; i++) acc[i] += v[i];
+            }
         }
         __syncthreads();  // the last job's sums have been read
-        sums[warp][lane] = acc;
+#pragma unroll
+        for (int i = 0; i < L; i++) sums[warp][i * 32 + lane] = acc[i];
         __syncthreads();
-        if (warp || c >= p.dim) continue;
-        for (int w = 1; w < kSumWarps && w * per < count; w++) acc += sums[w][lane];
-        if (job >= 2 && p.post_weight)
-            acc *= p.bf16_weights ? to_f32(((const Bf16*)p.post_weight)[c]) : ((const float*)p.post_weight)[c];
-        const int64_t at = (job < 2 ? 0 : g * p.dim) + c;
-        if (p.bf16_weights) put((Bf16*)out + at, acc);
-        else put((float*)out + at, acc);
+        if (warp) continue;
+#pragma unroll
+        for (int i = 0; i < L; i++) {
+            if (c + i >= p.dim) break;
+            for (int w = 1; w < kSumWarps && w * per < count; w++) acc[i] += sums[w][i * 32 + lane];
+            if (job >= 2 && p.post_weight)
+                acc[i] *= p.bf16_weights ? to_f32(((const Bf16*)p.post_weight)[c + i]) : ((const float*)p.post_weight)[c + i];
+            const int64_t at = (job < 2 ? 0 : g * p.dim) + c + i;
+            if (p.bf16_weights) put((Bf16*)out + at, acc[i]);
+            else put((float*)out + at, acc[i]);
+        }
     }
 }
 
 // Launch shape for rows of `dim` columns of es bytes, `ops` operands loaded.
-constexpr int kStageBytes = 200 << 10;  // of an SM's blocks together
-Layout2 row_layout(int64_t dim, int es, int ops, bool vec, int per_thread, int block_threads) {
+constexpr int kStageBytes = 192 << 10;  // of an SM's blocks together
+// Rows of up to 32 times `in_warp` columns are one warp's.
+Layout2 row_layout(int64_t dim, int es, int ops, bool vec, int in_warp, int per_thread, int block_threads) {
     Layout2 L = {};
     const int64_t threads = (dim + per_thread - 1) / per_thread;
     L.cs = 1;
-    if (threads <= 32) {
+    if (dim <= 32 * in_warp) {
         L.tx = 1;
-        while (L.tx < threads) L.tx *= 2;
+        while (L.tx * in_warp < dim) L.tx *= 2;
         L.ty = 256 / L.tx;
         return L;
     }
-    while (threads > (int64_t)kNormThreads * L.cs) L.cs *= 2;
+    // four fp32 rows of 8192 columns leave no room for a second stage
+    const bool weights = per_thread == kGradCols && ops == 4;
+    while (threads > (int64_t)(weights && es == 4 ? kNormThreads / 2 : kNormThreads) * L.cs) L.cs *= 2;
     L.tx = (int)(((threads + L.cs - 1) / L.cs + 31) / 32 * 32);
     L.ty = L.cs > 1 ? 1 : std::max(1, std::min(kMaxGroups, block_threads / L.tx));
     const int64_t cols = std::min<int64_t>(dim, (int64_t)L.tx * per_thread);
     L.slot = (int)((cols * es + (vec ? 0 : 16) + 15) / 16 * 16);
-    const int64_t share = (int64_t)kStageBytes / (kNormThreads / (L.tx * L.ty));
-    L.stages = (int)std::min<int64_t>(kStages, share / ((int64_t)L.slot * ops * L.ty));
+    if (weights) L.weights = L.tx * kGradCols * 2 * (int)sizeof(float);
+    const int64_t stage = (int64_t)L.slot * ops * L.ty;
+    L.stages = (int)std::min<int64_t>(kStages, (kStageBytes / (kNormThreads / (L.tx * L.ty)) - L.weights) / stage);
+    if (L.stages < 2) L.stages = (int)((kStageBytes - L.weights) / stage);  // one block an SM
     return L;
 }
 
@@ -655,7 +712,7 @@ cudaError_t launch_rows(const void* fn, Layout2* L, int ops, int64_t grid, void*
     L->hold = expiring_waits() ? 1 : 0;
     L->wait_ns = L->hold ? kTestWaitLimitNs : kWaitLimitNs;
     if (grid * L->cs > INT32_MAX) return cudaErrorInvalidValue;
-    const size_t smem = std::max(least_smem, (size_t)L->slot * ops * L->stages * L->ty);
+    const size_t smem = std::max(least_smem, (size_t)L->slot * ops * L->stages * L->ty + L->weights);
     if (!allow_smem((void*)fn, (int)smem)) return cudaErrorInvalidValue;
     const dim3 block = L->stages ? dim3(L->tx, L->ty) : dim3(L->tx * L->ty);
     return launch_op(fn, dim3((unsigned)(grid * L->cs)), block, args, smem, stream, L->cs);
@@ -668,7 +725,7 @@ cudaError_t run_norm(NormParams& p, cudaStream_t stream, int sms) {
                      wide<T>(p.r, p.r_stride, p.dim) && (!p.z || wide<T>(p.z, p.z_stride, p.dim)) &&
                      wide_weight(p.post_weight, p.bf16_weights, p.dim) && wide_weight(p.gate, p.bf16_weights, p.dim) &&
                      wide_weight(p.pre_weight, p.bf16_weights, p.dim);
-    p.lay = row_layout(p.dim, sizeof(T), 2, vec, kCols, kNormThreads / 2);
+    p.lay = row_layout(p.dim, sizeof(T), 2, vec, kCols, kCols, kNormThreads / 2);
     const bool ring = p.lay.stages > 0;
     int64_t grid = (p.tokens + p.lay.ty - 1) / p.lay.ty;
     if (ring) grid = std::min<int64_t>(grid, std::max(1, sms * (kNormThreads / (p.lay.tx * p.lay.ty)) / p.lay.cs));
@@ -682,7 +739,8 @@ cudaError_t run_norm(NormParams& p, cudaStream_t stream, int sms) {
 
 template <class T, int N, bool RING, bool FULL>
 const void* pick_grad(bool by_group) {
-    return by_group ? (const void*)norm_grad_kernel<T, N, RING, true, FULL> : (const void*)norm_grad_kernel<T, N, RING, false, FULL>;
+    return by_group ? (const void*)norm_grad_kernel<T, N, RING, true, FULL, kGradFewCols>
+                    : (const void*)norm_grad_kernel<T, N, RING, false, FULL, (RING && N > 1 ? kGradCols : kGradFewCols)>;
 }
 
 template <class T>
@@ -692,27 +750,33 @@ cudaError_t run_norm_grad(NormGradParams& p, bool by_group, cudaStream_t stream)
                wide_weight(p.post_weight, p.bf16_weights, p.dim) && wide_weight(p.gate, p.bf16_weights, p.dim) &&
                wide_weight(p.pre_weight, p.bf16_weights, p.dim) && wide_weight(p.grad_gate, p.bf16_weights, p.dim);
     for (const Operand& o : p.in) vec = vec && (!o.base || wide<T>(o.base, o.stride, p.dim));
-    p.lay = row_layout(p.dim, sizeof(T), 4, vec, kGradCols, kNormThreads);
+    int cols = vec && !by_group ? kGradCols : kGradFewCols;
+    p.lay = row_layout(p.dim, sizeof(T), 4, vec, kGradFewCols, cols, cols == kGradCols ? kNormThreads / 2 : kNormThreads);
+    if (!p.lay.stages) cols = kGradFewCols;
     const bool ring = p.lay.stages > 0;
-    const bool full = (int64_t)p.lay.tx * p.lay.cs * kGradCols == p.dim;
+    const bool full = (int64_t)p.lay.tx * p.lay.cs * cols == p.dim;
     const void* fn = vec ? (ring ? (full ? pick_grad<T, E, true, true>(by_group) : pick_grad<T, E, true, false>(by_group))
                                  : pick_grad<T, E, false, false>(by_group))
                          : (ring ? pick_grad<T, 1, true, false>(by_group) : pick_grad<T, 1, false, false>(by_group));
     void* args[] = {&p};
     if (p.blocks > 0) {
-        const size_t joined = p.lay.ty > 1 ? (size_t)p.lay.tx * p.lay.ty * kGradCols * sizeof(float) : 0;
+        const size_t joined = p.lay.ty > 1 ? (size_t)p.lay.tx * p.lay.ty * cols * sizeof(float) : 0;
         const cudaError_t e = launch_rows(fn, &p.lay, 4, p.blocks, args, joined, stream);
         if (e != cudaSuccess) return e;
     }
     // gate rows by_group blocks have not written; without tokens all are zeros
     p.jobs = 2 + (p.grad_gate && (!by_group || p.blocks == 0) ? p.gates : 0);
     if (!p.grad_post_weight && !p.grad_pre_weight && p.jobs == 2) return cudaSuccess;
-    return launch_op((const void*)norm_sum_kernel,
-                     dim3((unsigned)((p.dim + 31) / 32), (unsigned)(p.jobs < 65535 ? p.jobs : 65535)),
+    // 16-byte loads once there are blocks enough with them
+    const bool wide_sum = (int64_t)p.dim * p.jobs >= 128 * 100;
+    const int per_block = wide_sum ? 128 : 32;
+    return launch_op(wide_sum ? (const void*)norm_sum_kernel<4> : (const void*)norm_sum_kernel<1>,
+                     dim3((unsigned)((p.dim + per_block - 1) / per_block), (unsigned)(p.jobs < 65535 ? p.jobs : 65535)),
                      dim3(kSumWarps * 32), args, 0, stream);
 }
 
-constexpr int64_t kGradBlocks = 152;  // partial sums aimed at
+// Blocks (and partial sums) aimed at: two of 256 threads an SM, or one of 512.
+constexpr int64_t kGradBlocks = 152;
 
 }  // namespace
 
@@ -747,9 +811,8 @@ BlockNormPlan block_norm_plan(int64_t tokens, int64_t dim, int64_t gate_rows, bo
     if (!tokens) {
         q.by_group = gates >= kGradBlocks;  // nothing to divide: unit, per_group and blocks are 0
     } else if (gates < kGradBlocks) {
-        const int64_t want = (kGradBlocks + gates - 1) / gates;
-        q.unit = (per_gate + want - 1) / want;
-        if (q.unit < 1) q.unit = 1;
+        const int64_t want = ((dim <= kGradCols * kNormThreads / 2 ? 2 : 1) * kGradBlocks + gates - 1) / gates;
+        q.unit = std::max<int64_t>((per_gate + want - 1) / want, std::min<int64_t>(per_gate, 4));
         q.per_group = (per_gate + q.unit - 1) / q.unit;
         q.blocks = gates * q.per_group;
         q.slots = 3;
