@@ -16,8 +16,13 @@
 //  - rows longer than a block's threads hold are split over a cluster, whose
 //    blocks exchange their sums through distributed shared memory.
 //
-// Rows that do not start on 16-byte boundaries take the same kernels with one
-// element per access, neighbouring threads on neighbouring columns.
+// Rows that do not start on 16-byte boundaries: where all inputs' rows lie
+// alike (contiguous ones of an odd dim), every vectors-of-an-alignment-period-th
+// row starts at the same place in its first vector (the row's shift), so a
+// group of threads keeps to rows of one shift and its threads to the aligned
+// vectors of memory ("window"), the first and last of which hold only a part
+// of the row.  Otherwise the same kernels take one element per access,
+// neighbouring threads on neighbouring columns.
 //
 // Weight gradients: sums over tokens of dz * rhat (pre) and A = D * yhat,
 // from which the others follow: d gate = post_weight * sum A over the gate's
@@ -69,6 +74,7 @@ struct Ring {
     int64_t tokens;
     int first, cols;  // this block's slice of the columns
     bool ok = true;
+    int failed_at = 0;  // row whose wait gave up
 
     __device__ __forceinline__ static int shift_of(const T* p) {
         return ALIGNED ? 0 : (int)(((uintptr_t)p & 15) / sizeof(T));
@@ -86,7 +92,7 @@ struct Ring {
     // of the matrix; only before its first and after its last element there
     // may be nothing, so those two vectors are filled element by element.
     __device__ __forceinline__ void load(int stage, int64_t t, int o, const Operand& op) const {
-        if (!op.base || !cols) {  // the last block of a cluster may have no columns
+        if (!op.base || (ALIGNED && cols <= 0)) {  // the last block of a cluster may have no columns
             mbar_arrive(&full[stage]);
             return;
         }
@@ -98,6 +104,10 @@ struct Ring {
             return;
         }
         const int shift = shift_of(p), end = shift + cols;
+        if (end <= 0) {
+            mbar_arrive(&full[stage]);
+            return;
+        }
         int lo = 0, hi = (end * (int)sizeof(T) + 15) / 16;
         T* q = (T*)to;
         if (shift && t == 0 && first == 0) {
@@ -106,7 +116,7 @@ struct Ring {
         }
         if (end % kVecOf<T> && t == tokens - 1) {
             hi--;
-            for (int i = max(hi * kVecOf<T>, shift); i < end; i++) q[i] = p[i - shift];
+            for (int i = max(hi * kVecOf<T>, first ? 0 : shift); i < end; i++) q[i] = p[i - shift];
         }
         const unsigned bytes = hi > lo ? (unsigned)(hi - lo) * 16 : 0u;
         mbar_arrive_expect_tx(&full[stage], bytes);
@@ -117,6 +127,7 @@ struct Ring {
     __device__ __forceinline__ void wait(int stage, unsigned phase, bool first_row, bool leader) {
         if (!ok || mbar_wait_quick(&full[stage], phase & 1, first_row ? lay.wait_ns : kWaitLimitNs)) return;
         ok = false;
+        failed_at = (int)phase * lay.stages + stage;
         mbar_expired(&full[stage], lay.err, first_row ? lay.hold : 0, leader);
     }
     // After a wait gave up: let the copies of the first `issued` rows land
@@ -174,22 +185,43 @@ struct RowSum {
 
 // A thread's columns, in pairs: vectors v of N neighbouring ones, tx * N apart.
 // N is 1, or dim is a multiple of N and every row aligned, so that a vector
-// lies in the row as a whole or not at all.  FULL: every vector lies in it.
-template <class T, int N, int C, bool FULL>
+// lies in the row as a whole or not at all; FULL: every vector lies in it.
+// WIN: N elements are 16 aligned bytes of every row of this shift.
+template <class T, int N, int C, bool FULL, bool WIN>
 struct Columns {
     static constexpr int V = C / N;
-    int tid, tx, first, dim;  // first column of the block's slice
-    __device__ __forceinline__ int local(int v) const { return (v * tx + tid) * N; }
-    __device__ __forceinline__ int at(int v) const { return first + local(v); }
-    __device__ __forceinline__ bool in(int v) const { return FULL || at(v) < dim; }
+    int begin, step, first, dim;  // vector 0's column, columns between vectors, the block's slice
+    __device__ __forceinline__ Columns(int tid, int tx, int first_, int dim_, int shift)
+        : begin(first_ + tid * N - (WIN ? shift : 0)), step(tx * N), first(first_), dim(dim_) {}
+    __device__ __forceinline__ int at(int v) const { return begin + v * step; }
+    // the whole vector lies in the row
+    __device__ __forceinline__ bool in(int v) const {
+        return FULL || (WIN ? at(v) >= 0 && at(v) + N <= dim : at(v) < dim);
+    }
 
-    template <class S>
+    // ALIGNED: of a row with the shift (weights have none); SLOT: in shared
+    // memory, where a vector that only partly lies in the row may be read
+    template <class S, bool ALIGNED = true, bool SLOT = false>
     __device__ __forceinline__ void get(const S* row, bool live, Pair (&x)[C / 2]) const {
         float f[C];
 #pragma unroll
         for (int v = 0; v < V; v++) {
             float e[N];
-            load_whole<S, N>(row + at(v), live && in(v), e);
+            if (!WIN) {
+                load_whole<S, N>(row + at(v), live && in(v), e);
+            } else if (SLOT) {
+                load_whole<S, N>(row + at(v), at(v) < dim, e);
+                if (!in(v)) {
+#pragma unroll
+                    for (int i = 0; i < N; i++) e[i] = (unsigned)(at(v) + i) < (unsigned)dim ? e[i] : 0.0f;
+                }
+            } else if (ALIGNED && in(v)) {
+                load_whole<S, N>(row + at(v), live, e);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; i++)
+                    e[i] = live && (unsigned)(at(v) + i) < (unsigned)dim ? to_f32(row[at(v) + i]) : 0.0f;
+            }
 #pragma unroll
             for (int i = 0; i < N; i++) f[v * N + i] = e[i];
         }
@@ -197,11 +229,13 @@ struct Columns {
         for (int i = 0; i < C / 2; i++) x[i] = Pair(f[2 * i], f[2 * i + 1]);
     }
     __device__ __forceinline__ void load(const T* row, bool live, Pair (&x)[C / 2]) const { get<T>(row, live, x); }
-    // from a ring's slot, whose element `shift` is column `first`
-    __device__ __forceinline__ void load(const unsigned char* slot, int shift, Pair (&x)[C / 2]) const {
-        get<T>((const T*)slot + shift - first, true, x);
+    // from a ring's slot, whose element `place` is column `first`
+    __device__ __forceinline__ void load(const unsigned char* slot, int place, Pair (&x)[C / 2]) const {
+        get<T, true, true>((const T*)slot + place - first, true, x);
     }
-    __device__ __forceinline__ void store(T* row, bool live, const Pair (&x)[C / 2]) const {
+    // aligned: the row has the shift
+    template <class S>
+    __device__ __forceinline__ void put_all(S* row, bool live, const Pair (&x)[C / 2], bool aligned) const {
         float f[C];
 #pragma unroll
         for (int i = 0; i < C / 2; i++) x[i].get(f[2 * i], f[2 * i + 1]);
@@ -210,7 +244,13 @@ struct Columns {
             float e[N];
 #pragma unroll
             for (int i = 0; i < N; i++) e[i] = f[v * N + i];
-            store_whole<T, N>(row + at(v), live && in(v), e);
+            if (!WIN || (aligned && in(v))) {
+                store_whole<S, N>(row + at(v), live && in(v), e);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; i++)
+                    if (live && (unsigned)(at(v) + i) < (unsigned)dim) put(row + at(v) + i, e[i]);
+            }
         }
     }
     // a weight vector (ones where there is none)
@@ -219,9 +259,9 @@ struct Columns {
 #pragma unroll
             for (int i = 0; i < C / 2; i++) x[i] = Pair(1.0f, 1.0f);
         } else if (bf16) {
-            get<Bf16>((const Bf16*)w + row * dim, true, x);
+            get<Bf16, false>((const Bf16*)w + row * dim, true, x);
         } else {
-            get<float>((const float*)w + row * dim, true, x);
+            get<float, false>((const float*)w + row * dim, true, x);
         }
     }
 };
@@ -239,13 +279,13 @@ struct NormParams {
     int64_t tokens, r_stride, z_stride;
     unsigned per_gate;
     int dim;
-    bool bf16_weights;
+    bool bf16_weights, alike[2];  // r and z lie in their vectors as y and x do
     float residual_scale, eps;
     Layout2 lay;
 };
 
 // blockDim = (tx, ty) for a ring, (tx * ty) for rows in warps.
-template <class T, int N, bool RING, bool FULL>
+template <class T, int N, bool RING, bool FULL, bool WIN>
 __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p) {
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ uint64_t full[kMaxGroups][kStages];
@@ -256,12 +296,14 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p) 
     const int ty = RING ? threadIdx.y : threadIdx.x / L.tx;
     const int rank = RING ? blockIdx.x % L.cs : 0;
     constexpr int H = kCols / 2;
-    const Columns<T, N, kCols, FULL> col{tid, L.tx, rank * L.tx * kCols, p.dim};
     RowSum<RING> row_sum{warp_sums, rank_sums, L.tx, ty, L.cs};
     const int64_t start = (int64_t)(blockIdx.x / L.cs) * L.ty + ty;
     const int64_t step = (int64_t)(gridDim.x / L.cs) * L.ty;
-    Ring<T, 2, (N > 1)> ring{dyn + (size_t)ty * L.stages * 2 * L.slot, full[ty], L, p.tokens, col.first,
-                             max(0, min(L.tx * kCols, p.dim - col.first))};
+    // with a window, the rows of this group of threads all have this shift
+    const int shift = WIN ? (int)((uintptr_t)((const T*)p.in[0].base + start * p.in[0].stride) & 15) / (int)sizeof(T) : 0;
+    const Columns<T, N, kCols, FULL, WIN> col(tid, L.tx, rank * L.tx * kCols, p.dim, shift);
+    Ring<T, 2, (N > 1 && !WIN)> ring{dyn + (size_t)ty * L.stages * 2 * L.slot, full[ty], L, p.tokens, col.first,
+                             min(L.tx * kCols, p.dim - col.first)};
     if (RING) {
         if (tid == 0) ring.init();
         row_sum.init(threadIdx.y * L.tx + tid, L.tx * L.ty);
@@ -329,7 +371,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p) 
             x[i] = fma_pair(wg[i], y[i] * post2, scale * x[i]);
             s = fma_pair(x[i], x[i], s);
         }
-        col.store((T*)p.r + t * p.r_stride, live, x);
+        col.put_all((T*)p.r + t * p.r_stride, live, x, p.alike[0]);
         const bool first = tid == 0 && rank == 0 && live;
         if (first && p.post_rstd) p.post_rstd[t] = post;
         if (p.z) {
@@ -338,7 +380,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p) 
             const Pair pre2(pre, pre);
 #pragma unroll
             for (int i = 0; i < H; i++) x[i] = x[i] * (pre2 * pw[i]);
-            col.store((T*)p.z + t * p.z_stride, live, x);
+            col.put_all((T*)p.z + t * p.z_stride, live, x, p.alike[1]);
         }
         if (!RING) break;
     }
@@ -359,21 +401,21 @@ struct NormGradParams {
     int64_t blocks, per_group, pitch, jobs;
     unsigned per_gate, unit;
     int dim, slots;
-    bool bf16_weights;
+    bool bf16_weights, alike[2];  // grad_x and grad_y lie in their vectors as the inputs do
     float residual_scale;
     Layout2 lay;
 };
 
 // Add the rows' sums of a block into row 0's, in row order, and store them.
-template <class T, int N, int C, bool FULL>
-__device__ __forceinline__ void store_part(const Columns<T, N, C, FULL>& col, int ty, int rows, float* joined, float* part,
-                                           const Pair (&sums)[C / 2]) {
+template <class T, int N, int C, bool FULL, bool WIN>
+__device__ __forceinline__ void store_part(const Columns<T, N, C, FULL, WIN>& col, int tid, int tx, int ty, int rows, float* joined,
+                                           float* part, const Pair (&sums)[C / 2]) {
     float acc[C];
 #pragma unroll
     for (int i = 0; i < C / 2; i++) sums[i].get(acc[2 * i], acc[2 * i + 1]);
     if (rows > 1) {
-        float* mine = joined + ty * col.tx + col.tid;
-        const int pitch = rows * col.tx;
+        float* mine = joined + ty * tx + tid;
+        const int pitch = rows * tx;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < C; i++) mine[i * pitch] = acc[i];
@@ -381,24 +423,36 @@ __device__ __forceinline__ void store_part(const Columns<T, N, C, FULL>& col, in
         if (ty) return;
         for (int r = 1; r < rows; r++)
 #pragma unroll
-            for (int i = 0; i < C; i++) acc[i] += mine[i * pitch + r * col.tx];
+            for (int i = 0; i < C; i++) acc[i] += mine[i * pitch + r * tx];
     }
 #pragma unroll
     for (int v = 0; v < C / N; v++) {
         float e[N];
 #pragma unroll
         for (int i = 0; i < N; i++) e[i] = acc[v * N + i];
-        store_whole<float, N>(part + col.at(v), col.in(v), e);
+        if (!WIN) {
+            store_whole<float, N>(part + col.at(v), col.in(v), e);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i++)
+                if ((unsigned)(col.at(v) + i) < (unsigned)col.dim) part[col.at(v) + i] = e[i];
+        }
     }
 }
 
 // GROUPS false: the block's run of `unit` tokens lies in one gate row, its
-// tokens are dealt to the block's rows of threads.  true: the block has
-// `unit` whole gate rows, dealt to the rows of threads.
-template <class T, int N, bool RING, bool GROUPS, bool FULL, int C>
+// tokens are dealt to the block's rows of threads; with a window, the run is
+// of every kClasses-th token, which all have the same shift.  true: the block
+// has `unit` whole gate rows, dealt to the rows of threads.
+constexpr int kClasses = 8;
+template <class T, int N, bool RING, bool GROUPS, bool FULL, bool WIN, int C>
 __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradParams p) {
     constexpr int H = C / 2;
     constexpr bool SHARED_WEIGHTS = C == kGradCols;
+    // yhat between the sums: out of the stage again instead of 16 registers
+    // that spill (144 us instead of 158 for 16384 x 4096 bf16; in a window, whose
+    // reads take more, 240 us instead of 213 for 16384 x 3001)
+    constexpr bool REREAD = RING && C == kGradCols && !WIN;
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ uint64_t full[kMaxGroups][kStages];
     __shared__ __align__(16) float warp_sums[2][kMaxGroups * 4 + kRowWarps];
@@ -408,10 +462,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
     const int ty = RING ? threadIdx.y : threadIdx.x / L.tx;
     const int rank = RING ? blockIdx.x % L.cs : 0;
     const int64_t block = blockIdx.x / L.cs;
-    const Columns<T, N, C, FULL> col{tid, L.tx, rank * L.tx * C, p.dim};
     RowSum<RING> row_sum{warp_sums, rank_sums, L.tx, ty, L.cs};
-    Ring<T, 4, (N > 1)> ring{dyn + (size_t)ty * L.stages * 4 * L.slot, full[ty], L, p.tokens, col.first,
-                             max(0, min(L.tx * C, p.dim - col.first))};
     // this row of threads has `count` tokens; steps: what the warp goes
     // through together (rows in warps)
     unsigned count, steps;
@@ -425,12 +476,17 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
         base = 0;
     } else {
         gate_row = block / p.per_group;
-        const unsigned lo = (unsigned)(block % p.per_group) * p.unit;
-        const unsigned have = min(p.unit, p.per_gate - lo);
+        const unsigned b = (unsigned)(block % p.per_group), klass = WIN ? b % kClasses : 0, apart = WIN ? kClasses : 1;
+        const unsigned lo = b / apart * p.unit, all = (p.per_gate - klass + apart - 1) / apart;  // tokens of the class
+        const unsigned have = lo < all ? min(p.unit, all - lo) : 0u;
         count = (unsigned)ty < have ? (have - ty - 1) / L.ty + 1 : 0u;
         steps = (p.unit + L.ty - 1) / L.ty;
-        base = gate_row * p.per_gate + lo + ty;
+        base = gate_row * p.per_gate + klass + (int64_t)apart * (lo + ty);
     }
+    const int shift = WIN ? (int)((uintptr_t)((const T*)p.in[2].base + base * p.in[2].stride) & 15) / (int)sizeof(T) : 0;
+    const Columns<T, N, C, FULL, WIN> col(tid, L.tx, rank * L.tx * C, p.dim, shift);
+    Ring<T, 4, (N > 1 && !WIN)> ring{dyn + (size_t)ty * L.stages * 4 * L.slot, full[ty], L, p.tokens, col.first,
+                             min(L.tx * C, p.dim - col.first)};
     // the tokens in order: the one to do, and (lanes that bring rows) the next
     // one to bring
     struct Walk {
@@ -439,7 +495,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
     };
     auto advance = [&](Walk& w) {
         if (!GROUPS) {
-            w.t += L.ty;
+            w.t += WIN ? kClasses * L.ty : L.ty;
         } else if (++w.in_gate == p.per_gate) {
             w.in_gate = 0;
             w.gate += L.ty;
@@ -460,10 +516,9 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
     grid_wait();
     grid_release();
     Walk next = now;
-    unsigned issued = 0;
     if (RING && tid < 4)
-        for (; issued < (unsigned)L.stages && issued < count; issued++) {
-            ring.load(issued, next.t, tid, p.in[tid]);
+        for (unsigned i = 0; i < (unsigned)L.stages && i < count; i++) {
+            ring.load((int)i, next.t, tid, p.in[tid]);
             advance(next);
         }
     const float inv_dim = 1.0f / (float)p.dim;
@@ -518,6 +573,17 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
     for (unsigned k = 0; k < steps; k++) {
         const bool live = k < count;
         const int64_t t = now.t;
+        // every thread has taken its columns: bring the next row in their place
+        auto bring = [&]() {
+            if (tid < 4 && ring.ok && k + L.stages < count) {
+                ring.load(stage, GROUPS ? next.t : t + (WIN ? kClasses : 1) * L.ty * L.stages, tid, p.in[tid]);
+                if (GROUPS) advance(next);
+            }
+            if (++stage == L.stages) {
+                stage = 0;
+                phase++;
+            }
+        };
         Pair d0[H], y[H], rh[H];
 #pragma unroll
         for (int i = 0; i < H; i++) d0[i] = y[i] = rh[i] = zero;
@@ -525,21 +591,21 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
         const float pre = live && p.in[1].base ? p.pre_rstd[t] : 0.0f;
         // y -> yhat; x -> rhat; h = gz * pre_weight; d0 = gr + pre * h
         const Pair post2(post, post), pre2(pre, pre);
+        auto load = [&](int o, Pair (&v)[H]) {
+            const T* row = (const T*)p.in[o].base + t * p.in[o].stride;
+            if (!p.in[o].base) {
+#pragma unroll
+                for (int i = 0; i < H; i++) v[i] = zero;
+            } else if (RING) {
+                col.load(ring.slot(stage, o), ring.shift_of(row + col.first), v);
+            } else {
+                col.load(row, true, v);
+            }
+        };
         Pair s = zero;
         if (RING || live) {
             Pair gz[H];
             if (RING) ring.wait(stage, phase, k == 0, tid == 0);
-            auto load = [&](int o, Pair (&v)[H]) {
-                const T* row = (const T*)p.in[o].base + t * p.in[o].stride;
-                if (!p.in[o].base) {
-#pragma unroll
-                    for (int i = 0; i < H; i++) v[i] = zero;
-                } else if (RING) {
-                    col.load(ring.slot(stage, o), ring.shift_of(row + col.first), v);
-                } else {
-                    col.load(row, true, v);
-                }
-            };
             load(0, d0);
             load(1, gz);
             load(2, y);
@@ -557,25 +623,17 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
             }
         }
         const float m1 = -pre * (row_sum(both(s)) * inv_dim);
-        if (RING) {
-            if (tid < 4 && ring.ok && issued < count) {
-                ring.load(stage, next.t, tid, p.in[tid]);
-                issued++;
-                advance(next);
-            }
-            if (++stage == L.stages) {
-                stage = 0;
-                phase++;
-            }
-        }
+        if (RING && !REREAD) bring();
         // d = gr + pre (h - rhat mean(h rhat)), k = d * gate * post_weight
         s = zero;
         const Pair m12(m1, m1);
         if (RING || live) {
+            if (REREAD) load(2, y);
 #pragma unroll
             for (int i = 0; i < H; i++) {
                 Pair wg, pw;
                 weights(i, wg, pw);
+                if (REREAD) y[i] = y[i] * post2;
                 const Pair d = fma_pair(m12, rh[i], d0[i]);
                 a[i] = fma_pair(d, y[i], a[i]);
                 rh[i] = scale * d;
@@ -583,12 +641,13 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
                 s = fma_pair(d0[i], y[i], s);
             }
         }
-        col.store((T*)p.grad_x + t * p.grad_x_stride, live, rh);
+        col.put_all((T*)p.grad_x + t * p.grad_x_stride, live, rh, p.alike[0]);
         const float m2 = -row_sum(both(s)) * inv_dim;
+        if (REREAD) bring();
         const Pair m22(m2, m2);
 #pragma unroll
         for (int i = 0; i < H; i++) d0[i] = post2 * fma_pair(m22, y[i], d0[i]);
-        col.store((T*)p.grad_y + t * p.grad_y_stride, live, d0);
+        col.put_all((T*)p.grad_y + t * p.grad_y_stride, live, d0, p.alike[1]);
         if (GROUPS && now.in_gate + 1 == p.per_gate) {  // A of this gate row is complete
             Pair w[H];
             col.weight(p.gate, p.bf16_weights, live ? now.gate : 0, w);
@@ -600,8 +659,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
                 col.weight(p.post_weight, p.bf16_weights, 0, w);
 #pragma unroll
                 for (int i = 0; i < H; i++) w[i] = w[i] * a[i];
-                if (p.bf16_weights) Columns<Bf16, N, C, FULL>{tid, L.tx, col.first, p.dim}.store((Bf16*)p.grad_gate + now.gate * p.dim, true, w);
-                else Columns<float, N, C, FULL>{tid, L.tx, col.first, p.dim}.store((float*)p.grad_gate + now.gate * p.dim, true, w);
+                if (p.bf16_weights) col.put_all((Bf16*)p.grad_gate + now.gate * p.dim, true, w, false);
+                else col.put_all((float*)p.grad_gate + now.gate * p.dim, true, w, false);
             }
 #pragma unroll
             for (int i = 0; i < H; i++) a[i] = zero;
@@ -609,7 +668,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
         }
         advance(now);
     }
-    if (RING && tid == 0 && !ring.ok) ring.drain((int)issued);
+    if (RING && tid == 0 && !ring.ok) ring.drain((int)min(count, (unsigned)(ring.failed_at + L.stages)));
     __syncthreads();  // every row has left the ring, whose memory the sums reuse
     if (!GROUPS) {
         Pair gt[H];
@@ -619,9 +678,9 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
     }
     float* part = p.part + block * p.slots * p.pitch;
     float* joined = (float*)dyn;
-    store_part(col, ty, L.ty, joined, part, ga);
-    store_part(col, ty, L.ty, joined, part + p.pitch, pre_acc);
-    if (!GROUPS) store_part(col, ty, L.ty, joined, part + 2 * p.pitch, a);
+    store_part(col, tid, L.tx, ty, L.ty, joined, part, ga);
+    store_part(col, tid, L.tx, ty, L.ty, joined, part + p.pitch, pre_acc);
+    if (!GROUPS) store_part(col, tid, L.tx, ty, L.ty, joined, part + 2 * p.pitch, a);
 }
 
 // Sums of the partial rows: job 0: post weight, 1: pre weight, 2 + g: gate
@@ -673,13 +732,15 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_sum_kernel(const NormGrad
 // Launch shape for rows of `dim` columns of es bytes, `ops` operands loaded.
 constexpr int kStageBytes = 192 << 10;  // of an SM's blocks together
 // Rows of up to 32 times `in_warp` columns are one warp's.
-Layout2 row_layout(int64_t dim, int es, int ops, bool vec, int in_warp, int per_thread, int block_threads) {
+enum Access { ONE_BY_ONE, VECTORS, WINDOW };
+Layout2 row_layout(int64_t dim, int es, int ops, Access access, int in_warp, int per_thread, int block_threads) {
     Layout2 L = {};
-    const int64_t threads = (dim + per_thread - 1) / per_thread;
+    // a window begins up to a vector less one element before the row
+    const int64_t wide = dim + (access == WINDOW ? 16 / es - 1 : 0), threads = (wide + per_thread - 1) / per_thread;
     L.cs = 1;
-    if (dim <= 32 * in_warp) {
+    if (wide <= 32 * in_warp) {
         L.tx = 1;
-        while (L.tx * in_warp < dim) L.tx *= 2;
+        while (L.tx * in_warp < wide) L.tx *= 2;
         L.ty = 256 / L.tx;
         return L;
     }
@@ -689,7 +750,7 @@ Layout2 row_layout(int64_t dim, int es, int ops, bool vec, int in_warp, int per_
     L.tx = (int)(((threads + L.cs - 1) / L.cs + 31) / 32 * 32);
     L.ty = L.cs > 1 ? 1 : std::max(1, std::min(kMaxGroups, block_threads / L.tx));
     const int64_t cols = std::min<int64_t>(dim, (int64_t)L.tx * per_thread);
-    L.slot = (int)((cols * es + (vec ? 0 : 16) + 15) / 16 * 16);
+    L.slot = (int)((cols * es + (access == VECTORS ? 0 : 16) + 15) / 16 * 16);
     if (weights) L.weights = L.tx * kGradCols * 2 * (int)sizeof(float);
     const int64_t stage = (int64_t)L.slot * ops * L.ty;
     L.stages = (int)std::min<int64_t>(kStages, (kStageBytes / (kNormThreads / (L.tx * L.ty)) - L.weights) / stage);
@@ -701,6 +762,26 @@ template <class T>
 bool wide(const void* p, int64_t stride, int64_t dim) {
     return ((uintptr_t)p & 15) == 0 && (stride * (int64_t)sizeof(T) & 15) == 0 && (dim * (int64_t)sizeof(T) & 15) == 0;
 }
+// Places matrices' rows in 16-byte vectors: whether all lie alike.
+struct Alike {
+    bool any = false, alike = true;
+    uintptr_t phase = 0, pitch = 0;
+    template <class T>
+    void add(const T*, const void* p, int64_t stride) {
+        if (!p) return;
+        const uintptr_t a = (uintptr_t)p & 15, b = (uintptr_t)(stride * (int64_t)sizeof(T)) & 15;
+        if (any && (a != phase || b != pitch)) alike = false;
+        any = true;
+        phase = a;
+        pitch = b;
+    }
+    template <class T>
+    bool with(const T* t, const void* p, int64_t stride) const {
+        Alike both = *this;
+        both.add(t, p, stride);
+        return both.alike;
+    }
+};
 bool wide_weight(const void* w, bool bf16, int64_t dim) {
     return !w || (bf16 ? wide<Bf16>(w, dim, dim) : wide<float>(w, dim, dim));
 }
@@ -725,22 +806,38 @@ cudaError_t run_norm(NormParams& p, cudaStream_t stream, int sms) {
                      wide<T>(p.r, p.r_stride, p.dim) && (!p.z || wide<T>(p.z, p.z_stride, p.dim)) &&
                      wide_weight(p.post_weight, p.bf16_weights, p.dim) && wide_weight(p.gate, p.bf16_weights, p.dim) &&
                      wide_weight(p.pre_weight, p.bf16_weights, p.dim);
-    p.lay = row_layout(p.dim, sizeof(T), 2, vec, kCols, kCols, kNormThreads / 2);
+    Alike rows;
+    rows.add((const T*)nullptr, p.in[0].base, p.in[0].stride);
+    rows.add((const T*)nullptr, p.in[1].base, p.in[1].stride);
+    p.alike[0] = rows.with((const T*)nullptr, p.r, p.r_stride);
+    p.alike[1] = rows.with((const T*)nullptr, p.z, p.z_stride);
+    const Access access = vec ? VECTORS : rows.alike ? WINDOW : ONE_BY_ONE;
+    p.lay = row_layout(p.dim, sizeof(T), 2, access, kCols, kCols, kNormThreads / 2);
     const bool ring = p.lay.stages > 0;
     int64_t grid = (p.tokens + p.lay.ty - 1) / p.lay.ty;
-    if (ring) grid = std::min<int64_t>(grid, std::max(1, sms * (kNormThreads / (p.lay.tx * p.lay.ty)) / p.lay.cs));
+    if (ring) {
+        const int64_t resident = std::max(1, sms * (kNormThreads / (p.lay.tx * p.lay.ty)) / p.lay.cs);
+        // in a window, rows of a group are a multiple of 8 apart (or it has one):
+        // they have the same shift
+        if (grid > resident) grid = access != WINDOW ? resident : resident >= 8 ? resident / 8 * 8 : grid;
+    }
     const bool full = (int64_t)p.lay.tx * p.lay.cs * kCols == p.dim;
-    const void* fn = vec ? (ring ? (full ? (const void*)norm_kernel<T, E, true, true> : (const void*)norm_kernel<T, E, true, false>)
-                                 : (const void*)norm_kernel<T, E, false, false>)
-                         : (ring ? (const void*)norm_kernel<T, 1, true, false> : (const void*)norm_kernel<T, 1, false, false>);
+    const void* fn;
+    if (access == VECTORS)
+        fn = ring ? (full ? (const void*)norm_kernel<T, E, true, true, false> : (const void*)norm_kernel<T, E, true, false, false>)
+                  : (const void*)norm_kernel<T, E, false, false, false>;
+    else if (access == WINDOW)
+        fn = ring ? (const void*)norm_kernel<T, E, true, false, true> : (const void*)norm_kernel<T, E, false, false, true>;
+    else
+        fn = ring ? (const void*)norm_kernel<T, 1, true, false, false> : (const void*)norm_kernel<T, 1, false, false, false>;
     void* args[] = {&p};
     return launch_rows(fn, &p.lay, 2, grid, args, 0, stream);
 }
 
 template <class T, int N, bool RING, bool FULL>
 const void* pick_grad(bool by_group) {
-    return by_group ? (const void*)norm_grad_kernel<T, N, RING, true, FULL, kGradFewCols>
-                    : (const void*)norm_grad_kernel<T, N, RING, false, FULL, (RING && N > 1 ? kGradCols : kGradFewCols)>;
+    return by_group ? (const void*)norm_grad_kernel<T, N, RING, true, FULL, false, kGradFewCols>
+                    : (const void*)norm_grad_kernel<T, N, RING, false, FULL, false, (RING && N > 1 ? kGradCols : kGradFewCols)>;
 }
 
 template <class T>
@@ -750,14 +847,34 @@ cudaError_t run_norm_grad(NormGradParams& p, bool by_group, cudaStream_t stream)
                wide_weight(p.post_weight, p.bf16_weights, p.dim) && wide_weight(p.gate, p.bf16_weights, p.dim) &&
                wide_weight(p.pre_weight, p.bf16_weights, p.dim) && wide_weight(p.grad_gate, p.bf16_weights, p.dim);
     for (const Operand& o : p.in) vec = vec && (!o.base || wide<T>(o.base, o.stride, p.dim));
-    int cols = vec && !by_group ? kGradCols : kGradFewCols;
-    p.lay = row_layout(p.dim, sizeof(T), 4, vec, kGradFewCols, cols, cols == kGradCols ? kNormThreads / 2 : kNormThreads);
+    Alike rows;
+    for (const Operand& o : p.in) rows.add((const T*)nullptr, o.base, o.stride);
+    p.alike[0] = rows.with((const T*)nullptr, p.grad_x, p.grad_x_stride);
+    p.alike[1] = rows.with((const T*)nullptr, p.grad_y, p.grad_y_stride);
+    const bool window = !vec && rows.alike && !by_group && p.per_group >= kClasses;
+    if (window) {  // as many blocks for each class of tokens
+        const int64_t parts = p.per_group / kClasses;
+        p.unit = (unsigned)(((p.per_gate + kClasses - 1) / kClasses + parts - 1) / parts);
+        p.per_group = parts * kClasses;
+        p.blocks = p.gates * p.per_group;
+    }
+    const Access access = vec ? VECTORS : window ? WINDOW : ONE_BY_ONE;
+    // fp32 windows are faster with 8 (8192 x 3001: 125 us against 182), bf16 ones
+    // with 16 (16384 x 3001: 235 us against 281)
+    int cols = !by_group && (access == VECTORS || (access == WINDOW && sizeof(T) == 2)) ? kGradCols : kGradFewCols;
+    p.lay = row_layout(p.dim, sizeof(T), 4, access, kGradFewCols, cols, cols == kGradCols ? kNormThreads / 2 : kNormThreads);
     if (!p.lay.stages) cols = kGradFewCols;
     const bool ring = p.lay.stages > 0;
     const bool full = (int64_t)p.lay.tx * p.lay.cs * cols == p.dim;
-    const void* fn = vec ? (ring ? (full ? pick_grad<T, E, true, true>(by_group) : pick_grad<T, E, true, false>(by_group))
-                                 : pick_grad<T, E, false, false>(by_group))
-                         : (ring ? pick_grad<T, 1, true, false>(by_group) : pick_grad<T, 1, false, false>(by_group));
+    const void* fn;
+    if (access == VECTORS)
+        fn = ring ? (full ? pick_grad<T, E, true, true>(by_group) : pick_grad<T, E, true, false>(by_group))
+                  : pick_grad<T, E, false, false>(by_group);
+    else if (access == WINDOW)
+        fn = ring ? (const void*)norm_grad_kernel<T, E, true, false, false, true, (sizeof(T) == 2 ? kGradCols : kGradFewCols)>
+                  : (const void*)norm_grad_kernel<T, E, false, false, false, true, kGradFewCols>;
+    else
+        fn = ring ? pick_grad<T, 1, true, false>(by_group) : pick_grad<T, 1, false, false>(by_group);
     void* args[] = {&p};
     if (p.blocks > 0) {
         const size_t joined = p.lay.ty > 1 ? (size_t)p.lay.tx * p.lay.ty * cols * sizeof(float) : 0;
