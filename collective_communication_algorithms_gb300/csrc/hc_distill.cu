@@ -18,8 +18,19 @@
 // 16-byte vectors of memory, the vectors that also hold a neighbouring row's
 // elements (or lie past the matrix) are fetched element by element, the
 // foreign elements set to -inf.
-#include <algorithm>
-
+//
+// What bounds it: one pass over the logits and one over the gradient, 2.15 GB
+// for 4096 x 131072 bf16, 317 us at the copy bandwidth.  Measured: 363 us
+// (5.9 TB/s) with a tenth of the rows masked off, 384 us with none; the
+// instructions (13 an element: unpack, maximum, two exponentials, three sums
+// and products, pack) take half of the issue slots, and the chain of waits in
+// a cluster (copies, block sum, (m, l) of the others, stores) is covered by
+// the other five blocks of an SM.  That is why four vectors are taken at a
+// time (one comparison with the running maximum), pairs of binary32 go through
+// one instruction, and blocks are small (409 us with single vectors; 444 with
+// five blocks an SM; 384 with prefetches of later rows into L2, which cost 30 us
+// here).  One row a cluster measured faster than clusters that keep rows in
+// registers and work through many (570 us: one row under way is too few).
 #include "hc_ops.cuh"
 
 namespace hc {
@@ -50,7 +61,6 @@ struct DistillParams {
     unsigned long long wait_ns;
     int hold;
     bool in_place;    // the gradient replaces the logits
-    int64_t ahead;    // rows that the resident blocks hold
 };
 
 struct Shared {
@@ -111,9 +121,6 @@ __device__ __forceinline__ float largest(const uint4& u) {
         return fmaxf(bf_lo(m), bf_hi(m));
     }
     return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
-}
-__device__ __forceinline__ void bulk_prefetch_l2(uintptr_t p, unsigned bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 // Waits of the threads that go through the logits, and of the teacher's warp
 // for them.
@@ -333,16 +340,6 @@ __global__ void __launch_bounds__(kBlock, kResident) distill_kernel(const Distil
             mbar_arrive_expect_tx(&sh.full[lane], (unsigned)n * 16);
             bulk_g2s(buf + (a - lo), w.base + (uintptr_t)a * 16, (unsigned)n * 16, &sh.full[lane]);
         }
-        // the share of the row that takes this block's place comes into L2
-        // meanwhile: what shared memory holds is too little to keep the memory
-        // busy while blocks wait for each other
-        const int64_t then = t + p.ahead;
-        if (p.ahead && then < p.tokens && lane < kPieces && (!p.weight || p.weight[then] != 0.0f)) {
-            const Window<T> next((const T*)p.logits + then * p.logits_stride, p.vocab);
-            const int b = min((int)(rank + 1) * p.share, next.whole_hi());
-            const int a = max((int)rank * p.share, next.whole_lo()) + lane * p.piece, n = min(p.piece, b - a);
-            if (n > 0) bulk_prefetch_l2(next.base + (uintptr_t)a * 16, (unsigned)n * 16);
-        }
         __syncwarp();
         teacher_softmax(p, t, c, ids, prob, sh);
         __syncwarp();
@@ -485,7 +482,9 @@ __global__ void __launch_bounds__(kBlock, kResident) distill_kernel(const Distil
     stored_arrive();
 }
 
-// The gradient alone, from stats: blocks of `share` vectors, independent.
+// The gradient alone, from stats: blocks of `share` vectors, independent of
+// each other, four vectors a thread in flight; 4096 x 131072 bf16: 307 us, 7.0
+// TB/s.
 template <class T>
 __global__ void __launch_bounds__(kBlock, 2) distill_grad_kernel(const DistillParams p) {
     constexpr int E = kVecOf<T>;
@@ -588,7 +587,10 @@ cudaError_t launch_distill(const hc_distill_t& a, DistillMode mode, cudaStream_t
     void* args[] = {&p};
     const int entry_bytes = p.top * 12 + bucket_count(p.top) * 4;
     if (mode == DISTILL_GRAD) {
-        p.share = 4 * kThreads;
+        // shares of 32 KB once they fill the SMs several times over (4096 x 131072
+        // bf16: 307 us, 379 with 8 KB), of 8 KB for few rows (8 x 32768: 3.0 us, 3.4)
+        p.share = 16 * kThreads;
+        if (p.tokens * ((vecs + p.share - 1) / p.share) < 4 * sms) p.share = 4 * kThreads;
         p.cs = (vecs + p.share - 1) / p.share;
         const int64_t grid = p.tokens * p.cs;
         if (grid > INT32_MAX) return cudaErrorInvalidValue;
@@ -614,7 +616,6 @@ cudaError_t launch_distill(const hc_distill_t& a, DistillMode mode, cudaStream_t
     if (!allow_smem((void*)fn, smem)) return cudaErrorInvalidValue;
     const int64_t grid = p.tokens * p.cs;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    p.ahead = (int64_t)sms * std::max(1, std::min(kResident, (224 << 10) / smem)) / p.cs;
     return launch_op(fn, dim3((unsigned)grid), dim3(kBlock), args, (size_t)smem, stream, p.cs);
 }
 

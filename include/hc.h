@@ -2,7 +2,8 @@
  * hc.h -- C ABI of libhc: the data plane of HCCL-style AllReduce,
  * ReduceScatter and AllGather schedules (Ring, Recursive Halving-Doubling,
  * hierarchical Pipeline) for P virtual ranks whose buffers all live in the
- * memory of one GPU (sm_103a).
+ * memory of one GPU (sm_103a); and the training operators on either side of
+ * those collectives (see "Training operators" below).
  *
  * Sources (page title, section):
  *  - "深入分析HCCL集合通信库中Ring AllReduce和Recursive Halving-Doubling…"
@@ -337,8 +338,9 @@ hc_status_t hc_graph_destroy(hc_graph_t graph);
  *    aligned pointers and row pitches take the wide-access kernels.
  *  - Values are HC_FLOAT32 or HC_BFLOAT16 (HC_ERR_UNSUPPORTED otherwise).
  *    Arithmetic and sums are binary32, and every output is rounded once.
- *  - Sums over tokens run in an order fixed by the sizes, so a call repeated
- *    on the same inputs gives the same bits.
+ *  - Sums run in an order fixed by the sizes and by how the inputs lie in
+ *    memory, without floating-point atomics: a call repeated on the same inputs
+ *    gives the same bits.
  *  - An output may not overlap an input or another output, except exactly in
  *    place (same pointer and stride) where an entry point says so
  *    (HC_ERR_INVALID_ARG).  Rows of strided matrices may interleave.
@@ -413,7 +415,7 @@ size_t hc_embedding_grad_scratch_bytes(const hc_embedding_grad_t* args);
  *  z, pre_rstd : NULL: not computed (the last block's boundary).
  *  post_rstd   : NULL: not kept.  hc_block_norm_grad reads both.
  *  r, z        : either may be exactly x or y in place.
- *  dim         : 1 to 32768 (HC_ERR_UNSUPPORTED above).
+ *  dim         : 1 to 32768 (HC_ERR_UNSUPPORTED above); tokens at most 2^31 - 1.
  */
 typedef struct {
     size_t struct_size;
@@ -619,17 +621,18 @@ hc_status_t hc_select_algo(hc_coll_t coll, int P, int ranks_per_server, size_t c
 
 /*
  * Device-side status of the kernels that wait on shared-memory barriers (the
- * TMA-staged kernels: fused AllReduce / ReduceScatter, and the step kernel's
- * launches of wide reduces and broadcasts).  Each such wait gives up after
- * about 2 s; the kernel then records HC_ERR_TIMEOUT here and returns instead
- * of hanging.
+ * TMA-staged kernels: fused AllReduce / ReduceScatter, the step kernel's
+ * launches of wide reduces and broadcasts, the block norm and its gradient
+ * for rows of more than 256 columns, and the distillation loss).  Each such
+ * wait gives up after about 2 s; the kernel then records HC_ERR_TIMEOUT here
+ * and returns instead of hanging.
  * Returns HC_OK, HC_ERR_TIMEOUT, or HC_ERR_CUDA if the flag cannot be read.
  * Synchronises with the current device (it copies the flag to the host);
  * clear != 0 resets the flag.
  * A block whose wait gave up waits once more, also bounded, for the copies
- * into its own shared memory to land, and then exits without storing: the
- * outputs of the call that reported HC_ERR_TIMEOUT are undefined, and later
- * calls are unaffected.
+ * into its own shared memory to land, and then exits without storing (the
+ * block norm's kernels: after storing what they have): the outputs of the call
+ * that reported HC_ERR_TIMEOUT are undefined, and later calls are unaffected.
  */
 hc_status_t hc_device_status(int clear);
 

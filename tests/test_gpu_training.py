@@ -571,6 +571,33 @@ def test_distill_wait_expiry():
     assert torch.equal(o["grad"], ref["grad"]) and torch.equal(o["loss"], ref["loss"])
 
 
+def test_block_norm_wait_expiry():
+    """The same for the block norm and its gradient on rows of a ring."""
+    from collective_communication_algorithms_gb300 import _binding as B
+    for dim in (1000, 1001, 9000):
+        g = gen(dim)
+        y, x, post, gate, pre = norm_inputs(g, 3, dim, BF16, F32, 1)
+        dr, dz = normal(g, 3, dim, dtype=BF16), normal(g, 3, dim, dtype=BF16)
+        ref = hc.block_norm(y, x, post, gate, pre)
+        grads = hc.block_norm_grad(dr, dz, y, x, ref["post_rstd"], ref["pre_rstd"], post, gate, pre)
+        torch.cuda.synchronize()
+        for run in (lambda: hc.block_norm(y, x, post, gate, pre),
+                    lambda: hc.block_norm_grad(dr, dz, y, x, ref["post_rstd"], ref["pre_rstd"], post, gate, pre)):
+            assert B.hc_device_status() == 0
+            B.hc_test_expire_waits(True)
+            try:
+                run()
+                torch.cuda.synchronize()
+            finally:
+                B.hc_test_expire_waits(False)
+            assert B.hc_device_status(clear=True) == 6
+        o = hc.block_norm(y, x, post, gate, pre)
+        assert torch.equal(o["r"], ref["r"]) and torch.equal(o["z"], ref["z"])
+        o = hc.block_norm_grad(dr, dz, y, x, ref["post_rstd"], ref["pre_rstd"], post, gate, pre)
+        for name in grads:
+            assert torch.equal(o[name], grads[name]), name
+
+
 # ------------------------------------------------------------------ streams, graphs, binding
 def step_calls(stream=None):
     g = gen(77)
