@@ -42,20 +42,25 @@ constexpr int kLookupThreads = 256;
 // 8.5 us, 9.9 with one; no slower for a single token).
 constexpr int kLookupTokens = 4;
 
-// A block takes 2^tx_log2 threads x N columns of (256 >> tx_log2) * kLookupTokens
-// tokens.
+// Columns of a thread: one vector of 8 (or of the wider type's 4), or 8 single
+// ones, so that rows that are not aligned have as much on its way (19384 x 1694
+// fp32 to bf16: 28 us, 51 with one column a thread).
+constexpr int kLookupCols = 8;
+
+// A block takes (2^tx_log2 x kLookupCols) columns, in vectors of N a thread, 2^tx_log2
+// N apart, of (256 >> tx_log2) * kLookupTokens tokens.
 template <class TI, class TO, int N>
 __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const LookupParams p) {
-    constexpr int U = kLookupTokens;
+    constexpr int U = kLookupTokens, V = N == 1 ? kLookupCols : 1;
     const int tx = threadIdx.x & ((1 << p.tx_log2) - 1), ty = threadIdx.x >> p.tx_log2;
     const int ny = kLookupThreads >> p.tx_log2;
     const int64_t t0 = (int64_t)(blockIdx.x / p.col_blocks) * (ny * U) + ty;
-    const int c = ((blockIdx.x % p.col_blocks << p.tx_log2) + tx) * N;
+    const int c = (((int)(blockIdx.x % p.col_blocks) * V << p.tx_log2) + tx) * N, step = N << p.tx_log2;
     grid_wait();
     grid_release();
     if (c >= p.dim) return;
     uint64_t row[U];
-    float v[U][N];
+    float v[U][V][N];
 #pragma unroll
     for (int u = 0; u < U; u++) {
         const int64_t t = t0 + u * ny;
@@ -64,27 +69,34 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const LookupPara
     }
 #pragma unroll
     for (int u = 0; u < U; u++) {
-        load_whole<TI, N>((const TI*)p.table + (int64_t)row[u] * p.table_stride + c, row[u] < (uint64_t)p.rows, v[u]);
+        const TI* from = (const TI*)p.table + (int64_t)row[u] * p.table_stride + c;
+#pragma unroll
+        for (int k = 0; k < V; k++)
+            load_whole<TI, N>(from + k * step, row[u] < (uint64_t)p.rows && c + k * step < p.dim, v[u][k]);
     }
 #pragma unroll
     for (int u = 0; u < U; u++) {
         const int64_t t = t0 + u * ny;
         if (t >= p.tokens) break;
+        TO* to = (TO*)p.out + t * p.out_stride + c;
 #pragma unroll
-        for (int i = 0; i < N; i++) v[u][i] *= p.scale;
-        store_whole<TO, N>((TO*)p.out + t * p.out_stride + c, true, v[u]);
+        for (int k = 0; k < V; k++) {
+#pragma unroll
+            for (int i = 0; i < N; i++) v[u][k][i] *= p.scale;
+            store_whole<TO, N>(to + k * step, c + k * step < p.dim, v[u][k]);
+        }
     }
 }
 
 template <class TI, class TO>
 cudaError_t launch_lookup(LookupParams& p, bool vec, cudaStream_t stream) {
     constexpr int W = std::max(kVecOf<TI>, kVecOf<TO>);
-    const int nv = (int)((p.dim + (vec ? W : 1) - 1) / (vec ? W : 1));
+    const int per_thread = vec ? W : kLookupCols;
+    const int nv = (p.dim + per_thread - 1) / per_thread;
     p.tx_log2 = 5;
     while (p.tx_log2 < 8 && (1 << p.tx_log2) < nv) p.tx_log2++;
     p.col_blocks = (nv + (1 << p.tx_log2) - 1) >> p.tx_log2;
-    const int ny = kLookupThreads >> p.tx_log2;
-    const int64_t per = (int64_t)ny * kLookupTokens;
+    const int64_t per = (int64_t)(kLookupThreads >> p.tx_log2) * kLookupTokens;
     const int64_t grid = (p.tokens + per - 1) / per * p.col_blocks;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     const void* fn = vec ? (const void*)lookup_kernel<TI, TO, W> : (const void*)lookup_kernel<TI, TO, 1>;

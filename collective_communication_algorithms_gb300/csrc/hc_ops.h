@@ -33,6 +33,7 @@ struct BlockNormPlan {
     int64_t unit;        // tokens (by_group 0) or groups (1) of one block
     int64_t per_group;   // by_group 0: blocks of one group
     int by_group;
+    int direct;          // 1: one block, no partial sums
     int slots;           // partial sums kept by a block
     int64_t pitch;       // floats in one row of partial sums
     size_t bytes;

@@ -471,7 +471,7 @@ typedef struct {
 } hc_block_norm_grad_t;
 hc_status_t hc_block_norm_grad(const hc_block_norm_grad_t* args, hc_stream_t stream);
 /* Scratch bytes of hc_block_norm_grad (its pointers are not looked at); 0
- * for sizes that it refuses. */
+ * for sizes that it refuses, and for calls that need none. */
 size_t hc_block_norm_grad_scratch_bytes(const hc_block_norm_grad_t* args);
 
 /*

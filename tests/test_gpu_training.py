@@ -206,7 +206,8 @@ def rows_of(gate, tokens):
 
 NORM_SHAPES = [(1, 1, 1), (1, 4096, 1), (3, 7, 3), (5, 64, 0), (37, 257, 1), (64, 1000, 8), (33, 1001, 11),
                (1021, 96, 1021), (640, 40, 320), (12, 5128, 4), (4, 20008, 2), (3, 32768, 1), (1216, 136, 304), (5, 16400, 1),
-               (6, 8200, 2), (9, 300, 3), (1300, 515, 2), (330, 4097, 1), (400, 33, 1), (50, 8190, 1), (2500, 249, 5)]
+               (6, 8200, 2), (9, 300, 3), (1300, 515, 2), (330, 4097, 1), (400, 33, 1), (50, 8190, 1), (2500, 249, 5),
+               (24, 500, 1), (2, 4000, 2), (90, 63, 90), (6, 1001, 2)]
 
 
 def check_norm(tokens, dim, gates, dtype, wdtype, stride=None, offset=0, weights=True):

@@ -144,17 +144,21 @@ def test_optional_operands():
 
 @host_only
 def test_scratch():
-    for name in ("hc_embedding_grad", "hc_block_norm_grad"):
-        need = B.hc_operator_scratch_bytes(name, B.operator_args(name, **VALID[name]))
+    for name, tokens in (("hc_embedding_grad", 1000), ("hc_block_norm_grad", 1200)):
+        need = B.hc_operator_scratch_bytes(name, B.operator_args(name, **dict(VALID[name], tokens=tokens)))
         assert need > 0
-        assert status(name, scratch=0) == SCRATCH
-        assert status(name, scratch_bytes=need - 1) == SCRATCH
-        assert status(name, scratch_bytes=need) == CUDA
-        assert status(name, scratch=at(14) + 8) == ALIGN
-        assert status(name, scratch=at(0)) == INVALID         # over an input
+        assert status(name, tokens=tokens, scratch=0) == SCRATCH
+        assert status(name, tokens=tokens, scratch_bytes=need - 1) == SCRATCH
+        assert status(name, tokens=tokens, scratch_bytes=need) == CUDA
+        assert status(name, tokens=tokens, scratch=at(14) + 8) == ALIGN
+        assert status(name, tokens=tokens, scratch=at(0)) == INVALID         # over an input
     few = dict(VALID["hc_embedding_grad"], tokens=200)
     assert B.hc_operator_scratch_bytes("hc_embedding_grad", B.operator_args("hc_embedding_grad", **few)) == 0
     assert status("hc_embedding_grad", tokens=200, scratch=0, scratch_bytes=0) == CUDA
+    # few tokens of the block norm: one block, no partial sums
+    few = dict(VALID["hc_block_norm_grad"], tokens=4)
+    assert B.hc_operator_scratch_bytes("hc_block_norm_grad", B.operator_args("hc_block_norm_grad", **few)) == 0
+    assert status("hc_block_norm_grad", tokens=4, scratch=0, scratch_bytes=0) == CUDA
     bad = B.operator_args("hc_embedding_grad", **dict(VALID["hc_embedding_grad"], rows=0))
     assert B.hc_operator_scratch_bytes("hc_embedding_grad", bad) == 0
 
