@@ -20,17 +20,18 @@
 // foreign elements set to -inf.
 //
 // What bounds it: one pass over the logits and one over the gradient, 2.15 GB
-// for 4096 x 131072 bf16, 317 us at the copy bandwidth.  Measured: 363 us
-// (5.9 TB/s) with a tenth of the rows masked off, 384 us with none; the
+// for 4096 x 131072 bf16, 317 us at the copy bandwidth.  Measured: 360 us
+// (6.0 TB/s) with a tenth of the rows masked off, 384 us with none; the
 // instructions (13 an element: unpack, maximum, two exponentials, three sums
 // and products, pack) take half of the issue slots, and the chain of waits in
 // a cluster (copies, block sum, (m, l) of the others, stores) is covered by
 // the other five blocks of an SM.  That is why four vectors are taken at a
-// time (one comparison with the running maximum), pairs of binary32 go through
-// one instruction, and blocks are small (409 us with single vectors; 444 with
-// five blocks an SM; 384 with prefetches of later rows into L2, which cost 30 us
-// here).  One row a cluster measured faster than clusters that keep rows in
-// registers and work through many (570 us: one row under way is too few).
+// time (one comparison with the running maximum; 409 us with single vectors),
+// pairs of binary32 go through one instruction, and blocks are small.  With no
+// row masked, where six blocks an SM take 384 us, five take 444, and six with
+// prefetches of later rows into L2 take 414.  One row a cluster measured faster
+// than clusters that keep rows in registers and work through many (570 us
+// against 428 at the time: one row under way is too few).
 #include "hc_ops.cuh"
 
 namespace hc {
