@@ -982,8 +982,7 @@ BlockNormPlan block_norm_plan(int64_t tokens, int64_t dim, int64_t gate_rows, bo
     return q;
 }
 
-cudaError_t launch_block_norm_grad(const hc_block_norm_grad_t& a, cudaStream_t stream, int sms) {
-    (void)sms;
+cudaError_t launch_block_norm_grad(const hc_block_norm_grad_t& a, cudaStream_t stream) {
     const BlockNormPlan q = block_norm_plan((int64_t)a.tokens, (int64_t)a.dim, (int64_t)a.gate_rows, a.gate != nullptr);
     NormGradParams p = {};
     p.in[0] = {a.grad_r, (int64_t)a.grad_r_stride};

@@ -800,8 +800,7 @@ bool aligned16(const void* p, int64_t stride, int dim, int es) {
 
 }  // namespace
 
-cudaError_t launch_embedding(const hc_embedding_t& a, cudaStream_t stream, int sms) {
-    (void)sms;
+cudaError_t launch_embedding(const hc_embedding_t& a, cudaStream_t stream) {
     LookupParams p = {};
     p.table = a.table;
     p.ids = a.ids;

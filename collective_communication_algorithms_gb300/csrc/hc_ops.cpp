@@ -131,7 +131,7 @@ hc_status_t hc_embedding(const hc_embedding_t* args, hc_stream_t stream) {
     HC_TRY(check_overlaps(u, 3));
     if (!a.tokens) return HC_OK;
     const TraceRange range("hc_embedding", 0, (uint64_t)a.tokens);
-    return launch([&](int sms) { return launch_embedding(a, (cudaStream_t)stream, sms); });
+    return launch([&](int) { return launch_embedding(a, (cudaStream_t)stream); });
 }
 
 size_t hc_embedding_grad_scratch_bytes(const hc_embedding_grad_t* a) {
@@ -236,7 +236,7 @@ hc_status_t hc_block_norm_grad(const hc_block_norm_grad_t* args, hc_stream_t str
     u[9].in_place = u[10].in_place = true;
     HC_TRY(check_overlaps(u, 15));
     const TraceRange range("hc_block_norm_grad", 0, (uint64_t)a.tokens);
-    return launch([&](int sms) { return launch_block_norm_grad(a, (cudaStream_t)stream, sms); });
+    return launch([&](int) { return launch_block_norm_grad(a, (cudaStream_t)stream); });
 }
 
 static hc_status_t distill(const hc_distill_t* args, bool grad_only, hc_stream_t stream) {

@@ -6,7 +6,7 @@
 
 namespace hc {
 
-cudaError_t launch_embedding(const hc_embedding_t& a, cudaStream_t stream, int sms);
+cudaError_t launch_embedding(const hc_embedding_t& a, cudaStream_t stream);
 
 // Tokens up to which the gradient of the lookup needs no sort (and no
 // scratch), and the layout of its scratch above that.
@@ -39,7 +39,7 @@ struct BlockNormPlan {
     size_t bytes;
 };
 BlockNormPlan block_norm_plan(int64_t tokens, int64_t dim, int64_t gate_rows, bool gate);
-cudaError_t launch_block_norm_grad(const hc_block_norm_grad_t& a, cudaStream_t stream, int sms);
+cudaError_t launch_block_norm_grad(const hc_block_norm_grad_t& a, cudaStream_t stream);
 
 constexpr size_t kDistillMaxTop = 1024;
 constexpr size_t kDistillMaxVocab = 1u << 20;
