@@ -10,6 +10,8 @@ bound (or `stream`).  Outputs and scratch that are not passed are allocated by
 bind_*.  Matrices need unit column stride; rows may be strided.  Nothing here
 computes: the work happens in libhc's kernels.
 """
+import functools
+
 from . import _binding as B
 
 __all__ = ["embedding", "embedding_grad", "block_norm", "block_norm_grad", "distill", "distill_grad",
@@ -78,15 +80,51 @@ def _scratch(name, args, scratch, like):
 def _bind(name, args, stream, outputs, keep, like):
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream(like.device).cuda_stream
-    else:
-        stream = int(getattr(stream, "cuda_stream", stream))
-    call = B.bind_operator(name, args, keep, stream)
+        stream = torch.cuda.current_stream(like.device)
+    call = B.bind_operator(name, args, keep, stream.cuda_stream)
     call.outputs = outputs
     return call
 
 
-def bind_embedding(table, ids, out=None, scale=1.0, first_id=0, out_dtype=None, stream=None):
+def _tensors(kept):
+    for k in kept:
+        if isinstance(k, (tuple, list)):
+            yield from _tensors(k)
+        elif isinstance(k, dict):
+            yield from _tensors(k.values())
+        elif hasattr(k, "record_stream"):
+            yield k
+
+
+def _on_stream(bind):
+    """bind_* for a `stream` (a torch stream, or its handle) other than the
+    current one.  torch hands freed memory out again in the order of the stream
+    that it was allocated on, and the kernels run on another: what the call
+    allocates is therefore allocated on the call's stream, and every tensor is
+    recorded on the stream that it is a stranger to, so that none is handed out
+    while a kernel of the call may still use it."""
+    @functools.wraps(bind)
+    def run(*args, stream=None, **kw):
+        if stream is None:
+            return bind(*args, **kw)
+        import torch
+        current = torch.cuda.current_stream()
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+        if stream.cuda_stream == current.cuda_stream:
+            return bind(*args, **kw)
+        with torch.cuda.stream(stream):
+            call = bind(*args, stream=stream, **kw)
+        for t in _tensors(call.keep):
+            t.record_stream(stream)
+        for t in _tensors([call.outputs]):
+            t.record_stream(current)
+        return call
+    return run
+
+
+@_on_stream
+def bind_embedding(table, ids, out=None, scale=1.0, first_id=0, out_dtype=None, *, stream=None):
     """out[t] = scale * table[ids[t] - first_id], zero rows for ids elsewhere;
     `ids` of any shape, `out` (ids.numel(), dim) in out_dtype (the table's)."""
     import torch
@@ -105,8 +143,9 @@ def bind_embedding(table, ids, out=None, scale=1.0, first_id=0, out_dtype=None, 
     return _bind("hc_embedding", args, stream, {"out": out}, (table, ids, out), table)
 
 
+@_on_stream
 def bind_embedding_grad(grad_out, ids, grad_table, scale=1.0, first_id=0, padding_id=-1, accumulate=False,
-                        scratch=None, stream=None):
+                        scratch=None, *, stream=None):
     """grad_table[v] (+)= scale * sum of grad_out[t] over ids[t] == first_id + v
     (ids equal to padding_id left out)."""
     rows, dim = grad_table.shape
@@ -142,8 +181,9 @@ def _norm_weights(y, post_weight, gate, pre_weight):
     return gate_rows, _dtype(given[0]) if given else "float32"
 
 
+@_on_stream
 def bind_block_norm(y, x, post_weight=None, gate=None, pre_weight=None, r=None, z=None, post_rstd=None,
-                    pre_rstd=None, residual_scale=1.0, eps=1e-6, next_norm=True, stream=None):
+                    pre_rstd=None, residual_scale=1.0, eps=1e-6, next_norm=True, *, stream=None):
     """r = residual_scale * x + gate * rmsnorm(y) * post_weight and
     z = rmsnorm(r) * pre_weight, with the reciprocal root mean squares kept for
     the gradient.  r may be x or y, z too, in place; next_norm=False: r alone."""
@@ -176,9 +216,10 @@ def bind_block_norm(y, x, post_weight=None, gate=None, pre_weight=None, r=None, 
     return _bind("hc_block_norm", args, stream, outputs, (y, x, post_weight, gate, pre_weight, outputs), y)
 
 
+@_on_stream
 def bind_block_norm_grad(grad_r, grad_z, y, x, post_rstd, pre_rstd, post_weight=None, gate=None, pre_weight=None,
                          grad_y=None, grad_x=None, grad_post_weight=None, grad_gate=None, grad_pre_weight=None,
-                         residual_scale=1.0, scratch=None, stream=None):
+                         residual_scale=1.0, scratch=None, *, stream=None):
     """Gradients of y, x and of every weight that is given, from those of r
     and z (None: zeros, not both) and what block_norm kept."""
     import torch
@@ -253,8 +294,9 @@ def _distill_args(name, logits, teacher_logits, teacher_ids, row_weight, loss, s
                            temperature=temperature, scale=scale)
 
 
+@_on_stream
 def bind_distill(logits, teacher_logits, teacher_ids, row_weight=None, loss=None, stats=None, grad=True,
-                 temperature=1.0, scale=1.0, stream=None):
+                 temperature=1.0, scale=1.0, *, stream=None):
     """Per-row distillation loss, and with it the gradient of its sum over the
     logits: grad=True (a new tensor), a tensor (`logits` itself: in place), or
     False (the loss and stats alone, for distill_grad later)."""
@@ -275,8 +317,9 @@ def bind_distill(logits, teacher_logits, teacher_ids, row_weight=None, loss=None
                  logits)
 
 
+@_on_stream
 def bind_distill_grad(logits, teacher_logits, teacher_ids, stats, row_weight=None, grad=None, temperature=1.0,
-                      scale=1.0, stream=None):
+                      scale=1.0, *, stream=None):
     """The gradient alone, from the stats that distill kept; row_weight is
     then the gradient of the rows' losses."""
     grad = _new(logits, tuple(logits.shape), logits.dtype) if grad is None else grad

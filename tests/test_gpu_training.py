@@ -646,6 +646,39 @@ def test_bound_calls_repeat_on_a_side_stream_and_in_a_graph():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_memory_of_a_call_on_another_stream_is_not_handed_out_early(handle):
+    """A call on a busy side stream, its inputs dropped at once: what the
+    allocator hands out meanwhile is neither the call's inputs nor its scratch."""
+    g = gen(5)
+    T, V, d = 4000, 300, 64
+    ids, dout = some_ids(g, T, V, "skewed"), normal(g, T, d)
+    want = hc.embedding_grad(dout, ids, torch.empty(V, d, device="cuda"))["grad_table"]
+    side = torch.cuda.Stream()
+
+    def call():
+        i2, d2 = ids.clone(), dout.clone()
+        torch.cuda.current_stream().synchronize()
+        return hc.embedding_grad(d2, i2, torch.empty(V, d, device="cuda"),
+                                 stream=side.cuda_stream if handle else side)["grad_table"]
+
+    def more():
+        return [torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+                for n in (T * 8, T * d * 4, T * 8 + 512, 1 << 16, 1 << 18, 1 << 20) for _ in range(8)]
+    call(), more()  # the kernels are loaded and the allocator has its memory
+    torch.cuda._sleep(1 << 10)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(1 << 27)
+    got = call()
+    other = more()
+    torch.cuda.current_stream().synchronize()
+    assert not side.query()  # the call has not run yet
+    side.synchronize()
+    assert torch.equal(got, want)
+    assert all(bool((t == 255).all()) for t in other)
+
+
 def test_offsets_past_32_bits():
     """Rows that begin more than 2^31 elements after the first."""
     free = torch.cuda.mem_get_info()[0]
