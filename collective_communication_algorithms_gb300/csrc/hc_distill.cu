@@ -268,15 +268,22 @@ __device__ __forceinline__ void entry_grads(const DistillParams& p, const Window
 }
 
 // Gradient of the other columns: 2^((x - m) c) * gl.  What is rounded to bf16
-// takes the exponent as x c - m c: m c is off by half a unit of binary32, the
-// result by about 1e-6 of itself, far below a bf16 rounding.
+// takes the exponent as x c - m c (ROUGH) where m c is small: it is off by half
+// a unit of binary32, at most 2^-17 there, the result by 5e-6 of itself, far
+// below a bf16 rounding.  Larger ones (a row of the type's lowest value would
+// overflow) and binary32 results take the difference first.
+constexpr float kRoughLimit = 256.0f;
 template <class T>
+__device__ __forceinline__ bool rough_exponents(float m, float c) {
+    return sizeof(T) == 2 && fabsf(m * c) < kRoughLimit;
+}
+template <class T, bool ROUGH>
 __device__ __forceinline__ uint4 column_grads(const uint4& u, Pair minus_m, Pair minus_mc, Pair c, Pair gl) {
     Pair v[kVecOf<T> / 2];
     pairs_of(u, v);
 #pragma unroll
     for (int j = 0; j < kVecOf<T> / 2; j++)
-        v[j] = exp2_pair(sizeof(T) == 2 ? fma_pair(v[j], c, minus_mc) : (v[j] + minus_m) * c) * gl;
+        v[j] = exp2_pair(ROUGH ? fma_pair(v[j], c, minus_mc) : (v[j] + minus_m) * c) * gl;
     return pack_pairs(v);
 }
 template <class T>
@@ -425,6 +432,7 @@ __global__ void __launch_bounds__(kBlock, kResident) distill_kernel(const Distil
             sh.rank_l[0] = l;
         }
     }
+    __syncwarp();
     if (p.cs > 1) {
         // only these two warps have something for others (a releasing arrival
         // waits for what its warp has under way)
@@ -472,12 +480,19 @@ __global__ void __launch_bounds__(kBlock, kResident) distill_kernel(const Distil
         return;
     }
     const Pair minus(-m, -m), minus_c(-m * c, -m * c), cc(c, c), gg(gl, gl);
+    if (rough_exponents<T>(m, c)) {
 #pragma unroll 4
-    for (int i = wlo + tid; i < whi; i += kThreads) store_vector<T>(w, grow, same, i, column_grads<T>(buf[i - lo], minus, minus_c, cc, gg));
+        for (int i = wlo + tid; i < whi; i += kThreads)
+            store_vector<T>(w, grow, same, i, column_grads<T, true>(buf[i - lo], minus, minus_c, cc, gg));
+    } else {
+#pragma unroll 4
+        for (int i = wlo + tid; i < whi; i += kThreads)
+            store_vector<T>(w, grow, same, i, column_grads<T, false>(buf[i - lo], minus, minus_c, cc, gg));
+    }
     const int edge = tid == 0 && lo < wlo ? lo : tid == 32 && whi < hi && !(hi - 1 == lo && lo < wlo) ? hi - 1 : -1;
     if (edge >= 0) {
         float v[E];
-        unpack(column_grads<T>(buf[edge - lo], minus, minus_c, cc, gg), v);
+        unpack(column_grads<T, false>(buf[edge - lo], minus, minus_c, cc, gg), v);
         store_grad<T>(w, grow, same, edge, v);
     }
     stored_arrive();
@@ -530,6 +545,7 @@ __global__ void __launch_bounds__(kBlock, 2) distill_grad_kernel(const DistillPa
     float ev[E];
     if (edge >= 0) edge_vector<T>(w, edge, ev);
     const Pair minus(-m, -m), minus_c(-m * c, -m * c), cc(c, c), gg(gl, gl);
+    const bool rough = rough_exponents<T>(m, c);
     constexpr int B = 4;  // vectors in flight
     for (int i0 = wlo; i0 < whi; i0 += B * kThreads) {
         uint4 v[B];
@@ -543,13 +559,15 @@ __global__ void __launch_bounds__(kBlock, 2) distill_grad_kernel(const DistillPa
 #pragma unroll
         for (int b = 0; b < B; b++) {
             const int i = i0 + tid + b * kThreads;
-            if (i < whi) store_vector<T>(w, grow, same, i, column_grads<T>(v[b], minus, minus_c, cc, gg));
+            if (i >= whi) continue;
+            v[b] = rough ? column_grads<T, true>(v[b], minus, minus_c, cc, gg) : column_grads<T, false>(v[b], minus, minus_c, cc, gg);
+            store_vector<T>(w, grow, same, i, v[b]);
         }
     }
     if (p.in_place && wlo >= whi) __syncthreads();
     if (edge >= 0) {
         float v[E];
-        unpack(column_grads<T>(pack(ev), minus, minus_c, cc, gg), v);
+        unpack(column_grads<T, false>(pack(ev), minus, minus_c, cc, gg), v);
         store_grad<T>(w, grow, same, edge, v);
     }
     stored_arrive();

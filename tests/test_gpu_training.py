@@ -533,6 +533,30 @@ def test_distill_wide_range():
     assert_close(o["loss"], ref["loss"], ref["loss_mag"], 200, "loss")
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("vocab", [40, 5003, 70000])
+@pytest.mark.parametrize("tau", [0.5, 1.0])
+def test_distill_large_logits(dtype, vocab, tau):
+    """Rows whose mask leaves nothing (every logit the type's lowest value, but
+    for -inf), and rows of large logits, whose exponents need the difference
+    from the row's largest before anything is rounded."""
+    g = gen(vocab)
+    x, t, ids = distill_inputs(g, 8, vocab, 6, dtype)
+    low = torch.finfo(dtype).min
+    x[0] = low
+    x[1] = -torch.inf
+    x[1, ids[1]] = low
+    x[2] += 3e4
+    x[3] = -1e6
+    x[4] = torch.where(torch.rand(vocab, generator=g, device="cuda") < 0.5, 2.0 ** 20, low).to(dtype)
+    x[4, ids[4]] = 2.0 ** 20
+    x[5] = -1e30
+    x[5, 7] = 1e30
+    ids[5] = 7
+    x[6] *= 40
+    check_distill(x, t, ids, tau=tau)
+
+
 def test_distill_grad_against_differences():
     g = gen(12)
     x, t, ids = distill_inputs(g, 4, 300, 10, F32)
