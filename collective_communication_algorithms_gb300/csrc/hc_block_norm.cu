@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p) 
 // gradient
 // ---------------------------------------------------------------------------
 struct NormGradParams {
-    Operand in[4];  // grad_r, grad_z, y, x
+    Operand in[5];  // grad_r, grad_z, y, x, and the gate where every token has its own
     const void *post_weight, *gate, *pre_weight;
     const float *post_rstd, *pre_rstd;
     void *grad_y, *grad_x, *grad_post_weight, *grad_gate, *grad_pre_weight;
@@ -411,7 +411,7 @@ struct NormGradParams {
     int64_t blocks, per_group, pitch, jobs;
     unsigned per_gate, unit;
     int dim, slots;
-    bool bf16_weights, alike[2];  // grad_x and grad_y lie in their vectors as the inputs do
+    bool bf16_weights, alike[3];  // grad_x, grad_y (grad_gate, if each token's) lie in their vectors as the inputs do
     bool direct;  // one block: no partial sums
     float residual_scale;
     Layout2 lay;
@@ -458,11 +458,15 @@ __device__ __forceinline__ void store_direct(const Columns<T, N, C, FULL, WIN>& 
 // tokens are dealt to the block's rows of threads; with a window, the run is
 // of every kClasses-th token, which all have the same shift.  true: the block
 // has `unit` whole gate rows, dealt to the rows of threads.
+// EACH: every token has a gate row, of the values' type: one more operand of
+// its row, brought ahead with the others, and grad_gate one more output; else
+// as without gates.
 constexpr int kClasses = 8;
-template <class T, int N, bool RING, bool GROUPS, bool FULL, bool WIN, int C>
+template <class T, int N, bool RING, bool GROUPS, bool FULL, bool WIN, int C, bool EACH = false>
 __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradParams p) {
     constexpr int H = C / 2;
     constexpr bool SHARED_WEIGHTS = C == kGradCols;
+    constexpr int OPS = EACH ? 5 : 4;
     // yhat between the sums: out of the stage again instead of 16 registers
     // that spill (144 us instead of 158 for 16384 x 4096 bf16; in a window, whose
     // reads take more, 240 us instead of 213 for 16384 x 3001)
@@ -499,7 +503,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
     }
     const int shift = WIN ? (int)((uintptr_t)((const T*)p.in[2].base + base * p.in[2].stride) & 15) / (int)sizeof(T) : 0;
     const Columns<T, N, C, FULL, WIN> col(tid, L.tx, rank * L.tx * C, p.dim, shift);
-    Ring<T, 4, (N > 1 && !WIN)> ring{dyn + (size_t)ty * L.stages * 4 * L.slot, full[ty], L, p.tokens, col.first,
+    Ring<T, OPS, (N > 1 && !WIN)> ring{dyn + (size_t)ty * L.stages * OPS * L.slot, full[ty], L, p.tokens, col.first,
                              min(L.tx * C, p.dim - col.first)};
     // the tokens in order: the one to do, and (lanes that bring rows) the next
     // one to bring
@@ -530,7 +534,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
     grid_wait();
     grid_release();
     Walk next = now;
-    if (RING && tid < 4)
+    if (RING && tid < OPS)
         for (unsigned i = 0; i < (unsigned)L.stages && i < count; i++) {
             ring.load((int)i, next.t, tid, p.in[tid]);
             advance(next);
@@ -540,17 +544,17 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
     Pair a[H], ga[H], pre_acc[H];
 #pragma unroll
     for (int i = 0; i < H; i++) a[i] = ga[i] = pre_acc[i] = zero;
-    // post_weight * gate and pre_weight: in registers, or a pair of columns
+    // post_weight * gate (EACH: post_weight) and pre_weight: in registers, or a pair of columns
     // each in shared memory (one copy a block: its tokens share the gate)
     Pair wg_[SHARED_WEIGHTS ? 1 : H], pw_[SHARED_WEIGHTS ? 1 : H];
-    float4* const shared_weights = (float4*)(dyn + (size_t)L.ty * L.stages * 4 * L.slot) + tid;
+    float4* const shared_weights = (float4*)(dyn + (size_t)L.ty * L.stages * OPS * L.slot) + tid;
     auto load_gate = [&](int64_t g) {
         Pair wg[H], gt[H];
         col.weight(p.post_weight, p.bf16_weights, 0, wg);
-        col.weight(p.gate, p.bf16_weights, g, gt);
+        if (!EACH) col.weight(p.gate, p.bf16_weights, g, gt);
 #pragma unroll
         for (int i = 0; i < H; i++) {
-            wg[i] = wg[i] * gt[i];
+            if (!EACH) wg[i] = wg[i] * gt[i];
             if constexpr (!SHARED_WEIGHTS) wg_[i] = wg[i];
         }
         if constexpr (SHARED_WEIGHTS) {
@@ -589,7 +593,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
         const int64_t t = now.t;
         // every thread has taken its columns: bring the next row in their place
         auto bring = [&]() {
-            if (tid < 4 && ring.ok && k + L.stages < count) {
+            if (tid < OPS && ring.ok && k + L.stages < count) {
                 ring.load(stage, GROUPS ? next.t : t + (WIN ? kClasses : 1) * L.ty * L.stages, tid, p.in[tid]);
                 if (GROUPS) advance(next);
             }
@@ -598,7 +602,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
                 phase++;
             }
         };
-        Pair d0[H], y[H], rh[H];
+        Pair d0[H], y[H], rh[H], gt[H];  // gt: EACH, the gate, then its gradient
 #pragma unroll
         for (int i = 0; i < H; i++) d0[i] = y[i] = rh[i] = zero;
         const float post = live ? p.post_rstd[t] : 0.0f;
@@ -624,10 +628,12 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
             load(1, gz);
             load(2, y);
             load(3, rh);
+            if constexpr (EACH) load(4, gt);
 #pragma unroll
             for (int i = 0; i < H; i++) {
                 Pair wg, pw;
                 weights(i, wg, pw);
+                if (EACH) wg = wg * gt[i];
                 y[i] = y[i] * post2;
                 rh[i] = fma_pair(wg, y[i], scale * rh[i]) * pre2;
                 pre_acc[i] = fma_pair(gz[i], rh[i], pre_acc[i]);
@@ -643,19 +649,28 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
         const Pair m12(m1, m1);
         if (RING || live) {
             if (REREAD) load(2, y);
+            if constexpr (EACH && REREAD) load(4, gt);
 #pragma unroll
             for (int i = 0; i < H; i++) {
                 Pair wg, pw;
                 weights(i, wg, pw);
                 if (REREAD) y[i] = y[i] * post2;
                 const Pair d = fma_pair(m12, rh[i], d0[i]);
-                a[i] = fma_pair(d, y[i], a[i]);
+                if (EACH) {
+                    const Pair dy = d * y[i], g = gt[i];
+                    ga[i] = fma_pair(g, dy, ga[i]);
+                    gt[i] = wg * dy;
+                    wg = wg * g;
+                } else {
+                    a[i] = fma_pair(d, y[i], a[i]);
+                }
                 rh[i] = scale * d;
                 d0[i] = d * wg;
                 s = fma_pair(d0[i], y[i], s);
             }
         }
         col.put_all((T*)p.grad_x + t * p.grad_x_stride, live, rh, p.alike[0]);
+        if (EACH && p.grad_gate) col.put_all((T*)p.grad_gate + t * p.dim, live, gt, p.alike[2]);
         const float m2 = -row_sum(both(s)) * inv_dim;
         if (REREAD) bring();
         const Pair m22(m2, m2);
@@ -684,14 +699,14 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
     }
     if (RING && tid == 0 && !ring.ok) ring.drain((int)min(count, (unsigned)(ring.failed_at + L.stages)));
     __syncthreads();  // every row has left the ring, whose memory the sums reuse
-    if (!GROUPS) {
+    if (!GROUPS && !EACH) {
         Pair gt[H];
         col.weight(p.gate, p.bf16_weights, gate_row, gt);
 #pragma unroll
         for (int i = 0; i < H; i++) ga[i] = gt[i] * a[i];
     }
     float* joined = (float*)dyn;
-    if (!WIN && p.direct) {  // the only block: these are the sums
+    if (!WIN && !EACH && p.direct) {  // the only block: these are the sums
         store_direct(col, tid, L.tx, ty, L.ty, joined, p.grad_post_weight, p.bf16_weights, ga);
         store_direct(col, tid, L.tx, ty, L.ty, joined, p.grad_pre_weight, p.bf16_weights, pre_acc);
         if (!GROUPS) {
@@ -707,7 +722,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
     float* part = p.part + block * p.slots * p.pitch;
     store_part(col, tid, L.tx, ty, L.ty, joined, part, ga);
     store_part(col, tid, L.tx, ty, L.ty, joined, part + p.pitch, pre_acc);
-    if (!GROUPS) store_part(col, tid, L.tx, ty, L.ty, joined, part + 2 * p.pitch, a);
+    if (!GROUPS && !EACH) store_part(col, tid, L.tx, ty, L.ty, joined, part + 2 * p.pitch, a);
 }
 
 // Sums of the partial rows: job 0: post weight, 1: pre weight, 2 + g: gate
@@ -764,7 +779,7 @@ Layout2 row_layout(int64_t dim, int es, int ops, Access access, int in_warp, int
         return L;
     }
     // four fp32 rows of 8192 columns leave no room for a second stage
-    const bool weights = per_thread == kGradCols && ops == 4;
+    const bool weights = per_thread == kGradCols && ops >= 4;
     while (threads > (int64_t)(weights && es == 4 ? kNormThreads / 2 : kNormThreads) * L.cs) L.cs *= 2;
     L.tx = (int)(((threads + L.cs - 1) / L.cs + 31) / 32 * 32);
     L.ty = L.cs > 1 ? 1 : std::max(1, std::min(kMaxGroups, block_threads / L.tx));
@@ -859,8 +874,13 @@ const void* pick_grad(bool by_group) {
                     : (const void*)norm_grad_kernel<T, N, RING, false, FULL, false, (RING && N > 1 ? kGradCols : kGradFewCols)>;
 }
 
+// Threads of 16 bf16 columns whose stages of five operands fit twice beside
+// their weights: 2 * 5 * 32 + 128 bytes a thread.
+constexpr int kEachThreads = 416;
+static_assert(kEachThreads * (2 * 5 * kGradCols * 2 + kGradCols * 2 * 4) <= kStageBytes, "two stages");
+
 template <class T>
-cudaError_t run_norm_grad(NormGradParams& p, bool by_group, cudaStream_t stream) {
+cudaError_t run_norm_grad(NormGradParams& p, bool by_group, bool each, cudaStream_t stream) {
     constexpr int E = kVecOf<T>;
     bool vec = wide<T>(p.grad_y, p.grad_y_stride, p.dim) && wide<T>(p.grad_x, p.grad_x_stride, p.dim) &&
                wide_weight(p.post_weight, p.bf16_weights, p.dim) && wide_weight(p.gate, p.bf16_weights, p.dim) &&
@@ -872,6 +892,7 @@ cudaError_t run_norm_grad(NormGradParams& p, bool by_group, cudaStream_t stream)
     for (const Operand& o : p.in) rows.add((const T*)nullptr, o.base, o.stride);
     p.alike[0] = rows.with((const T*)nullptr, p.grad_x, p.grad_x_stride);
     p.alike[1] = rows.with((const T*)nullptr, p.grad_y, p.grad_y_stride);
+    p.alike[2] = rows.with((const T*)nullptr, p.grad_gate, p.dim);
     const bool window = !vec && rows.alike && !by_group && p.per_group >= kClasses;
     if (window) {  // as many blocks for each class of tokens
         const int64_t parts = p.per_group / kClasses;
@@ -882,13 +903,25 @@ cudaError_t run_norm_grad(NormGradParams& p, bool by_group, cudaStream_t stream)
     const Access access = vec ? VECTORS : window ? WINDOW : ONE_BY_ONE;
     // fp32 windows are faster with 8 (8192 x 3001: 125 us against 182), bf16 ones
     // with 16 (16384 x 3001: 235 us against 281)
-    int cols = !by_group && (access == VECTORS || (access == WINDOW && sizeof(T) == 2)) ? kGradCols : kGradFewCols;
-    p.lay = row_layout(p.dim, sizeof(T), 4, access, kGradFewCols, cols, cols == kGradCols ? kNormThreads / 2 : kNormThreads);
+    // with each token's gate 8, which leave no spills (8192 x 4096 bf16: 117 us
+    // against 222; 4096 x 3001: 88 against 93), but for bf16 rows that 8 would
+    // split over a cluster of half-filled blocks and 16 leave room for two stages
+    // (3600 x 4512: 113 us against 160)
+    const bool one_block = each && access == VECTORS && sizeof(T) == 2 && p.dim > kNormThreads * kGradFewCols &&
+                           p.dim <= kEachThreads * kGradCols;
+    int cols = one_block || (!by_group && !each && (access == VECTORS || (access == WINDOW && sizeof(T) == 2))) ? kGradCols : kGradFewCols;
+    const int ops = each ? 5 : 4;
+    p.lay = row_layout(p.dim, sizeof(T), ops, access, kGradFewCols, cols, cols == kGradCols ? kNormThreads / 2 : kNormThreads);
     if (!p.lay.stages) cols = kGradFewCols;
     const bool ring = p.lay.stages > 0;
     const bool full = (int64_t)p.lay.tx * p.lay.cs * cols == p.dim;
     const void* fn;
-    if (access == VECTORS)
+    if (each)  // rows of more than kWarpDim columns: always a ring
+        fn = one_block ? (const void*)norm_grad_kernel<Bf16, kVecOf<Bf16>, true, false, false, false, kGradCols, true>
+             : access == VECTORS ? (const void*)norm_grad_kernel<T, E, true, false, false, false, kGradFewCols, true>
+             : access == WINDOW ? (const void*)norm_grad_kernel<T, E, true, false, false, true, kGradFewCols, true>
+                                : (const void*)norm_grad_kernel<T, 1, true, false, false, false, kGradFewCols, true>;
+    else if (access == VECTORS)
         fn = ring ? (full ? pick_grad<T, E, true, true>(by_group) : pick_grad<T, E, true, false>(by_group))
                   : pick_grad<T, E, false, false>(by_group);
     else if (access == WINDOW)
@@ -899,11 +932,11 @@ cudaError_t run_norm_grad(NormGradParams& p, bool by_group, cudaStream_t stream)
     void* args[] = {&p};
     if (p.blocks > 0) {
         const size_t joined = p.lay.ty > 1 ? (size_t)p.lay.tx * p.lay.ty * cols * sizeof(float) : 0;
-        const cudaError_t e = launch_rows(fn, &p.lay, 4, p.blocks, args, joined, stream);
+        const cudaError_t e = launch_rows(fn, &p.lay, ops, p.blocks, args, joined, stream);
         if (e != cudaSuccess) return e;
     }
     // gate rows by_group blocks have not written; without tokens all are zeros
-    p.jobs = 2 + (p.grad_gate && (!by_group || p.blocks == 0) ? p.gates : 0);
+    p.jobs = 2 + (p.grad_gate && !each && (!by_group || p.blocks == 0) ? p.gates : 0);
     if (p.direct || (!p.grad_post_weight && !p.grad_pre_weight && p.jobs == 2)) return cudaSuccess;
     return launch_op((const void*)norm_sum_kernel,
                      dim3((unsigned)((p.dim + 31) / 32), (unsigned)(p.jobs < 65535 ? p.jobs : 65535)),
@@ -950,10 +983,9 @@ int64_t few_rows(int64_t dim) {
 }
 }  // namespace
 
-BlockNormPlan block_norm_plan(int64_t tokens, int64_t dim, int64_t gate_rows, bool gate) {
+BlockNormPlan block_norm_plan(int64_t tokens, int64_t dim, int64_t gate_rows, bool gate, bool same_types) {
     BlockNormPlan q = {};
-    const int64_t gates = gate ? gate_rows : 1;
-    const int64_t per_gate = tokens / gates;
+    int64_t gates = gate ? gate_rows : 1, per_gate = tokens / gates;
     q.pitch = (dim + 7) / 8 * 8;
     q.slots = 2;
     if (!tokens) {
@@ -967,12 +999,17 @@ BlockNormPlan block_norm_plan(int64_t tokens, int64_t dim, int64_t gate_rows, bo
         q.by_group = gates > 1;
         q.unit = gates > 1 ? gates : tokens;
         q.per_group = gates > 1 ? 0 : 1;
-    } else if (gates < kGradBlocks) {
+    } else if (gates < kGradBlocks || (per_gate == 1 && same_types && dim > kWarpDim)) {
+        // gate rows of every token's own and of the values' type: as one more
+        // operand (16384 x 1024 bf16: 66 us, 82 by gate rows; 4096 x 3001: 88,
+        // 143; 509 x 1001 fp32: 10.2, 12.5; 509 x 4096 bf16: 17, 20)
+        q.each = gates >= kGradBlocks;
+        if (q.each) gates = 1, per_gate = tokens;
         const int64_t want = ((dim <= kGradCols * kNormThreads / 2 ? 2 : 1) * kGradBlocks + gates - 1) / gates;
         q.unit = std::max<int64_t>((per_gate + want - 1) / want, std::min<int64_t>(per_gate, 4));
         q.per_group = (per_gate + q.unit - 1) / q.unit;
         q.blocks = gates * q.per_group;
-        q.slots = 3;
+        q.slots = q.each ? 2 : 3;
     } else {
         q.by_group = 1;
         q.unit = (gates + kGradBlocks - 1) / kGradBlocks;
@@ -983,7 +1020,8 @@ BlockNormPlan block_norm_plan(int64_t tokens, int64_t dim, int64_t gate_rows, bo
 }
 
 cudaError_t launch_block_norm_grad(const hc_block_norm_grad_t& a, cudaStream_t stream) {
-    const BlockNormPlan q = block_norm_plan((int64_t)a.tokens, (int64_t)a.dim, (int64_t)a.gate_rows, a.gate != nullptr);
+    const BlockNormPlan q = block_norm_plan((int64_t)a.tokens, (int64_t)a.dim, (int64_t)a.gate_rows, a.gate != nullptr,
+                                            a.dtype == a.weight_dtype);
     NormGradParams p = {};
     p.in[0] = {a.grad_r, (int64_t)a.grad_r_stride};
     p.in[1] = {a.grad_z, (int64_t)a.grad_z_stride};
@@ -1001,7 +1039,8 @@ cudaError_t launch_block_norm_grad(const hc_block_norm_grad_t& a, cudaStream_t s
     p.grad_pre_weight = a.grad_pre_weight;
     p.part = (float*)a.scratch;
     p.tokens = (int64_t)a.tokens;
-    p.gates = a.gate ? (int64_t)a.gate_rows : 1;
+    if (q.each) p.in[4] = {a.gate, (int64_t)a.dim};
+    p.gates = a.gate && !q.each ? (int64_t)a.gate_rows : 1;
     p.per_gate = (unsigned)(p.tokens / p.gates);
     p.grad_y_stride = (int64_t)a.grad_y_stride;
     p.grad_x_stride = (int64_t)a.grad_x_stride;
@@ -1014,7 +1053,7 @@ cudaError_t launch_block_norm_grad(const hc_block_norm_grad_t& a, cudaStream_t s
     p.dim = (int)a.dim;
     p.bf16_weights = a.weight_dtype == HC_BFLOAT16;
     p.residual_scale = a.residual_scale;
-    return a.dtype == HC_BFLOAT16 ? run_norm_grad<Bf16>(p, q.by_group, stream) : run_norm_grad<float>(p, q.by_group, stream);
+    return a.dtype == HC_BFLOAT16 ? run_norm_grad<Bf16>(p, q.by_group, q.each, stream) : run_norm_grad<float>(p, q.by_group, q.each, stream);
 }
 
 }  // namespace hc

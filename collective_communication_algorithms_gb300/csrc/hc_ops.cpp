@@ -196,8 +196,8 @@ size_t hc_block_norm_grad_scratch_bytes(const hc_block_norm_grad_t* a) {
     // rows, so one size serves calls with and without it
     const size_t rows = a->gate_rows ? a->gate_rows : 1;
     if (norm_sizes(a->tokens, a->dim, true, rows) != HC_OK) return 0;
-    const size_t with = block_norm_plan((int64_t)a->tokens, (int64_t)a->dim, (int64_t)rows, true).bytes;
-    const size_t without = block_norm_plan((int64_t)a->tokens, (int64_t)a->dim, 1, false).bytes;
+    const size_t with = block_norm_plan((int64_t)a->tokens, (int64_t)a->dim, (int64_t)rows, true, a->dtype == a->weight_dtype).bytes;
+    const size_t without = block_norm_plan((int64_t)a->tokens, (int64_t)a->dim, 1, false, false).bytes;
     return with > without ? with : without;
 }
 
@@ -228,7 +228,8 @@ hc_status_t hc_block_norm_grad(const hc_block_norm_grad_t* args, hc_stream_t str
     HC_TRY(vector(a.grad_gate, a.gate ? a.dim * a.gate_rows : 0, ws, &u[12].m));
     HC_TRY(vector(a.grad_pre_weight, a.dim, ws, &u[13].m));
     const size_t need =
-        block_norm_plan((int64_t)a.tokens, (int64_t)a.dim, (int64_t)a.gate_rows, a.gate != nullptr).bytes;
+        block_norm_plan((int64_t)a.tokens, (int64_t)a.dim, (int64_t)a.gate_rows, a.gate != nullptr,
+                        a.dtype == a.weight_dtype).bytes;
     HC_TRY(check_scratch(a.scratch, a.scratch_bytes, need));
     if (need) HC_TRY(vector(a.scratch, need, 1, &u[14].m));
     for (int i = 9; i < 15; i++) u[i].write = true;

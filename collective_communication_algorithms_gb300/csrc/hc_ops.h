@@ -33,12 +33,13 @@ struct BlockNormPlan {
     int64_t unit;        // tokens (by_group 0) or groups (1) of one block
     int64_t per_group;   // by_group 0: blocks of one group
     int by_group;
+    int each;            // 1: every token has a gate row, taken along with its other rows
     int direct;          // 1: one block, no partial sums
     int slots;           // partial sums kept by a block
     int64_t pitch;       // floats in one row of partial sums
     size_t bytes;
 };
-BlockNormPlan block_norm_plan(int64_t tokens, int64_t dim, int64_t gate_rows, bool gate);
+BlockNormPlan block_norm_plan(int64_t tokens, int64_t dim, int64_t gate_rows, bool gate, bool same_types);
 cudaError_t launch_block_norm_grad(const hc_block_norm_grad_t& a, cudaStream_t stream);
 
 constexpr size_t kDistillMaxTop = 1024;

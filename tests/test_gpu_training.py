@@ -338,6 +338,36 @@ def test_block_norm_grad_strided_and_partial(stride, offset):
         check_norm_grad(620, 100, 310, dtype, F32, gz=False)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("tokens,dim", [(152, 257), (509, 1001), (200, 1024), (331, 3001), (160, 4512), (153, 5000),
+                                        (152, 6656), (155, 6664), (154, 8192), (152, 20001), (170, 32768), (2500, 264)])
+def test_block_norm_grad_with_a_gate_for_every_token(tokens, dim, dtype):
+    check_norm_grad(tokens, dim, tokens, dtype, dtype)
+
+
+@pytest.mark.parametrize("stride,offset", [(304, 0), (301, 0), (312, 3)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_block_norm_grad_with_a_gate_for_every_token_strided_and_partial(dtype, stride, offset):
+    check_norm_grad(160, 300, 160, dtype, dtype, stride, offset)
+    check_norm_grad(160, 300, 160, dtype, dtype, stride, offset, weights=False)
+    check_norm_grad(161, 299, 161, dtype, dtype, gr=False)
+    check_norm_grad(161, 304, 161, dtype, dtype, gz=False)
+
+
+@pytest.mark.parametrize("dim", [301, 1024, 5000])
+def test_block_norm_grad_with_a_gate_for_every_token_in_place(dim):
+    g = gen(8)
+    y, x, post, gate, pre = norm_inputs(g, 200, dim, BF16, BF16, 200)
+    dr, dz = normal(g, 200, dim, dtype=BF16), normal(g, 200, dim, dtype=BF16)
+    f = hc.block_norm(y, x, post, gate, pre)
+    args = (f["post_rstd"], f["pre_rstd"], post, gate, pre)
+    ref = hc.block_norm_grad(dr, dz, y, x, *args)
+    y2, x2 = y.clone(), x.clone()
+    o = hc.block_norm_grad(dr, dz, y2, x2, *args, grad_x=y2, grad_y=x2)
+    for name in ref:
+        assert torch.equal(o[name], ref[name]), name
+
+
 @pytest.mark.parametrize("dim", [64, 5000])
 def test_block_norm_grad_in_place(dim):
     g = gen(8)
