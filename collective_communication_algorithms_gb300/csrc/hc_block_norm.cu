@@ -874,6 +874,9 @@ const void* pick_grad(bool by_group) {
                     : (const void*)norm_grad_kernel<T, N, RING, false, FULL, false, (RING && N > 1 ? kGradCols : kGradFewCols)>;
 }
 
+// Blocks (and partial sums) aimed at: two of 256 threads an SM, or one of 512.
+constexpr int64_t kGradBlocks = 152;
+
 // Threads of 16 bf16 columns whose stages of five operands fit twice beside
 // their weights: 2 * 5 * 32 + 128 bytes a thread.
 constexpr int kEachThreads = 416;
@@ -910,8 +913,10 @@ cudaError_t run_norm_grad(NormGradParams& p, bool by_group, bool each, cudaStrea
     const bool one_block = each && access == VECTORS && sizeof(T) == 2 && p.dim > kNormThreads * kGradFewCols &&
                            p.dim <= kEachThreads * kGradCols;
     int cols = one_block || (!by_group && !each && (access == VECTORS || (access == WINDOW && sizeof(T) == 2))) ? kGradCols : kGradFewCols;
+    // more blocks than SMs are halved (16384 x 1024 bf16, each token's gate: 59 us
+    // with 256 threads, 66 with 512; fewer keep a row a group: 509 x 1001 fp32)
     const int ops = each ? 5 : 4;
-    p.lay = row_layout(p.dim, sizeof(T), ops, access, kGradFewCols, cols, cols == kGradCols ? kNormThreads / 2 : kNormThreads);
+    p.lay = row_layout(p.dim, sizeof(T), ops, access, kGradFewCols, cols, cols == kGradCols || (each && p.blocks > kGradBlocks) ? kNormThreads / 2 : kNormThreads);
     if (!p.lay.stages) cols = kGradFewCols;
     const bool ring = p.lay.stages > 0;
     const bool full = (int64_t)p.lay.tx * p.lay.cs * cols == p.dim;
@@ -942,9 +947,6 @@ cudaError_t run_norm_grad(NormGradParams& p, bool by_group, bool each, cudaStrea
                      dim3((unsigned)((p.dim + 31) / 32), (unsigned)(p.jobs < 65535 ? p.jobs : 65535)),
                      dim3(kSumWarps * 32), args, 0, stream);
 }
-
-// Blocks (and partial sums) aimed at: two of 256 threads an SM, or one of 512.
-constexpr int64_t kGradBlocks = 152;
 
 }  // namespace
 
@@ -1001,7 +1003,7 @@ BlockNormPlan block_norm_plan(int64_t tokens, int64_t dim, int64_t gate_rows, bo
         q.per_group = gates > 1 ? 0 : 1;
     } else if (gates < kGradBlocks || (per_gate == 1 && same_types && dim > kWarpDim)) {
         // gate rows of every token's own and of the values' type: as one more
-        // operand (16384 x 1024 bf16: 66 us, 82 by gate rows; 4096 x 3001: 88,
+        // operand (16384 x 1024 bf16: 59 us, 82 by gate rows; 4096 x 3001: 88,
         // 143; 509 x 1001 fp32: 10.2, 12.5; 509 x 4096 bf16: 17, 20)
         q.each = gates >= kGradBlocks;
         if (q.each) gates = 1, per_gate = tokens;
