@@ -59,17 +59,6 @@ struct Operand {
     int64_t stride;
 };
 
-// Shape of a launch: tx threads (or lanes) have a row, ty rows a block.
-struct Layout2 {
-    int tx, ty, cs;     // cs: blocks of a cluster
-    int stages;         // 0: rows in a warp, loaded directly
-    int slot;           // bytes of one row (slice) of one operand in a stage
-    int weights;        // bytes of weights kept after the stages
-    int* err;
-    unsigned long long wait_ns;
-    int hold;           // wait-expiry test mode
-};
-
 // The ring of one group of threads: OPS operands a stage, operand o brought by
 // lane o of the group's first warp (so that a row's copies are set up side by
 // side).  ALIGNED: every row and slice starts and ends on 16 bytes.
@@ -77,7 +66,7 @@ template <class T, int OPS, bool ALIGNED>
 struct Ring {
     unsigned char* data;
     uint64_t* full;
-    const Layout2& lay;
+    const RowLayout& lay;
     int64_t tokens;
     int first, cols;  // this block's slice of the columns
     bool ok = true;
@@ -291,7 +280,7 @@ struct NormParams {
     int dim;
     bool bf16_weights, alike[2];  // r and z lie in their vectors as y and x do
     float residual_scale, eps;
-    Layout2 lay;
+    RowLayout lay;
 };
 
 // blockDim = (tx, ty) for a ring, (tx * ty) for rows in warps.
@@ -301,7 +290,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormParams p) 
     __shared__ uint64_t full[kMaxGroups][kStages];
     __shared__ __align__(16) float warp_sums[2][kMaxGroups * 4 + kRowWarps];
     __shared__ float rank_sums[2][kMaxCluster];
-    const Layout2& L = p.lay;
+    const RowLayout& L = p.lay;
     const int tid = RING ? threadIdx.x : threadIdx.x % L.tx;
     const int ty = RING ? threadIdx.y : threadIdx.x / L.tx;
     const int rank = RING ? blockIdx.x % L.cs : 0;
@@ -414,7 +403,7 @@ struct NormGradParams {
     bool bf16_weights, alike[3];  // grad_x, grad_y (grad_gate, if each token's) lie in their vectors as the inputs do
     bool direct;  // one block: no partial sums
     float residual_scale;
-    Layout2 lay;
+    RowLayout lay;
 };
 
 // Add the rows' sums of a block into row 0's, in row order.
@@ -475,7 +464,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradP
     __shared__ uint64_t full[kMaxGroups][kStages];
     __shared__ __align__(16) float warp_sums[2][kMaxGroups * 4 + kRowWarps];
     __shared__ float rank_sums[2][kMaxCluster];
-    const Layout2& L = p.lay;
+    const RowLayout& L = p.lay;
     const int tid = RING ? threadIdx.x : threadIdx.x % L.tx;
     const int ty = RING ? threadIdx.y : threadIdx.x / L.tx;
     const int rank = RING ? blockIdx.x % L.cs : 0;
@@ -766,11 +755,10 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_sum_kernel(const NormGrad
 constexpr int64_t kWarpDim = 256;
 constexpr int kStageBytes = 192 << 10;  // of an SM's blocks together
 // Rows of up to 256 columns are one warp's, in_warp columns a lane.
-enum Access { ONE_BY_ONE, VECTORS, WINDOW };
-Layout2 row_layout(int64_t dim, int es, int ops, Access access, int in_warp, int per_thread, int block_threads) {
-    Layout2 L = {};
+RowLayout row_layout(int64_t dim, int es, int ops, RowAccess access, int in_warp, int per_thread, int block_threads) {
+    RowLayout L = {};
     // a window begins up to a vector less one element before the row
-    const int64_t wide = dim + (access == WINDOW ? 16 / es - 1 : 0), threads = (wide + per_thread - 1) / per_thread;
+    const int64_t wide = dim + (access == ROWS_WINDOW ? 16 / es - 1 : 0), threads = (wide + per_thread - 1) / per_thread;
     L.cs = 1;
     if (wide <= kWarpDim) {
         L.tx = 1;
@@ -784,7 +772,7 @@ Layout2 row_layout(int64_t dim, int es, int ops, Access access, int in_warp, int
     L.tx = (int)(((threads + L.cs - 1) / L.cs + 31) / 32 * 32);
     L.ty = L.cs > 1 ? 1 : std::max(1, std::min(kMaxGroups, block_threads / L.tx));
     const int64_t cols = std::min<int64_t>(dim, (int64_t)L.tx * per_thread);
-    L.slot = (int)((cols * es + (access == VECTORS ? 0 : 16) + 15) / 16 * 16);
+    L.slot = (int)((cols * es + (access == ROWS_VECTORS ? 0 : 16) + 15) / 16 * 16);
     if (weights) L.weights = L.tx * kGradCols * 2 * (int)sizeof(float);
     const int64_t stage = (int64_t)L.slot * ops * L.ty;
     L.stages = (int)std::min<int64_t>(kStages, (kStageBytes / (kNormThreads / (L.tx * L.ty)) - L.weights) / stage);
@@ -821,9 +809,9 @@ bool wide_weight(const void* w, bool bf16, int64_t dim) {
 }
 
 // Fills the parts of the layout that depend on the device, and launches.
-cudaError_t launch_rows(const void* fn, Layout2* L, int ops, int64_t grid, void** args, size_t least_smem, cudaStream_t stream) {
+cudaError_t launch_rows(const void* fn, RowLayout* L, int ops, int64_t grid, void** args, size_t least_smem, cudaStream_t stream) {
     L->err = device_error_flag();
-    if (!L->err) return cudaErrorInvalidValue;
+    if (!L->err || L->cs > kMaxCluster) return cudaErrorInvalidValue;
     L->hold = expiring_waits() ? 1 : 0;
     L->wait_ns = L->hold ? kTestWaitLimitNs : kWaitLimitNs;
     if (grid * L->cs > INT32_MAX) return cudaErrorInvalidValue;
@@ -845,22 +833,23 @@ cudaError_t run_norm(NormParams& p, cudaStream_t stream, int sms) {
     rows.add((const T*)nullptr, p.in[1].base, p.in[1].stride);
     p.alike[0] = rows.with((const T*)nullptr, p.r, p.r_stride);
     p.alike[1] = rows.with((const T*)nullptr, p.z, p.z_stride);
-    const Access access = vec ? VECTORS : rows.alike ? WINDOW : ONE_BY_ONE;
-    p.lay = row_layout(p.dim, sizeof(T), 2, access, kCols, kCols, kNormThreads / 2);
+    const BlockNormRows shape = block_norm_rows(p.dim, sizeof(T), vec, rows.alike);
+    const RowAccess access = shape.access;
+    p.lay = shape.lay;
     const bool ring = p.lay.stages > 0;
     int64_t grid = (p.tokens + p.lay.ty - 1) / p.lay.ty;
     if (ring) {
         const int64_t resident = std::max(1, sms * (kNormThreads / (p.lay.tx * p.lay.ty)) / p.lay.cs);
         // in a window, rows of a group are a multiple of 8 apart (or it has one):
         // they have the same shift
-        if (grid > resident) grid = access != WINDOW ? resident : resident >= 8 ? resident / 8 * 8 : grid;
+        if (grid > resident) grid = access != ROWS_WINDOW ? resident : resident >= 8 ? resident / 8 * 8 : grid;
     }
     const bool full = (int64_t)p.lay.tx * p.lay.cs * kCols == p.dim;
     const void* fn;
-    if (access == VECTORS)
+    if (access == ROWS_VECTORS)
         fn = ring ? (full ? (const void*)norm_kernel<T, E, true, true, false> : (const void*)norm_kernel<T, E, true, false, false>)
                   : (const void*)norm_kernel<T, E, false, false, false>;
-    else if (access == WINDOW)
+    else if (access == ROWS_WINDOW)
         fn = ring ? (const void*)norm_kernel<T, E, true, false, true> : (const void*)norm_kernel<T, E, false, false, true>;
     else
         fn = ring ? (const void*)norm_kernel<T, 1, true, false, false> : (const void*)norm_kernel<T, 1, false, false, false>;
@@ -883,7 +872,7 @@ constexpr int kEachThreads = 416;
 static_assert(kEachThreads * (2 * 5 * kGradCols * 2 + kGradCols * 2 * 4) <= kStageBytes, "two stages");
 
 template <class T>
-cudaError_t run_norm_grad(NormGradParams& p, bool by_group, bool each, cudaStream_t stream) {
+cudaError_t run_norm_grad(NormGradParams& p, const BlockNormPlan& q, cudaStream_t stream) {
     constexpr int E = kVecOf<T>;
     bool vec = wide<T>(p.grad_y, p.grad_y_stride, p.dim) && wide<T>(p.grad_x, p.grad_x_stride, p.dim) &&
                wide_weight(p.post_weight, p.bf16_weights, p.dim) && wide_weight(p.gate, p.bf16_weights, p.dim) &&
@@ -896,40 +885,27 @@ cudaError_t run_norm_grad(NormGradParams& p, bool by_group, bool each, cudaStrea
     p.alike[0] = rows.with((const T*)nullptr, p.grad_x, p.grad_x_stride);
     p.alike[1] = rows.with((const T*)nullptr, p.grad_y, p.grad_y_stride);
     p.alike[2] = rows.with((const T*)nullptr, p.grad_gate, p.dim);
-    const bool window = !vec && rows.alike && !by_group && p.per_group >= kClasses;
-    if (window) {  // as many blocks for each class of tokens
-        const int64_t parts = p.per_group / kClasses;
-        p.unit = (unsigned)(((p.per_gate + kClasses - 1) / kClasses + parts - 1) / parts);
-        p.per_group = parts * kClasses;
-        p.blocks = p.gates * p.per_group;
-    }
-    const Access access = vec ? VECTORS : window ? WINDOW : ONE_BY_ONE;
-    // fp32 windows are faster with 8 (8192 x 3001: 125 us against 182), bf16 ones
-    // with 16 (16384 x 3001: 235 us against 281)
-    // with each token's gate 8, which leave no spills (8192 x 4096 bf16: 117 us
-    // against 222; 4096 x 3001: 88 against 93), but for bf16 rows that 8 would
-    // split over a cluster of half-filled blocks and 16 leave room for two stages
-    // (3600 x 4512: 113 us against 160)
-    const bool one_block = each && access == VECTORS && sizeof(T) == 2 && p.dim > kNormThreads * kGradFewCols &&
-                           p.dim <= kEachThreads * kGradCols;
-    int cols = one_block || (!by_group && !each && (access == VECTORS || (access == WINDOW && sizeof(T) == 2))) ? kGradCols : kGradFewCols;
-    // more blocks than SMs are halved (16384 x 1024 bf16, each token's gate: 59 us
-    // with 256 threads, 66 with 512; fewer keep a row a group: 509 x 1001 fp32)
-    const int ops = each ? 5 : 4;
-    p.lay = row_layout(p.dim, sizeof(T), ops, access, kGradFewCols, cols, cols == kGradCols || (each && p.blocks > kGradBlocks) ? kNormThreads / 2 : kNormThreads);
-    if (!p.lay.stages) cols = kGradFewCols;
+    BlockNormPlan plan = q;
+    const BlockNormRows shape = block_norm_grad_rows(&plan, p.tokens, p.dim, sizeof(T), vec, rows.alike);
+    p.unit = (unsigned)plan.unit;
+    p.per_group = plan.per_group;
+    p.blocks = plan.blocks;
+    p.lay = shape.lay;
+    const RowAccess access = shape.access;
+    const int cols = shape.cols, ops = shape.ops;
+    const bool by_group = plan.by_group, each = plan.each, one_block = each && cols == kGradCols;
     const bool ring = p.lay.stages > 0;
     const bool full = (int64_t)p.lay.tx * p.lay.cs * cols == p.dim;
     const void* fn;
     if (each)  // rows of more than kWarpDim columns: always a ring
         fn = one_block ? (const void*)norm_grad_kernel<Bf16, kVecOf<Bf16>, true, false, false, false, kGradCols, true>
-             : access == VECTORS ? (const void*)norm_grad_kernel<T, E, true, false, false, false, kGradFewCols, true>
-             : access == WINDOW ? (const void*)norm_grad_kernel<T, E, true, false, false, true, kGradFewCols, true>
+             : access == ROWS_VECTORS ? (const void*)norm_grad_kernel<T, E, true, false, false, false, kGradFewCols, true>
+             : access == ROWS_WINDOW ? (const void*)norm_grad_kernel<T, E, true, false, false, true, kGradFewCols, true>
                                 : (const void*)norm_grad_kernel<T, 1, true, false, false, false, kGradFewCols, true>;
-    else if (access == VECTORS)
+    else if (access == ROWS_VECTORS)
         fn = ring ? (full ? pick_grad<T, E, true, true>(by_group) : pick_grad<T, E, true, false>(by_group))
                   : pick_grad<T, E, false, false>(by_group);
-    else if (access == WINDOW)
+    else if (access == ROWS_WINDOW)
         fn = ring ? (const void*)norm_grad_kernel<T, E, true, false, false, true, (sizeof(T) == 2 ? kGradCols : kGradFewCols)>
                   : (const void*)norm_grad_kernel<T, E, false, false, false, true, kGradFewCols>;
     else
@@ -1021,6 +997,49 @@ BlockNormPlan block_norm_plan(int64_t tokens, int64_t dim, int64_t gate_rows, bo
     return q;
 }
 
+BlockNormRows block_norm_rows(int64_t dim, int es, bool vectors, bool alike) {
+    BlockNormRows r = {};
+    r.access = vectors ? ROWS_VECTORS : alike ? ROWS_WINDOW : ROWS_ONE_BY_ONE;
+    r.cols = kCols;
+    r.ops = 2;
+    r.lay = row_layout(dim, es, r.ops, r.access, kCols, kCols, kNormThreads / 2);
+    return r;
+}
+
+BlockNormRows block_norm_grad_rows(BlockNormPlan* q, int64_t tokens, int64_t dim, int es, bool vectors, bool alike) {
+    BlockNormRows r = {};
+    // with 8 columns a thread a cluster has just enough for the longest rows, and
+    // none for what a window begins before them (fp32 rows of 32766 columns):
+    // those are taken element by element
+    const int window_cols = !q->each && es == 2 ? kGradCols : kGradFewCols;
+    const bool window = !vectors && alike && !q->by_group && q->per_group >= kClasses &&
+                        dim + 16 / es - 1 <= (int64_t)kMaxCluster * kNormThreads * window_cols;
+    if (window) {  // as many blocks for each class of tokens
+        const int64_t gates = q->blocks / q->per_group, parts = q->per_group / kClasses, per_gate = tokens / gates;
+        q->unit = ((per_gate + kClasses - 1) / kClasses + parts - 1) / parts;
+        q->per_group = parts * kClasses;
+        q->blocks = gates * q->per_group;
+    }
+    r.access = vectors ? ROWS_VECTORS : window ? ROWS_WINDOW : ROWS_ONE_BY_ONE;
+    // fp32 windows are faster with 8 (8192 x 3001: 125 us against 182), bf16 ones
+    // with 16 (16384 x 3001: 235 us against 281)
+    // with each token's gate 8, which leave no spills (8192 x 4096 bf16: 117 us
+    // against 222; 4096 x 3001: 88 against 93), but for bf16 rows that 8 would
+    // split over a cluster of half-filled blocks and 16 leave room for two stages
+    // (3600 x 4512: 113 us against 160)
+    const bool one_block = q->each && r.access == ROWS_VECTORS && es == 2 && dim > kNormThreads * kGradFewCols &&
+                           dim <= kEachThreads * kGradCols;
+    r.cols = one_block || (!q->by_group && !q->each && (r.access == ROWS_VECTORS || (r.access == ROWS_WINDOW && es == 2)))
+                 ? kGradCols : kGradFewCols;
+    // more blocks than SMs are halved (16384 x 1024 bf16, each token's gate: 59 us
+    // with 256 threads, 66 with 512; fewer keep a row a group: 509 x 1001 fp32)
+    r.ops = q->each ? 5 : 4;
+    r.lay = row_layout(dim, es, r.ops, r.access, kGradFewCols, r.cols,
+                       r.cols == kGradCols || (q->each && q->blocks > kGradBlocks) ? kNormThreads / 2 : kNormThreads);
+    if (!r.lay.stages) r.cols = kGradFewCols;
+    return r;
+}
+
 cudaError_t launch_block_norm_grad(const hc_block_norm_grad_t& a, cudaStream_t stream) {
     const BlockNormPlan q = block_norm_plan((int64_t)a.tokens, (int64_t)a.dim, (int64_t)a.gate_rows, a.gate != nullptr,
                                             a.dtype == a.weight_dtype);
@@ -1046,16 +1065,13 @@ cudaError_t launch_block_norm_grad(const hc_block_norm_grad_t& a, cudaStream_t s
     p.per_gate = (unsigned)(p.tokens / p.gates);
     p.grad_y_stride = (int64_t)a.grad_y_stride;
     p.grad_x_stride = (int64_t)a.grad_x_stride;
-    p.blocks = q.blocks;
-    p.unit = (unsigned)q.unit;
-    p.per_group = q.per_group;
     p.pitch = q.pitch;
     p.slots = q.slots;
     p.direct = q.direct;
     p.dim = (int)a.dim;
     p.bf16_weights = a.weight_dtype == HC_BFLOAT16;
     p.residual_scale = a.residual_scale;
-    return a.dtype == HC_BFLOAT16 ? run_norm_grad<Bf16>(p, q.by_group, q.each, stream) : run_norm_grad<float>(p, q.by_group, q.each, stream);
+    return a.dtype == HC_BFLOAT16 ? run_norm_grad<Bf16>(p, q, stream) : run_norm_grad<float>(p, q, stream);
 }
 
 }  // namespace hc

@@ -26,6 +26,28 @@ EmbeddingScratch embedding_scratch(int64_t tokens, int64_t rows, int64_t dim);
 cudaError_t launch_embedding_grad(const hc_embedding_grad_t& a, cudaStream_t stream, int sms);
 
 constexpr size_t kBlockNormMaxDim = 32768;
+// How the threads of a block norm's kernels take their rows: one element an
+// access, 16-byte vectors of 16-byte aligned rows, or the aligned vectors of
+// memory that hold rows which all lie alike.
+enum RowAccess { ROWS_ONE_BY_ONE, ROWS_VECTORS, ROWS_WINDOW };
+// Shape of a launch: tx threads (or lanes) have a row, ty rows a block.
+struct RowLayout {
+    int tx, ty, cs;     // cs: blocks of a cluster
+    int stages;         // 0: rows in a warp, loaded directly
+    int slot;           // bytes of one row (slice) of one operand in a stage
+    int weights;        // bytes of weights kept after the stages
+    int* err;
+    unsigned long long wait_ns;
+    int hold;           // wait-expiry test mode
+};
+struct BlockNormRows {
+    RowAccess access;
+    int cols, ops;      // columns of a thread, operands of a stage
+    RowLayout lay;      // without the fields that depend on the device
+};
+// vectors: every operand takes 16-byte accesses; alike: the inputs' rows lie
+// alike in their 16-byte vectors; es: bytes of an element.
+BlockNormRows block_norm_rows(int64_t dim, int es, bool vectors, bool alike);
 cudaError_t launch_block_norm(const hc_block_norm_t& a, cudaStream_t stream, int sms);
 // How the rows are divided among the blocks that sum weight gradients.
 struct BlockNormPlan {
@@ -40,6 +62,8 @@ struct BlockNormPlan {
     size_t bytes;
 };
 BlockNormPlan block_norm_plan(int64_t tokens, int64_t dim, int64_t gate_rows, bool gate, bool same_types);
+// Windows divide the tokens by their rows' shift: they change unit, per_group and blocks.
+BlockNormRows block_norm_grad_rows(BlockNormPlan* q, int64_t tokens, int64_t dim, int es, bool vectors, bool alike);
 cudaError_t launch_block_norm_grad(const hc_block_norm_grad_t& a, cudaStream_t stream);
 
 constexpr size_t kDistillMaxTop = 1024;

@@ -354,6 +354,22 @@ def test_block_norm_grad_with_a_gate_for_every_token_strided_and_partial(dtype, 
     check_norm_grad(161, 304, 161, dtype, dtype, gz=False)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dim", [32761, 32762, 32765, 32766, 32767])
+def test_block_norm_grad_of_the_longest_odd_rows(dim, dtype):
+    """Rows whose 16-byte windows would begin before a cluster's columns."""
+    check_norm(40, dim, 1, dtype, dtype)
+    check_norm_grad(40, dim, 1, dtype, dtype)
+    check_norm_grad(160, dim, 160, dtype, dtype)
+
+
+@pytest.mark.parametrize("stride,offset", [(32768, 1), (32769, 0), (32771, 3)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_block_norm_grad_of_the_longest_rows_strided(dtype, stride, offset):
+    check_norm_grad(40, 32768, 1, dtype, dtype, stride, offset)
+    check_norm_grad(153, 32768, 153, dtype, dtype, stride, offset)
+
+
 @pytest.mark.parametrize("dim", [301, 1024, 5000])
 def test_block_norm_grad_with_a_gate_for_every_token_in_place(dim):
     g = gen(8)
