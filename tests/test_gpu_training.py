@@ -153,6 +153,16 @@ def test_embedding_grad_many(tokens, rows):
     run_embedding_grad(gen(rows), tokens, rows, 16, "uniform", F32, F32, False)
 
 
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("tokens,rows", [(2049, 700), (16411, 8001), (32768, 700), (32769, 700), (40000, (1 << 18) + 7),
+                                         (262144, 5000), (262145, (1 << 18) + 7)])
+def test_embedding_grad_sorts(tokens, rows, accumulate):
+    """The largest sorts of one cluster and the smallest over global memory, both
+    sizes of its blocks, with two and three radix passes."""
+    run_embedding_grad(gen(rows), tokens, rows, 9, "skewed", BF16, F32, accumulate)
+    run_embedding_grad(gen(rows), tokens, rows, 16, "uniform", F32, F32, accumulate)
+
+
 def test_embedding_grad_ignores_rows_of_tokens_elsewhere():
     g = gen(9)
     for tokens in (100, 3000):
