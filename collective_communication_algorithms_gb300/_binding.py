@@ -434,10 +434,10 @@ def hc_operator_scratch_bytes(name, args):
     return getattr(lib(), name + "_scratch_bytes")(ctypes.byref(args))
 
 
-def bind_operator(name, args, keep=(), stream=0):
+def bind_operator(name, args, keep=(), stream=0, kind=BoundCall):
     """The training operator `name` with the struct `args`, as a BoundCall."""
-    return BoundCall(name, (ctypes.byref(args), ctypes.c_void_p(int(stream)) if stream else None),
-                     (args, keep))
+    return kind(name, (ctypes.byref(args), ctypes.c_void_p(int(stream)) if stream else None),
+                (args, keep))
 
 
 def hc_device_status(clear=True):

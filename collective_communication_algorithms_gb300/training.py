@@ -1,6 +1,7 @@
 """Training operators on torch CUDA tensors: the embedding lookup, the norms
 and the gate at a block's boundary and the distillation loss, each with its
-gradient (include/hc.h, "Training operators").
+gradient (include/hc.h, "Training operators").  They run on their tensors' GPU,
+whichever is current.
 
 Every operator comes as a function that runs once and returns its outputs,
 and as bind_*, which returns a BoundCall with `.outputs` (a dict of tensors)
@@ -77,11 +78,29 @@ def _scratch(name, args, scratch, like):
     return scratch
 
 
+class _DeviceCall(B.BoundCall):
+    """A bound call in a process with several GPUs: the library launches on the
+    current one, which has to be that of the tensors and the stream."""
+
+    __slots__ = ("device",)
+
+    def __call__(self):
+        import torch
+        with torch.cuda.device(self.device):
+            super().__call__()
+
+
 def _bind(name, args, stream, outputs, keep, like):
     import torch
     if stream is None:
         stream = torch.cuda.current_stream(like.device)
-    call = B.bind_operator(name, args, keep, stream.cuda_stream)
+    elif stream.device != like.device:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, like.device))
+    if torch.cuda.device_count() > 1:
+        call = B.bind_operator(name, args, keep, stream.cuda_stream, _DeviceCall)
+        call.device = like.device
+    else:
+        call = B.bind_operator(name, args, keep, stream.cuda_stream)
     call.outputs = outputs
     return call
 
@@ -108,10 +127,15 @@ def _on_stream(bind):
         if stream is None:
             return bind(*args, **kw)
         import torch
-        current = torch.cuda.current_stream()
+        first = next(_tensors([args, kw]), None)
+        if first is None or not first.is_cuda:
+            raise ValueError("stream= is for CUDA tensors")
+        device = first.device
+        current = torch.cuda.current_stream(device)
         if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-        if stream.cuda_stream == current.cuda_stream:
+            stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                      else torch.cuda.default_stream(device))
+        if stream.device == device and stream.cuda_stream == current.cuda_stream:
             return bind(*args, **kw)
         with torch.cuda.stream(stream):
             call = bind(*args, stream=stream, **kw)
