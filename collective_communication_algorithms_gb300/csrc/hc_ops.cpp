@@ -193,11 +193,13 @@ hc_status_t hc_block_norm(const hc_block_norm_t* args, hc_stream_t stream) {
 size_t hc_block_norm_grad_scratch_bytes(const hc_block_norm_grad_t* a) {
     if (!a || a->struct_size < sizeof(hc_block_norm_grad_t)) return 0;
     // a gate that is NULL only because no pointer is known yet counts by its
-    // rows, so one size serves calls with and without it
-    const size_t rows = a->gate_rows ? a->gate_rows : 1;
-    if (norm_sizes(a->tokens, a->dim, true, rows) != HC_OK) return 0;
-    const size_t with = block_norm_plan((int64_t)a->tokens, (int64_t)a->dim, (int64_t)rows, true, a->dtype == a->weight_dtype).bytes;
+    // rows, so one size serves calls with and without it; a call without a gate
+    // does not look at them
+    if (norm_sizes(a->tokens, a->dim, false, 0) != HC_OK) return 0;
     const size_t without = block_norm_plan((int64_t)a->tokens, (int64_t)a->dim, 1, false, false).bytes;
+    const size_t rows = a->gate_rows ? a->gate_rows : 1;
+    if (norm_sizes(a->tokens, a->dim, true, rows) != HC_OK) return without;
+    const size_t with = block_norm_plan((int64_t)a->tokens, (int64_t)a->dim, (int64_t)rows, true, a->dtype == a->weight_dtype).bytes;
     return with > without ? with : without;
 }
 

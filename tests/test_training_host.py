@@ -164,6 +164,18 @@ def test_scratch():
 
 
 @host_only
+def test_scratch_of_a_call_without_a_gate_does_not_depend_on_gate_rows():
+    name = "hc_block_norm_grad"
+    for rows in (0, 1, 5, 7, 1200, 5000):  # 7 and 5000 do not divide the tokens
+        call = dict(VALID[name], tokens=1200, gate=0, grad_gate=0, gate_rows=rows)
+        need = B.hc_operator_scratch_bytes(name, B.operator_args(name, **call))
+        assert need > 0
+        assert status(name, **dict(call, scratch_bytes=need)) == CUDA
+    refused = dict(VALID[name], tokens=1200, dim=32769, gate_rows=7)
+    assert B.hc_operator_scratch_bytes(name, B.operator_args(name, **refused)) == 0
+
+
+@host_only
 def test_overlaps():
     assert status("hc_embedding", out=at(0) + 64) == INVALID
     assert status("hc_embedding", out=at(1)) == INVALID
