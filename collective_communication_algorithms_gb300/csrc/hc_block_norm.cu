@@ -1047,10 +1047,12 @@ cudaError_t launch_block_norm_grad(const hc_block_norm_grad_t& a, cudaStream_t s
     p.in[0] = {a.grad_r, (int64_t)a.grad_r_stride};
     p.in[1] = {a.grad_z, (int64_t)a.grad_z_stride};
     p.in[2] = {a.y, (int64_t)a.y_stride};
-    p.in[3] = {a.x, (int64_t)a.x_stride};
+    // without a next norm, x and its weight are no operands: what they hold (0 *
+    // inf) is kept out of the gradients, and x is not read
+    p.in[3] = {a.grad_z ? a.x : nullptr, (int64_t)a.x_stride};
     p.post_weight = a.post_weight;
     p.gate = a.gate;
-    p.pre_weight = a.pre_weight;
+    p.pre_weight = a.grad_z ? a.pre_weight : nullptr;
     p.post_rstd = a.post_rstd;
     p.pre_rstd = a.pre_rstd;
     p.grad_y = a.grad_y;

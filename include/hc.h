@@ -439,8 +439,10 @@ hc_status_t hc_block_norm(const hc_block_norm_t* args, hc_stream_t stream);
 /*
  * Gradient of the block boundary, from the gradients of r (by its later
  * uses) and z, the forward inputs and the kept post_rstd and pre_rstd.
- *  grad_r, grad_z : NULL stands for zeros (not both; without grad_z,
- *                   pre_rstd, pre_weight and grad_pre_weight are not used).
+ *  grad_r, grad_z : NULL stands for zeros (not both).  Without grad_z there
+ *                   is no next norm: x, pre_rstd and pre_weight have no part,
+ *                   whatever they hold, and grad_pre_weight is written as
+ *                   zeros.
  *  grad_y, grad_x : may be exactly any of grad_r, grad_z, y, x in place.
  *  grad_post_weight, grad_gate, grad_pre_weight : in weight_dtype,
  *                   contiguous; NULL: not computed.

@@ -394,6 +394,28 @@ def test_block_norm_grad_with_a_gate_for_every_token_in_place(dim):
         assert torch.equal(o[name], ref[name]), name
 
 
+@pytest.mark.parametrize("dtype,wdtype", [(F32, F32), (BF16, F32), (BF16, BF16)])
+@pytest.mark.parametrize("tokens,dim,gates", [(3, 40, 1), (40, 100, 2), (620, 100, 310), (37, 301, 1), (90, 1000, 3),
+                                              (620, 520, 310), (200, 301, 200), (200, 1024, 200), (20, 9000, 1)])
+def test_block_norm_grad_without_a_next_norm(tokens, dim, gates, dtype, wdtype):
+    """Without grad_z neither x nor the next norm's weight has a part in any
+    gradient, whatever they hold, and grad_x = a grad_r."""
+    a = 0.75
+    g = gen(dim)
+    y, x, post, gate, pre = norm_inputs(g, tokens, dim, dtype, wdtype, gates)
+    dr = normal(g, tokens, dim, dtype=dtype)
+    s = hc.block_norm(y, x, post, gate, residual_scale=a, next_norm=False)["post_rstd"]
+    ref = hc.block_norm_grad(dr, None, y, x, s, None, post, gate, pre, residual_scale=a)
+    assert all(bool(torch.isfinite(t).all()) for t in ref.values())
+    x[0], x[-1, 3], pre[1], pre[2] = math.inf, math.nan, math.nan, -math.inf
+    pre_grad = torch.full_like(pre, 9.0)
+    o = hc.block_norm_grad(dr, None, y, x, s, None, post, gate, pre, residual_scale=a, grad_pre_weight=pre_grad)
+    assert not bool(pre_grad.any())
+    for name in ref:
+        assert torch.equal(o[name], ref[name]), name
+    assert torch.equal(o["grad_x"], (dr.double() * a).to(dtype))
+
+
 @pytest.mark.parametrize("dim", [64, 5000])
 def test_block_norm_grad_in_place(dim):
     g = gen(8)
