@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_sum_kernel(const NormGrad
         __syncthreads();
         if (warp || c >= p.dim) continue;
         for (int w = 1; w < kSumWarps && w * per < count; w++) acc += sums[w][lane];
-        if (job >= 2 && p.post_weight)
+        if (job >= 2 && p.post_weight && count)  // no tokens: zeros (0 * inf)
             acc *= p.bf16_weights ? to_f32(((const Bf16*)p.post_weight)[c]) : ((const float*)p.post_weight)[c];
         const int64_t at = (job < 2 ? 0 : g * p.dim) + c;
         if (p.bf16_weights) put((Bf16*)out + at, acc);

@@ -446,6 +446,16 @@ def test_block_norm_grad_without_tokens():
         assert not any(bool(t.any()) for t in outs)
 
 
+def test_block_norm_grad_without_tokens_is_zeros_whatever_the_weights():
+    y, s = torch.empty(0, 24, device="cuda"), torch.empty(0, device="cuda")
+    w = torch.full((24,), math.inf, device="cuda")
+    w[3] = math.nan
+    for gates in (1, 400):
+        gate = w.repeat(gates, 1)
+        o = hc.block_norm_grad(y, y, y, y, s, s, w, gate, w)
+        assert not any(bool(o[k].any()) for k in ("grad_post_weight", "grad_gate", "grad_pre_weight"))
+
+
 def test_block_norm_grad_against_differences():
     """Directional derivatives of the 64-bit forward pass by central
     differences: truncation of order h^2, the kernels' binary32 gradients."""
