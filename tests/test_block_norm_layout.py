@@ -74,3 +74,9 @@ def test_every_shape_can_be_launched(layouts):
                 and shared <= 226 << 10 and (s["stages"] >= 1 or s["tx"] <= 32)):
             bad.append(s)
     assert not bad, "%d of %d, the first: %s" % (len(bad), len(layouts), bad[:3])
+
+
+def test_rows_are_brought_ahead(layouts):
+    """Every ring holds the row after the one under way."""
+    bad = [s for s in layouts if s["stages"] == 1]
+    assert not bad, "%d of %d, the first: %s" % (len(bad), len(layouts), bad[:3])
