@@ -79,11 +79,10 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const LookupPara
         const int64_t t = t0 + u * ny;
         if (t >= p.tokens) break;
         TO* to = (TO*)p.out + t * p.out_stride + c;
-        const float scale = row[u] < (uint64_t)p.rows ? p.scale : 1.0f;  // zeros stay zeros (0 * inf)
 #pragma unroll
         for (int k = 0; k < V; k++) {
 #pragma unroll
-            for (int i = 0; i < N; i++) v[u][k][i] *= scale;
+            for (int i = 0; i < N; i++) v[u][k][i] *= p.scale;
             store_whole<TO, N>(to + k * step, c + k * step < p.dim, v[u][k]);
         }
     }

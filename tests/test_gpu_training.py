@@ -94,19 +94,6 @@ def test_embedding_far_ids():
     assert torch.equal(out[0], table[0]) and not bool(out[1:].any())
 
 
-@pytest.mark.parametrize("scale", [math.inf, math.nan, -2.0])
-@pytest.mark.parametrize("dim", [24, 33])
-def test_embedding_rows_elsewhere_are_zeros_whatever_the_scale(dim, scale):
-    g = gen(dim)
-    table, ids = normal(g, 20, dim), some_ids(g, 300, 40, "uniform")
-    here = ids < 20
-    for out_dtype in (F32, BF16):
-        out = hc.embedding(table, ids, scale=scale, out_dtype=out_dtype)["out"]
-        assert not bool(out[~here].any()) and not bool(torch.signbit(out[~here]).any())
-        if not math.isfinite(scale):
-            assert not bool(torch.isfinite(out[here]).any())
-
-
 def test_vocabulary_split_over_ranks_and_allreduced_is_the_whole_lookup():
     P, vocab, dim, tokens = 4, 1003, 64, 500
     g = gen(5)
