@@ -122,6 +122,7 @@ hc_status_t hc_embedding(const hc_embedding_t* args, hc_stream_t stream) {
     HC_TRY(check_float(a.out_dtype));
     if (!known_id(a.id_type)) return HC_ERR_INVALID_ARG;
     HC_TRY(embedding_sizes(a.tokens, a.rows, a.dim));
+    if (!std::isfinite(a.scale)) return HC_ERR_INVALID_ARG;  // would make NaN of the zero rows
     Use u[3] = {};
     u[2].write = true;
     if (a.tokens && (!a.table || !a.ids || !a.out)) return HC_ERR_INVALID_ARG;

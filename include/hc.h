@@ -354,7 +354,8 @@ typedef enum { HC_ID32 = 0, HC_ID64 = 1 } hc_id_t;
  * when ids[t] - first_id is not in [0, rows).  The table is then one rank's
  * share of a vocabulary split by rows: a sum hc_allreduce of the ranks'
  * outputs is the whole lookup (one rank contributes each row, all others
- * zeros).  Negative ids (padding) give zero rows.
+ * zeros).  Negative ids (padding) give zero rows.  The scale must be finite
+ * (HC_ERR_INVALID_ARG).
  */
 typedef struct {
     size_t struct_size;

@@ -128,6 +128,15 @@ def test_sizes():
 
 
 @host_only
+def test_lookup_scale():
+    """Zero rows stay zeros: a scale that would make NaN of them is refused."""
+    for scale in (float("inf"), float("-inf"), float("nan")):
+        assert status("hc_embedding", scale=scale) == INVALID
+    assert status("hc_embedding", scale=-2.0) == CUDA
+    assert status("hc_embedding", scale=0.0) == CUDA
+
+
+@host_only
 def test_optional_operands():
     assert status("hc_block_norm", z=0, pre_rstd=0) == CUDA
     assert status("hc_block_norm", z=0) == INVALID            # pre_rstd without the norm
