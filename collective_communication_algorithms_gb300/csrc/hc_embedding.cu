@@ -366,6 +366,9 @@ __global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(const GradPa
 
 // ---------------------------------------------------------------------------
 // the same sort in passes over global memory: a block orders `chunk` tokens.
+// Every block reads the digit counts of all chunks, which is quadratic in them:
+// nothing up to a million tokens (128 chunks; 191 us of 8 columns), about a
+// third of the time of 2^24 (2048 chunks; 4.8 ms).
 // ---------------------------------------------------------------------------
 // Digit counts of every chunk for the first pass; zeroes the next pass's.
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const GradParams p) {

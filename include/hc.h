@@ -334,10 +334,13 @@ hc_status_t hc_graph_destroy(hc_graph_t graph);
  *    validation happens before any launch.
  *  - Matrices are row-major with unit column stride; a *_stride is the
  *    distance between rows in elements, 0 meaning the row length.  Pointers
- *    are aligned to their element type (HC_ERR_ALIGN otherwise); 16-byte
- *    aligned pointers and row pitches take the wide-access kernels.
+ *    are aligned to their element type (HC_ERR_ALIGN otherwise).  Pointers
+ *    and row pitches of whole 16 bytes take the wide-access kernels, if a row
+ *    too is whole 16 bytes (lookup and its gradient: dim a multiple of 8).
  *  - Values are HC_FLOAT32 or HC_BFLOAT16 (HC_ERR_UNSUPPORTED otherwise).
  *    Arithmetic and sums are binary32, and every output is rounded once.
+ *  - Kernels run on the current device, which has to be that of the stream
+ *    and the operands.
  *  - Sums run in an order fixed by the sizes and by how the inputs lie in
  *    memory, without floating-point atomics: a call repeated on the same inputs
  *    gives the same bits.
@@ -380,7 +383,8 @@ hc_status_t hc_embedding(const hc_embedding_t* args, hc_stream_t stream);
  *               as zeros; 1: the sums are added to what grad_table holds (in
  *               binary32, rounded once), and only rows with tokens are touched.
  *  tokens, rows at most 2^31 - 1, dim at most 2^24 (HC_ERR_UNSUPPORTED), as
- *  for the lookup.
+ *  for the lookup.  The time of the sort grows faster than the tokens from
+ *  about 2^24 of them.
  */
 typedef struct {
     size_t struct_size;
@@ -486,8 +490,9 @@ size_t hc_block_norm_grad_scratch_bytes(const hc_block_norm_grad_t* args);
  * An entry whose id is not in [0, vocab) (a row with fewer than `top`
  * entries) or whose teacher logit is -inf has no part; entries with the same
  * id add up.  A row with w == 0 or without entries has loss 0, stats 0 and
- * gradient 0 whatever its logits hold (they are not read).  Logits of -inf
- * (masked columns) have q = 0.
+ * gradient 0 whatever its logits hold.  Logits of -inf (masked columns) have
+ * q = 0, and so do those whose exponential relative to the row's largest is
+ * below 2^-126 (the smallest normal binary32).
  *  stats       : [t] = (largest logit, sum of exp((logit - largest) /
  *                temperature)), what hc_distill_grad needs; NULL: not kept.
  *  grad_logits : NULL: the loss alone.  May be exactly logits in place.
