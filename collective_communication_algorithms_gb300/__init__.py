@@ -9,16 +9,21 @@ lists of torch tensors (one per virtual rank: CUDA tensors, or pinned host
 tensors that the kernels then read and write over the host link) and pass
 their pointers and the current CUDA stream.  training.py adds the training
 operators on either side of the collectives (embedding lookup, block-boundary
-norms, distillation loss, with gradients).  PyTorch only provides device memory and streams.
+norms, distillation loss, with gradients; gradient clipping) and experts.py
+those of an expert layer.  PyTorch only provides device memory and streams.
 """
 from ._binding import (ALGOS, COLLS, DTYPES, MODES, OPS, Graph, HcError, hc_allgather, hc_allreduce,
                        hc_broadcast,
                        hc_num_segments, hc_reduce_scatter, hc_schedule_stats, hc_scratch_bytes,
                        hc_segment_range, hc_step_plan, hc_version, lib, make_opts)
 from ._binding import LIB_PATH as library_path
-from .training import (bind_block_norm, bind_block_norm_grad, bind_distill, bind_distill_grad,
-                       bind_embedding, bind_embedding_grad, block_norm, block_norm_grad, distill,
-                       distill_grad, embedding, embedding_grad)
+from .experts import (bind_expert_combine, bind_expert_combine_grad, bind_expert_matmul,
+                      bind_expert_matmul_grad, bind_expert_plan, expert_combine, expert_combine_grad,
+                      expert_matmul, expert_matmul_grad, expert_plan)
+from .training import (bind_block_norm, bind_block_norm_grad, bind_clip_grads, bind_distill,
+                       bind_distill_grad, bind_embedding, bind_embedding_grad, bind_grad_norm, block_norm,
+                       block_norm_grad, clip_grads, distill, distill_grad, embedding, embedding_grad,
+                       grad_norm)
 
 __all__ = ["allreduce", "reduce_scatter", "allgather", "broadcast", "segment_range", "segments",
            "Graph", "hc_broadcast",
@@ -27,6 +32,10 @@ __all__ = ["allreduce", "reduce_scatter", "allgather", "broadcast", "segment_ran
            "embedding", "embedding_grad", "block_norm", "block_norm_grad", "distill", "distill_grad",
            "bind_embedding", "bind_embedding_grad", "bind_block_norm", "bind_block_norm_grad",
            "bind_distill", "bind_distill_grad",
+           "clip_grads", "grad_norm", "bind_clip_grads", "bind_grad_norm",
+           "expert_plan", "expert_matmul", "expert_matmul_grad", "expert_combine", "expert_combine_grad",
+           "bind_expert_plan", "bind_expert_matmul", "bind_expert_matmul_grad", "bind_expert_combine",
+           "bind_expert_combine_grad",
            "hc_version", "HcError", "make_opts", "library_path", "lib"]
 
 _TORCH_DTYPE = {"torch.int32": "int32", "torch.float32": "float32", "torch.bfloat16": "bfloat16"}

@@ -19,6 +19,7 @@ OPS = {"sum": 0, "prod": 1, "max": 2, "min": 3}
 ALGOS = {"ring": 0, "rhd": 1, "pipeline": 2, "hier": 3}
 COLLS = {"allreduce": 0, "reducescatter": 1, "allgather": 2, "broadcast": 3}
 MODES = {"fused": 0, "step": 1}
+LAYOUTS = {"out_in": 0, "in_out": 1}
 STATUS = {0: "HC_OK", 1: "HC_ERR_INVALID_ARG", 2: "HC_ERR_UNSUPPORTED", 3: "HC_ERR_ALIGN",
           4: "HC_ERR_SCRATCH", 5: "HC_ERR_CUDA", 6: "HC_ERR_TIMEOUT"}
 
@@ -104,10 +105,55 @@ class hc_distill_t(ctypes.Structure):
                        (_int, "dtype teacher_dtype id_type"), (_f, "temperature scale"))
 
 
+class hc_grad_t(ctypes.Structure):
+    _fields_ = [("in_", _vp), ("out", _vp), ("count", _sz), ("in_dtype", _int), ("out_dtype", _int)]
+
+
+class hc_clip_grads_t(ctypes.Structure):
+    _fields_ = _fields((_vp, "tensors norm factor scratch"), (_sz, "scratch_bytes num"),
+                       (_f, "scale max_norm eps"))
+
+
+class hc_expert_plan_t(ctypes.Structure):
+    _fields_ = _fields((_vp, "expert_ids offsets row_tokens slots scratch"),
+                       (_sz, "scratch_bytes tokens top experts"), (_int, "id_type"), (_i64, "first_expert"))
+
+
+class hc_expert_matmul_t(ctypes.Structure):
+    _fields_ = _fields((_vp, "x weight offsets out scratch"),
+                       (_sz, "scratch_bytes rows experts in_dim out_dim x_stride weight_stride expert_stride "
+                             "out_stride"), (_int, "dtype out_dtype weight_layout"))
+
+
+class hc_expert_matmul_grad_t(ctypes.Structure):
+    _fields_ = _fields((_vp, "grad_out x weight offsets grad_x grad_weight scratch"),
+                       (_sz, "scratch_bytes rows experts in_dim out_dim grad_out_stride x_stride weight_stride "
+                             "expert_stride grad_x_stride grad_weight_stride grad_expert_stride"),
+                       (_int, "dtype grad_weight_dtype weight_layout accumulate"))
+
+
+class hc_expert_combine_t(ctypes.Structure):
+    _fields_ = _fields((_vp, "y slots weights out"), (_sz, "tokens top rows dim y_stride out_stride"),
+                       (_int, "dtype weight_dtype"))
+
+
+class hc_expert_combine_grad_t(ctypes.Structure):
+    _fields_ = _fields((_vp, "grad_out y slots weights grad_y grad_weights"),
+                       (_sz, "tokens top rows dim grad_out_stride y_stride grad_y_stride"),
+                       (_int, "dtype weight_dtype"))
+
+
 # the training operators and their argument structs
 OPERATORS = {"hc_embedding": hc_embedding_t, "hc_embedding_grad": hc_embedding_grad_t,
              "hc_block_norm": hc_block_norm_t, "hc_block_norm_grad": hc_block_norm_grad_t,
-             "hc_distill": hc_distill_t, "hc_distill_grad": hc_distill_t}
+             "hc_distill": hc_distill_t, "hc_distill_grad": hc_distill_t,
+             "hc_clip_grads": hc_clip_grads_t, "hc_grad_norm": hc_clip_grads_t,
+             "hc_expert_plan": hc_expert_plan_t, "hc_expert_matmul": hc_expert_matmul_t,
+             "hc_expert_matmul_grad": hc_expert_matmul_grad_t, "hc_expert_combine": hc_expert_combine_t,
+             "hc_expert_combine_grad": hc_expert_combine_grad_t}
+# those that may need scratch
+SCRATCH = ("hc_embedding_grad", "hc_block_norm_grad", "hc_clip_grads", "hc_expert_plan", "hc_expert_matmul",
+           "hc_expert_matmul_grad")
 
 # every symbol include/hc.h declares
 EXPORTS = ("hc_allreduce", "hc_reduce_scatter", "hc_reduce_scatter_static_scratch",
@@ -118,6 +164,11 @@ EXPORTS = ("hc_allreduce", "hc_reduce_scatter", "hc_reduce_scatter_static_scratc
            "hc_embedding", "hc_embedding_grad", "hc_embedding_grad_scratch_bytes",
            "hc_block_norm", "hc_block_norm_grad", "hc_block_norm_grad_scratch_bytes",
            "hc_distill", "hc_distill_grad",
+           "hc_clip_grads", "hc_grad_norm", "hc_clip_grads_scratch_bytes",
+           "hc_expert_plan", "hc_expert_plan_scratch_bytes",
+           "hc_expert_matmul", "hc_expert_matmul_scratch_bytes",
+           "hc_expert_matmul_grad", "hc_expert_matmul_grad_scratch_bytes",
+           "hc_expert_combine", "hc_expert_combine_grad",
            "hc_num_segments", "hc_scratch_bytes", "hc_schedule_stats", "hc_step_plan",
            "hc_select_algo", "hc_device_status", "hc_test_expire_waits", "hc_last_cuda_error",
            "hc_status_string",
@@ -149,7 +200,7 @@ def lib():
             f = getattr(L, name)
             f.argtypes = [ctypes.POINTER(args), vp]
             f.restype = i32
-        for name in ("hc_embedding_grad", "hc_block_norm_grad"):
+        for name in SCRATCH:
             f = getattr(L, name + "_scratch_bytes")
             f.argtypes = [ctypes.POINTER(OPERATORS[name])]
             f.restype = sz
@@ -419,6 +470,8 @@ def operator_args(name, **kw):
             v = _enum(IDS, v)
         elif k.endswith("dtype"):
             v = _enum(DTYPES, v)
+        elif k == "weight_layout":
+            v = _enum(LAYOUTS, v)
         setattr(a, k, v)
     return a
 
@@ -430,7 +483,7 @@ def hc_operator(name, args, stream=0):
 
 
 def hc_operator_scratch_bytes(name, args):
-    """Scratch bytes of hc_embedding_grad or hc_block_norm_grad with `args`."""
+    """Scratch bytes of one of the operators in SCRATCH with `args`."""
     return getattr(lib(), name + "_scratch_bytes")(ctypes.byref(args))
 
 

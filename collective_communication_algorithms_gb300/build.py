@@ -18,7 +18,8 @@ LIB = os.path.join(OUT, "libhc.so")
 ARCHIVE = os.path.join(OUT, "libhc.a")
 SOURCES = ["hc_kernels.cu", "hc_fused_ring.cu", "hc_fused_rhd.cu", "hc_fused_pipe.cu",
            "hc_fused_hier.cu", "hc_sched.cpp", "hc_api.cpp", "hc_graph.cpp", "hc_static_scratch.cu",
-           "hc_trace.cpp", "hc_ops.cpp", "hc_embedding.cu", "hc_block_norm.cu", "hc_distill.cu"]
+           "hc_trace.cpp", "hc_ops.cpp", "hc_embedding.cu", "hc_block_norm.cu", "hc_distill.cu",
+           "hc_clip.cu", "hc_expert.cu", "hc_expert_matmul.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,6 +1,9 @@
 // hc_ops.cpp -- the C ABI of the training operators (see include/hc.h):
 // argument validation, strides, overlap checks and dispatch to the kernels.
+#include <algorithm>
 #include <cmath>
+#include <memory>
+#include <new>
 
 #include "hc_ops.h"
 
@@ -108,6 +111,140 @@ hc_status_t norm_sizes(size_t tokens, size_t dim, bool gate, size_t gate_rows) {
     if (!dim) return HC_ERR_INVALID_ARG;
     if (gate && (!gate_rows || tokens % gate_rows)) return HC_ERR_INVALID_ARG;
     if (dim > kBlockNormMaxDim || tokens > kMaxTokens || (gate && gate_rows > kMaxTokens)) return HC_ERR_UNSUPPORTED;
+    return HC_OK;
+}
+
+// ---------------------------------------------------------------- clipping
+struct Span {
+    uintptr_t lo, hi;
+    bool write;
+};
+
+hc_status_t clip_tensors(const hc_clip_grads_t& a, bool apply) {
+    if (a.num && !a.tensors) return HC_ERR_INVALID_ARG;
+    if (a.num > kMaxTokens) return HC_ERR_UNSUPPORTED;
+    for (size_t i = 0; i < a.num; i++) {
+        const hc_grad_t& g = a.tensors[i];
+        HC_TRY(check_float(g.in_dtype));
+        if (g.count >> 56) return HC_ERR_UNSUPPORTED;
+        if (g.count && !g.in) return HC_ERR_INVALID_ARG;
+        if ((uintptr_t)g.in % elem_bytes(g.in_dtype)) return HC_ERR_ALIGN;
+        if (!apply || !g.out) continue;
+        HC_TRY(check_float(g.out_dtype));
+        if ((uintptr_t)g.out % elem_bytes(g.out_dtype)) return HC_ERR_ALIGN;
+        if (g.out == g.in && g.out_dtype != g.in_dtype) return HC_ERR_INVALID_ARG;
+    }
+    return HC_OK;
+}
+
+// Whether an output shares a byte with another operand.
+hc_status_t clip_overlaps(const hc_clip_grads_t& a, bool apply, size_t scratch) {
+    std::unique_ptr<Span[]> s(new (std::nothrow) Span[2 * a.num + 3]);
+    if (!s) return cuda_status(cudaErrorMemoryAllocation);
+    size_t n = 0;
+    for (size_t i = 0; i < a.num; i++) {
+        const hc_grad_t& g = a.tensors[i];
+        if (!g.count) continue;
+        const bool in_place = !g.out || g.out == g.in;
+        s[n++] = Span{(uintptr_t)g.in, (uintptr_t)g.in + g.count * elem_bytes(g.in_dtype), apply && in_place};
+        if (apply && !in_place) s[n++] = Span{(uintptr_t)g.out, (uintptr_t)g.out + g.count * elem_bytes(g.out_dtype), true};
+    }
+    s[n++] = Span{(uintptr_t)a.norm, (uintptr_t)a.norm + sizeof(float), true};
+    if (apply && a.factor) s[n++] = Span{(uintptr_t)a.factor, (uintptr_t)a.factor + sizeof(float), true};
+    if (scratch) s[n++] = Span{(uintptr_t)a.scratch, (uintptr_t)a.scratch + scratch, true};
+    const auto before = [](const Span& x, const Span& y) { return x.lo < y.lo; };
+    if (!std::is_sorted(s.get(), s.get() + n, before)) std::sort(s.get(), s.get() + n, before);
+    uintptr_t any = 0, written = 0;  // where the spans so far end
+    for (size_t i = 0; i < n; i++) {
+        if (s[i].lo < (s[i].write ? any : written)) return HC_ERR_INVALID_ARG;
+        any = std::max(any, s[i].hi);
+        if (s[i].write) written = std::max(written, s[i].hi);
+    }
+    return HC_OK;
+}
+
+hc_status_t clip(const hc_clip_grads_t* args, bool apply, hc_stream_t stream) {
+    if (!args || args->struct_size < sizeof(hc_clip_grads_t)) return HC_ERR_INVALID_ARG;
+    const hc_clip_grads_t a = *args;
+    if (!std::isfinite(a.scale) || !a.norm) return HC_ERR_INVALID_ARG;
+    if (apply && (!(a.max_norm > 0.0f) || !(a.eps >= 0.0f) || !std::isfinite(a.eps))) return HC_ERR_INVALID_ARG;
+    HC_TRY(clip_tensors(a, apply));
+    if ((uintptr_t)a.norm % sizeof(float) || (apply && (uintptr_t)a.factor % sizeof(float))) return HC_ERR_ALIGN;
+    const size_t need = clip_scratch_bytes(a);
+    HC_TRY(check_scratch(a.scratch, a.scratch_bytes, need));
+    HC_TRY(clip_overlaps(a, apply, need));
+    const TraceRange range(apply ? "hc_clip_grads" : "hc_grad_norm", 0, (uint64_t)a.num);
+    return launch([&](int) { return launch_clip(a, apply, (cudaStream_t)stream); });
+}
+
+// ---------------------------------------------------------------- expert layer
+// The weights of all experts: `rows` rows of `cols` elements each, experts
+// `expert` elements apart.
+hc_status_t weights(const void* p, size_t experts, size_t rows, size_t cols, size_t* stride, size_t* expert, size_t es,
+                    Matrix* out) {
+    Matrix one;
+    HC_TRY(matrix(p, rows, cols, stride, es, &one));
+    const size_t extent = (rows - 1) * *stride + cols;
+    if (*expert == 0) *expert = rows * *stride;
+    if (experts > 1 && *expert < extent) return HC_ERR_INVALID_ARG;
+    if (*expert > (size_t)INT64_MAX / 16 / experts) return HC_ERR_INVALID_ARG;
+    *out = one;
+    if (*expert == rows * *stride) {
+        out->rows = rows * experts;
+    } else {  // taken as one piece
+        out->rows = 1;
+        out->row_bytes = ((experts - 1) * *expert + extent) * es;
+        out->pitch = out->row_bytes;
+    }
+    return HC_OK;
+}
+
+hc_status_t matmul_sizes(size_t rows, size_t experts, size_t in_dim, size_t out_dim) {
+    if (!experts || !in_dim || !out_dim) return HC_ERR_INVALID_ARG;
+    if (experts > kMaxExperts || rows > kMaxTokens || in_dim > kMaxExpertDim || out_dim > kMaxExpertDim)
+        return HC_ERR_UNSUPPORTED;
+    return HC_OK;
+}
+bool known_layout(hc_weight_layout_t l) { return l == HC_WEIGHT_OUT_IN || l == HC_WEIGHT_IN_OUT; }
+
+// Strides and operands of the products, without the scratch.
+hc_status_t matmul_operands(hc_expert_matmul_t& a, Use* u) {
+    HC_TRY(check_float(a.dtype));
+    HC_TRY(check_float(a.out_dtype));
+    if (!known_layout(a.weight_layout)) return HC_ERR_INVALID_ARG;
+    HC_TRY(matmul_sizes(a.rows, a.experts, a.in_dim, a.out_dim));
+    const size_t es = elem_bytes(a.dtype);
+    const bool out_in = a.weight_layout == HC_WEIGHT_OUT_IN;
+    HC_TRY(matrix(a.x, a.rows, a.in_dim, &a.x_stride, es, &u[0].m));
+    HC_TRY(weights(a.weight, a.experts, out_in ? a.out_dim : a.in_dim, out_in ? a.in_dim : a.out_dim, &a.weight_stride,
+                   &a.expert_stride, es, &u[1].m));
+    HC_TRY(vector(a.offsets, a.experts + 1, sizeof(int32_t), &u[2].m));
+    HC_TRY(matrix(a.out, a.rows, a.out_dim, &a.out_stride, elem_bytes(a.out_dtype), &u[3].m));
+    u[3].write = true;
+    return HC_OK;
+}
+hc_status_t matmul_grad_operands(hc_expert_matmul_grad_t& a, Use* u) {
+    HC_TRY(check_float(a.dtype));
+    HC_TRY(check_float(a.grad_weight_dtype));
+    if (!known_layout(a.weight_layout) || (a.accumulate != 0 && a.accumulate != 1)) return HC_ERR_INVALID_ARG;
+    HC_TRY(matmul_sizes(a.rows, a.experts, a.in_dim, a.out_dim));
+    const size_t es = elem_bytes(a.dtype);
+    const bool out_in = a.weight_layout == HC_WEIGHT_OUT_IN;
+    const size_t wr = out_in ? a.out_dim : a.in_dim, wc = out_in ? a.in_dim : a.out_dim;
+    HC_TRY(matrix(a.grad_out, a.rows, a.out_dim, &a.grad_out_stride, es, &u[0].m));
+    HC_TRY(matrix(a.grad_weight ? a.x : nullptr, a.rows, a.in_dim, &a.x_stride, es, &u[1].m));
+    HC_TRY(weights(a.grad_x ? a.weight : nullptr, a.experts, wr, wc, &a.weight_stride, &a.expert_stride, es, &u[2].m));
+    HC_TRY(vector(a.offsets, a.experts + 1, sizeof(int32_t), &u[3].m));
+    HC_TRY(matrix(a.grad_x, a.rows, a.in_dim, &a.grad_x_stride, es, &u[4].m));
+    HC_TRY(weights(a.grad_weight, a.experts, wr, wc, &a.grad_weight_stride, &a.grad_expert_stride,
+                   elem_bytes(a.grad_weight_dtype), &u[5].m));
+    u[4].write = u[5].write = true;
+    return HC_OK;
+}
+
+hc_status_t combine_sizes(size_t tokens, size_t top, size_t rows, size_t dim) {
+    if (!top || !dim) return HC_ERR_INVALID_ARG;
+    if (tokens > kMaxTokens / top || rows > kMaxTokens || dim > kMaxEmbeddingDim) return HC_ERR_UNSUPPORTED;
     return HC_OK;
 }
 
@@ -279,5 +416,131 @@ static hc_status_t distill(const hc_distill_t* args, bool grad_only, hc_stream_t
 
 hc_status_t hc_distill(const hc_distill_t* args, hc_stream_t stream) { return distill(args, false, stream); }
 hc_status_t hc_distill_grad(const hc_distill_t* args, hc_stream_t stream) { return distill(args, true, stream); }
+
+hc_status_t hc_clip_grads(const hc_clip_grads_t* args, hc_stream_t stream) { return clip(args, true, stream); }
+hc_status_t hc_grad_norm(const hc_clip_grads_t* args, hc_stream_t stream) { return clip(args, false, stream); }
+size_t hc_clip_grads_scratch_bytes(const hc_clip_grads_t* a) {
+    if (!a || a->struct_size < sizeof(hc_clip_grads_t) || clip_tensors(*a, false) != HC_OK) return 0;
+    return clip_scratch_bytes(*a);
+}
+
+static hc_status_t plan_sizes(const hc_expert_plan_t& a) {
+    if (!a.top || !a.experts) return HC_ERR_INVALID_ARG;
+    if (a.experts > kMaxExperts || a.top > kMaxTokens || a.tokens > kMaxTokens / a.top) return HC_ERR_UNSUPPORTED;
+    return HC_OK;
+}
+size_t hc_expert_plan_scratch_bytes(const hc_expert_plan_t* a) {
+    if (!a || a->struct_size < sizeof(hc_expert_plan_t) || plan_sizes(*a) != HC_OK) return 0;
+    return expert_plan_shape((int64_t)(a->tokens * a->top), (int64_t)a->experts).bytes;
+}
+hc_status_t hc_expert_plan(const hc_expert_plan_t* args, hc_stream_t stream) {
+    if (!args || args->struct_size < sizeof(hc_expert_plan_t)) return HC_ERR_INVALID_ARG;
+    const hc_expert_plan_t a = *args;
+    if (!known_id(a.id_type)) return HC_ERR_INVALID_ARG;
+    HC_TRY(plan_sizes(a));
+    const size_t n = a.tokens * a.top;
+    if ((n && !a.expert_ids) || !a.offsets) return HC_ERR_INVALID_ARG;
+    Use u[5] = {};
+    HC_TRY(vector(a.expert_ids, n, id_bytes(a.id_type), &u[0].m));
+    HC_TRY(vector(a.offsets, a.experts + 1, sizeof(int32_t), &u[1].m));
+    HC_TRY(vector(a.row_tokens, n, sizeof(int32_t), &u[2].m));
+    HC_TRY(vector(a.slots, n, sizeof(int32_t), &u[3].m));
+    const size_t need = hc_expert_plan_scratch_bytes(&a);
+    HC_TRY(check_scratch(a.scratch, a.scratch_bytes, need));
+    if (need) HC_TRY(vector(a.scratch, need, 1, &u[4].m));
+    for (int i = 1; i < 5; i++) u[i].write = true;
+    HC_TRY(check_overlaps(u, 5));
+    const TraceRange range("hc_expert_plan", 0, (uint64_t)a.tokens);
+    return launch([&](int) { return launch_expert_plan(a, (cudaStream_t)stream); });
+}
+
+size_t hc_expert_matmul_scratch_bytes(const hc_expert_matmul_t* args) {
+    if (!args || args->struct_size < sizeof(hc_expert_matmul_t)) return 0;
+    hc_expert_matmul_t a = *args;
+    Use u[4] = {};
+    return matmul_operands(a, u) == HC_OK ? expert_matmul_scratch(a) : 0;
+}
+hc_status_t hc_expert_matmul(const hc_expert_matmul_t* args, hc_stream_t stream) {
+    if (!args || args->struct_size < sizeof(hc_expert_matmul_t)) return HC_ERR_INVALID_ARG;
+    hc_expert_matmul_t a = *args;
+    Use u[5] = {};
+    HC_TRY(matmul_operands(a, u));
+    if (a.rows && (!a.x || !a.weight || !a.offsets || !a.out)) return HC_ERR_INVALID_ARG;
+    const size_t need = expert_matmul_scratch(a);
+    HC_TRY(check_scratch(a.scratch, a.scratch_bytes, need));
+    if (need) HC_TRY(vector(a.scratch, need, 1, &u[4].m));
+    u[4].write = true;
+    HC_TRY(check_overlaps(u, 5));
+    if (!a.rows) return HC_OK;
+    const TraceRange range("hc_expert_matmul", 0, (uint64_t)a.rows);
+    return launch([&](int sms) { return launch_expert_matmul(a, (cudaStream_t)stream, sms); });
+}
+
+size_t hc_expert_matmul_grad_scratch_bytes(const hc_expert_matmul_grad_t* args) {
+    if (!args || args->struct_size < sizeof(hc_expert_matmul_grad_t)) return 0;
+    hc_expert_matmul_grad_t a = *args;
+    Use u[6] = {};
+    return matmul_grad_operands(a, u) == HC_OK ? expert_matmul_grad_scratch(a) : 0;
+}
+hc_status_t hc_expert_matmul_grad(const hc_expert_matmul_grad_t* args, hc_stream_t stream) {
+    if (!args || args->struct_size < sizeof(hc_expert_matmul_grad_t)) return HC_ERR_INVALID_ARG;
+    hc_expert_matmul_grad_t a = *args;
+    Use u[7] = {};
+    HC_TRY(matmul_grad_operands(a, u));
+    if ((!a.grad_x && !a.grad_weight && a.rows) || !a.offsets) return HC_ERR_INVALID_ARG;
+    if (a.rows && (!a.grad_out || (a.grad_x && !a.weight) || (a.grad_weight && !a.x))) return HC_ERR_INVALID_ARG;
+    const size_t need = expert_matmul_grad_scratch(a);
+    HC_TRY(check_scratch(a.scratch, a.scratch_bytes, need));
+    if (need) HC_TRY(vector(a.scratch, need, 1, &u[6].m));
+    u[6].write = true;
+    HC_TRY(check_overlaps(u, 7));
+    if (!a.rows && (a.accumulate || !a.grad_weight)) return HC_OK;
+    const TraceRange range("hc_expert_matmul_grad", 0, (uint64_t)a.rows);
+    return launch([&](int sms) { return launch_expert_matmul_grad(a, (cudaStream_t)stream, sms); });
+}
+
+hc_status_t hc_expert_combine(const hc_expert_combine_t* args, hc_stream_t stream) {
+    if (!args || args->struct_size < sizeof(hc_expert_combine_t)) return HC_ERR_INVALID_ARG;
+    hc_expert_combine_t a = *args;
+    HC_TRY(check_float(a.dtype));
+    if (a.weights) HC_TRY(check_float(a.weight_dtype));
+    HC_TRY(combine_sizes(a.tokens, a.top, a.rows, a.dim));
+    if (a.tokens && ((a.rows && !a.y) || !a.slots || !a.out)) return HC_ERR_INVALID_ARG;
+    const size_t es = elem_bytes(a.dtype), n = a.tokens * a.top;
+    Use u[4] = {};
+    HC_TRY(matrix(a.y, a.rows, a.dim, &a.y_stride, es, &u[0].m));
+    HC_TRY(vector(a.slots, n, sizeof(int32_t), &u[1].m));
+    if (a.weights) HC_TRY(vector(a.weights, n, elem_bytes(a.weight_dtype), &u[2].m));
+    HC_TRY(matrix(a.out, a.tokens, a.dim, &a.out_stride, es, &u[3].m));
+    u[3].write = true;
+    HC_TRY(check_overlaps(u, 4));
+    if (!a.tokens) return HC_OK;
+    const TraceRange range("hc_expert_combine", 0, (uint64_t)a.tokens);
+    return launch([&](int sms) { return launch_expert_combine(a, (cudaStream_t)stream, sms); });
+}
+
+hc_status_t hc_expert_combine_grad(const hc_expert_combine_grad_t* args, hc_stream_t stream) {
+    if (!args || args->struct_size < sizeof(hc_expert_combine_grad_t)) return HC_ERR_INVALID_ARG;
+    hc_expert_combine_grad_t a = *args;
+    HC_TRY(check_float(a.dtype));
+    if (a.weights || a.grad_weights) HC_TRY(check_float(a.weight_dtype));
+    HC_TRY(combine_sizes(a.tokens, a.top, a.rows, a.dim));
+    if (a.tokens && (!a.grad_out || !a.slots || (!a.grad_y && !a.grad_weights) || (a.rows && a.grad_weights && !a.y)))
+        return HC_ERR_INVALID_ARG;
+    const size_t es = elem_bytes(a.dtype), n = a.tokens * a.top;
+    Use u[6] = {};
+    HC_TRY(matrix(a.grad_out, a.tokens, a.dim, &a.grad_out_stride, es, &u[0].m));
+    HC_TRY(matrix(a.grad_weights ? a.y : nullptr, a.rows, a.dim, &a.y_stride, es, &u[1].m));
+    HC_TRY(vector(a.slots, n, sizeof(int32_t), &u[2].m));
+    if (a.weights) HC_TRY(vector(a.weights, n, elem_bytes(a.weight_dtype), &u[3].m));
+    HC_TRY(matrix(a.grad_y, a.rows, a.dim, &a.grad_y_stride, es, &u[4].m));
+    if (a.grad_weights) HC_TRY(vector(a.grad_weights, n, elem_bytes(a.weight_dtype), &u[5].m));
+    u[4].write = u[5].write = true;
+    u[1].in_place = u[4].in_place = true;
+    HC_TRY(check_overlaps(u, 6));
+    if (!a.tokens) return HC_OK;
+    const TraceRange range("hc_expert_combine_grad", 0, (uint64_t)a.tokens);
+    return launch([&](int sms) { return launch_expert_combine_grad(a, (cudaStream_t)stream, sms); });
+}
 
 }  // extern "C"

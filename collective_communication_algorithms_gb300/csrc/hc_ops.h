@@ -72,6 +72,27 @@ constexpr size_t kDistillMaxRowBytes = 3u << 19;
 enum DistillMode { DISTILL_LOSS = 0, DISTILL_BOTH = 1, DISTILL_GRAD = 2 };
 cudaError_t launch_distill(const hc_distill_t& a, DistillMode mode, cudaStream_t stream, int sms);
 
+size_t clip_scratch_bytes(const hc_clip_grads_t& a);  // 0 also for lists that no launch takes
+cudaError_t launch_clip(const hc_clip_grads_t& a, bool apply, cudaStream_t stream);
+
+constexpr size_t kMaxExperts = 1024;
+// How the plan's assignments are divided among blocks.
+struct ExpertPlanShape {
+    int64_t run;   // assignments of a block
+    int blocks;    // 1: no scratch, no counting kernel
+    size_t bytes;  // scratch
+};
+ExpertPlanShape expert_plan_shape(int64_t assignments, int64_t experts);
+cudaError_t launch_expert_plan(const hc_expert_plan_t& a, cudaStream_t stream);
+cudaError_t launch_expert_combine(const hc_expert_combine_t& a, cudaStream_t stream, int sms);
+cudaError_t launch_expert_combine_grad(const hc_expert_combine_grad_t& a, cudaStream_t stream, int sms);
+
+constexpr size_t kMaxExpertDim = 65536;
+size_t expert_matmul_scratch(const hc_expert_matmul_t& a);
+size_t expert_matmul_grad_scratch(const hc_expert_matmul_grad_t& a);
+cudaError_t launch_expert_matmul(const hc_expert_matmul_t& a, cudaStream_t stream, int sms);
+cudaError_t launch_expert_matmul_grad(const hc_expert_matmul_grad_t& a, cudaStream_t stream, int sms);
+
 // hc_api.cpp / hc_kernels.cu
 hc_status_t cuda_status(cudaError_t e);
 int sm_count_of_current_device();

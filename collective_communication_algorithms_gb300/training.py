@@ -1,7 +1,7 @@
 """Training operators on torch CUDA tensors: the embedding lookup, the norms
 and the gate at a block's boundary and the distillation loss, each with its
-gradient (include/hc.h, "Training operators").  They run on their tensors' GPU,
-whichever is current.
+gradient, and the clipping of gradients by their common norm (include/hc.h,
+"Training operators").  They run on their tensors' GPU, whichever is current.
 
 Every operator comes as a function that runs once and returns its outputs,
 and as bind_*, which returns a BoundCall with `.outputs` (a dict of tensors)
@@ -11,13 +11,14 @@ bound (or `stream`).  Outputs and scratch that are not passed are allocated by
 bind_*.  Matrices need unit column stride; rows may be strided.  Nothing here
 computes: the work happens in libhc's kernels.
 """
+import ctypes
 import functools
 
 from . import _binding as B
 
 __all__ = ["embedding", "embedding_grad", "block_norm", "block_norm_grad", "distill", "distill_grad",
            "bind_embedding", "bind_embedding_grad", "bind_block_norm", "bind_block_norm_grad",
-           "bind_distill", "bind_distill_grad"]
+           "bind_distill", "bind_distill_grad", "clip_grads", "grad_norm", "bind_clip_grads", "bind_grad_norm"]
 
 _FLOATS = {"torch.float32": "float32", "torch.bfloat16": "bfloat16"}
 _IDS = {"torch.int32": "int32", "torch.int64": "int64"}
@@ -353,6 +354,52 @@ def bind_distill_grad(logits, teacher_logits, teacher_ids, stats, row_weight=Non
                  (logits, teacher_logits, teacher_ids, row_weight, stats, grad), logits)
 
 
+def _clip(name, grads, out, norm, factor, scratch, stream, **kw):
+    import torch
+    grads = list(grads)
+    if not grads:
+        raise ValueError("no gradients")
+    first = grads[0]
+    if out is not None:
+        out = list(out)
+        if len(out) != len(grads):
+            raise ValueError("%d outputs for %d gradients" % (len(out), len(grads)))
+    table = (B.hc_grad_t * len(grads))()
+    for i, g in enumerate(grads):
+        _check("grads[%d]" % i, g, g.shape, device=first.device, contiguous=True)
+        table[i].in_, table[i].count, table[i].in_dtype = g.data_ptr(), g.numel(), B.DTYPES[_dtype(g)]
+        if out is not None:
+            o = _check("out[%d]" % i, out[i], g.shape, device=first.device, contiguous=True)
+            table[i].out, table[i].out_dtype = o.data_ptr(), B.DTYPES[_dtype(o)]
+    norm = _new(first, (1,), torch.float32) if norm is None else norm
+    _check("norm", norm, (1,), torch.float32, first.device, contiguous=True)
+    outputs = {"norm": norm}
+    if name == "hc_clip_grads":
+        factor = _new(first, (1,), torch.float32) if factor is None else factor
+        outputs["factor"] = _check("factor", factor, (1,), torch.float32, first.device, contiguous=True)
+        outputs["grads"] = grads if out is None else out
+    args = B.operator_args(name, tensors=ctypes.addressof(table), num=len(grads), norm=_ptr(norm), factor=_ptr(factor),
+                           **kw)
+    scratch = _scratch("hc_clip_grads", args, scratch, first)
+    return _bind(name, args, stream, outputs, (table, grads, scratch, outputs), first)
+
+
+@_on_stream
+def bind_clip_grads(grads, max_norm, out=None, norm=None, factor=None, scale=1.0, eps=1e-6, scratch=None, *,
+                    stream=None):
+    """The gradients (a sequence of contiguous tensors, bf16 and fp32 mixed as
+    they come) times scale * min(1, max_norm / (norm + eps)), where norm =
+    |scale| * the root of the sum of all their squares: in place, or into the
+    tensors of `out` (of either type)."""
+    return _clip("hc_clip_grads", grads, out, norm, factor, scratch, stream, scale=scale, max_norm=max_norm, eps=eps)
+
+
+@_on_stream
+def bind_grad_norm(grads, norm=None, scale=1.0, scratch=None, *, stream=None):
+    """|scale| * the root of the sum of all the gradients' squares."""
+    return _clip("hc_grad_norm", grads, None, norm, None, scratch, stream, scale=scale)
+
+
 def _once(bind, doc):
     def run(*args, **kw):
         call = bind(*args, **kw)
@@ -370,3 +417,5 @@ block_norm_grad = _once(bind_block_norm_grad, "One gradient of the block boundar
                                               "grad_post_weight, grad_gate, grad_pre_weight}.")
 distill = _once(bind_distill, "One distillation loss; returns {loss, stats, grad}.")
 distill_grad = _once(bind_distill_grad, "One gradient of the distillation loss; returns {grad}.")
+clip_grads = _once(bind_clip_grads, "Clips the gradients once; returns {norm, factor, grads}.")
+grad_norm = _once(bind_grad_norm, "Their norm alone; returns {norm}.")

@@ -522,6 +522,193 @@ typedef struct {
 hc_status_t hc_distill(const hc_distill_t* args, hc_stream_t stream);
 hc_status_t hc_distill_grad(const hc_distill_t* args, hc_stream_t stream);
 
+/*
+ * Gradient clipping: the norm over all elements of `num` gradients, and the
+ * gradients scaled by it,
+ *   norm   = |scale| * sqrt(sum of in^2)
+ *   factor = scale * min(1, max_norm / (norm + eps))
+ *   out[i] = factor * in[i]
+ * after an AllReduce of the gradients (scale = 1 / ranks makes a mean of its
+ * sum) or on the segments that a ReduceScatter left.
+ *  tensors  : host array, read during the call.  Every tensor has its own
+ *             types and size (0 elements: no part).  out == NULL stands for
+ *             in place; else out may be exactly `in` if the types are alike.
+ *             Outputs may overlap neither each other nor another input
+ *             (HC_ERR_INVALID_ARG): a tensor that is listed twice is refused
+ *             in hc_clip_grads, and counts twice in hc_grad_norm.
+ *  norm     : one binary32; factor: one binary32, NULL: not kept.
+ *  max_norm : above 0; infinity: no limit.  eps at least 0.
+ * Tensors clipped in place are left alone when factor is exactly 1.  A NaN
+ * among the inputs, or an infinite norm's factor of 0 times its infinities,
+ * spreads as in the formula.  Squares are summed so that no finite input
+ * overflows or vanishes on the way.
+ * hc_grad_norm writes norm alone; outputs, max_norm, eps and factor have no
+ * part.
+ */
+typedef struct {
+    const void* in;
+    void* out;
+    size_t count;
+    hc_dtype_t in_dtype, out_dtype;
+} hc_grad_t;
+typedef struct {
+    size_t struct_size;
+    const hc_grad_t* tensors;
+    float* norm;
+    float* factor;
+    void* scratch;
+    size_t scratch_bytes;
+    size_t num;
+    float scale, max_norm, eps;
+} hc_clip_grads_t;
+hc_status_t hc_clip_grads(const hc_clip_grads_t* args, hc_stream_t stream);
+hc_status_t hc_grad_norm(const hc_clip_grads_t* args, hc_stream_t stream);
+/* Scratch bytes of both (args->tensors is read for its counts). */
+size_t hc_clip_grads_scratch_bytes(const hc_clip_grads_t* args);
+
+/*
+ * Expert layer
+ * ------------
+ * Tokens are sent to the experts that a router chose for them (`top` each),
+ * every expert's weight is multiplied with its own tokens' rows, and the
+ * weighted rows of a token are summed.  "Rows" below are the assignments
+ * (token, choice) sorted by expert: those of local expert e are
+ * offsets[e] .. offsets[e + 1] - 1.
+ *
+ * hc_expert_plan sorts the assignments, those of one expert in order of
+ * token, then choice:
+ *  expert_ids : tokens x top; local expert of an assignment is
+ *               expert_ids[t][j] - first_expert (one rank's share of the
+ *               experts); ids outside [0, experts) (experts elsewhere,
+ *               negative: padding) have no row.
+ *  offsets    : experts + 1 int32
+ *  row_tokens : tokens * top int32: the token of each row, -1 behind the last
+ *               row.  hc_embedding with the activations as the table and these
+ *               as its ids gathers the rows.
+ *  slots      : tokens x top int32: the row of each assignment, -1 for none.
+ * experts at most 1024 (HC_ERR_UNSUPPORTED), tokens * top at most 2^31 - 1.
+ */
+typedef struct {
+    size_t struct_size;
+    const void* expert_ids;
+    int32_t* offsets;
+    int32_t* row_tokens;  /* NULL: not computed */
+    int32_t* slots;       /* NULL: not computed */
+    void* scratch;
+    size_t scratch_bytes;
+    size_t tokens, top, experts;
+    hc_id_t id_type;
+    int64_t first_expert;
+} hc_expert_plan_t;
+hc_status_t hc_expert_plan(const hc_expert_plan_t* args, hc_stream_t stream);
+size_t hc_expert_plan_scratch_bytes(const hc_expert_plan_t* args);
+
+/*
+ * Products of each expert's rows with its weight:
+ *   out[r] = weight[e] x[r]      for offsets[e] <= r < offsets[e + 1]
+ * weight is experts x out_dim x in_dim (weight_layout HC_WEIGHT_OUT_IN) or
+ * experts x in_dim x out_dim (HC_WEIGHT_IN_OUT).
+ * Rows in no group are not read, and are left as they were in out.  Offsets
+ * are clamped to [0, rows] and to non-decreasing order.
+ *  dtype     : x and weight; out_dtype: out.  Products of bf16 values are
+ *              exact and are summed in binary32 by the tensor cores; binary32
+ *              values are multiplied and summed in binary32 (no TF32).
+ *  experts at most 1024, rows at most 2^31 - 1, in_dim and out_dim at most
+ *  65536 (HC_ERR_UNSUPPORTED).
+ *  scratch   : bf16 operands whose pointers or strides are not whole 16 bytes
+ *              are copied into it first; 0 bytes are needed when all are.
+ */
+typedef enum { HC_WEIGHT_OUT_IN = 0, HC_WEIGHT_IN_OUT = 1 } hc_weight_layout_t;
+typedef struct {
+    size_t struct_size;
+    const void* x;           /* rows x in_dim */
+    const void* weight;
+    const int32_t* offsets;  /* experts + 1 */
+    void* out;               /* rows x out_dim */
+    void* scratch;
+    size_t scratch_bytes;
+    size_t rows, experts, in_dim, out_dim;
+    size_t x_stride, weight_stride, expert_stride, out_stride;  /* expert_stride: between experts' weights */
+    hc_dtype_t dtype, out_dtype;
+    hc_weight_layout_t weight_layout;
+} hc_expert_matmul_t;
+hc_status_t hc_expert_matmul(const hc_expert_matmul_t* args, hc_stream_t stream);
+size_t hc_expert_matmul_scratch_bytes(const hc_expert_matmul_t* args);
+
+/*
+ * Gradients of the products:
+ *   grad_x[r] = weight[e]^T grad_out[r]
+ *   grad_weight[e] (+)= sum over e's rows of grad_out[r] x[r]^T  (in weight's layout)
+ *  grad_x, grad_weight : either may be NULL (not computed); weight is only
+ *               read for grad_x, x only for grad_weight.
+ *  accumulate : 1: added to what grad_weight holds (in binary32, rounded
+ *               once); experts without rows are then left alone.  0: their
+ *               gradients are written as zeros.
+ */
+typedef struct {
+    size_t struct_size;
+    const void* grad_out;    /* rows x out_dim */
+    const void* x;           /* rows x in_dim */
+    const void* weight;
+    const int32_t* offsets;
+    void* grad_x;            /* rows x in_dim */
+    void* grad_weight;
+    void* scratch;
+    size_t scratch_bytes;
+    size_t rows, experts, in_dim, out_dim;
+    size_t grad_out_stride, x_stride, weight_stride, expert_stride, grad_x_stride, grad_weight_stride,
+        grad_expert_stride;
+    hc_dtype_t dtype;        /* grad_out, x, weight, grad_x */
+    hc_dtype_t grad_weight_dtype;
+    hc_weight_layout_t weight_layout;
+    int accumulate;
+} hc_expert_matmul_grad_t;
+hc_status_t hc_expert_matmul_grad(const hc_expert_matmul_grad_t* args, hc_stream_t stream);
+size_t hc_expert_matmul_grad_scratch_bytes(const hc_expert_matmul_grad_t* args);
+
+/*
+ * Back from the experts' rows to the tokens:
+ *   out[t] = sum over j of weights[t][j] * y[slots[t][j]]
+ * Slots outside [0, rows) have no part, whatever weight they have.  weights
+ * NULL stands for ones: the gradient of the gather of the rows.
+ */
+typedef struct {
+    size_t struct_size;
+    const void* y;           /* rows x dim */
+    const int32_t* slots;    /* tokens x top */
+    const void* weights;     /* tokens x top */
+    void* out;               /* tokens x dim */
+    size_t tokens, top, rows, dim;
+    size_t y_stride, out_stride;
+    hc_dtype_t dtype;        /* y, out */
+    hc_dtype_t weight_dtype;
+} hc_expert_combine_t;
+hc_status_t hc_expert_combine(const hc_expert_combine_t* args, hc_stream_t stream);
+
+/*
+ * Its gradient:
+ *   grad_y[slots[t][j]] = weights[t][j] * grad_out[t]
+ *   grad_weights[t][j]  = <grad_out[t], y[slots[t][j]]>, 0 for no row
+ *  grad_y       : rows that no slot names are left as they were; may be
+ *                 exactly y in place.  No row may be named twice (such rows
+ *                 hold one of the products).  NULL: not computed.
+ *  grad_weights : NULL: not computed, and y is not read.
+ */
+typedef struct {
+    size_t struct_size;
+    const void* grad_out;    /* tokens x dim */
+    const void* y;
+    const int32_t* slots;
+    const void* weights;
+    void* grad_y;            /* rows x dim */
+    void* grad_weights;      /* tokens x top */
+    size_t tokens, top, rows, dim;
+    size_t grad_out_stride, y_stride, grad_y_stride;
+    hc_dtype_t dtype;
+    hc_dtype_t weight_dtype;
+} hc_expert_combine_grad_t;
+hc_status_t hc_expert_combine_grad(const hc_expert_combine_grad_t* args, hc_stream_t stream);
+
 /* Segment k's element range (see the layout rule above).  k < S, where
  * S = hc_num_segments(algo, coll, P). */
 hc_status_t hc_segment_range(hc_algo_t algo, hc_coll_t coll, int P, size_t count,
