@@ -10,7 +10,7 @@
 // the rows are what is summed along, and every expert has all of its tiles.
 #include <algorithm>
 
-#include "hc_ops.cuh"
+#include "hc_tensor.cuh"
 
 namespace hc {
 namespace {
@@ -90,19 +90,18 @@ struct PlainParams {
 
 constexpr int kPT = 128, kPK = 16, kPThreads = 256, kPPad = 4;
 
-template <class T>
-__device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&v)[8]) {
+__device__ __forceinline__ void load8(const float* p, int n, bool vec, float (&v)[8]) {
     if (vec && n >= 8) {
-        load_n<T, 8>(p, 8, v);
+        load_n<float, 8>(p, 8, v);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = i < n ? to_f32(p[i]) : 0.0f;
+        for (int i = 0; i < 8; i++) v[i] = i < n ? p[i] : 0.0f;
     }
 }
 
 // ROWS: the first two products, whose sums run along a's rows; b is summed
 // along its rows (BK) or across them.
-template <class T, class TO, bool ROWS, bool BK>
+template <class TO, bool ROWS, bool BK>
 __global__ void __launch_bounds__(kPThreads) plain_product_kernel(const PlainParams p) {
     __shared__ __align__(16) float as[kPK][kPT + kPPad], bs[kPK][kPT + kPPad];
     __shared__ int bound[kMaxExperts + 1], tile[kMaxExperts + 1];
@@ -133,8 +132,8 @@ __global__ void __launch_bounds__(kPThreads) plain_product_kernel(const PlainPar
             if (!K && p.accumulate) continue;
         }
         const int nlen = min(kPT, p.N - n0);
-        const T* a = (const T*)p.a + first * p.a_stride + m0;
-        const T* b = (const T*)p.b + (ROWS ? e * p.b_expert + (BK ? (int64_t)n0 * p.b_stride : n0)
+        const float* a = (const float*)p.a + first * p.a_stride + m0;
+        const float* b = (const float*)p.b + (ROWS ? e * p.b_expert + (BK ? (int64_t)n0 * p.b_stride : n0)
                                            : first * p.b_stride + n0);
         // places of this thread's 8 elements: along k (row, k) or along m (k, column)
         const int kr = tid / 2, kc = (tid % 2) * 8, mr = tid / 16, mc = (tid % 16) * 8;
@@ -192,91 +191,569 @@ __global__ void __launch_bounds__(kPThreads) plain_product_kernel(const PlainPar
     }
 }
 
+// ---------------------------------------------------------------------------
+// bf16 products on the tensor cores
+//
+// A block has an SM to itself and takes tiles of 128 x TN sums in turn.  One
+// thread starts tiled copies of 64 steps of the sum into a ring of stages, one
+// thread issues the products of each stage, and four warps bring finished sums
+// from tensor memory through shared memory to the output while the next
+// tile's products run (two sets of sums).
+//
+// A tile that reaches beyond its group (ragged rows) multiplies rows of the
+// next group too and does not store them: sums of different rows have nothing
+// to do with each other.  In the weights' gradient the rows are what is summed
+// along, so those behind the group's last are overwritten with zeros in shared
+// memory, by a warp of their own, before the products may start.
+// ---------------------------------------------------------------------------
+constexpr int kTM = 128, kTK = 64, kTThreads = 256;
+constexpr int kTStagingBytes = 4 * 32 * 128;
+template <int TN>
+constexpr int kTStages = TN == 256 ? 4 : 6;
+template <int TN>
+constexpr int kTStageBytes = (kTM + TN) * kTK * 2;
+
+struct TensorParams {
+    CUtensorMap a, b;
+    void* out;
+    const int32_t* offsets;
+    int64_t rows, out_stride, out_expert;
+    int E, M, N, K;           // M: weights' gradient's rows; K: of the first two products
+    int accumulate, out_vec;  // out: whole 16 bytes
+    int* err;
+    unsigned long long wait_ns;
+    int hold;                 // wait-expiry test mode
+};
+
+template <int TN>
+struct TensorBarriers {
+    uint64_t full[kTStages<TN>], empty[kTStages<TN>], raw[kTStages<TN>];  // raw: landed, to be overwritten in part
+    uint64_t sums_full[2], sums_empty[2], drain;
+    uint32_t tmem;
+};
+template <int TN>
+constexpr int kTSmem = 1024 + kTStages<TN> * kTStageBytes<TN> + kTStagingBytes + (int)sizeof(TensorBarriers<TN>) + 8;
+
+struct TensorTile {
+    int e, m0, mlen, n0, nlen, K;
+    int64_t first;  // ROWS: the tile's first row; else the group's
+};
+template <bool ROWS, int TN>
+__device__ __forceinline__ TensorTile tensor_tile(const TensorParams& p, const int* bound, const int* tile, int64_t i, int nt) {
+    TensorTile t;
+    const int m = (int)(i / nt);
+    t.n0 = (int)(i - (int64_t)m * nt) * TN;
+    t.nlen = min(TN, p.N - t.n0);
+    if (ROWS) {
+        t.e = group_of(tile, p.E, m);
+        t.first = bound[t.e] + (int64_t)(m - tile[t.e]) * kTM;
+        t.m0 = 0;
+        t.mlen = (int)min((int64_t)kTM, bound[t.e + 1] - t.first);
+        t.K = p.K;
+    } else {
+        const int per = (p.M + kTM - 1) / kTM;
+        t.e = m / per;
+        t.m0 = (m - t.e * per) * kTM;
+        t.mlen = min(kTM, p.M - t.m0);
+        t.first = bound[t.e];
+        t.K = bound[t.e + 1] - bound[t.e];
+    }
+    return t;
+}
+
+// V elements at p, of which n are in range.
+template <class T, int V>
+__device__ __forceinline__ void load_v(const T* p, int n, bool vec, float (&v)[V]) {
+    if (vec && n >= V) {
+        load_n<T, V>(p, V, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i++) v[i] = i < n ? to_f32(p[i]) : 0.0f;
+    }
+}
+template <class T, int V>
+__device__ __forceinline__ void store_v(T* p, int n, bool vec, const float (&v)[V]) {
+    if (vec && n >= V) {
+        store_n<T, V>(p, V, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i++)
+            if (i < n) put(p + i, v[i]);
+    }
+}
+
+// ROWS, BK: as in the plain kernel.
+template <bool ROWS, bool BK, int TN, class TO>
+__global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __grid_constant__ TensorParams p) {
+    constexpr int S = kTStages<TN>, STAGE = kTStageBytes<TN>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ int bound[kMaxExperts + 1], tile[kMaxExperts + 1];
+    unsigned char* stages = smem + (1024 - (smem_addr(smem) & 1023)) % 1024;
+    unsigned char* staging = stages + S * STAGE;
+    TensorBarriers<TN>& bar = *(TensorBarriers<TN>*)(staging + kTStagingBytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int s = 0; s < S; s++) {
+            mbar_init(&bar.full[s], 1 + p.hold);
+            mbar_init(&bar.empty[s], 1);
+            mbar_init(&bar.raw[s], 1);
+        }
+        for (int s = 0; s < 2; s++) {
+            mbar_init(&bar.sums_full[s], 1);
+            mbar_init(&bar.sums_empty[s], 4);
+        }
+        mbar_init(&bar.drain, 1);
+        mbar_init_fence();
+        prefetch_map(&p.a);
+        prefetch_map(&p.b);
+    }
+    if (warp == 2) tmem_alloc(&bar.tmem, 2 * TN);
+    grid_wait();
+    grid_release();
+    if (warp == 3) read_groups(p.offsets, p.E, p.rows, kTM, bound, tile);
+    tensor_fence_before();
+    __syncthreads();
+    tensor_fence_after();
+    const uint32_t tmem = bar.tmem;
+    const int nt = (p.N + TN - 1) / TN;
+    const int64_t tiles = (ROWS ? (int64_t)tile[p.E] : (int64_t)((p.M + kTM - 1) / kTM) * p.E) * nt;
+    const auto expired = [&] { atomicExch(p.err, (int)HC_ERR_TIMEOUT); };
+
+    if (warp == 0 && lane == 0) {  // copies
+        int64_t it = 0;
+        uint32_t raw_used = 0;  // stages whose last copies went to raw
+        uint32_t raw_phase = 0;
+        bool ok = true;
+        for (int64_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
+            const TensorTile t = tensor_tile<ROWS, TN>(p, bound, tile, i, nt);
+            for (int k0 = 0; k0 < t.K; k0 += kTK, it++) {
+                const int s = (int)(it % S);
+                if (!mbar_wait_quick(&bar.empty[s], ((uint32_t)(it / S) & 1) ^ 1, p.wait_ns)) {
+                    expired();
+                    ok = false;
+                    break;
+                }
+                unsigned char* a = stages + s * STAGE;
+                unsigned char* b = a + kTM * kTK * 2;
+                const bool part = !ROWS && t.K - k0 < kTK;
+                uint64_t* to = part ? &bar.raw[s] : &bar.full[s];
+                if (part) raw_used |= 1u << s, raw_phase ^= 1u << s;
+                else raw_used &= ~(1u << s);
+                mbar_arrive_expect_tx(to, STAGE);
+                if (ROWS) {
+                    tile_g2s(a, &p.a, k0, (int)t.first, to);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kTM / 64; j++) tile_g2s(a + j * 8192, &p.a, t.m0 + 64 * j, (int)t.first + k0, to);
+                }
+                if (ROWS && BK) {
+                    tile_g2s(b, &p.b, k0, t.n0, t.e, to);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < TN / 64; j++) {
+                        if (ROWS) tile_g2s(b + j * 8192, &p.b, t.n0 + 64 * j, k0, t.e, to);
+                        else tile_g2s(b + j * 8192, &p.b, t.n0 + 64 * j, (int)t.first + k0, to);
+                    }
+                }
+            }
+        }
+        // a block does not leave while copies into its shared memory are under way
+        const int64_t n = it < S ? it : S;
+        for (int64_t j = it - n; j < it; j++) {
+            const int s = (int)(j % S);
+            if (raw_used >> s & 1) {
+                mbar_wait_quick(&bar.raw[s], (raw_phase >> s & 1) ^ 1, kWaitLimitNs);
+            } else {
+                if (p.hold) mbar_arrive(&bar.full[s]);
+                mbar_wait_quick(&bar.full[s], (uint32_t)(j / S) & 1, kWaitLimitNs);
+            }
+        }
+    } else if (warp == 1 && lane == 0) {  // products
+        constexpr uint32_t shape = product_shape(!ROWS, !BK, kTM, TN);
+        int64_t it = 0;
+        uint32_t n = 0;
+        bool ok = true;
+        for (int64_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
+            const TensorTile t = tensor_tile<ROWS, TN>(p, bound, tile, i, nt);
+            if (!t.K) continue;
+            const uint32_t set = n & 1;
+            if (!(ok = mbar_wait_quick(&bar.sums_empty[set], ((n >> 1) & 1) ^ 1, p.wait_ns))) break;
+            tensor_fence_after();
+            for (int k0 = 0; k0 < t.K; k0 += kTK, it++) {
+                const int s = (int)(it % S);
+                if (!(ok = mbar_wait_quick(&bar.full[s], (uint32_t)(it / S) & 1, p.wait_ns))) break;
+                tensor_fence_after();
+                const uint32_t a = smem_addr(stages + s * STAGE), b = a + kTM * kTK * 2;
+                const int steps = (min(kTK, t.K - k0) + 15) / 16;
+                for (int j = 0; j < steps; j++) {
+                    const uint64_t da = ROWS ? operand_along(a + 32 * j) : operand_across(a + 2048 * j, 8192);
+                    const uint64_t db = BK ? operand_along(b + 32 * j) : operand_across(b + 2048 * j, 8192);
+                    product16(tmem + set * TN, da, db, shape, k0 > 0 || j > 0);
+                }
+                products_arrive(&bar.empty[s]);
+            }
+            if (!ok) break;
+            products_arrive(&bar.sums_full[set]);
+            n++;
+        }
+        if (!ok) expired();
+        products_arrive(&bar.drain);  // tensor memory is freed after the last products
+        mbar_wait_quick(&bar.drain, 0, kWaitLimitNs);
+    } else if (!ROWS && warp == 3) {  // zeros behind the last row of a group
+        int64_t it = 0;
+        uint32_t phase = 0;
+        for (int64_t i = blockIdx.x; i < tiles; i += gridDim.x) {
+            const TensorTile t = tensor_tile<ROWS, TN>(p, bound, tile, i, nt);
+            it += (t.K + kTK - 1) / kTK;
+            const int rest = t.K % kTK;
+            if (!rest) continue;
+            const int s = (int)((it - 1) % S);
+            if (!mbar_wait_quick(&bar.raw[s], phase >> s & 1, p.wait_ns)) {
+                if (lane == 0) expired();
+                break;
+            }
+            phase ^= 1u << s;
+            const int zeros = (16 - rest % 16) % 16 * 8;  // rows that a product reads, 16 bytes each
+            for (int j = lane; j < zeros * ((kTM + TN) / 64); j += 32)
+                *(uint4*)(stages + s * STAGE + j / zeros * 8192 + rest * 128 + j % zeros * 16) = make_uint4(0, 0, 0, 0);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.full[s]);
+        }
+    } else if (warp >= 4) {  // sums to the output
+        constexpr int V = 16 / (int)sizeof(TO), PER = 32 / V;  // elements of a lane, lanes of 32 columns
+        const int q = warp - 4;
+        unsigned char* mine = staging + q * 32 * 128;
+        uint32_t n = 0;
+        for (int64_t i = blockIdx.x; i < tiles; i += gridDim.x) {
+            const TensorTile t = tensor_tile<ROWS, TN>(p, bound, tile, i, nt);
+            if (!t.K && p.accumulate) continue;
+            const uint32_t set = n & 1;
+            if (t.K) {
+                if (!mbar_wait_quick(&bar.sums_full[set], n >> 1 & 1, p.wait_ns)) {
+                    if (lane == 0) expired();
+                    break;
+                }
+                tensor_fence_after();
+                n++;
+            }
+            TO* out = (TO*)p.out + (ROWS ? t.first * p.out_stride : t.e * p.out_expert + (int64_t)t.m0 * p.out_stride) + t.n0;
+            const int rows = t.mlen - q * 32;  // of this warp
+            for (int c = 0; c < TN; c += 32) {
+                uint32_t v[32];
+                if (t.K) {
+                    __syncwarp();
+                    tmem_load32(tmem + ((uint32_t)(q * 32) << 16) + set * TN + c, v);
+                    tmem_load_wait();
+                    if (c + 32 == TN || c + 32 >= t.nlen) {
+                        tensor_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.sums_empty[set]);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; j++) v[j] = 0;
+                }
+                __syncwarp();  // the stores of the columns before have been read
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    *(uint4*)(mine + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 32 / V; j++) {
+                    const int r = j * V + lane / PER, at = lane % PER * V;
+                    float x[V];
+#pragma unroll
+                    for (int h = 0; h < V / 4; h++) {
+                        const uint4 w = *(const uint4*)(mine + r * 128 + (((at / 4 + h) ^ (r & 7)) << 4));
+                        x[4 * h] = __uint_as_float(w.x);
+                        x[4 * h + 1] = __uint_as_float(w.y);
+                        x[4 * h + 2] = __uint_as_float(w.z);
+                        x[4 * h + 3] = __uint_as_float(w.w);
+                    }
+                    const int left = t.nlen - c - at;
+                    if (r >= rows || left <= 0) continue;
+                    TO* to = out + (int64_t)(q * 32 + r) * p.out_stride + c + at;
+                    if (!ROWS && p.accumulate) {
+                        float old[V];
+                        load_v<TO, V>(to, left, p.out_vec, old);
+#pragma unroll
+                        for (int h = 0; h < V; h++) x[h] += old[h];
+                    }
+                    store_v<TO, V>(to, left, p.out_vec, x);
+                }
+                if (c + 32 >= t.nlen) break;
+            }
+        }
+    }
+    __syncwarp();
+    tensor_fence_before();
+    __syncthreads();
+    tensor_fence_after();
+    if (warp == 2) tmem_free(tmem, 2 * TN);
+}
+
 bool whole(const void* p, size_t stride, size_t expert, int es) {
     return (uintptr_t)p % 16 == 0 && stride * es % 16 == 0 && expert * es % 16 == 0;
 }
 
-template <class T, class TO, bool ROWS, bool BK>
+template <class TO, bool ROWS, bool BK>
 cudaError_t launch_plain(PlainParams p, cudaStream_t stream, int sms) {
     const int64_t nt = (p.N + kPT - 1) / kPT;
     const int64_t mt = ROWS ? p.rows / kPT + std::min<int64_t>(p.E, p.rows) + 1 : (int64_t)((p.M + kPT - 1) / kPT) * p.E;
     const int64_t grid = std::min<int64_t>(mt * nt, (int64_t)sms * 2);
     void* args[] = {&p};
-    return launch_op((const void*)plain_product_kernel<T, TO, ROWS, BK>, dim3((unsigned)grid), dim3(kPThreads), args, 0, stream);
+    return launch_op((const void*)plain_product_kernel<TO, ROWS, BK>, dim3((unsigned)grid), dim3(kPThreads), args, 0, stream);
 }
 template <bool ROWS, bool BK>
-cudaError_t launch_plain(const PlainParams& p, hc_dtype_t in, hc_dtype_t out, cudaStream_t stream, int sms) {
-    if (in == HC_BFLOAT16)
-        return out == HC_BFLOAT16 ? launch_plain<Bf16, Bf16, ROWS, BK>(p, stream, sms)
-                                  : launch_plain<Bf16, float, ROWS, BK>(p, stream, sms);
-    return out == HC_BFLOAT16 ? launch_plain<float, Bf16, ROWS, BK>(p, stream, sms)
-                              : launch_plain<float, float, ROWS, BK>(p, stream, sms);
+cudaError_t launch_plain(const PlainParams& p, hc_dtype_t out, cudaStream_t stream, int sms) {
+    return out == HC_BFLOAT16 ? launch_plain<Bf16, ROWS, BK>(p, stream, sms) : launch_plain<float, ROWS, BK>(p, stream, sms);
+}
+
+// ---------------------------------------------------------------------------
+// operands that tiled copies cannot take (pointers or strides that are not
+// whole 16 bytes) are copied row by row into scratch first
+// ---------------------------------------------------------------------------
+struct PackParams {
+    const Bf16* from;
+    Bf16* to;
+    int64_t rows, per;          // rows in all, rows of one expert
+    int64_t stride, expert;     // of `from`
+    int cols, pitch;            // pitch: of `to`
+};
+constexpr int kPackThreads = 256;
+__global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackParams p) {
+    grid_wait();
+    grid_release();
+    const int lane = threadIdx.x & 31;
+    for (int64_t r = (int64_t)blockIdx.x * (kPackThreads / 32) + threadIdx.x / 32; r < p.rows;
+         r += (int64_t)gridDim.x * (kPackThreads / 32)) {
+        const Bf16* from = p.from + r / p.per * p.expert + r % p.per * p.stride;
+        Bf16* to = p.to + r * p.pitch;
+#pragma unroll 8
+        for (int c = lane; c < p.cols; c += 32) to[c] = from[c];
+    }
+}
+
+// A bf16 operand of the tensor cores: `experts` times `rows` rows of `cols`.
+struct Operand {
+    const void* p;
+    int64_t experts, rows, cols, stride, expert;
+    bool aligned() const { return (uintptr_t)p % 16 == 0 && stride % 8 == 0 && expert % 8 == 0; }
+    int64_t pitch() const { return (cols + 7) / 8 * 8; }
+    size_t packed_bytes() const { return (size_t)(experts * rows * pitch() * 2 + 255) / 256 * 256; }
+};
+
+cudaError_t pack(Operand& x, unsigned char*& scratch, cudaStream_t stream, int sms) {
+    if (x.aligned()) return cudaSuccess;
+    PackParams p;
+    p.from = (const Bf16*)x.p;
+    p.to = (Bf16*)scratch;
+    p.rows = x.experts * x.rows;
+    p.per = x.rows;
+    p.stride = x.stride;
+    p.expert = x.expert;
+    p.cols = (int)x.cols;
+    p.pitch = (int)x.pitch();
+    scratch += x.packed_bytes();
+    x.p = p.to;
+    x.stride = p.pitch;
+    x.expert = x.rows * p.pitch;
+    if (!p.rows) return cudaSuccess;
+    const int64_t blocks = std::min<int64_t>((p.rows + 7) / 8, (int64_t)sms * 8);
+    void* args[] = {&p};
+    return launch_op((const void*)pack_kernel, dim3((unsigned)blocks), dim3(kPackThreads), args, 0, stream);
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return (EncodeTiled)f;
+    }();
+    return fn;
+}
+// Boxes of box_rows rows of 64 columns; what lies outside reads as zeros.
+cudaError_t describe(CUtensorMap* map, const Operand& x, int box_rows, bool experts) {
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)x.cols, (cuuint64_t)std::max<int64_t>(1, x.rows), (cuuint64_t)x.experts};
+    const cuuint64_t strides[2] = {(cuuint64_t)x.stride * 2, (cuuint64_t)x.expert * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, experts ? 3 : 2, const_cast<void*>(x.p), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
+template <bool ROWS, bool BK, int TN, class TO>
+cudaError_t launch_tensor(TensorParams& p, const Operand& a, const Operand& b, cudaStream_t stream, int sms) {
+    cudaError_t e = describe(&p.a, a, ROWS ? kTM : kTK, false);
+    if (e == cudaSuccess) e = describe(&p.b, b, ROWS && BK ? TN : kTK, ROWS);
+    if (e != cudaSuccess) return e;
+    p.err = device_error_flag();
+    if (!p.err) return cudaErrorInvalidValue;
+    p.hold = expiring_waits() ? 1 : 0;
+    p.wait_ns = p.hold ? kTestWaitLimitNs : kWaitLimitNs;
+    const void* fn = (const void*)tensor_product_kernel<ROWS, BK, TN, TO>;
+    if (!allow_smem((void*)fn, kTSmem<TN>)) return cudaErrorInvalidValue;
+    const int64_t nt = (p.N + TN - 1) / TN;
+    const int64_t mt = ROWS ? p.rows / kTM + std::min<int64_t>(p.E, p.rows) + 1 : (int64_t)((p.M + kTM - 1) / kTM) * p.E;
+    void* args[] = {&p};
+    return launch_op(fn, dim3((unsigned)std::min<int64_t>(mt * nt, sms)), dim3(kTThreads), args, kTSmem<TN>, stream);
+}
+template <bool ROWS, bool BK>
+cudaError_t launch_tensor(TensorParams& p, const Operand& a, const Operand& b, hc_dtype_t out, cudaStream_t stream, int sms) {
+    // Wider tiles read less for each product, narrower ones are more in number:
+    // the wider, unless they leave SMs without a tile.
+    const int64_t mt = ROWS ? (p.rows + kTM - 1) / kTM : (int64_t)((p.M + kTM - 1) / kTM) * p.E;
+    const bool wide = p.N > 128 && mt * ((p.N + 255) / 256) >= sms;
+    if (out == HC_BFLOAT16)
+        return wide ? launch_tensor<ROWS, BK, 256, Bf16>(p, a, b, stream, sms) : launch_tensor<ROWS, BK, 128, Bf16>(p, a, b, stream, sms);
+    return wide ? launch_tensor<ROWS, BK, 256, float>(p, a, b, stream, sms) : launch_tensor<ROWS, BK, 128, float>(p, a, b, stream, sms);
+}
+
+Operand rows_operand(const void* p, size_t rows, size_t cols, size_t stride) {
+    // a single row has no next one: any stride will do
+    return Operand{p, 1, (int64_t)rows, (int64_t)cols, rows > 1 ? (int64_t)stride : ((int64_t)cols + 7) / 8 * 8, 0};
+}
+Operand weight_operand(const void* p, size_t experts, size_t in, size_t out, hc_weight_layout_t layout, size_t stride, size_t expert) {
+    const bool out_in = layout == HC_WEIGHT_OUT_IN;
+    return Operand{p, (int64_t)experts, (int64_t)(out_in ? out : in), (int64_t)(out_in ? in : out), (int64_t)stride, (int64_t)expert};
+}
+size_t packed(const Operand& x) { return x.aligned() ? 0 : x.packed_bytes(); }
+
+// The first two products: rows of `a` times the weight, which is summed along
+// its own rows (along) or across them.
+cudaError_t rows_product(Operand a, Operand w, bool along, void* out, size_t out_stride, size_t N, hc_dtype_t in, hc_dtype_t to,
+                         const int32_t* offsets, unsigned char*& scratch, cudaStream_t stream, int sms) {
+    if (in == HC_FLOAT32) {
+        PlainParams p = {};
+        p.a = a.p;
+        p.b = w.p;
+        p.out = out;
+        p.offsets = offsets;
+        p.rows = a.rows;
+        p.a_stride = a.stride;
+        p.b_stride = w.stride;
+        p.b_expert = w.expert;
+        p.out_stride = (int64_t)out_stride;
+        p.E = (int)w.experts;
+        p.N = (int)N;
+        p.K = (int)a.cols;
+        p.a_vec = whole(a.p, (size_t)a.stride, 0, 4);
+        p.b_vec = whole(w.p, (size_t)w.stride, (size_t)w.expert, 4);
+        return along ? launch_plain<true, true>(p, to, stream, sms) : launch_plain<true, false>(p, to, stream, sms);
+    }
+    cudaError_t e = pack(a, scratch, stream, sms);
+    if (e == cudaSuccess) e = pack(w, scratch, stream, sms);
+    if (e != cudaSuccess) return e;
+    TensorParams p;
+    p.out = out;
+    p.offsets = offsets;
+    p.rows = a.rows;
+    p.out_stride = (int64_t)out_stride;
+    p.out_expert = 0;
+    p.E = (int)w.experts;
+    p.M = 0;
+    p.N = (int)N;
+    p.K = (int)a.cols;
+    p.accumulate = 0;
+    p.out_vec = whole(out, out_stride, 0, elem_bytes(to));
+    return along ? launch_tensor<true, true>(p, a, w, to, stream, sms) : launch_tensor<true, false>(p, a, w, to, stream, sms);
 }
 
 }  // namespace
 
-size_t expert_matmul_scratch(const hc_expert_matmul_t&) { return 0; }
-size_t expert_matmul_grad_scratch(const hc_expert_matmul_grad_t&) { return 0; }
+size_t expert_matmul_scratch(const hc_expert_matmul_t& a) {
+    if (a.dtype != HC_BFLOAT16 || !a.rows) return 0;
+    return packed(rows_operand(a.x, a.rows, a.in_dim, a.x_stride)) +
+           packed(weight_operand(a.weight, a.experts, a.in_dim, a.out_dim, a.weight_layout, a.weight_stride, a.expert_stride));
+}
+
+size_t expert_matmul_grad_scratch(const hc_expert_matmul_grad_t& a) {
+    if (a.dtype != HC_BFLOAT16 || !a.rows) return 0;
+    size_t n = packed(rows_operand(a.grad_out, a.rows, a.out_dim, a.grad_out_stride));
+    if (a.grad_x)
+        n += packed(weight_operand(a.weight, a.experts, a.in_dim, a.out_dim, a.weight_layout, a.weight_stride, a.expert_stride));
+    if (a.grad_weight) n += packed(rows_operand(a.x, a.rows, a.in_dim, a.x_stride));
+    return n;
+}
 
 cudaError_t launch_expert_matmul(const hc_expert_matmul_t& a, cudaStream_t stream, int sms) {
-    PlainParams p = {};
-    const int es = elem_bytes(a.dtype);
-    p.a = a.x;
-    p.b = a.weight;
-    p.out = a.out;
-    p.offsets = a.offsets;
-    p.rows = (int64_t)a.rows;
-    p.a_stride = (int64_t)a.x_stride;
-    p.b_stride = (int64_t)a.weight_stride;
-    p.b_expert = (int64_t)a.expert_stride;
-    p.out_stride = (int64_t)a.out_stride;
-    p.E = (int)a.experts;
-    p.N = (int)a.out_dim;
-    p.K = (int)a.in_dim;
-    p.a_vec = whole(a.x, a.x_stride, 0, es);
-    p.b_vec = whole(a.weight, a.weight_stride, a.expert_stride, es);
-    return a.weight_layout == HC_WEIGHT_OUT_IN ? launch_plain<true, true>(p, a.dtype, a.out_dtype, stream, sms)
-                                               : launch_plain<true, false>(p, a.dtype, a.out_dtype, stream, sms);
+    unsigned char* scratch = (unsigned char*)a.scratch;
+    return rows_product(rows_operand(a.x, a.rows, a.in_dim, a.x_stride),
+                        weight_operand(a.weight, a.experts, a.in_dim, a.out_dim, a.weight_layout, a.weight_stride, a.expert_stride),
+                        a.weight_layout == HC_WEIGHT_OUT_IN, a.out, a.out_stride, a.out_dim, a.dtype, a.out_dtype, a.offsets,
+                        scratch, stream, sms);
 }
 
 cudaError_t launch_expert_matmul_grad(const hc_expert_matmul_grad_t& a, cudaStream_t stream, int sms) {
-    const int es = elem_bytes(a.dtype);
-    PlainParams p = {};
-    p.offsets = a.offsets;
-    p.rows = (int64_t)a.rows;
-    p.E = (int)a.experts;
+    unsigned char* scratch = (unsigned char*)a.scratch;
+    const bool out_in = a.weight_layout == HC_WEIGHT_OUT_IN;
+    Operand go = rows_operand(a.grad_out, a.rows, a.out_dim, a.grad_out_stride);
+    if (a.dtype == HC_BFLOAT16 && a.rows) {  // once for both products
+        const cudaError_t e = pack(go, scratch, stream, sms);
+        if (e != cudaSuccess) return e;
+    }
     if (a.grad_x && a.rows) {
-        p.a = a.grad_out;
-        p.b = a.weight;
-        p.out = a.grad_x;
-        p.a_stride = (int64_t)a.grad_out_stride;
-        p.b_stride = (int64_t)a.weight_stride;
-        p.b_expert = (int64_t)a.expert_stride;
-        p.out_stride = (int64_t)a.grad_x_stride;
-        p.N = (int)a.in_dim;
-        p.K = (int)a.out_dim;
-        p.a_vec = whole(a.grad_out, a.grad_out_stride, 0, es);
-        p.b_vec = whole(a.weight, a.weight_stride, a.expert_stride, es);
-        const cudaError_t e = a.weight_layout == HC_WEIGHT_OUT_IN
-                                  ? launch_plain<true, false>(p, a.dtype, a.dtype, stream, sms)
-                                  : launch_plain<true, true>(p, a.dtype, a.dtype, stream, sms);
+        const cudaError_t e =
+            rows_product(go, weight_operand(a.weight, a.experts, a.in_dim, a.out_dim, a.weight_layout, a.weight_stride, a.expert_stride),
+                         !out_in, a.grad_x, a.grad_x_stride, a.in_dim, a.dtype, a.dtype, a.offsets, scratch, stream, sms);
         if (e != cudaSuccess) return e;
     }
     if (!a.grad_weight) return cudaSuccess;
-    const bool out_in = a.weight_layout == HC_WEIGHT_OUT_IN;
-    p.a = out_in ? a.grad_out : a.x;
-    p.b = out_in ? a.x : a.grad_out;
-    p.a_stride = (int64_t)(out_in ? a.grad_out_stride : a.x_stride);
-    p.b_stride = (int64_t)(out_in ? a.x_stride : a.grad_out_stride);
-    p.M = (int)(out_in ? a.out_dim : a.in_dim);
-    p.N = (int)(out_in ? a.in_dim : a.out_dim);
+    Operand x = rows_operand(a.x, a.rows, a.in_dim, a.x_stride);
+    const size_t M = out_in ? a.out_dim : a.in_dim, N = out_in ? a.in_dim : a.out_dim;
+    if (a.dtype == HC_FLOAT32) {
+        const Operand &m = out_in ? go : x, &n = out_in ? x : go;
+        PlainParams p = {};
+        p.a = m.p;
+        p.b = n.p;
+        p.out = a.grad_weight;
+        p.offsets = a.offsets;
+        p.rows = (int64_t)a.rows;
+        p.a_stride = m.stride;
+        p.b_stride = n.stride;
+        p.out_stride = (int64_t)a.grad_weight_stride;
+        p.out_expert = (int64_t)a.grad_expert_stride;
+        p.E = (int)a.experts;
+        p.M = (int)M;
+        p.N = (int)N;
+        p.a_vec = whole(m.p, (size_t)m.stride, 0, 4);
+        p.b_vec = whole(n.p, (size_t)n.stride, 0, 4);
+        p.accumulate = a.accumulate;
+        return launch_plain<false, false>(p, a.grad_weight_dtype, stream, sms);
+    }
+    if (a.rows) {
+        const cudaError_t e = pack(x, scratch, stream, sms);
+        if (e != cudaSuccess) return e;
+    } else {
+        // no row is read, but a copy's description wants an address and a stride
+        go.p = x.p = (const void*)((uintptr_t)a.grad_weight / 16 * 16);
+        go.stride = go.pitch();
+        x.stride = x.pitch();
+    }
+    TensorParams p;
     p.out = a.grad_weight;
+    p.offsets = a.offsets;
+    p.rows = (int64_t)a.rows;
     p.out_stride = (int64_t)a.grad_weight_stride;
     p.out_expert = (int64_t)a.grad_expert_stride;
-    p.a_vec = whole(p.a, (size_t)p.a_stride, 0, es);
-    p.b_vec = whole(p.b, (size_t)p.b_stride, 0, es);
+    p.E = (int)a.experts;
+    p.M = (int)M;
+    p.N = (int)N;
+    p.K = 0;
     p.accumulate = a.accumulate;
-    return launch_plain<false, false>(p, a.dtype, a.grad_weight_dtype, stream, sms);
+    p.out_vec = whole(a.grad_weight, a.grad_weight_stride, a.grad_expert_stride, elem_bytes(a.grad_weight_dtype));
+    return launch_tensor<false, false>(p, out_in ? go : x, out_in ? x : go, a.grad_weight_dtype, stream, sms);
 }
 
 }  // namespace hc

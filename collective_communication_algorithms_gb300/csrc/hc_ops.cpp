@@ -185,7 +185,7 @@ hc_status_t weights(const void* p, size_t experts, size_t rows, size_t cols, siz
     Matrix one;
     HC_TRY(matrix(p, rows, cols, stride, es, &one));
     const size_t extent = (rows - 1) * *stride + cols;
-    if (*expert == 0) *expert = rows * *stride;
+    if (*expert == 0 || experts == 1) *expert = rows * *stride;
     if (experts > 1 && *expert < extent) return HC_ERR_INVALID_ARG;
     if (*expert > (size_t)INT64_MAX / 16 / experts) return HC_ERR_INVALID_ARG;
     *out = one;
@@ -201,7 +201,7 @@ hc_status_t weights(const void* p, size_t experts, size_t rows, size_t cols, siz
 
 hc_status_t matmul_sizes(size_t rows, size_t experts, size_t in_dim, size_t out_dim) {
     if (!experts || !in_dim || !out_dim) return HC_ERR_INVALID_ARG;
-    if (experts > kMaxExperts || rows > kMaxTokens || in_dim > kMaxExpertDim || out_dim > kMaxExpertDim)
+    if (experts > kMaxExperts || rows > kMaxExpertRows || in_dim > kMaxExpertDim || out_dim > kMaxExpertDim)
         return HC_ERR_UNSUPPORTED;
     return HC_OK;
 }

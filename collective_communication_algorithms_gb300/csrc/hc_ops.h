@@ -88,6 +88,7 @@ cudaError_t launch_expert_combine(const hc_expert_combine_t& a, cudaStream_t str
 cudaError_t launch_expert_combine_grad(const hc_expert_combine_grad_t& a, cudaStream_t stream, int sms);
 
 constexpr size_t kMaxExpertDim = 65536;
+constexpr size_t kMaxExpertRows = 1u << 30;
 size_t expert_matmul_scratch(const hc_expert_matmul_t& a);
 size_t expert_matmul_grad_scratch(const hc_expert_matmul_grad_t& a);
 cudaError_t launch_expert_matmul(const hc_expert_matmul_t& a, cudaStream_t stream, int sms);

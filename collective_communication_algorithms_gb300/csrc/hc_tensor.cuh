@@ -1,0 +1,95 @@
+// hc_tensor.cuh -- tensor-core building blocks: matrix instructions whose
+// operands lie in shared memory and whose sums lie in tensor memory (TMEM),
+// tiled bulk copies, and the descriptors of both.  Internal; not installed.
+#pragma once
+
+#include <cuda.h>
+
+#include "hc_ops.cuh"
+
+namespace hc {
+namespace {
+
+// ---------------------------------------------------------------------------
+// tensor memory: 128 lanes of 512 columns of 32 bits
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tmem_alloc(uint32_t* where, uint32_t columns) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(where)), "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns) : "memory");
+}
+// 32 columns of the warp's 32 lanes: a thread has its lane's.
+__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(at));
+}
+__device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tensor_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tensor_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// ---------------------------------------------------------------------------
+// operands in shared memory, written by tiled copies with 128-byte swizzling:
+// rows of 128 bytes (64 bf16), eight rows a pattern, tiles on 1024 bytes.
+//   along the sum's direction: a row is one m (or n) and 64 k; 8 rows to the
+//     next pattern is 1024 bytes; 16 k further on is 32 bytes;
+//   across it: a row is one k and 64 m (or n); the next 8 k are 1024 bytes on,
+//     the next 64 m are `group` bytes on; 16 k further on is 2048 bytes.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint64_t operand_along(uint32_t addr) {
+    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
+}
+__device__ __forceinline__ uint64_t operand_across(uint32_t addr, uint32_t group) {
+    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(group >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// bf16 operands, binary32 sums; m x n of one instruction.
+__host__ __device__ constexpr uint32_t product_shape(bool a_across, bool b_across, int m, int n) {
+    return 1u << 4 | 1u << 7 | 1u << 10 | (a_across ? 1u << 15 : 0u) | (b_across ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 |
+           (uint32_t)(m >> 4) << 24;
+}
+// sums[m][n] (+)= a[m][0..15] b[n][0..15], by one thread
+__device__ __forceinline__ void product16(uint32_t sums, uint64_t a, uint64_t b, uint32_t shape, bool add) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(sums),
+        "l"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
+        : "memory");
+}
+// An arrival on `m` once all products that this thread issued are done.
+__device__ __forceinline__ void products_arrive(uint64_t* m) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(m)) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// tiled copies; x counts elements along the innermost direction and is a
+// multiple of 64 (128 bytes) in every use
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tile_g2s(void* dst, const CUtensorMap* map, int x, int y, uint64_t* m) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                     smem_addr(dst)),
+                 "l"(map), "r"(x), "r"(y), "r"(smem_addr(m))
+                 : "memory");
+}
+__device__ __forceinline__ void tile_g2s(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* m) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(m))
+        : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+}  // namespace
+}  // namespace hc

@@ -613,8 +613,8 @@ size_t hc_expert_plan_scratch_bytes(const hc_expert_plan_t* args);
  *  dtype     : x and weight; out_dtype: out.  Products of bf16 values are
  *              exact and are summed in binary32 by the tensor cores; binary32
  *              values are multiplied and summed in binary32 (no TF32).
- *  experts at most 1024, rows at most 2^31 - 1, in_dim and out_dim at most
- *  65536 (HC_ERR_UNSUPPORTED).
+ *  experts at most 1024, rows at most 2^30, in_dim and out_dim at most 65536
+ *  (HC_ERR_UNSUPPORTED).
  *  scratch   : bf16 operands whose pointers or strides are not whole 16 bytes
  *              are copied into it first; 0 bytes are needed when all are.
  */
