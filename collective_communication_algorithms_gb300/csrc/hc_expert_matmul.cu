@@ -194,11 +194,15 @@ __global__ void __launch_bounds__(kPThreads) plain_product_kernel(const PlainPar
 // ---------------------------------------------------------------------------
 // bf16 products on the tensor cores
 //
-// A block has an SM to itself and takes tiles of 128 x TN sums in turn.  One
-// thread starts tiled copies of 64 steps of the sum into a ring of stages, one
-// thread issues the products of each stage, and four warps bring finished sums
-// from tensor memory through shared memory to the output while the next
-// tile's products run (two sets of sums).
+// G = 2: the two blocks of a cluster, on two neighbouring SMs, take tiles of
+// 256 x 256 sums in turn; each brings in half of both operands, so that a byte
+// of shared memory serves twice the products.  G = 1: single blocks and tiles
+// of 128 x 128, for products with few tiles or few rows a group.
+//
+// In a block one thread starts tiled copies of 64 steps of the sum into a ring
+// of stages, one (of the first block) issues the products of each stage, and
+// four warps bring finished sums from tensor memory through shared memory to
+// the output while the next tile's products run (two sets of sums).
 //
 // A tile that reaches beyond its group (ragged rows) multiplies rows of the
 // next group too and does not store them: sums of different rows have nothing
@@ -206,12 +210,9 @@ __global__ void __launch_bounds__(kPThreads) plain_product_kernel(const PlainPar
 // along, so those behind the group's last are overwritten with zeros in shared
 // memory, by a warp of their own, before the products may start.
 // ---------------------------------------------------------------------------
-constexpr int kTM = 128, kTK = 64, kTThreads = 256;
+constexpr int kTM = 128, kTK = 64, kTThreads = 256, kTStages = 6;  // kTM: of one block, of both operands
+constexpr int kTOperandBytes = kTM * kTK * 2, kTStageBytes = 2 * kTOperandBytes;
 constexpr int kTStagingBytes = 4 * 32 * 128;
-template <int TN>
-constexpr int kTStages = TN == 256 ? 4 : 6;
-template <int TN>
-constexpr int kTStageBytes = (kTM + TN) * kTK * 2;
 
 struct TensorParams {
     CUtensorMap a, b;
@@ -225,36 +226,56 @@ struct TensorParams {
     int hold;                 // wait-expiry test mode
 };
 
-template <int TN>
 struct TensorBarriers {
-    uint64_t full[kTStages<TN>], empty[kTStages<TN>], raw[kTStages<TN>];  // raw: landed, to be overwritten in part
+    uint64_t full[kTStages], empty[kTStages], raw[kTStages];  // raw: landed, to be overwritten in part
+    uint64_t zeroed;  // by the other block
     uint64_t sums_full[2], sums_empty[2], drain;
     uint32_t tmem;
 };
-template <int TN>
-constexpr int kTSmem = 1024 + kTStages<TN> * kTStageBytes<TN> + kTStagingBytes + (int)sizeof(TensorBarriers<TN>) + 8;
+constexpr int kTSmem = 1024 + kTStages * kTStageBytes + kTStagingBytes + (int)sizeof(TensorBarriers) + 8;
+
+// A place in the ring of stages: the stage, and the parity of its turn.
+struct Ring {
+    int s = 0;
+    uint32_t turn = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == kTStages) {
+            s = 0;
+            turn ^= 1;
+        }
+    }
+    __device__ __forceinline__ void skip(int n) {  // n stages on
+        s += n % kTStages;
+        turn ^= n / kTStages & 1;
+        if (s >= kTStages) {
+            s -= kTStages;
+            turn ^= 1;
+        }
+    }
+};
 
 struct TensorTile {
     int e, m0, mlen, n0, nlen, K;
     int64_t first;  // ROWS: the tile's first row; else the group's
 };
-template <bool ROWS, int TN>
+// Tile i of T x T sums.
+template <bool ROWS, int T>
 __device__ __forceinline__ TensorTile tensor_tile(const TensorParams& p, const int* bound, const int* tile, int64_t i, int nt) {
     TensorTile t;
     const int m = (int)(i / nt);
-    t.n0 = (int)(i - (int64_t)m * nt) * TN;
-    t.nlen = min(TN, p.N - t.n0);
+    t.n0 = (int)(i - (int64_t)m * nt) * T;
+    t.nlen = min(T, p.N - t.n0);
     if (ROWS) {
         t.e = group_of(tile, p.E, m);
-        t.first = bound[t.e] + (int64_t)(m - tile[t.e]) * kTM;
+        t.first = bound[t.e] + (int64_t)(m - tile[t.e]) * T;
         t.m0 = 0;
-        t.mlen = (int)min((int64_t)kTM, bound[t.e + 1] - t.first);
+        t.mlen = (int)min((int64_t)T, bound[t.e + 1] - t.first);
         t.K = p.K;
     } else {
-        const int per = (p.M + kTM - 1) / kTM;
+        const int per = (p.M + T - 1) / T;
         t.e = m / per;
-        t.m0 = (m - t.e * per) * kTM;
-        t.mlen = min(kTM, p.M - t.m0);
+        t.m0 = (m - t.e * per) * T;
+        t.mlen = min(T, p.M - t.m0);
         t.first = bound[t.e];
         t.K = bound[t.e + 1] - bound[t.e];
     }
@@ -283,172 +304,228 @@ __device__ __forceinline__ void store_v(T* p, int n, bool vec, const float (&v)[
 }
 
 // ROWS, BK: as in the plain kernel.
-template <bool ROWS, bool BK, int TN, class TO>
+template <bool ROWS, bool BK, int G, class TO>
 __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __grid_constant__ TensorParams p) {
-    constexpr int S = kTStages<TN>, STAGE = kTStageBytes<TN>;
+    constexpr int T = kTM * G;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int bound[kMaxExperts + 1], tile[kMaxExperts + 1];
     unsigned char* stages = smem + (1024 - (smem_addr(smem) & 1023)) % 1024;
-    unsigned char* staging = stages + S * STAGE;
-    TensorBarriers<TN>& bar = *(TensorBarriers<TN>*)(staging + kTStagingBytes);
+    unsigned char* staging = stages + kTStages * kTStageBytes;
+    TensorBarriers& bar = *(TensorBarriers*)(staging + kTStagingBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = G == 1 ? 0 : (int)(blockIdx.x % G);  // in the cluster
     if (tid == 0) {
-        for (int s = 0; s < S; s++) {
+        for (int s = 0; s < kTStages; s++) {
             mbar_init(&bar.full[s], 1 + p.hold);
             mbar_init(&bar.empty[s], 1);
             mbar_init(&bar.raw[s], 1);
         }
         for (int s = 0; s < 2; s++) {
             mbar_init(&bar.sums_full[s], 1);
-            mbar_init(&bar.sums_empty[s], 4);
+            mbar_init(&bar.sums_empty[s], 4 * G);
         }
+        mbar_init(&bar.zeroed, 1);
         mbar_init(&bar.drain, 1);
         mbar_init_fence();
         prefetch_map(&p.a);
         prefetch_map(&p.b);
     }
-    if (warp == 2) tmem_alloc(&bar.tmem, 2 * TN);
+    if (warp == 2) tmem_alloc<G>(&bar.tmem, 2 * T);
     grid_wait();
     grid_release();
-    if (warp == 3) read_groups(p.offsets, p.E, p.rows, kTM, bound, tile);
+    if (warp == 3) read_groups(p.offsets, p.E, p.rows, T, bound, tile);
     tensor_fence_before();
     __syncthreads();
+    if constexpr (G > 1) {  // the other block's barriers are set up
+        cluster_arrive();
+        cluster_wait();
+    }
     tensor_fence_after();
     const uint32_t tmem = bar.tmem;
-    const int nt = (p.N + TN - 1) / TN;
-    const int64_t tiles = (ROWS ? (int64_t)tile[p.E] : (int64_t)((p.M + kTM - 1) / kTM) * p.E) * nt;
+    const int nt = (p.N + T - 1) / T;
+    const int64_t tiles = (ROWS ? (int64_t)tile[p.E] : (int64_t)((p.M + T - 1) / T) * p.E) * nt;
+    const int64_t step = gridDim.x / G;
     const auto expired = [&] { atomicExch(p.err, (int)HC_ERR_TIMEOUT); };
 
     if (warp == 0 && lane == 0) {  // copies
-        int64_t it = 0;
-        uint32_t raw_used = 0;  // stages whose last copies went to raw
+        Ring at;
+        int issued = 0;           // stages that hold copies, at most all
+        uint32_t turns = 0;       // the parity of each stage's last turn
+        uint32_t raw_used = 0;    // stages whose last copies went to raw
         uint32_t raw_phase = 0;
         bool ok = true;
-        for (int64_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
-            const TensorTile t = tensor_tile<ROWS, TN>(p, bound, tile, i, nt);
-            for (int k0 = 0; k0 < t.K; k0 += kTK, it++) {
-                const int s = (int)(it % S);
-                if (!mbar_wait_quick(&bar.empty[s], ((uint32_t)(it / S) & 1) ^ 1, p.wait_ns)) {
+        for (int64_t i = blockIdx.x / G; ok && i < tiles; i += step) {
+            const TensorTile t = tensor_tile<ROWS, T>(p, bound, tile, i, nt);
+            const int am = t.m0 + rank * kTM, ar = (int)t.first + (ROWS ? rank * kTM : 0), bn = t.n0 + rank * kTM;
+            for (int k0 = 0; k0 < t.K; k0 += kTK, at.next()) {
+                const int s = at.s;
+                if (!mbar_wait_quick(&bar.empty[s], at.turn ^ 1, p.wait_ns)) {
                     expired();
                     ok = false;
                     break;
                 }
-                unsigned char* a = stages + s * STAGE;
-                unsigned char* b = a + kTM * kTK * 2;
+                issued = max(issued, s + 1);
+                turns = (turns & ~(1u << s)) | at.turn << s;
+                unsigned char* a = stages + s * kTStageBytes;
+                unsigned char* b = a + kTOperandBytes;
                 const bool part = !ROWS && t.K - k0 < kTK;
-                uint64_t* to = part ? &bar.raw[s] : &bar.full[s];
-                if (part) raw_used |= 1u << s, raw_phase ^= 1u << s;
-                else raw_used &= ~(1u << s);
-                mbar_arrive_expect_tx(to, STAGE);
+                uint32_t to;
+                if (part) {
+                    raw_used |= 1u << s;
+                    raw_phase ^= 1u << s;
+                    to = smem_addr(&bar.raw[s]);
+                    mbar_arrive_expect_tx(&bar.raw[s], kTStageBytes);
+                } else {
+                    raw_used &= ~(1u << s);
+                    // both blocks' copies land on the first one's barrier (the
+                    // other's may do so before the bytes are announced)
+                    to = first_blocks<G>(&bar.full[s]);
+                    if (rank == 0) mbar_arrive_expect_tx(&bar.full[s], G * kTStageBytes);
+                }
                 if (ROWS) {
-                    tile_g2s(a, &p.a, k0, (int)t.first, to);
+                    tile_g2s<G>(a, &p.a, k0, ar, to);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < kTM / 64; j++) tile_g2s(a + j * 8192, &p.a, t.m0 + 64 * j, (int)t.first + k0, to);
+                    for (int j = 0; j < kTM / 64; j++) tile_g2s<G>(a + j * 8192, &p.a, am + 64 * j, ar + k0, to);
                 }
                 if (ROWS && BK) {
-                    tile_g2s(b, &p.b, k0, t.n0, t.e, to);
+                    tile_g2s<G>(b, &p.b, k0, bn, t.e, to);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < TN / 64; j++) {
-                        if (ROWS) tile_g2s(b + j * 8192, &p.b, t.n0 + 64 * j, k0, t.e, to);
-                        else tile_g2s(b + j * 8192, &p.b, t.n0 + 64 * j, (int)t.first + k0, to);
+                    for (int j = 0; j < kTM / 64; j++) {
+                        if (ROWS) tile_g2s<G>(b + j * 8192, &p.b, bn + 64 * j, k0, t.e, to);
+                        else tile_g2s<G>(b + j * 8192, &p.b, bn + 64 * j, ar + k0, to);
                     }
                 }
             }
         }
-        // a block does not leave while copies into its shared memory are under way
-        const int64_t n = it < S ? it : S;
-        for (int64_t j = it - n; j < it; j++) {
-            const int s = (int)(j % S);
+        // a block does not leave while copies into its shared memory are under
+        // way: the first block waits for those of both (the other leaves after it)
+        for (int s = 0; s < issued; s++) {
             if (raw_used >> s & 1) {
                 mbar_wait_quick(&bar.raw[s], (raw_phase >> s & 1) ^ 1, kWaitLimitNs);
-            } else {
+            } else if (rank == 0) {
                 if (p.hold) mbar_arrive(&bar.full[s]);
-                mbar_wait_quick(&bar.full[s], (uint32_t)(j / S) & 1, kWaitLimitNs);
+                mbar_wait_quick(&bar.full[s], turns >> s & 1, kWaitLimitNs);
             }
         }
-    } else if (warp == 1 && lane == 0) {  // products
-        constexpr uint32_t shape = product_shape(!ROWS, !BK, kTM, TN);
-        int64_t it = 0;
+        if (G > 1 && !ok)  // and if either has given up, some time beyond any copy's
+            for (const unsigned long long t0 = global_ns(); global_ns() - t0 < kTestWaitLimitNs;) {}
+    } else if (warp == 1 && lane == 0 && rank == 0) {  // products
+        constexpr uint32_t shape = product_shape(!ROWS, !BK, T, T);
+        // 16 steps of the sum further on, in units of a descriptor's address
+        constexpr uint32_t a_on = (ROWS ? 32 : 2048) >> 4, b_on = (BK ? 32 : 2048) >> 4;
+        const uint32_t base = smem_addr(stages);
+        const uint64_t a0 = ROWS ? operand_along(base) : operand_across(base, 8192);
+        const uint64_t b0 = BK ? operand_along(base + kTOperandBytes) : operand_across(base + kTOperandBytes, 8192);
+        Ring at;
         uint32_t n = 0;
         bool ok = true;
-        for (int64_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
-            const TensorTile t = tensor_tile<ROWS, TN>(p, bound, tile, i, nt);
+        for (int64_t i = blockIdx.x / G; ok && i < tiles; i += step) {
+            const TensorTile t = tensor_tile<ROWS, T>(p, bound, tile, i, nt);
             if (!t.K) continue;
-            const uint32_t set = n & 1;
-            if (!(ok = mbar_wait_quick(&bar.sums_empty[set], ((n >> 1) & 1) ^ 1, p.wait_ns))) break;
+            const uint32_t set = n & 1, sums = tmem + set * T;
+            if (!(ok = first_wait<G>(&bar.sums_empty[set], ((n >> 1) & 1) ^ 1, p.wait_ns))) break;
             tensor_fence_after();
-            for (int k0 = 0; k0 < t.K; k0 += kTK, it++) {
-                const int s = (int)(it % S);
-                if (!(ok = mbar_wait_quick(&bar.full[s], (uint32_t)(it / S) & 1, p.wait_ns))) break;
+            for (int k0 = 0; k0 < t.K; k0 += kTK, at.next()) {
+                const int s = at.s;
+                if (!(ok = mbar_wait_quick(&bar.full[s], at.turn, p.wait_ns))) break;
                 tensor_fence_after();
-                const uint32_t a = smem_addr(stages + s * STAGE), b = a + kTM * kTK * 2;
-                const int steps = (min(kTK, t.K - k0) + 15) / 16;
-                for (int j = 0; j < steps; j++) {
-                    const uint64_t da = ROWS ? operand_along(a + 32 * j) : operand_across(a + 2048 * j, 8192);
-                    const uint64_t db = BK ? operand_along(b + 32 * j) : operand_across(b + 2048 * j, 8192);
-                    product16(tmem + set * TN, da, db, shape, k0 > 0 || j > 0);
+                const uint64_t a = a0 + (uint32_t)(s * (kTStageBytes >> 4)), b = b0 + (uint32_t)(s * (kTStageBytes >> 4));
+                if (t.K - k0 >= kTK) {
+#pragma unroll
+                    for (int j = 0; j < kTK / 16; j++) product16<G>(sums, a + j * a_on, b + j * b_on, shape, k0 > 0 || j > 0);
+                } else {
+                    for (int j = 0; j < (t.K - k0 + 15) / 16; j++)
+                        product16<G>(sums, a + j * a_on, b + j * b_on, shape, k0 > 0 || j > 0);
                 }
-                products_arrive(&bar.empty[s]);
+                products_arrive<G>(&bar.empty[s]);
             }
             if (!ok) break;
-            products_arrive(&bar.sums_full[set]);
+            products_arrive<G>(&bar.sums_full[set]);
             n++;
         }
         if (!ok) expired();
-        products_arrive(&bar.drain);  // tensor memory is freed after the last products
+        products_arrive<G>(&bar.drain, false);  // tensor memory is freed after the last products
         mbar_wait_quick(&bar.drain, 0, kWaitLimitNs);
     } else if (!ROWS && warp == 3) {  // zeros behind the last row of a group
-        int64_t it = 0;
-        uint32_t phase = 0;
-        for (int64_t i = blockIdx.x; i < tiles; i += gridDim.x) {
-            const TensorTile t = tensor_tile<ROWS, TN>(p, bound, tile, i, nt);
-            it += (t.K + kTK - 1) / kTK;
+        Ring at;
+        uint32_t phase = 0, zeroed = 0;
+        for (int64_t i = blockIdx.x / G; i < tiles; i += step) {
+            const TensorTile t = tensor_tile<ROWS, T>(p, bound, tile, i, nt);
             const int rest = t.K % kTK;
+            at.skip(t.K / kTK);
             if (!rest) continue;
-            const int s = (int)((it - 1) % S);
+            const int s = at.s;
+            at.next();
             if (!mbar_wait_quick(&bar.raw[s], phase >> s & 1, p.wait_ns)) {
                 if (lane == 0) expired();
                 break;
             }
             phase ^= 1u << s;
             const int zeros = (16 - rest % 16) % 16 * 8;  // rows that a product reads, 16 bytes each
-            for (int j = lane; j < zeros * ((kTM + TN) / 64); j += 32)
-                *(uint4*)(stages + s * STAGE + j / zeros * 8192 + rest * 128 + j % zeros * 16) = make_uint4(0, 0, 0, 0);
+            for (int j = lane; j < zeros * (kTStageBytes / 8192); j += 32)
+                *(uint4*)(stages + s * kTStageBytes + j / zeros * 8192 + rest * 128 + j % zeros * 16) = make_uint4(0, 0, 0, 0);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.full[s]);
+            if (rank > 0) {
+                if (lane == 0) first_arrive<G>(&bar.zeroed);
+            } else {
+                if (G > 1) {
+                    if (!first_wait<G>(&bar.zeroed, zeroed & 1, p.wait_ns)) {
+                        if (lane == 0) expired();
+                        break;
+                    }
+                    zeroed++;
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(&bar.full[s]);
+            }
         }
     } else if (warp >= 4) {  // sums to the output
         constexpr int V = 16 / (int)sizeof(TO), PER = 32 / V;  // elements of a lane, lanes of 32 columns
         const int q = warp - 4;
         unsigned char* mine = staging + q * 32 * 128;
+        const int r0 = lane / PER, at = lane % PER * V;  // of the lane, when it stores
         uint32_t n = 0;
-        for (int64_t i = blockIdx.x; i < tiles; i += gridDim.x) {
-            const TensorTile t = tensor_tile<ROWS, TN>(p, bound, tile, i, nt);
+        for (int64_t i = blockIdx.x / G; i < tiles; i += step) {
+            const TensorTile t = tensor_tile<ROWS, T>(p, bound, tile, i, nt);
             if (!t.K && p.accumulate) continue;
             const uint32_t set = n & 1;
+            const int m = rank * kTM + q * 32;
+            const int rows = t.mlen - m;  // of this warp
+            TO* out = (TO*)p.out + (ROWS ? t.first * p.out_stride : t.e * p.out_expert + (int64_t)t.m0 * p.out_stride) + t.n0 +
+                      (m + r0) * p.out_stride + at;
+            // what is added to, a step of 32 columns ahead
+            float old[2][32 / V][V];
+            const bool add = !ROWS && p.accumulate;
+            const auto fetch = [&](int c, float (&v)[32 / V][V]) {
+#pragma unroll
+                for (int j = 0; j < 32 / V; j++)
+                    if (j * V + r0 < rows && c + at < t.nlen)
+                        load_v<TO, V>(out + (int64_t)(j * V) * p.out_stride + c, t.nlen - c - at, p.out_vec, v[j]);
+            };
+            if (add) fetch(0, old[0]);
             if (t.K) {
-                if (!mbar_wait_quick(&bar.sums_full[set], n >> 1 & 1, p.wait_ns)) {
+                if (!mbar_wait_quick(&bar.sums_full[set], (n >> 1) & 1, p.wait_ns)) {
                     if (lane == 0) expired();
                     break;
                 }
                 tensor_fence_after();
                 n++;
             }
-            TO* out = (TO*)p.out + (ROWS ? t.first * p.out_stride : t.e * p.out_expert + (int64_t)t.m0 * p.out_stride) + t.n0;
-            const int rows = t.mlen - q * 32;  // of this warp
-            for (int c = 0; c < TN; c += 32) {
+#pragma unroll 2
+            for (int c = 0; c < T; c += 32) {
+                if (add && c + 32 < t.nlen) fetch(c + 32, old[(c / 32 + 1) & 1]);
                 uint32_t v[32];
                 if (t.K) {
                     __syncwarp();
-                    tmem_load32(tmem + ((uint32_t)(q * 32) << 16) + set * TN + c, v);
+                    tmem_load32(tmem + ((uint32_t)(q * 32) << 16) + set * T + c, v);
                     tmem_load_wait();
-                    if (c + 32 == TN || c + 32 >= t.nlen) {
+                    if (c + 32 == T || c + 32 >= t.nlen) {
                         tensor_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.sums_empty[set]);
+                        if (lane == 0) first_arrive<G>(&bar.sums_empty[set]);
                     }
                 } else {
 #pragma unroll
@@ -461,7 +538,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
                 __syncwarp();
 #pragma unroll
                 for (int j = 0; j < 32 / V; j++) {
-                    const int r = j * V + lane / PER, at = lane % PER * V;
+                    const int r = j * V + r0;
                     float x[V];
 #pragma unroll
                     for (int h = 0; h < V / 4; h++) {
@@ -473,14 +550,11 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
                     }
                     const int left = t.nlen - c - at;
                     if (r >= rows || left <= 0) continue;
-                    TO* to = out + (int64_t)(q * 32 + r) * p.out_stride + c + at;
-                    if (!ROWS && p.accumulate) {
-                        float old[V];
-                        load_v<TO, V>(to, left, p.out_vec, old);
+                    if (add) {
 #pragma unroll
-                        for (int h = 0; h < V; h++) x[h] += old[h];
+                        for (int h = 0; h < V; h++) x[h] += old[(c / 32) & 1][j][h];
                     }
-                    store_v<TO, V>(to, left, p.out_vec, x);
+                    store_v<TO, V>(out + (int64_t)(j * V) * p.out_stride + c, left, p.out_vec, x);
                 }
                 if (c + 32 >= t.nlen) break;
             }
@@ -489,8 +563,12 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
     __syncwarp();
     tensor_fence_before();
     __syncthreads();
+    if constexpr (G > 1) {  // neither block's shared or tensor memory goes while the other uses it
+        cluster_arrive();
+        cluster_wait();
+    }
     tensor_fence_after();
-    if (warp == 2) tmem_free(tmem, 2 * TN);
+    if (warp == 2) tmem_free<G>(tmem, 2 * T);
 }
 
 bool whole(const void* p, size_t stride, size_t expert, int es) {
@@ -593,31 +671,32 @@ cudaError_t describe(CUtensorMap* map, const Operand& x, int box_rows, bool expe
                : cudaErrorInvalidValue;
 }
 
-template <bool ROWS, bool BK, int TN, class TO>
+template <bool ROWS, bool BK, int G, class TO>
 cudaError_t launch_tensor(TensorParams& p, const Operand& a, const Operand& b, cudaStream_t stream, int sms) {
+    constexpr int T = kTM * G;
     cudaError_t e = describe(&p.a, a, ROWS ? kTM : kTK, false);
-    if (e == cudaSuccess) e = describe(&p.b, b, ROWS && BK ? TN : kTK, ROWS);
+    if (e == cudaSuccess) e = describe(&p.b, b, ROWS && BK ? kTM : kTK, ROWS);
     if (e != cudaSuccess) return e;
     p.err = device_error_flag();
     if (!p.err) return cudaErrorInvalidValue;
     p.hold = expiring_waits() ? 1 : 0;
     p.wait_ns = p.hold ? kTestWaitLimitNs : kWaitLimitNs;
-    const void* fn = (const void*)tensor_product_kernel<ROWS, BK, TN, TO>;
-    if (!allow_smem((void*)fn, kTSmem<TN>)) return cudaErrorInvalidValue;
-    const int64_t nt = (p.N + TN - 1) / TN;
-    const int64_t mt = ROWS ? p.rows / kTM + std::min<int64_t>(p.E, p.rows) + 1 : (int64_t)((p.M + kTM - 1) / kTM) * p.E;
+    const void* fn = (const void*)tensor_product_kernel<ROWS, BK, G, TO>;
+    if (!allow_smem((void*)fn, kTSmem)) return cudaErrorInvalidValue;
+    const int64_t nt = (p.N + T - 1) / T;
+    const int64_t mt = ROWS ? p.rows / T + std::min<int64_t>(p.E, p.rows) + 1 : (int64_t)((p.M + T - 1) / T) * p.E;
     void* args[] = {&p};
-    return launch_op(fn, dim3((unsigned)std::min<int64_t>(mt * nt, sms)), dim3(kTThreads), args, kTSmem<TN>, stream);
+    const int64_t grid = std::min<int64_t>(mt * nt, sms / G) * G;
+    return launch_op(fn, dim3((unsigned)grid), dim3(kTThreads), args, kTSmem, stream, G);
 }
 template <bool ROWS, bool BK>
 cudaError_t launch_tensor(TensorParams& p, const Operand& a, const Operand& b, hc_dtype_t out, cudaStream_t stream, int sms) {
-    // Wider tiles read less for each product, narrower ones are more in number:
-    // the wider, unless they leave SMs without a tile.
-    const int64_t mt = ROWS ? (p.rows + kTM - 1) / kTM : (int64_t)((p.M + kTM - 1) / kTM) * p.E;
-    const bool wide = p.N > 128 && mt * ((p.N + 255) / 256) >= sms;
+    // Two blocks a tile, unless that leaves pairs of SMs without one.
+    const int64_t mt = ROWS ? (p.rows + 255) / 256 : (int64_t)((p.M + 255) / 256) * p.E;
+    const bool two = mt * ((p.N + 255) / 256) >= sms / 2;
     if (out == HC_BFLOAT16)
-        return wide ? launch_tensor<ROWS, BK, 256, Bf16>(p, a, b, stream, sms) : launch_tensor<ROWS, BK, 128, Bf16>(p, a, b, stream, sms);
-    return wide ? launch_tensor<ROWS, BK, 256, float>(p, a, b, stream, sms) : launch_tensor<ROWS, BK, 128, float>(p, a, b, stream, sms);
+        return two ? launch_tensor<ROWS, BK, 2, Bf16>(p, a, b, stream, sms) : launch_tensor<ROWS, BK, 1, Bf16>(p, a, b, stream, sms);
+    return two ? launch_tensor<ROWS, BK, 2, float>(p, a, b, stream, sms) : launch_tensor<ROWS, BK, 1, float>(p, a, b, stream, sms);
 }
 
 Operand rows_operand(const void* p, size_t rows, size_t cols, size_t stride) {

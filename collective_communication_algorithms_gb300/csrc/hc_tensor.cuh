@@ -13,13 +13,26 @@ namespace {
 // ---------------------------------------------------------------------------
 // tensor memory: 128 lanes of 512 columns of 32 bits
 // ---------------------------------------------------------------------------
+// G: blocks that work on a tile together (1, or a cluster of 2, both of which
+// then call this).
+template <int G>
 __device__ __forceinline__ void tmem_alloc(uint32_t* where, uint32_t columns) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(where)), "r"(columns)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if constexpr (G == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(where)), "r"(columns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(where)), "r"(columns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
 }
+template <int G>
 __device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns) : "memory");
+    if constexpr (G == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns) : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns) : "memory");
 }
 // 32 columns of the warp's 32 lanes: a thread has its lane's.
 __device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&v)[32]) {
@@ -57,35 +70,107 @@ __host__ __device__ constexpr uint32_t product_shape(bool a_across, bool b_acros
     return 1u << 4 | 1u << 7 | 1u << 10 | (a_across ? 1u << 15 : 0u) | (b_across ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 |
            (uint32_t)(m >> 4) << 24;
 }
-// sums[m][n] (+)= a[m][0..15] b[n][0..15], by one thread
+// sums[m][n] (+)= a[m][0..15] b[n][0..15], by one thread.  With G = 2 each block
+// holds half of a's m and of b's n at the same places of its shared memory, and
+// the sums of its m; a thread of the first block issues.
+template <int G>
 __device__ __forceinline__ void product16(uint32_t sums, uint64_t a, uint64_t b, uint32_t shape, bool add) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(sums),
-        "l"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
-        : "memory");
+    if constexpr (G == 1)
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(sums),
+            "l"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(sums),
+            "l"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
+            : "memory");
 }
-// An arrival on `m` once all products that this thread issued are done.
-__device__ __forceinline__ void products_arrive(uint64_t* m) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(m)) : "memory");
+// An arrival on `m` (of both blocks, if G = 2 and `both`) once all products
+// that this thread issued are done.
+template <int G>
+__device__ __forceinline__ void products_arrive(uint64_t* m, bool both = true) {
+    if constexpr (G == 1)
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(m)) : "memory");
+    else if (both)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                         smem_addr(m)),
+                     "h"((uint16_t)3)
+                     : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(m)) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// barriers of the first block of a cluster of two (G = 2), or of the block
+// itself, which then uses no cluster instruction
+// ---------------------------------------------------------------------------
+template <int G>
+__device__ __forceinline__ uint32_t first_blocks(const uint64_t* m) {
+    uint32_t a = smem_addr(m);
+    if constexpr (G > 1) asm("mapa.shared::cluster.u32 %0, %0, 0;" : "+r"(a));
+    return a;
+}
+template <int G>
+__device__ __forceinline__ void first_arrive(uint64_t* m) {
+    if constexpr (G == 1) mbar_arrive(m);
+    else asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(first_blocks<G>(m)) : "memory");
+}
+// mbar_wait_quick for arrivals from both blocks.
+template <int G>
+__device__ __forceinline__ bool first_wait(uint64_t* m, unsigned parity, unsigned long long limit_ns) {
+    if constexpr (G == 1) return mbar_wait_quick(m, parity, limit_ns);
+    unsigned long long t0 = 0;
+    for (bool first = true;; first = false) {
+        unsigned ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(smem_addr(m)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        const unsigned long long t = global_ns();
+        if (first) t0 = t;
+        else if (t - t0 > limit_ns) return false;
+    }
 }
 
 // ---------------------------------------------------------------------------
 // tiled copies; x counts elements along the innermost direction and is a
 // multiple of 64 (128 bytes) in every use
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void tile_g2s(void* dst, const CUtensorMap* map, int x, int y, uint64_t* m) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-                     smem_addr(dst)),
-                 "l"(map), "r"(x), "r"(y), "r"(smem_addr(m))
-                 : "memory");
+// G = 2: the barrier may be the cluster's first block's (first_blocks).
+template <int G>
+__device__ __forceinline__ void tile_g2s(void* dst, const CUtensorMap* map, int x, int y, uint32_t m) {
+    if constexpr (G == 1)
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                         smem_addr(dst)),
+                     "l"(map), "r"(x), "r"(y), "r"(m)
+                     : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                smem_addr(dst)),
+            "l"(map), "r"(x), "r"(y), "r"(m)
+            : "memory");
 }
-__device__ __forceinline__ void tile_g2s(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* m) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-            smem_addr(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(m))
-        : "memory");
+template <int G>
+__device__ __forceinline__ void tile_g2s(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t m) {
+    if constexpr (G == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                smem_addr(dst)),
+            "l"(map), "r"(x), "r"(y), "r"(z), "r"(m)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                smem_addr(dst)),
+            "l"(map), "r"(x), "r"(y), "r"(z), "r"(m)
+            : "memory");
 }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
