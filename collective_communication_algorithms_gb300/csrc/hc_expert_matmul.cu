@@ -204,11 +204,13 @@ __global__ void __launch_bounds__(kPThreads) plain_product_kernel(const PlainPar
 // four warps bring finished sums from tensor memory through shared memory to
 // the output while the next tile's products run (two sets of sums).
 //
-// A tile that reaches beyond its group (ragged rows) multiplies rows of the
-// next group too and does not store them: sums of different rows have nothing
-// to do with each other.  In the weights' gradient the rows are what is summed
-// along, so those behind the group's last are overwritten with zeros in shared
-// memory, by a warp of their own, before the products may start.
+// The first two products have the weight's columns as m and a group's rows as
+// n, whose number in an instruction is any multiple of 32: the last tile of a
+// group multiplies at most 31 rows of the next one, which it does not store
+// (sums of different rows have nothing to do with each other).  In the
+// weights' gradient the rows are what is summed along, so those behind the
+// group's last are overwritten with zeros in shared memory, by a warp of their
+// own, before the products may start.
 // ---------------------------------------------------------------------------
 constexpr int kTM = 128, kTK = 64, kTThreads = 256, kTStages = 6;  // kTM: of one block, of both operands
 constexpr int kTOperandBytes = kTM * kTK * 2, kTStageBytes = 2 * kTOperandBytes;
@@ -254,27 +256,34 @@ struct Ring {
     }
 };
 
+// One tile: sums m0 .. m0 + mlen, n0 .. n0 + nlen of expert e, over K steps.
+// The first two products: m counts the weight's columns, n rows from `first`
+// on; the weights' gradient: m and n count its rows and columns, the steps are
+// the rows from `first` on.
 struct TensorTile {
     int e, m0, mlen, n0, nlen, K;
-    int64_t first;  // ROWS: the tile's first row; else the group's
+    int64_t first;
+    __device__ __forceinline__ int n() const { return (nlen + 31) / 32 * 32; }  // of an instruction
 };
-// Tile i of T x T sums.
+// Tile i of T x T sums, of `across` in a row.
 template <bool ROWS, int T>
-__device__ __forceinline__ TensorTile tensor_tile(const TensorParams& p, const int* bound, const int* tile, int64_t i, int nt) {
+__device__ __forceinline__ TensorTile tensor_tile(const TensorParams& p, const int* bound, const int* tile, int64_t i, int across) {
     TensorTile t;
-    const int m = (int)(i / nt);
-    t.n0 = (int)(i - (int64_t)m * nt) * T;
-    t.nlen = min(T, p.N - t.n0);
+    const int down = (int)(i / across), at = (int)(i - (int64_t)down * across) * T;
     if (ROWS) {
-        t.e = group_of(tile, p.E, m);
-        t.first = bound[t.e] + (int64_t)(m - tile[t.e]) * T;
-        t.m0 = 0;
-        t.mlen = (int)min((int64_t)T, bound[t.e + 1] - t.first);
+        t.m0 = at;
+        t.mlen = min(T, p.N - at);
+        t.e = group_of(tile, p.E, down);
+        t.first = bound[t.e] + (int64_t)(down - tile[t.e]) * T;
+        t.n0 = 0;
+        t.nlen = (int)min((int64_t)T, bound[t.e + 1] - t.first);
         t.K = p.K;
     } else {
+        t.n0 = at;
+        t.nlen = min(T, p.N - at);
         const int per = (p.M + T - 1) / T;
-        t.e = m / per;
-        t.m0 = (m - t.e * per) * T;
+        t.e = down / per;
+        t.m0 = (down - t.e * per) * T;
         t.mlen = min(T, p.M - t.m0);
         t.first = bound[t.e];
         t.K = bound[t.e + 1] - bound[t.e];
@@ -303,8 +312,8 @@ __device__ __forceinline__ void store_v(T* p, int n, bool vec, const float (&v)[
     }
 }
 
-// ROWS, BK: as in the plain kernel.
-template <bool ROWS, bool BK, int G, class TO>
+// ROWS: the first two products; WK: their weight is summed along its rows.
+template <bool ROWS, bool WK, int G, class TO>
 __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __grid_constant__ TensorParams p) {
     constexpr int T = kTM * G;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -342,8 +351,8 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
     }
     tensor_fence_after();
     const uint32_t tmem = bar.tmem;
-    const int nt = (p.N + T - 1) / T;
-    const int64_t tiles = (ROWS ? (int64_t)tile[p.E] : (int64_t)((p.M + T - 1) / T) * p.E) * nt;
+    const int across = (p.N + T - 1) / T;
+    const int64_t tiles = (ROWS ? (int64_t)tile[p.E] : (int64_t)((p.M + T - 1) / T) * p.E) * across;
     const int64_t step = gridDim.x / G;
     const auto expired = [&] { atomicExch(p.err, (int)HC_ERR_TIMEOUT); };
 
@@ -355,8 +364,10 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
         uint32_t raw_phase = 0;
         bool ok = true;
         for (int64_t i = blockIdx.x / G; ok && i < tiles; i += step) {
-            const TensorTile t = tensor_tile<ROWS, T>(p, bound, tile, i, nt);
-            const int am = t.m0 + rank * kTM, ar = (int)t.first + (ROWS ? rank * kTM : 0), bn = t.n0 + rank * kTM;
+            const TensorTile t = tensor_tile<ROWS, T>(p, bound, tile, i, across);
+            const int am = t.m0 + rank * kTM, half = t.n() / G, bn = (ROWS ? (int)t.first : t.n0) + rank * half;
+            const int boxes = (half + 63) / 64;  // of 64 n
+            const unsigned bytes = kTOperandBytes + boxes * 8192;
             for (int k0 = 0; k0 < t.K; k0 += kTK, at.next()) {
                 const int s = at.s;
                 if (!mbar_wait_quick(&bar.empty[s], at.turn ^ 1, p.wait_ns)) {
@@ -374,28 +385,26 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
                     raw_used |= 1u << s;
                     raw_phase ^= 1u << s;
                     to = smem_addr(&bar.raw[s]);
-                    mbar_arrive_expect_tx(&bar.raw[s], kTStageBytes);
+                    mbar_arrive_expect_tx(&bar.raw[s], bytes);
                 } else {
                     raw_used &= ~(1u << s);
                     // both blocks' copies land on the first one's barrier (the
                     // other's may do so before the bytes are announced)
                     to = first_blocks<G>(&bar.full[s]);
-                    if (rank == 0) mbar_arrive_expect_tx(&bar.full[s], G * kTStageBytes);
+                    if (rank == 0) mbar_arrive_expect_tx(&bar.full[s], G * bytes);
                 }
-                if (ROWS) {
-                    tile_g2s<G>(a, &p.a, k0, ar, to);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kTM / 64; j++) tile_g2s<G>(a + j * 8192, &p.a, am + 64 * j, ar + k0, to);
-                }
-                if (ROWS && BK) {
-                    tile_g2s<G>(b, &p.b, k0, bn, t.e, to);
+                if (ROWS && WK) {
+                    tile_g2s<G>(a, &p.a, k0, am, t.e, to);
                 } else {
 #pragma unroll
                     for (int j = 0; j < kTM / 64; j++) {
-                        if (ROWS) tile_g2s<G>(b + j * 8192, &p.b, bn + 64 * j, k0, t.e, to);
-                        else tile_g2s<G>(b + j * 8192, &p.b, bn + 64 * j, ar + k0, to);
+                        if (ROWS) tile_g2s<G>(a + j * 8192, &p.a, am + 64 * j, k0, t.e, to);
+                        else tile_g2s<G>(a + j * 8192, &p.a, am + 64 * j, (int)t.first + k0, to);
                     }
+                }
+                for (int j = 0; j < boxes; j++) {
+                    if (ROWS) tile_g2s<G>(b + j * 8192, &p.b, k0, bn + 64 * j, to);
+                    else tile_g2s<G>(b + j * 8192, &p.b, bn + 64 * j, (int)t.first + k0, to);
                 }
             }
         }
@@ -412,19 +421,19 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
         if (G > 1 && !ok)  // and if either has given up, some time beyond any copy's
             for (const unsigned long long t0 = global_ns(); global_ns() - t0 < kTestWaitLimitNs;) {}
     } else if (warp == 1 && lane == 0 && rank == 0) {  // products
-        constexpr uint32_t shape = product_shape(!ROWS, !BK, T, T);
         // 16 steps of the sum further on, in units of a descriptor's address
-        constexpr uint32_t a_on = (ROWS ? 32 : 2048) >> 4, b_on = (BK ? 32 : 2048) >> 4;
+        constexpr bool AK = ROWS && WK, BK = ROWS;  // summed along rows in shared memory
+        constexpr uint32_t a_on = (AK ? 32 : 2048) >> 4, b_on = (BK ? 32 : 2048) >> 4;
         const uint32_t base = smem_addr(stages);
-        const uint64_t a0 = ROWS ? operand_along(base) : operand_across(base, 8192);
+        const uint64_t a0 = AK ? operand_along(base) : operand_across(base, 8192);
         const uint64_t b0 = BK ? operand_along(base + kTOperandBytes) : operand_across(base + kTOperandBytes, 8192);
         Ring at;
         uint32_t n = 0;
         bool ok = true;
         for (int64_t i = blockIdx.x / G; ok && i < tiles; i += step) {
-            const TensorTile t = tensor_tile<ROWS, T>(p, bound, tile, i, nt);
+            const TensorTile t = tensor_tile<ROWS, T>(p, bound, tile, i, across);
             if (!t.K) continue;
-            const uint32_t set = n & 1, sums = tmem + set * T;
+            const uint32_t set = n & 1, sums = tmem + set * T, shape = product_shape(!AK, !BK, T, t.n());
             if (!(ok = first_wait<G>(&bar.sums_empty[set], ((n >> 1) & 1) ^ 1, p.wait_ns))) break;
             tensor_fence_after();
             for (int k0 = 0; k0 < t.K; k0 += kTK, at.next()) {
@@ -452,7 +461,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
         Ring at;
         uint32_t phase = 0, zeroed = 0;
         for (int64_t i = blockIdx.x / G; i < tiles; i += step) {
-            const TensorTile t = tensor_tile<ROWS, T>(p, bound, tile, i, nt);
+            const TensorTile t = tensor_tile<ROWS, T>(p, bound, tile, i, across);
             const int rest = t.K % kTK;
             at.skip(t.K / kTK);
             if (!rest) continue;
@@ -464,7 +473,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
             }
             phase ^= 1u << s;
             const int zeros = (16 - rest % 16) % 16 * 8;  // rows that a product reads, 16 bytes each
-            for (int j = lane; j < zeros * (kTStageBytes / 8192); j += 32)
+            for (int j = lane; j < zeros * (kTStageBytes / 8192); j += 32)  // in all boxes
                 *(uint4*)(stages + s * kTStageBytes + j / zeros * 8192 + rest * 128 + j % zeros * 16) = make_uint4(0, 0, 0, 0);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
@@ -483,29 +492,36 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
             }
         }
     } else if (warp >= 4) {  // sums to the output
-        constexpr int V = 16 / (int)sizeof(TO), PER = 32 / V;  // elements of a lane, lanes of 32 columns
+        constexpr int V = 16 / (int)sizeof(TO), PER = 32 / V, N = 32 / V;  // elements of a lane, lanes and steps of 32 columns
         const int q = warp - 4;
-        unsigned char* mine = staging + q * 32 * 128;
+        const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+        unsigned char* mine = staging + q * 32 * 128;  // 32 rows of 32 sums, whose 16-byte pieces are swapped about
         const int r0 = lane / PER, at = lane % PER * V;  // of the lane, when it stores
         uint32_t n = 0;
         for (int64_t i = blockIdx.x / G; i < tiles; i += step) {
-            const TensorTile t = tensor_tile<ROWS, T>(p, bound, tile, i, nt);
+            const TensorTile t = tensor_tile<ROWS, T>(p, bound, tile, i, across);
             if (!t.K && p.accumulate) continue;
             const uint32_t set = n & 1;
-            const int m = rank * kTM + q * 32;
-            const int rows = t.mlen - m;  // of this warp
-            TO* out = (TO*)p.out + (ROWS ? t.first * p.out_stride : t.e * p.out_expert + (int64_t)t.m0 * p.out_stride) + t.n0 +
-                      (m + r0) * p.out_stride + at;
-            // what is added to, a step of 32 columns ahead
-            float old[2][32 / V][V];
+            const int m = rank * kTM + q * 32;  // of this warp's 32 lanes of sums
+            // the tile's place in the output, and the lane's in the warp's part
+            TO* out = ROWS ? (TO*)p.out + (t.first + r0) * p.out_stride + t.m0 + m + at
+                           : (TO*)p.out + t.e * p.out_expert + (int64_t)(t.m0 + m + r0) * p.out_stride + t.n0 + at;
+            // c: columns of sums; the step's rows and columns of output left for the lane
+            const auto rows_left = [&](int c, int j) { return (ROWS ? t.nlen - c : t.mlen - m) - j * V - r0; };
+            const auto cols_left = [&](int c) { return (ROWS ? t.mlen - m : t.nlen - c) - at; };
+            const auto place = [&](int c, int j) { return out + (ROWS ? (int64_t)(c + j * V) * p.out_stride : (int64_t)(j * V) * p.out_stride + c); };
             const bool add = !ROWS && p.accumulate;
-            const auto fetch = [&](int c, float (&v)[32 / V][V]) {
+            constexpr int AHEAD = ROWS ? 1 : 4;  // steps of 32 columns that what is added to is loaded ahead
+            float old[AHEAD][N][V];
+            const auto fetch = [&](int c, float (&v)[N][V]) {
 #pragma unroll
-                for (int j = 0; j < 32 / V; j++)
-                    if (j * V + r0 < rows && c + at < t.nlen)
-                        load_v<TO, V>(out + (int64_t)(j * V) * p.out_stride + c, t.nlen - c - at, p.out_vec, v[j]);
+                for (int j = 0; j < N; j++)
+                    if (rows_left(c, j) > 0 && cols_left(c) > 0) load_v<TO, V>(place(c, j), cols_left(c), p.out_vec, v[j]);
             };
-            if (add) fetch(0, old[0]);
+            if (add)
+#pragma unroll
+                for (int h = 0; h < AHEAD; h++)
+                    if (h * 32 < t.nlen) fetch(h * 32, old[h]);
             if (t.K) {
                 if (!mbar_wait_quick(&bar.sums_full[set], (n >> 1) & 1, p.wait_ns)) {
                     if (lane == 0) expired();
@@ -514,50 +530,57 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
                 tensor_fence_after();
                 n++;
             }
-#pragma unroll 2
-            for (int c = 0; c < T; c += 32) {
-                if (add && c + 32 < t.nlen) fetch(c + 32, old[(c / 32 + 1) & 1]);
-                uint32_t v[32];
-                if (t.K) {
-                    __syncwarp();
-                    tmem_load32(tmem + ((uint32_t)(q * 32) << 16) + set * T + c, v);
-                    tmem_load_wait();
-                    if (c + 32 == T || c + 32 >= t.nlen) {
-                        tensor_fence_before();
+            for (int c0 = 0; c0 < t.nlen; c0 += 32 * AHEAD)
+#pragma unroll
+                for (int h = 0; h < AHEAD; h++) {
+                    const int c = c0 + 32 * h;
+                    if (c >= t.nlen) break;
+                    uint32_t v[32];
+                    if (t.K) {
                         __syncwarp();
-                        if (lane == 0) first_arrive<G>(&bar.sums_empty[set]);
-                    }
-                } else {
+                        tmem_load32(lanes + set * T + c, v);
+                        tmem_load_wait();
+                        if (c + 32 >= t.nlen) {
+                            tensor_fence_before();
+                            __syncwarp();
+                            if (lane == 0) first_arrive<G>(&bar.sums_empty[set]);
+                        }
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < 32; j++) v[j] = 0;
+                        for (int j = 0; j < 32; j++) v[j] = 0;
+                    }
+                    __syncwarp();  // the sums of the step before have been read
+                    if constexpr (ROWS) {  // a column of sums is a row of the output
+#pragma unroll
+                        for (int j = 0; j < 32; j++)
+                            *(uint32_t*)(mine + j * 128 + (((lane >> 2) ^ (j & 7)) << 4) + (lane & 3) * 4) = v[j];
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; j++)
+                            *(uint4*)(mine + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < N; j++) {
+                        const int r = j * V + r0;
+                        float x[V];
+#pragma unroll
+                        for (int g = 0; g < V / 4; g++) {
+                            const uint4 w = *(const uint4*)(mine + r * 128 + (((at / 4 + g) ^ (r & 7)) << 4));
+                            x[4 * g] = __uint_as_float(w.x);
+                            x[4 * g + 1] = __uint_as_float(w.y);
+                            x[4 * g + 2] = __uint_as_float(w.z);
+                            x[4 * g + 3] = __uint_as_float(w.w);
+                        }
+                        if (rows_left(c, j) <= 0 || cols_left(c) <= 0) continue;
+                        if (add) {
+#pragma unroll
+                            for (int g = 0; g < V; g++) x[g] += old[h][j][g];
+                        }
+                        store_v<TO, V>(place(c, j), cols_left(c), p.out_vec, x);
+                    }
+                    if (add && c + 32 * AHEAD < t.nlen) fetch(c + 32 * AHEAD, old[h]);
                 }
-                __syncwarp();  // the stores of the columns before have been read
-#pragma unroll
-                for (int j = 0; j < 8; j++)
-                    *(uint4*)(mine + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                __syncwarp();
-#pragma unroll
-                for (int j = 0; j < 32 / V; j++) {
-                    const int r = j * V + r0;
-                    float x[V];
-#pragma unroll
-                    for (int h = 0; h < V / 4; h++) {
-                        const uint4 w = *(const uint4*)(mine + r * 128 + (((at / 4 + h) ^ (r & 7)) << 4));
-                        x[4 * h] = __uint_as_float(w.x);
-                        x[4 * h + 1] = __uint_as_float(w.y);
-                        x[4 * h + 2] = __uint_as_float(w.z);
-                        x[4 * h + 3] = __uint_as_float(w.w);
-                    }
-                    const int left = t.nlen - c - at;
-                    if (r >= rows || left <= 0) continue;
-                    if (add) {
-#pragma unroll
-                        for (int h = 0; h < V; h++) x[h] += old[(c / 32) & 1][j][h];
-                    }
-                    store_v<TO, V>(out + (int64_t)(j * V) * p.out_stride + c, left, p.out_vec, x);
-                }
-                if (c + 32 >= t.nlen) break;
-            }
         }
     }
     __syncwarp();
@@ -671,17 +694,17 @@ cudaError_t describe(CUtensorMap* map, const Operand& x, int box_rows, bool expe
                : cudaErrorInvalidValue;
 }
 
-template <bool ROWS, bool BK, int G, class TO>
+template <bool ROWS, bool WK, int G, class TO>
 cudaError_t launch_tensor(TensorParams& p, const Operand& a, const Operand& b, cudaStream_t stream, int sms) {
     constexpr int T = kTM * G;
-    cudaError_t e = describe(&p.a, a, ROWS ? kTM : kTK, false);
-    if (e == cudaSuccess) e = describe(&p.b, b, ROWS && BK ? kTM : kTK, ROWS);
+    cudaError_t e = describe(&p.a, a, ROWS && WK ? kTM : 64, ROWS);
+    if (e == cudaSuccess) e = describe(&p.b, b, 64, false);
     if (e != cudaSuccess) return e;
     p.err = device_error_flag();
     if (!p.err) return cudaErrorInvalidValue;
     p.hold = expiring_waits() ? 1 : 0;
     p.wait_ns = p.hold ? kTestWaitLimitNs : kWaitLimitNs;
-    const void* fn = (const void*)tensor_product_kernel<ROWS, BK, G, TO>;
+    const void* fn = (const void*)tensor_product_kernel<ROWS, WK, G, TO>;
     if (!allow_smem((void*)fn, kTSmem)) return cudaErrorInvalidValue;
     const int64_t nt = (p.N + T - 1) / T;
     const int64_t mt = ROWS ? p.rows / T + std::min<int64_t>(p.E, p.rows) + 1 : (int64_t)((p.M + T - 1) / T) * p.E;
@@ -689,14 +712,14 @@ cudaError_t launch_tensor(TensorParams& p, const Operand& a, const Operand& b, c
     const int64_t grid = std::min<int64_t>(mt * nt, sms / G) * G;
     return launch_op(fn, dim3((unsigned)grid), dim3(kTThreads), args, kTSmem, stream, G);
 }
-template <bool ROWS, bool BK>
+template <bool ROWS, bool WK>
 cudaError_t launch_tensor(TensorParams& p, const Operand& a, const Operand& b, hc_dtype_t out, cudaStream_t stream, int sms) {
     // Two blocks a tile, unless that leaves pairs of SMs without one.
     const int64_t mt = ROWS ? (p.rows + 255) / 256 : (int64_t)((p.M + 255) / 256) * p.E;
     const bool two = mt * ((p.N + 255) / 256) >= sms / 2;
     if (out == HC_BFLOAT16)
-        return two ? launch_tensor<ROWS, BK, 2, Bf16>(p, a, b, stream, sms) : launch_tensor<ROWS, BK, 1, Bf16>(p, a, b, stream, sms);
-    return two ? launch_tensor<ROWS, BK, 2, float>(p, a, b, stream, sms) : launch_tensor<ROWS, BK, 1, float>(p, a, b, stream, sms);
+        return two ? launch_tensor<ROWS, WK, 2, Bf16>(p, a, b, stream, sms) : launch_tensor<ROWS, WK, 1, Bf16>(p, a, b, stream, sms);
+    return two ? launch_tensor<ROWS, WK, 2, float>(p, a, b, stream, sms) : launch_tensor<ROWS, WK, 1, float>(p, a, b, stream, sms);
 }
 
 Operand rows_operand(const void* p, size_t rows, size_t cols, size_t stride) {
@@ -746,7 +769,7 @@ cudaError_t rows_product(Operand a, Operand w, bool along, void* out, size_t out
     p.K = (int)a.cols;
     p.accumulate = 0;
     p.out_vec = whole(out, out_stride, 0, elem_bytes(to));
-    return along ? launch_tensor<true, true>(p, a, w, to, stream, sms) : launch_tensor<true, false>(p, a, w, to, stream, sms);
+    return along ? launch_tensor<true, true>(p, w, a, to, stream, sms) : launch_tensor<true, false>(p, w, a, to, stream, sms);
 }
 
 }  // namespace
