@@ -291,27 +291,6 @@ __device__ __forceinline__ TensorTile tensor_tile(const TensorParams& p, const i
     return t;
 }
 
-// V elements at p, of which n are in range.
-template <class T, int V>
-__device__ __forceinline__ void load_v(const T* p, int n, bool vec, float (&v)[V]) {
-    if (vec && n >= V) {
-        load_n<T, V>(p, V, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; i++) v[i] = i < n ? to_f32(p[i]) : 0.0f;
-    }
-}
-template <class T, int V>
-__device__ __forceinline__ void store_v(T* p, int n, bool vec, const float (&v)[V]) {
-    if (vec && n >= V) {
-        store_n<T, V>(p, V, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; i++)
-            if (i < n) put(p + i, v[i]);
-    }
-}
-
 // ROWS: the first two products; WK: their weight is summed along its rows.
 template <bool ROWS, bool WK, int G, class TO>
 __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __grid_constant__ TensorParams p) {
@@ -511,14 +490,17 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
             const auto cols_left = [&](int c) { return (ROWS ? t.mlen - m : t.nlen - c) - at; };
             const auto place = [&](int c, int j) { return out + (ROWS ? (int64_t)(c + j * V) * p.out_stride : (int64_t)(j * V) * p.out_stride + c); };
             const bool add = !ROWS && p.accumulate;
+            // 16-byte accesses of whole steps of columns, without a branch within a
+            // lane's rows: those would keep loads from overlapping
+            const bool fast = p.out_vec && (ROWS ? t.mlen - m >= 32 : t.nlen % 32 == 0);
             constexpr int AHEAD = ROWS ? 1 : 4;  // steps of 32 columns that what is added to is loaded ahead
-            float old[AHEAD][N][V];
-            const auto fetch = [&](int c, float (&v)[N][V]) {
+            uint4 old[AHEAD][N];
+            const auto fetch = [&](int c, uint4 (&v)[N]) {
 #pragma unroll
                 for (int j = 0; j < N; j++)
-                    if (rows_left(c, j) > 0 && cols_left(c) > 0) load_v<TO, V>(place(c, j), cols_left(c), p.out_vec, v[j]);
+                    if (rows_left(c, j) > 0) v[j] = *(const uint4*)place(c, j);
             };
-            if (add)
+            if (add && fast)
 #pragma unroll
                 for (int h = 0; h < AHEAD; h++)
                     if (h * 32 < t.nlen) fetch(h * 32, old[h]);
@@ -572,14 +554,23 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
                             x[4 * g + 2] = __uint_as_float(w.z);
                             x[4 * g + 3] = __uint_as_float(w.w);
                         }
-                        if (rows_left(c, j) <= 0 || cols_left(c) <= 0) continue;
-                        if (add) {
+                        if (fast) {
+                            if (add) {
+                                float y[V];
+                                unpack(old[h][j], y);
 #pragma unroll
-                            for (int g = 0; g < V; g++) x[g] += old[h][j][g];
+                                for (int g = 0; g < V; g++) x[g] += y[g];
+                            }
+                            if (rows_left(c, j) > 0) *(uint4*)place(c, j) = pack(x);
+                        } else if (rows_left(c, j) > 0) {
+                            TO* to = place(c, j);
+                            const int left = cols_left(c);
+#pragma unroll
+                            for (int g = 0; g < V; g++)
+                                if (g < left) put(to + g, add ? x[g] + to_f32(to[g]) : x[g]);
                         }
-                        store_v<TO, V>(place(c, j), cols_left(c), p.out_vec, x);
                     }
-                    if (add && c + 32 * AHEAD < t.nlen) fetch(c + 32 * AHEAD, old[h]);
+                    if (add && fast && c + 32 * AHEAD < t.nlen) fetch(c + 32 * AHEAD, old[h]);
                 }
         }
     }
