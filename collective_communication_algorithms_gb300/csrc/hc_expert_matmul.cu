@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
     unsigned char* stages = smem + (1024 - (smem_addr(smem) & 1023)) % 1024;
     unsigned char* staging = stages + kTStages * kTStageBytes;
     TensorBarriers& bar = *(TensorBarriers*)(staging + kTStagingBytes);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const int rank = G == 1 ? 0 : (int)(blockIdx.x % G);  // in the cluster
     if (tid == 0) {
         for (int s = 0; s < kTStages; s++) {
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
         cluster_wait();
     }
     tensor_fence_after();
-    const uint32_t tmem = bar.tmem;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, bar.tmem, 0);
     const int across = (p.N + T - 1) / T;
     const int64_t tiles = (ROWS ? (int64_t)tile[p.E] : (int64_t)((p.M + T - 1) / T) * p.E) * across;
     const int64_t step = gridDim.x / G;
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
         }
         if (G > 1 && !ok)  // and if either has given up, some time beyond any copy's
             for (const unsigned long long t0 = global_ns(); global_ns() - t0 < kTestWaitLimitNs;) {}
-    } else if (warp == 1 && lane == 0 && rank == 0) {  // products
+    } else if (warp == 1 && rank == 0) {  // products
         // 16 steps of the sum further on, in units of a descriptor's address
         constexpr bool AK = ROWS && WK, BK = ROWS;  // summed along rows in shared memory
         constexpr uint32_t a_on = (AK ? 32 : 2048) >> 4, b_on = (BK ? 32 : 2048) >> 4;
@@ -420,21 +420,26 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
                 if (!(ok = mbar_wait_quick(&bar.full[s], at.turn, p.wait_ns))) break;
                 tensor_fence_after();
                 const uint64_t a = a0 + (uint32_t)(s * (kTStageBytes >> 4)), b = b0 + (uint32_t)(s * (kTStageBytes >> 4));
-                if (t.K - k0 >= kTK) {
+                if (elected()) {
+                    if (t.K - k0 >= kTK) {
 #pragma unroll
-                    for (int j = 0; j < kTK / 16; j++) product16<G>(sums, a + j * a_on, b + j * b_on, shape, k0 > 0 || j > 0);
-                } else {
-                    for (int j = 0; j < (t.K - k0 + 15) / 16; j++)
-                        product16<G>(sums, a + j * a_on, b + j * b_on, shape, k0 > 0 || j > 0);
+                        for (int j = 0; j < kTK / 16; j++) product16<G>(sums, a + j * a_on, b + j * b_on, shape, k0 > 0 || j > 0);
+                    } else {
+                        for (int j = 0; j < (t.K - k0 + 15) / 16; j++)
+                            product16<G>(sums, a + j * a_on, b + j * b_on, shape, k0 > 0 || j > 0);
+                    }
+                    products_arrive<G>(&bar.empty[s]);
                 }
-                products_arrive<G>(&bar.empty[s]);
+                __syncwarp();
             }
             if (!ok) break;
-            products_arrive<G>(&bar.sums_full[set]);
+            if (elected()) products_arrive<G>(&bar.sums_full[set]);
+            __syncwarp();
             n++;
         }
-        if (!ok) expired();
-        products_arrive<G>(&bar.drain, false);  // tensor memory is freed after the last products
+        if (!ok && lane == 0) expired();
+        if (elected()) products_arrive<G>(&bar.drain, false);  // tensor memory is freed after the last products
+        __syncwarp();
         mbar_wait_quick(&bar.drain, 0, kWaitLimitNs);
     } else if (!ROWS && warp == 3) {  // zeros behind the last row of a group
         Ring at;

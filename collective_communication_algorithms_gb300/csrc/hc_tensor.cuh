@@ -103,6 +103,15 @@ __device__ __forceinline__ void products_arrive(uint64_t* m, bool both = true) {
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(m)) : "memory");
 }
 
+// One thread of a warp that is together here: matrix instructions take their
+// operands from registers that a warp shares, which the compiler only keeps
+// them in where the warp has not parted.
+__device__ __forceinline__ bool elected() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one != 0;
+}
+
 // ---------------------------------------------------------------------------
 // barriers of the first block of a cluster of two (G = 2), or of the block
 // itself, which then uses no cluster instruction
