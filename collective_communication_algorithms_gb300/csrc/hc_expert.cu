@@ -20,13 +20,15 @@ namespace {
 // only add to counters.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanBatch = 8;         // ids of a lane loaded together
+constexpr int kPlanMaxBlocks = 128;   // also the pitch of an expert's counts
 
 struct PlanParams {
     const void* ids;
     int32_t* offsets;
     int32_t* row_tokens;
     int32_t* slots;
-    int32_t* counts;  // blocks x E
+    int32_t* counts;  // E x kPlanMaxBlocks
     int64_t first;
     int64_t n;
     int64_t run;      // assignments of a block, a multiple of kPlanThreads
@@ -43,6 +45,24 @@ __device__ __forceinline__ int expert_at(const PlanParams& p, int64_t i) {
     return d < (uint64_t)p.E ? (int)d : p.E;
 }
 
+// f(assignment, its expert) for a warp's run, 32 neighbours at a time; E and an
+// assignment behind the end for lanes without one.
+template <class F>
+__device__ __forceinline__ void for_run(const PlanParams& p, int64_t begin, int64_t end, F f) {
+    const int lane = threadIdx.x & 31;
+    for (int64_t i0 = begin; i0 < end; i0 += 32 * kPlanBatch) {
+        int e[kPlanBatch];
+#pragma unroll
+        for (int k = 0; k < kPlanBatch; k++) {
+            const int64_t i = i0 + 32 * k + lane;
+            e[k] = i < end ? expert_at(p, i) : p.E;
+        }
+#pragma unroll
+        for (int k = 0; k < kPlanBatch; k++)
+            if (i0 + 32 * k < end) f(i0 + 32 * k + lane, e[k]);
+    }
+}
+
 __global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const PlanParams p) {
     extern __shared__ __align__(128) unsigned char smem[];
     int32_t* cnt = (int32_t*)smem;
@@ -51,12 +71,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const PlanPara
     grid_wait();
     grid_release();
     const int64_t begin = (int64_t)blockIdx.x * p.run, end = min(p.n, begin + p.run);
-    for (int64_t i = begin + threadIdx.x; i < end; i += kPlanThreads) {
-        const int e = expert_at(p, i);
+    const int64_t per = p.run / kPlanWarps, wb = begin + (threadIdx.x >> 5) * per;
+    for_run(p, wb, min(end, wb + per), [&](int64_t, int e) {
         if (e < p.E) atomicAdd(&cnt[e], 1);
-    }
+    });
     __syncthreads();
-    for (int e = threadIdx.x; e < p.E; e += kPlanThreads) p.counts[(int64_t)blockIdx.x * p.E + e] = cnt[e];
+    for (int e = threadIdx.x; e < p.E; e += kPlanThreads) p.counts[e * kPlanMaxBlocks + blockIdx.x] = cnt[e];
 }
 
 // Exclusive sums of v over the block's threads (every thread's v), and the total.
@@ -82,14 +102,16 @@ __device__ __forceinline__ int block_exclusive(int v, int* sh, int* total) {
     return before + s - v;
 }
 
-// Shared memory: the next place per warp and expert [kPlanWarps][E].
+// Shared memory: the next place per warp and expert [kPlanWarps][E]; of several
+// blocks also the experts' totals and what the blocks before hold [2][E].
 template <bool SINGLE>
 __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanParams p) {
     extern __shared__ __align__(128) unsigned char smem[];
-    int32_t* places = (int32_t*)smem;
     __shared__ int sh[kPlanWarps];
     const int E = p.E, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int32_t* places = (int32_t*)smem;
     int32_t* place = places + warp * E;
+    int32_t *total = places + kPlanWarps * E, *before = total + E;
     for (int e = lane; e < E; e += 32) place[e] = 0;
     __syncwarp();
     grid_wait();
@@ -97,33 +119,44 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanPara
     const int64_t begin = (int64_t)blockIdx.x * p.run, end = min(p.n, begin + p.run);
     const int64_t per = p.run / kPlanWarps;  // a multiple of 32
     const int64_t wb = begin + warp * per, we = min(end, wb + per);
-    for (int64_t i = wb + lane; i < we; i += 32) {
-        const int e = expert_at(p, i);
+    for_run(p, wb, we, [&](int64_t, int e) {
         if (e < E) atomicAdd(&place[e], 1);
+    });
+    if (!SINGLE) {  // a warp takes an expert's counts of all blocks, four a lane
+        static_assert(kPlanMaxBlocks == 128, "four counts a lane");
+        const int b = lane * 4, me = blockIdx.x;
+#pragma unroll 4
+        for (int e = warp; e < E; e += kPlanWarps) {
+            int4 c = b < p.blocks ? *(const int4*)&p.counts[e * kPlanMaxBlocks + b] : make_int4(0, 0, 0, 0);
+            if (b + 1 >= p.blocks) c.y = 0;
+            if (b + 2 >= p.blocks) c.z = 0;
+            if (b + 3 >= p.blocks) c.w = 0;
+            const int all = __reduce_add_sync(0xFFFFFFFFu, c.x + c.y + c.z + c.w);
+            const int mine = __reduce_add_sync(
+                0xFFFFFFFFu, (b < me ? c.x : 0) + (b + 1 < me ? c.y : 0) + (b + 2 < me ? c.z : 0) + (b + 3 < me ? c.w : 0));
+            if (lane == 0) {
+                total[e] = all;
+                before[e] = mine;
+            }
+        }
     }
     __syncthreads();
-    // experts in runs of kPlanThreads: totals, their sums, and this block's start
+    // experts in runs of kPlanThreads: where each begins, and this block's and its warps' places in it
     int carry = 0;
     for (int e0 = 0; e0 < E; e0 += kPlanThreads) {
         const int e = e0 + tid;
-        int all = 0, before = 0;
+        int all = 0;
         if (e < E) {
-            if (SINGLE) {
+            if (SINGLE)
                 for (int w = 0; w < kPlanWarps; w++) all += places[w * E + e];
-            } else {
-#pragma unroll 8
-                for (int b = 0; b < p.blocks; b++) {
-                    const int c = p.counts[(int64_t)b * E + e];
-                    all += c;
-                    if (b < (int)blockIdx.x) before += c;
-                }
-            }
+            else
+                all = total[e];
         }
-        int total;
-        const int start = carry + block_exclusive(all, sh, &total);
-        carry += total;
+        int sum;
+        const int start = carry + block_exclusive(all, sh, &sum);
+        carry += sum;
         if (e < E) {
-            int at = start + before;
+            int at = start + (SINGLE ? 0 : before[e]);
             for (int w = 0; w < kPlanWarps; w++) {
                 const int c = places[w * E + e];
                 places[w * E + e] = at;
@@ -134,12 +167,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanPara
     }
     if (blockIdx.x == 0 && tid == 0) p.offsets[E] = carry;
     __syncthreads();
-    for (int64_t i0 = wb; i0 < we; i0 += 32) {
-        const int64_t i = i0 + lane;
-        const int e = i < we ? expert_at(p, i) : E;
+    for_run(p, wb, we, [&](int64_t i, int e) {
         const unsigned same = __match_any_sync(0xFFFFFFFFu, e);
-        int at = -1;
-        if (e < E) at = place[e] + __popc(same & ((1u << lane) - 1));
+        const int at = e < E ? place[e] + __popc(same & ((1u << lane) - 1)) : -1;
         __syncwarp();
         if (e < E) {
             if (p.row_tokens) p.row_tokens[at] = (int32_t)((uint32_t)i / p.top);
@@ -147,7 +177,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanPara
         }
         if (p.slots && i < we) p.slots[i] = at;
         __syncwarp();
-    }
+    });
     if (p.row_tokens)  // behind the last row
         for (int64_t i = carry + (int64_t)blockIdx.x * kPlanThreads + tid; i < p.n; i += (int64_t)p.blocks * kPlanThreads)
             p.row_tokens[i] = -1;
@@ -158,7 +188,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanPara
 // elements a step; rows of the experts are read once each.
 //
 // Bound by bytes: a token reads `top` rows scattered over y.  All of a step's
-// loads over up to kSlots choices are under way together.
+// loads over up to kSlots choices are under way together; rows of whole 16
+// bytes take them in pieces of 16, others element by element.
 // ---------------------------------------------------------------------------
 constexpr int kCombineWarps = 8, kSlots = 8;
 
@@ -179,6 +210,31 @@ __device__ __forceinline__ float weight_at(const CombineParams& p, int64_t i) {
     return p.weight_bf ? to_f32(((const Bf16*)p.weights)[i]) : ((const float*)p.weights)[i];
 }
 
+// V elements as they lie in memory: 16 bytes, or one element.
+template <class T, int V>
+struct Piece {
+    uint4 w;
+    __device__ __forceinline__ void load(const T* p) { w = *(const uint4*)p; }
+    __device__ __forceinline__ void get(float (&v)[V]) const { unpack(w, v); }
+    static __device__ __forceinline__ void store(T* p, const float (&v)[V]) { *(uint4*)p = pack(v); }
+};
+template <class T>
+struct Piece<T, 1> {
+    T w;
+    __device__ __forceinline__ void load(const T* p) { w = *p; }
+    __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = to_f32(w); }
+    static __device__ __forceinline__ void store(T* p, const float (&v)[1]) { put(p, v[0]); }
+};
+
+// Rows of a token's choices j0 .. j0 + kSlots, -1 for none.
+__device__ __forceinline__ void slots_at(const CombineParams& p, int64_t t, int j0, int (&s)[kSlots]) {
+#pragma unroll
+    for (int j = 0; j < kSlots; j++) {
+        s[j] = j0 + j < p.top ? p.slots[t * p.top + j0 + j] : -1;
+        if ((uint64_t)(uint32_t)s[j] >= (uint64_t)p.rows) s[j] = -1;
+    }
+}
+
 template <class T, int V>
 __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const CombineParams p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -188,33 +244,35 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Combi
     if (t >= p.tokens) return;
     const T* y = (const T*)p.y;
     T* out = (T*)p.out + t * p.out_stride;
-    const int64_t step = (int64_t)p.warps * 32 * V;
-    for (int64_t c = ((int64_t)(warp % p.warps) * 32 + lane) * V; c < p.dim; c += step) {
-        const int64_t left = p.dim - c;
-        const int n = left < V ? (int)left : V;
+    const int64_t step = (int64_t)p.warps * 32 * V, c0 = ((int64_t)(warp % p.warps) * 32 + lane) * V;
+    int s[kSlots];
+    float w[kSlots];
+    const auto choices = [&](int j0) {
+        slots_at(p, t, j0, s);
+#pragma unroll
+        for (int j = 0; j < kSlots; j++) w[j] = s[j] >= 0 ? weight_at(p, t * p.top + j0 + j) : 0.0f;
+    };
+    choices(0);
+    for (int64_t c = c0; c < p.dim; c += step) {
         float acc[V];
 #pragma unroll
         for (int v = 0; v < V; v++) acc[v] = 0.0f;
         for (int j0 = 0; j0 < p.top; j0 += kSlots) {
-            float x[kSlots][V], w[kSlots];
-            bool in[kSlots];
-#pragma unroll
-            for (int j = 0; j < kSlots; j++) {
-                const int64_t at = t * p.top + j0 + j;
-                const int s = j0 + j < p.top ? p.slots[at] : -1;
-                in[j] = (uint32_t)s < (uint64_t)p.rows && s >= 0;
-                if (in[j]) {
-                    w[j] = weight_at(p, at);
-                    load_n<T, V>(y + s * p.y_stride + c, n, x[j]);
-                }
-            }
+            if (p.top > kSlots) choices(j0);
+            Piece<T, V> x[kSlots];
 #pragma unroll
             for (int j = 0; j < kSlots; j++)
-                if (in[j])
+                if (s[j] >= 0) x[j].load(y + s[j] * p.y_stride + c);
 #pragma unroll
-                    for (int v = 0; v < V; v++) acc[v] = fmaf(w[j], x[j][v], acc[v]);
+            for (int j = 0; j < kSlots; j++)
+                if (s[j] >= 0) {
+                    float v[V];
+                    x[j].get(v);
+#pragma unroll
+                    for (int k = 0; k < V; k++) acc[k] = fmaf(w[j], v[k], acc[k]);
+                }
         }
-        store_n<T, V>(out + c, n, acc);
+        Piece<T, V>::store(out + c, acc);
     }
 }
 
@@ -228,7 +286,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_grad_kernel(const 
     const T* y = (const T*)p.y;
     const T* g = (const T*)p.grad_out + t * p.grad_out_stride;
     T* gy = (T*)p.out;
-    const int64_t step = (int64_t)p.warps * 32 * V;
+    const int64_t step = (int64_t)p.warps * 32 * V, c0 = ((int64_t)mine * 32 + lane) * V;
     for (int j0 = 0; j0 < p.top; j0 += kSlots) {
         float dot[kSlots];
 #pragma unroll
@@ -236,38 +294,36 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_grad_kernel(const 
         if (t < p.tokens) {
             int s[kSlots];
             float w[kSlots];
+            slots_at(p, t, j0, s);
 #pragma unroll
-            for (int j = 0; j < kSlots; j++) {
-                const int64_t at = t * p.top + j0 + j;
-                s[j] = j0 + j < p.top ? p.slots[at] : -1;
-                if ((uint64_t)(uint32_t)s[j] >= (uint64_t)p.rows) s[j] = -1;
-                w[j] = s[j] >= 0 ? weight_at(p, at) : 0.0f;
-            }
-            for (int64_t c = ((int64_t)mine * 32 + lane) * V; c < p.dim; c += step) {
-                const int64_t left = p.dim - c;
-                const int n = left < V ? (int)left : V;
-                float gv[V], x[kSlots][V];
-                load_n<T, V>(g + c, n, gv);
-                if (p.grad_weights) {
+            for (int j = 0; j < kSlots; j++) w[j] = s[j] >= 0 ? weight_at(p, t * p.top + j0 + j) : 0.0f;
+            for (int64_t c = c0; c < p.dim; c += step) {
+                Piece<T, V> go, x[kSlots];
+                go.load(g + c);
+                if (p.grad_weights)
 #pragma unroll
                     for (int j = 0; j < kSlots; j++)
-                        if (s[j] >= 0) load_n<T, V>(y + s[j] * p.y_stride + c, n, x[j]);
+                        if (s[j] >= 0) x[j].load(y + s[j] * p.y_stride + c);
+                float gv[V];
+                go.get(gv);
+                if (p.grad_weights)
 #pragma unroll
                     for (int j = 0; j < kSlots; j++)
-                        if (s[j] >= 0)
+                        if (s[j] >= 0) {
+                            float v[V];
+                            x[j].get(v);
 #pragma unroll
-                            for (int v = 0; v < V; v++) dot[j] = fmaf(gv[v], x[j][v], dot[j]);
-                }
-                if (gy) {
+                            for (int k = 0; k < V; k++) dot[j] = fmaf(gv[k], v[k], dot[j]);
+                        }
+                if (gy)
 #pragma unroll
                     for (int j = 0; j < kSlots; j++)
                         if (s[j] >= 0) {
                             float o[V];
 #pragma unroll
-                            for (int v = 0; v < V; v++) o[v] = w[j] * gv[v];
-                            store_n<T, V>(gy + s[j] * p.out_stride + c, n, o);
+                            for (int k = 0; k < V; k++) o[k] = w[j] * gv[k];
+                            Piece<T, V>::store(gy + s[j] * p.out_stride + c, o);
                         }
-                }
             }
         }
         if (!p.grad_weights) continue;
@@ -330,8 +386,7 @@ bool wide_rows(const void* p, size_t stride, size_t dim, int es) {
 }  // namespace
 
 // Runs of the counting kernels: none up to this many assignments.
-constexpr int64_t kPlanSingle = 8192;
-constexpr int64_t kPlanMaxBlocks = 128, kPlanMinRun = 4096;
+constexpr int64_t kPlanSingle = 8192, kPlanMinRun = 4096;
 
 ExpertPlanShape expert_plan_shape(int64_t n, int64_t experts) {
     ExpertPlanShape s;
@@ -345,7 +400,7 @@ ExpertPlanShape expert_plan_shape(int64_t n, int64_t experts) {
     s.run = std::max(kPlanMinRun, (n + kPlanMaxBlocks - 1) / kPlanMaxBlocks);
     s.run = (s.run + unit - 1) / unit * unit;
     s.blocks = (int)((n + s.run - 1) / s.run);
-    s.bytes = (size_t)s.blocks * experts * sizeof(int32_t);
+    s.bytes = (size_t)kPlanMaxBlocks * experts * sizeof(int32_t);
     return s;
 }
 
@@ -365,7 +420,7 @@ cudaError_t launch_expert_plan(const hc_expert_plan_t& a, cudaStream_t stream) {
     p.run = s.run;
     p.blocks = s.blocks;
     void* args[] = {&p};
-    const int smem = kPlanWarps * p.E * (int)sizeof(int32_t);
+    const int smem = (kPlanWarps + (s.blocks > 1 ? 2 : 0)) * p.E * (int)sizeof(int32_t);
     if (s.blocks > 1) {
         const cudaError_t e = launch_op((const void*)plan_count_kernel, dim3((unsigned)s.blocks), dim3(kPlanThreads), args,
                                         p.E * sizeof(int32_t), stream);

@@ -88,71 +88,79 @@ struct PlainParams {
     int accumulate;
 };
 
-constexpr int kPT = 128, kPK = 16, kPThreads = 256, kPPad = 4;
+constexpr int kPK = 16, kPThreads = 256, kPPad = 4;
 
-__device__ __forceinline__ void load8(const float* p, int n, bool vec, float (&v)[8]) {
-    if (vec && n >= 8) {
-        load_n<float, 8>(p, 8, v);
+// L elements at p, of which n (any value) are in range.
+template <int L>
+__device__ __forceinline__ void load_l(const float* p, int n, bool vec, float (&v)[L]) {
+    if (vec && n >= L) {
+#pragma unroll
+        for (int i = 0; i < L; i += 4) {
+            const float4 w = *(const float4*)(p + i);
+            v[i] = w.x; v[i + 1] = w.y; v[i + 2] = w.z; v[i + 3] = w.w;
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = i < n ? p[i] : 0.0f;
+        for (int i = 0; i < L; i++) v[i] = i < n ? p[i] : 0.0f;
     }
 }
 
 // ROWS: the first two products, whose sums run along a's rows; b is summed
 // along its rows (BK) or across them.
-template <class TO, bool ROWS, bool BK>
+// T x T sums a block, L x L a thread, in pieces of four.
+template <class TO, bool ROWS, bool BK, int T>
 __global__ void __launch_bounds__(kPThreads) plain_product_kernel(const PlainParams p) {
-    __shared__ __align__(16) float as[kPK][kPT + kPPad], bs[kPK][kPT + kPPad];
+    constexpr int L = T / 16;
+    __shared__ __align__(16) float as[kPK][T + kPPad], bs[kPK][T + kPPad];
     __shared__ int bound[kMaxExperts + 1], tile[kMaxExperts + 1];
     const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
     grid_wait();
     grid_release();
-    if (tid < 32) read_groups(p.offsets, p.E, p.rows, kPT, bound, tile);
+    if (tid < 32) read_groups(p.offsets, p.E, p.rows, T, bound, tile);
     __syncthreads();
-    const int nt = (p.N + kPT - 1) / kPT;
-    const int64_t mt = ROWS ? tile[p.E] : (int64_t)((p.M + kPT - 1) / kPT) * p.E;
+    const int nt = (p.N + T - 1) / T;
+    const int64_t mt = ROWS ? tile[p.E] : (int64_t)((p.M + T - 1) / T) * p.E;
     for (int64_t i = blockIdx.x; i < mt * nt; i += gridDim.x) {
-        const int m = (int)(i / nt), n0 = (int)(i % nt) * kPT;
+        const int m = (int)(i / nt), n0 = (int)(i % nt) * T;
         int e, m0, mlen, K;
         int64_t first;  // ROWS: the tile's first row; else the group's
         if (ROWS) {
             e = group_of(tile, p.E, m);
-            first = bound[e] + (int64_t)(m - tile[e]) * kPT;
+            first = bound[e] + (int64_t)(m - tile[e]) * T;
             m0 = 0;
-            mlen = (int)min((int64_t)kPT, bound[e + 1] - first);
+            mlen = (int)min((int64_t)T, bound[e + 1] - first);
             K = p.K;
         } else {
-            const int per = (p.M + kPT - 1) / kPT;
+            const int per = (p.M + T - 1) / T;
             e = m / per;
-            m0 = (m % per) * kPT;
-            mlen = min(kPT, p.M - m0);
+            m0 = (m % per) * T;
+            mlen = min(T, p.M - m0);
             first = bound[e];
             K = bound[e + 1] - bound[e];
             if (!K && p.accumulate) continue;
         }
-        const int nlen = min(kPT, p.N - n0);
+        const int nlen = min(T, p.N - n0);
         const float* a = (const float*)p.a + first * p.a_stride + m0;
         const float* b = (const float*)p.b + (ROWS ? e * p.b_expert + (BK ? (int64_t)n0 * p.b_stride : n0)
-                                           : first * p.b_stride + n0);
-        // places of this thread's 8 elements: along k (row, k) or along m (k, column)
-        const int kr = tid / 2, kc = (tid % 2) * 8, mr = tid / 16, mc = (tid % 16) * 8;
-        float av[8], bv[8], acc[8][8];
+                                                   : first * p.b_stride + n0);
+        // places of this thread's L elements: along k (row, k) or along m (k, column)
+        const int kr = tid / (16 / L), kc = (tid % (16 / L)) * L, mr = tid / 16, mc = (tid % 16) * L;
+        float av[L], bv[L], acc[L][L];
 #pragma unroll
-        for (int x = 0; x < 8; x++)
+        for (int x = 0; x < L; x++)
 #pragma unroll
-            for (int y = 0; y < 8; y++) acc[x][y] = 0.0f;
+            for (int y = 0; y < L; y++) acc[x][y] = 0.0f;
         auto fetch = [&](int k0) {
-            if (ROWS) load8(a + kr * p.a_stride + k0 + kc, kr < mlen ? K - k0 - kc : 0, p.a_vec, av);
-            else load8(a + (int64_t)(k0 + mr) * p.a_stride + mc, k0 + mr < K ? mlen - mc : 0, p.a_vec, av);
-            if (BK) load8(b + kr * p.b_stride + k0 + kc, kr < nlen ? K - k0 - kc : 0, p.b_vec, bv);
-            else load8(b + (int64_t)(k0 + mr) * p.b_stride + mc, k0 + mr < K ? nlen - mc : 0, p.b_vec, bv);
+            if (ROWS) load_l<L>(a + kr * p.a_stride + k0 + kc, kr < mlen ? K - k0 - kc : 0, p.a_vec, av);
+            else load_l<L>(a + (int64_t)(k0 + mr) * p.a_stride + mc, k0 + mr < K ? mlen - mc : 0, p.a_vec, av);
+            if (BK) load_l<L>(b + kr * p.b_stride + k0 + kc, kr < nlen ? K - k0 - kc : 0, p.b_vec, bv);
+            else load_l<L>(b + (int64_t)(k0 + mr) * p.b_stride + mc, k0 + mr < K ? nlen - mc : 0, p.b_vec, bv);
         };
         if (K) fetch(0);
         for (int k0 = 0; k0 < K; k0 += kPK) {
             __syncthreads();
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
+            for (int j = 0; j < L; j++) {
                 if (ROWS) as[kc + j][kr] = av[j];
                 else as[mr][mc + j] = av[j];
                 if (BK) bs[kc + j][kr] = bv[j];
@@ -162,26 +170,26 @@ __global__ void __launch_bounds__(kPThreads) plain_product_kernel(const PlainPar
             if (k0 + kPK < K) fetch(k0 + kPK);
 #pragma unroll
             for (int k = 0; k < kPK; k++) {
-                float x[8], y[8];
+                float x[L], y[L];
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
+                for (int h = 0; h < L / 4; h++) {
                     const float4 u = *(const float4*)&as[k][h * 64 + ty * 4], w = *(const float4*)&bs[k][h * 64 + tx * 4];
                     x[4 * h] = u.x; x[4 * h + 1] = u.y; x[4 * h + 2] = u.z; x[4 * h + 3] = u.w;
                     y[4 * h] = w.x; y[4 * h + 1] = w.y; y[4 * h + 2] = w.z; y[4 * h + 3] = w.w;
                 }
 #pragma unroll
-                for (int q = 0; q < 8; q++)
+                for (int q = 0; q < L; q++)
 #pragma unroll
-                    for (int r = 0; r < 8; r++) acc[q][r] = fmaf(x[q], y[r], acc[q][r]);
+                    for (int r = 0; r < L; r++) acc[q][r] = fmaf(x[q], y[r], acc[q][r]);
             }
         }
         TO* out = (TO*)p.out + (ROWS ? first * p.out_stride : e * p.out_expert + (int64_t)m0 * p.out_stride) + n0;
 #pragma unroll
-        for (int q = 0; q < 8; q++) {
+        for (int q = 0; q < L; q++) {
             const int row = (q / 4) * 64 + ty * 4 + q % 4;
             if (row >= mlen) continue;
 #pragma unroll
-            for (int r = 0; r < 8; r++) {
+            for (int r = 0; r < L; r++) {
                 const int col = (r / 4) * 64 + tx * 4 + r % 4;
                 if (col >= nlen) continue;
                 TO* at = out + row * p.out_stride + col;
@@ -596,11 +604,15 @@ bool whole(const void* p, size_t stride, size_t expert, int es) {
 
 template <class TO, bool ROWS, bool BK>
 cudaError_t launch_plain(PlainParams p, cudaStream_t stream, int sms) {
-    const int64_t nt = (p.N + kPT - 1) / kPT;
-    const int64_t mt = ROWS ? p.rows / kPT + std::min<int64_t>(p.E, p.rows) + 1 : (int64_t)((p.M + kPT - 1) / kPT) * p.E;
-    const int64_t grid = std::min<int64_t>(mt * nt, (int64_t)sms * 2);
+    const auto tiles = [&](int64_t T) {
+        return (ROWS ? p.rows / T + std::min<int64_t>(p.E, p.rows) + 1 : (p.M + T - 1) / T * p.E) * ((p.N + T - 1) / T);
+    };
+    // tiles of 128 (half the loads a product) while there are two for every SM, of 64 for fewer
+    const bool large = tiles(128) >= 2 * (int64_t)sms;
+    const int64_t grid = std::min<int64_t>(tiles(large ? 128 : 64), (int64_t)sms * (large ? 2 : 4));
     void* args[] = {&p};
-    return launch_op((const void*)plain_product_kernel<TO, ROWS, BK>, dim3((unsigned)grid), dim3(kPThreads), args, 0, stream);
+    const void* fn = large ? (const void*)plain_product_kernel<TO, ROWS, BK, 128> : (const void*)plain_product_kernel<TO, ROWS, BK, 64>;
+    return launch_op(fn, dim3((unsigned)grid), dim3(kPThreads), args, 0, stream);
 }
 template <bool ROWS, bool BK>
 cudaError_t launch_plain(const PlainParams& p, hc_dtype_t out, cudaStream_t stream, int sms) {
@@ -619,16 +631,48 @@ struct PackParams {
     int cols, pitch;            // pitch: of `to`
 };
 constexpr int kPackThreads = 256;
+
+// The 16 bytes that begin s (even) bytes behind the first of two vectors.
+__device__ __forceinline__ uint4 bytes_from(const uint4& u, const uint4& v, int s) {
+    uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+    if (s & 8)
+#pragma unroll
+        for (int i = 0; i < 6; i++) w[i] = w[i + 2];
+    if (s & 4)
+#pragma unroll
+        for (int i = 0; i < 5; i++) w[i] = w[i + 1];
+    const int bits = (s & 2) * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                      __funnelshift_r(w[3], w[4], bits));
+}
+
+// A warp takes a row, a lane eight elements: the aligned vectors that hold
+// them (none without a byte of the row), shifted into place.  What a row's last
+// vector holds behind the row is not read by anyone.
 __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackParams p) {
     grid_wait();
     grid_release();
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, vectors = p.pitch / 8;
     for (int64_t r = (int64_t)blockIdx.x * (kPackThreads / 32) + threadIdx.x / 32; r < p.rows;
          r += (int64_t)gridDim.x * (kPackThreads / 32)) {
-        const Bf16* from = p.from + r / p.per * p.expert + r % p.per * p.stride;
-        Bf16* to = p.to + r * p.pitch;
-#pragma unroll 8
-        for (int c = lane; c < p.cols; c += 32) to[c] = from[c];
+        const int64_t e = r / p.per;
+        const uintptr_t from = (uintptr_t)(p.from + e * p.expert + (r - e * p.per) * p.stride);
+        const uintptr_t end = from + 2 * (uintptr_t)p.cols, base = from & ~(uintptr_t)15;
+        const int s = (int)(from & 15);
+        uint4* to = (uint4*)(p.to + r * p.pitch);
+        for (int c0 = lane; c0 < vectors; c0 += 128) {
+            uint4 u[4], v[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const uintptr_t a = base + 16 * (uintptr_t)(c0 + 32 * k);
+                u[k] = v[k] = make_uint4(0, 0, 0, 0);
+                if (a < end) u[k] = *(const uint4*)a;
+                if (s && a + 16 < end) v[k] = *(const uint4*)(a + 16);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                if (c0 + 32 * k < vectors) to[c0 + 32 * k] = bytes_from(u[k], v[k], s);
+        }
     }
 }
 
