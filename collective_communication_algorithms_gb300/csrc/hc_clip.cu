@@ -28,7 +28,7 @@ constexpr int kChunkBytes = kClipThreads * kClipBatch * 16;
 struct ClipTensor {
     uintptr_t in, out;
     uint64_t count : 56;
-    uint64_t peel : 3;      // elements before the first 8 that lie on whole 16 bytes
+    uint64_t peel : 3;      // elements before the first 8 that lie on whole 16 (bf16) or 32 bytes (fp32)
     uint64_t scalar : 1;    // in and out never do at the same place
     uint64_t in_bf : 1, out_bf : 1;
     uint64_t in_place : 1;
@@ -206,22 +206,21 @@ __device__ __forceinline__ Factor factor_of(const P& p) {
     return Factor{(float)norm, (float)(c * (double)p.scale)};
 }
 
-// Eight elements, which lie on whole 16 bytes in both tensors.
+// Eight elements, which lie on whole 16 bytes (bf16) or 32 (fp32).
 template <bool BF>
 struct Eight {
-    uint4 w[BF ? 1 : 2];
-    __device__ __forceinline__ void load(const uint4* p) {
-#pragma unroll
-        for (int j = 0; j < (BF ? 1 : 2); j++) w[j] = p[j];
-    }
+    uint4 w;
+    __device__ __forceinline__ void load(const uint4* p) { w = *p; }
+    __device__ __forceinline__ void get(float (&v)[8]) const { unpack(w, v); }
+};
+template <>
+struct Eight<false> {
+    ulonglong4_32a w;  // one access of 32 bytes
+    __device__ __forceinline__ void load(const uint4* p) { w = *(const ulonglong4_32a*)p; }
     __device__ __forceinline__ void get(float (&v)[8]) const {
-        if constexpr (BF) {
-            unpack(w[0], v);
-        } else {
-            const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+        const unsigned long long u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int j = 0; j < 8; j++) v[j] = __uint_as_float(u[j]);
-        }
+        for (int j = 0; j < 4; j++) asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2 * j]), "=f"(v[2 * j + 1]) : "l"(u[j]));
     }
 };
 template <bool IB, bool OB>
@@ -233,8 +232,10 @@ __device__ __forceinline__ void scale_eight(const Eight<IB>& x, uint4* out, floa
     if constexpr (OB) {
         *out = pack(v);
     } else {
-        out[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-        out[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+        unsigned long long u[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) asm("mov.b64 %0, {%1, %2};" : "=l"(u[j]) : "f"(v[2 * j]), "f"(v[2 * j + 1]));
+        *(ulonglong4_32a*)out = ulonglong4_32a{u[0], u[1], u[2], u[3]};
     }
 }
 
@@ -350,7 +351,8 @@ ClipTensor describe(const hc_grad_t& g) {
     const int is = t.in_bf ? 2 : 4, os = t.out_bf ? 2 : 4;
     int peel = -1, in_peel = -1;
     for (int k = 0; k < 8; k++) {
-        const bool i = (t.in + (uintptr_t)(k * is)) % 16 == 0, o = (t.out + (uintptr_t)(k * os)) % 16 == 0;
+        // eight elements on whole 16 bytes (bf16) or 32 (fp32)
+        const bool i = (t.in + (uintptr_t)(k * is)) % (8 * is) == 0, o = (t.out + (uintptr_t)(k * os)) % (8 * os) == 0;
         if (i && in_peel < 0) in_peel = k;
         if (i && o && peel < 0) peel = k;
     }

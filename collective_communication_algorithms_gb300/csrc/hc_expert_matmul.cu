@@ -115,7 +115,8 @@ __global__ void __launch_bounds__(kPThreads) plain_product_kernel(const PlainPar
     __shared__ int bound[kMaxExperts + 1], tile[kMaxExperts + 1];
     const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
     grid_wait();
-    grid_release();
+    // no early release: the next kernel's blocks would pile up on the SMs with
+    // room, and stay there (two products in turn: 108 us, against 57 apart)
     if (tid < 32) read_groups(p.offsets, p.E, p.rows, T, bound, tile);
     __syncthreads();
     const int nt = (p.N + T - 1) / T;
@@ -498,9 +499,8 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
             // the tile's place in the output, and the lane's in the warp's part
             TO* out = ROWS ? (TO*)p.out + (t.first + r0) * p.out_stride + t.m0 + m + at
                            : (TO*)p.out + t.e * p.out_expert + (int64_t)(t.m0 + m + r0) * p.out_stride + t.n0 + at;
-            // c: columns of sums; the step's rows and columns of output left for the lane
+            // c: columns of sums; the step's rows of output left for the lane
             const auto rows_left = [&](int c, int j) { return (ROWS ? t.nlen - c : t.mlen - m) - j * V - r0; };
-            const auto cols_left = [&](int c) { return (ROWS ? t.mlen - m : t.nlen - c) - at; };
             const auto place = [&](int c, int j) { return out + (ROWS ? (int64_t)(c + j * V) * p.out_stride : (int64_t)(j * V) * p.out_stride + c); };
             const bool add = !ROWS && p.accumulate;
             // 16-byte accesses of whole steps of columns, without a branch within a
@@ -555,6 +555,18 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
                             *(uint4*)(mine + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                     }
                     __syncwarp();
+                    if (!fast) {  // element by element: a lane has a column
+                        const int rows = (ROWS ? t.nlen - c : t.mlen - m), cols = (ROWS ? t.mlen - m : t.nlen - c);
+                        if (lane < cols) {
+                            TO* to = place(c, 0) - r0 * p.out_stride - at + lane;
+#pragma unroll 8
+                            for (int r = 0; r < min(rows, 32); r++) {
+                                const float x = *(const float*)(mine + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+                                put(to + r * p.out_stride, add ? x + to_f32(to[r * p.out_stride]) : x);
+                            }
+                        }
+                        continue;
+                    }
 #pragma unroll
                     for (int j = 0; j < N; j++) {
                         const int r = j * V + r0;
@@ -567,21 +579,13 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
                             x[4 * g + 2] = __uint_as_float(w.z);
                             x[4 * g + 3] = __uint_as_float(w.w);
                         }
-                        if (fast) {
-                            if (add) {
-                                float y[V];
-                                unpack(old[h][j], y);
+                        if (add) {
+                            float y[V];
+                            unpack(old[h][j], y);
 #pragma unroll
-                                for (int g = 0; g < V; g++) x[g] += y[g];
-                            }
-                            if (rows_left(c, j) > 0) *(uint4*)place(c, j) = pack(x);
-                        } else if (rows_left(c, j) > 0) {
-                            TO* to = place(c, j);
-                            const int left = cols_left(c);
-#pragma unroll
-                            for (int g = 0; g < V; g++)
-                                if (g < left) put(to + g, add ? x[g] + to_f32(to[g]) : x[g]);
+                            for (int g = 0; g < V; g++) x[g] += y[g];
                         }
+                        if (rows_left(c, j) > 0) *(uint4*)place(c, j) = pack(x);
                     }
                     if (add && fast && c + 32 * AHEAD < t.nlen) fetch(c + 32 * AHEAD, old[h]);
                 }
