@@ -4,10 +4,10 @@
 //   norm = |scale| sqrt(sum g^2),  out = scale min(1, max_norm / (norm + eps)) g
 //
 // Bound by bytes: every gradient is read for the norm, read again for the
-// product, and written.  Two kernels: the first leaves one binary64 partial
-// sum a block, the second adds those up in every block (in the same order, so
-// all get the same factor) and scales.  The second goes through the tensors
-// from the end, so that what the first read last still comes from L2.
+// product, and written.  Two kernels: the first leaves one partial sum a block, the second adds those up in every block (in the same order, so
+// all get the same factor) and scales.  A block has the same run of the
+// tensors in both and goes through it forwards, then backwards, so that what
+// it read last still comes from L2.
 //
 // The tensors' table travels in the kernel's parameters (up to 32 KB), so a
 // call needs no copy to the device and can be captured; longer lists take
@@ -22,13 +22,39 @@ namespace hc {
 namespace {
 
 constexpr int kClipThreads = 256;
-constexpr int kClipBatch = 8;        // 16-byte loads of one thread under way
-constexpr int kChunkBytes = kClipThreads * kClipBatch * 16;
+constexpr int kClipBatch = 8;     // 16-byte loads of one thread at a time
+constexpr int kClipResident = 4;  // blocks of an SM, whose loads and stores overlap
+constexpr int kChunkBytes = 16384;  // tensors are divided among blocks in pieces of this
+
+// A sum of squares: binary32 with the error of every addition kept, and a
+// binary64 side for what binary32 squares cannot hold.  Binary64 arithmetic is
+// slow here (about two operations a cycle and SM), and is kept to that side.
+struct SquareSum {
+    float hi, lo;
+    double wide;
+    // s: the sum of some squares.  Between 2^-90 and 2^80 no square of weight
+    // underflowed (one below 2^-126 loses at most 2^-150, against 64 terms that
+    // make 2^-90) and no sum of these overflows; outside, the caller squares in
+    // binary64.
+    static __device__ __forceinline__ bool fits(float s) { return s >= 8.0779357e-28f && s <= 1.2089258e24f; }
+    __device__ __forceinline__ void add(float s) {  // two-sum
+        const float t = __fadd_rn(hi, s);
+        const float b = __fadd_rn(t, -hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(hi, -__fadd_rn(t, -b)), __fadd_rn(s, -b)));
+        hi = t;
+    }
+    __device__ __forceinline__ void add(const SquareSum& o) {
+        add(o.hi);
+        lo = __fadd_rn(lo, o.lo);
+        if (o.wide != 0.0) wide += o.wide;  // a NaN is not 0 either
+    }
+};
+static_assert(sizeof(SquareSum) == 16, "a partial sum's place in scratch");
 
 struct ClipTensor {
     uintptr_t in, out;
     uint64_t count : 56;
-    uint64_t peel : 3;      // elements before the first 8 that lie on whole 16 (bf16) or 32 bytes (fp32)
+    uint64_t peel : 3;      // elements before the first 8 that lie on whole 16 bytes
     uint64_t scalar : 1;    // in and out never do at the same place
     uint64_t in_bf : 1, out_bf : 1;
     uint64_t in_place : 1;
@@ -37,7 +63,7 @@ static_assert(sizeof(ClipTensor) == 24, "ClipTensor layout");
 
 template <int MAXT>
 struct ClipParams {
-    double* part;          // partial sums of all launches
+    SquareSum* part;       // partial sums of all launches
     float* norm;
     float* factor;
     int first_part;        // of this launch
@@ -54,7 +80,7 @@ struct ClipParams {
 constexpr int kFewTensors = 32, kMoreTensors = 256, kMostTensors = 1160;
 static_assert(sizeof(ClipParams<kMostTensors>) <= 32764, "kernel parameters");
 
-// Tensor of a chunk: the first whose last chunk lies behind it.
+// Tensor of a chunk: the first whose chunks end behind it.
 template <class P>
 __device__ __forceinline__ int tensor_of(const P& p, int chunk) {
     int lo = 0, hi = p.num - 1;
@@ -73,24 +99,6 @@ __device__ __forceinline__ void store_one(uintptr_t p, bool bf, uint64_t i, floa
     if (bf) put((Bf16*)p + i, v);
     else ((float*)p)[i] = v;
 }
-
-// A running sum of squares: binary32 with the error of every addition kept,
-// and a binary64 side for what binary32 squares cannot hold.
-struct SquareSum {
-    float hi = 0.0f, lo = 0.0f;
-    double wide = 0.0;
-    // s: the sum of some squares.  Between 2^-90 and 2^100 no square of weight
-    // underflowed (one below 2^-126 loses at most 2^-150, against 64 terms of
-    // 2^-90) and no sum overflows; outside, the caller squares in binary64.
-    static __device__ __forceinline__ bool fits(float s) { return s >= 8.0779357e-28f && s <= 1.2676506e30f; }
-    __device__ __forceinline__ void add(float s) {  // two-sum
-        const float t = __fadd_rn(hi, s);
-        const float b = __fadd_rn(t, -hi);
-        lo = __fadd_rn(lo, __fadd_rn(__fadd_rn(hi, -__fadd_rn(t, -b)), __fadd_rn(s, -b)));
-        hi = t;
-    }
-    __device__ __forceinline__ double total() const { return wide + (double)hi + (double)lo; }
-};
 
 template <bool BF>
 __device__ __forceinline__ void words_of(const uint4& w, float (&v)[BF ? 8 : 4]) {
@@ -135,60 +143,92 @@ __device__ __forceinline__ void add_vectors(SquareSum& q, const uint4 (&w)[kClip
     }
 }
 
+// Elements before and behind a tensor's vectors of V, at most 7 each: f(index)
+// on a thread of its own.
+template <class F>
+__device__ __forceinline__ void for_ends(const ClipTensor& t, int V, F f) {
+    const uint64_t peel = min((uint64_t)t.peel, (uint64_t)t.count), body = (t.count - peel) / V * V;
+    const unsigned tid = threadIdx.x;
+    if (tid < peel) f((uint64_t)tid);
+    else if (tid >= 8 && tid < 16 && peel + body + tid - 8 < t.count) f(peel + body + tid - 8);
+}
+
+// The squares of the chunks [c0, c1) of a tensor.
 template <bool BF>
-__device__ __forceinline__ void add_chunk(SquareSum& q, const ClipTensor& t, int chunk_in_tensor) {
-    const uint64_t body = (t.count - (t.peel < t.count ? t.peel : t.count)) / (BF ? 8 : 4);  // whole vectors
-    const uint4* base = (const uint4*)(t.in + t.peel * (BF ? 2 : 4));
-    const uint64_t start = (uint64_t)chunk_in_tensor * (kClipThreads * kClipBatch);
-    base += start;
-    const int left = (int)min(body > start ? body - start : 0, (uint64_t)(kClipThreads * kClipBatch));
-    uint4 w[kClipBatch];
+__device__ __forceinline__ void add_chunks(SquareSum& q, const ClipTensor& t, int c0, int c1) {
+    constexpr int V = BF ? 8 : 4, CHUNK = kChunkBytes / 16, STEP = kClipThreads * kClipBatch;
+    const uint64_t peel = min((uint64_t)t.peel, (uint64_t)t.count), body = (t.count - peel) / V;  // whole vectors
+    const uint64_t begin = (uint64_t)c0 * CHUNK, end = min((uint64_t)c1 * CHUNK, body);
+    const uint4* base = (const uint4*)(t.in + t.peel * (BF ? 2 : 4)) + begin;
+    // vectors of this thread's column; a block's share of any list that fits
+    // the memory ends well below 2^31
+    const int n = end > begin ? (int)(end - begin) - (int)threadIdx.x : 0;
+    base += threadIdx.x;
+#pragma unroll 1
+    for (int at = 0; at < n; at += STEP) {
+        uint4 w[kClipBatch];
 #pragma unroll
-    for (int i = 0; i < kClipBatch; i++) {
-        const int k = (int)threadIdx.x + i * kClipThreads;
-        w[i] = k < left ? base[k] : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kClipBatch; i++) {
+            w[i] = make_uint4(0, 0, 0, 0);
+            if (at + i * kClipThreads < n) w[i] = base[at + i * kClipThreads];
+        }
+        add_vectors<BF>(q, w);
     }
-    add_vectors<BF>(q, w);
-    if (chunk_in_tensor == 0) {  // what lies before and behind the vectors: at most 7 elements each
-        const int tid = threadIdx.x;
-        const uint64_t tail = t.peel + body * (BF ? 8 : 4);
-        uint64_t i = t.count;
-        if (tid < 8) i = tid < (int)t.peel ? tid : t.count;
-        else if (tid < 16) i = tail + tid - 8;
-        if (i < t.count) {
+    if (c0 == 0)
+        for_ends(t, V, [&](uint64_t i) {
             const double v = load_one(t.in, BF, i);
             q.wide = fma(v, v, q.wide);
-        }
+        });
+}
+
+// The chunks of a block, tensor by tensor: f(tensor, its chunks c0, c1), from
+// the first on or from the last.
+template <bool FORWARDS, class P, class F>
+__device__ __forceinline__ void for_block(const P& p, F f) {
+    const int from = (int)((int64_t)p.chunks * blockIdx.x / gridDim.x), to = (int)((int64_t)p.chunks * (blockIdx.x + 1) / gridDim.x);
+    if (from >= to) return;
+    int k = tensor_of(p, FORWARDS ? from : to - 1);
+    for (int c = FORWARDS ? from : to; FORWARDS ? c < to : c > from; k += FORWARDS ? 1 : -1) {
+        const int first = k ? p.chunk_end[k - 1] : 0, last = p.chunk_end[k];
+        const int lo = max(from, first), hi = min(to, last);
+        if (lo < hi) f(p.t[k], lo - first, hi - first);
+        c = FORWARDS ? hi : lo;
     }
 }
 
-__device__ __forceinline__ double block_sum(double v) {
-    __shared__ double sh[kClipThreads / 32];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+// The sum over `lanes` lanes (a power of two), in the first of them.
+__device__ __forceinline__ void lanes_sum(SquareSum& q, int lanes) {
+    for (int o = lanes / 2; o > 0; o >>= 1) {
+        SquareSum x;
+        x.hi = __shfl_down_sync(0xFFFFFFFFu, q.hi, o);
+        x.lo = __shfl_down_sync(0xFFFFFFFFu, q.lo, o);
+        x.wide = __shfl_down_sync(0xFFFFFFFFu, q.wide, o);
+        q.add(x);
+    }
+}
+// The sum over the block's threads, in the first.
+__device__ __forceinline__ void block_sum(SquareSum& q) {
+    __shared__ SquareSum sh[kClipThreads / 32];
+    lanes_sum(q, 32);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = q;
     __syncthreads();
-    double s = 0.0;
-#pragma unroll
-    for (int i = 0; i < kClipThreads / 32; i++) s += sh[i];
-    return s;
+    if (threadIdx.x < 32) {
+        q = sh[threadIdx.x % (kClipThreads / 32)];
+        lanes_sum(q, kClipThreads / 32);
+    }
 }
 
-// 64 registers: four blocks an SM.
 template <int MAXT>
-__global__ void __launch_bounds__(kClipThreads, 4) square_kernel(const __grid_constant__ ClipParams<MAXT> p) {
+__global__ void __launch_bounds__(kClipThreads, kClipResident) square_kernel(const __grid_constant__ ClipParams<MAXT> p) {
     grid_wait();
     grid_release();
-    SquareSum q;
-    for (int c = blockIdx.x; c < p.chunks; c += gridDim.x) {
-        const int k = tensor_of(p, c);
-        const ClipTensor t = p.t[k];
-        const int first = k ? p.chunk_end[k - 1] : 0;
-        if (t.in_bf) add_chunk<true>(q, t, c - first);
-        else add_chunk<false>(q, t, c - first);
-    }
-    const double s = block_sum(q.total());
-    if (threadIdx.x == 0) p.part[p.first_part + blockIdx.x] = s;
+    SquareSum q = {0.0f, 0.0f, 0.0};
+    for_block<true>(p, [&](const ClipTensor& t, int c0, int c1) {
+        if (t.in_bf) add_chunks<true>(q, t, c0, c1);
+        else add_chunks<false>(q, t, c0, c1);
+    });
+    block_sum(q);
+    if (threadIdx.x == 0) p.part[p.first_part + blockIdx.x] = q;
 }
 
 struct Factor {
@@ -197,83 +237,94 @@ struct Factor {
 // Every block adds the partial sums up in the same order.
 template <class P>
 __device__ __forceinline__ Factor factor_of(const P& p) {
-    double s = 0.0;
-    for (int i = threadIdx.x; i < p.parts; i += kClipThreads) s += p.part[i];
-    s = block_sum(s);
-    const double norm = sqrt(s) * fabs((double)p.scale);
-    double c = isinf(p.max_norm) ? 1.0 : (double)p.max_norm / (norm + (double)p.eps);
-    if (c > 1.0) c = 1.0;  // a NaN stays
-    return Factor{(float)norm, (float)(c * (double)p.scale)};
+    __shared__ Factor f;
+    SquareSum q = {0.0f, 0.0f, 0.0};
+    for (int i = threadIdx.x; i < p.parts; i += kClipThreads) q.add(p.part[i]);
+    block_sum(q);
+    if (threadIdx.x == 0) {
+        const float norm = __fsqrt_rn(__fadd_rn(q.hi, q.lo)), scaled = norm * fabsf(p.scale), limit = p.max_norm;
+        // all that follows lies well inside binary32's range
+        const auto middling = [](float v) { return v > 1e-18f && v < 1e18f; };
+        if (q.wide == 0.0 && middling(scaled) && middling(fabsf(p.scale)) && (middling(limit) || isinf(limit))) {
+            f.norm = scaled;
+            f.factor = fminf(1.0f, __fdiv_rn(limit, scaled + p.eps)) * p.scale;
+        } else {
+            const double n = sqrt(q.wide + (double)q.hi + (double)q.lo) * fabs((double)p.scale);
+            double c = isinf(limit) ? 1.0 : (double)limit / (n + (double)p.eps);
+            if (c > 1.0) c = 1.0;  // a NaN stays
+            f.norm = (float)n;
+            f.factor = (float)(c * (double)p.scale);
+        }
+    }
+    __syncthreads();
+    return f;
 }
 
-// Eight elements, which lie on whole 16 bytes (bf16) or 32 (fp32).
+// Eight elements, which lie on whole 16 bytes in both tensors.
 template <bool BF>
 struct Eight {
-    uint4 w;
-    __device__ __forceinline__ void load(const uint4* p) { w = *p; }
-    __device__ __forceinline__ void get(float (&v)[8]) const { unpack(w, v); }
-};
-template <>
-struct Eight<false> {
-    ulonglong4_32a w;  // one access of 32 bytes
-    __device__ __forceinline__ void load(const uint4* p) { w = *(const ulonglong4_32a*)p; }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        const unsigned long long u[4] = {w.x, w.y, w.z, w.w};
+    uint4 w[BF ? 1 : 2];
+    __device__ __forceinline__ void load(const uint4* p, uint64_t policy) {
 #pragma unroll
-        for (int j = 0; j < 4; j++) asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2 * j]), "=f"(v[2 * j + 1]) : "l"(u[j]));
+        for (int j = 0; j < (BF ? 1 : 2); j++) w[j] = ld_vec_hint((uintptr_t)(p + j), policy);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        if constexpr (BF) {
+            unpack(w[0], v);
+        } else {
+            const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[j] = __uint_as_float(u[j]);
+        }
     }
 };
 template <bool IB, bool OB>
-__device__ __forceinline__ void scale_eight(const Eight<IB>& x, uint4* out, float f) {
+__device__ __forceinline__ void scale_eight(const Eight<IB>& x, uint4* out, float f, uint64_t policy) {
     float v[8];
     x.get(v);
 #pragma unroll
     for (int j = 0; j < 8; j++) v[j] *= f;
     if constexpr (OB) {
-        *out = pack(v);
+        st_vec_hint((uintptr_t)out, pack(v), policy);
     } else {
-        unsigned long long u[4];
-#pragma unroll
-        for (int j = 0; j < 4; j++) asm("mov.b64 %0, {%1, %2};" : "=l"(u[j]) : "f"(v[2 * j]), "f"(v[2 * j + 1]));
-        *(ulonglong4_32a*)out = ulonglong4_32a{u[0], u[1], u[2], u[3]};
+        const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
+        st_vec_hint((uintptr_t)out, pack(lo), policy);
+        st_vec_hint((uintptr_t)(out + 1), pack(hi), policy);
     }
 }
 
+// The chunks [c0, c1) of a tensor, from the last on.
 template <bool IB, bool OB>
-__device__ __noinline__ void scale_chunk(uintptr_t tin, uintptr_t tout, uint64_t count, unsigned peel, int chunk, float f) {
-    constexpr int VI = IB ? 1 : 2, VO = OB ? 1 : 2;      // 16-byte accesses of 8 elements
-    constexpr int N = IB ? kClipBatch : kClipBatch / 2;  // places of a thread
-    if (peel > count) peel = (unsigned)count;
-    const uint64_t body = (count - peel) / 8;
-    const uint64_t start = (uint64_t)chunk * (kClipThreads * N);
-    const uint4* in = (const uint4*)(tin + peel * (IB ? 2 : 4)) + start * VI;
-    uint4* out = (uint4*)(tout + peel * (OB ? 2 : 4)) + start * VO;
-    const int left = (int)min(body > start ? body - start : 0, (uint64_t)(kClipThreads * N));
-    const int tid = threadIdx.x;
-    if (left == kClipThreads * N) {
-        Eight<IB> x[N];
+__device__ __forceinline__ void scale_chunks(const ClipTensor& t, int c0, int c1, float f, uint64_t policy) {
+    constexpr int VI = IB ? 1 : 2, VO = OB ? 1 : 2;                // 16-byte vectors of 8 elements
+    constexpr int N = IB ? kClipBatch : kClipBatch / 2, STEP = kClipThreads * N;  // places of a thread, of a step
+    constexpr int CHUNK = kChunkBytes / 16 / VI;
+    const uint64_t peel = min((uint64_t)t.peel, (uint64_t)t.count), body = (t.count - peel) / 8;
+    const uint64_t begin = (uint64_t)c0 * CHUNK, end = min((uint64_t)c1 * CHUNK, body);
+    const uint4* in = (const uint4*)(t.in + peel * (IB ? 2 : 4)) + (begin + threadIdx.x) * VI;
+    uint4* out = (uint4*)(t.out + peel * (OB ? 2 : 4)) + (begin + threadIdx.x) * VO;
+    const int all = end > begin ? (int)(end - begin) : 0;
+    const int n = all - (int)threadIdx.x;
+    if (n > 0) {
+        int at = (all - 1) / STEP * STEP;
+        const auto step = [&](bool whole) {
+            Eight<IB> x[N];
 #pragma unroll
-        for (int i = 0; i < N; i++) x[i].load(in + (tid + i * kClipThreads) * VI);
+            for (int i = 0; i < N; i++)  // beyond the end: the last place again
+                x[i].load(in + (whole ? at + i * kClipThreads : min(at + i * kClipThreads, n - 1)) * VI, policy);
 #pragma unroll
-        for (int i = 0; i < N; i++) scale_eight<IB, OB>(x[i], out + (tid + i * kClipThreads) * VO, f);
-    } else {
+            for (int i = 0; i < N; i++)
+                if (whole || at + i * kClipThreads < n) scale_eight<IB, OB>(x[i], out + (at + i * kClipThreads) * VO, f, policy);
+        };
+        step(false);
 #pragma unroll 1
-        for (int k = tid; k < left; k += kClipThreads) {
-            Eight<IB> x;
-            x.load(in + k * VI);
-            scale_eight<IB, OB>(x, out + k * VO, f);
-        }
+        for (at -= STEP; at >= 0; at -= STEP) step(true);
     }
-    if (chunk == 0) {
-        uint64_t i = count;
-        if (tid < 8) i = tid < (int)peel ? tid : count;
-        else if (tid < 16) i = peel + body * 8 + tid - 8;
-        if (i < count) store_one(tout, OB, i, load_one(tin, IB, i) * f);
-    }
+    if (c0 == 0) for_ends(t, 8, [&](uint64_t i) { store_one(t.out, OB, i, load_one(t.in, IB, i) * f); });
 }
 
 template <int MAXT>
-__global__ void __launch_bounds__(kClipThreads, 4) scale_kernel(const __grid_constant__ ClipParams<MAXT> p) {
+__global__ void __launch_bounds__(kClipThreads, kClipResident) scale_kernel(const __grid_constant__ ClipParams<MAXT> p) {
     grid_wait();
     grid_release();
     const Factor f = factor_of(p);
@@ -281,25 +332,24 @@ __global__ void __launch_bounds__(kClipThreads, 4) scale_kernel(const __grid_con
         *p.norm = f.norm;
         if (p.factor) *p.factor = f.factor;
     }
-    for (int c = p.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
-        const int k = tensor_of(p, c);
-        const ClipTensor t = p.t[k];
-        if (t.in_place && f.factor == 1.0f) continue;
-        const int n = c - (k ? p.chunk_end[k - 1] : 0);
+    // neither what is read for the last time nor what is written stays in L2 in
+    // the place of gradients that are still to be read
+    const uint64_t policy = l2_evict_first_policy();
+    for_block<false>(p, [&](const ClipTensor& t, int c0, int c1) {
+        if (t.in_place && f.factor == 1.0f) return;
         if (t.scalar) {
-            const uint64_t per = kChunkBytes / (t.in_bf ? 2 : 4);
-            const uint64_t end = min((uint64_t)t.count, (uint64_t)(n + 1) * per);
+            const uint64_t per = kChunkBytes / (t.in_bf ? 2 : 4), end = min((uint64_t)t.count, c1 * per);
 #pragma unroll 4
-            for (uint64_t i = (uint64_t)n * per + threadIdx.x; i < end; i += kClipThreads)
+            for (uint64_t i = c0 * per + threadIdx.x; i < end; i += kClipThreads)
                 store_one(t.out, t.out_bf, i, load_one(t.in, t.in_bf, i) * f.factor);
         } else if (t.in_bf) {
-            if (t.out_bf) scale_chunk<true, true>(t.in, t.out, t.count, t.peel, n, f.factor);
-            else scale_chunk<true, false>(t.in, t.out, t.count, t.peel, n, f.factor);
+            if (t.out_bf) scale_chunks<true, true>(t, c0, c1, f.factor, policy);
+            else scale_chunks<true, false>(t, c0, c1, f.factor, policy);
         } else {
-            if (t.out_bf) scale_chunk<false, true>(t.in, t.out, t.count, t.peel, n, f.factor);
-            else scale_chunk<false, false>(t.in, t.out, t.count, t.peel, n, f.factor);
+            if (t.out_bf) scale_chunks<false, true>(t, c0, c1, f.factor, policy);
+            else scale_chunks<false, false>(t, c0, c1, f.factor, policy);
         }
-    }
+    });
 }
 
 template <int MAXT>
@@ -317,7 +367,7 @@ int64_t chunks_of(const hc_grad_t& g) {
 
 // Launches of a list: runs of tensors that fit a table, and the partial sums
 // of each.  A block has at least one chunk, and several once all SMs are full.
-constexpr int kClipMaxBlocks = 152 * 4;
+constexpr int kClipMaxBlocks = 152 * kClipResident;
 int clip_blocks(int64_t chunks) { return (int)std::min<int64_t>(chunks, kClipMaxBlocks); }
 
 template <class F>
@@ -351,8 +401,7 @@ ClipTensor describe(const hc_grad_t& g) {
     const int is = t.in_bf ? 2 : 4, os = t.out_bf ? 2 : 4;
     int peel = -1, in_peel = -1;
     for (int k = 0; k < 8; k++) {
-        // eight elements on whole 16 bytes (bf16) or 32 (fp32)
-        const bool i = (t.in + (uintptr_t)(k * is)) % (8 * is) == 0, o = (t.out + (uintptr_t)(k * os)) % (8 * os) == 0;
+        const bool i = (t.in + (uintptr_t)(k * is)) % 16 == 0, o = (t.out + (uintptr_t)(k * os)) % 16 == 0;
         if (i && in_peel < 0) in_peel = k;
         if (i && o && peel < 0) peel = k;
     }
@@ -365,7 +414,7 @@ template <int MAXT>
 cudaError_t launch_run(const hc_clip_grads_t& a, size_t at, size_t n, int64_t chunks, int stage, int first_part,
                        int parts, bool last, cudaStream_t stream) {
     ClipParams<MAXT> p;
-    p.part = (double*)a.scratch;
+    p.part = (SquareSum*)a.scratch;
     p.norm = a.norm;
     p.factor = a.factor;
     p.first_part = first_part;
@@ -373,8 +422,8 @@ cudaError_t launch_run(const hc_clip_grads_t& a, size_t at, size_t n, int64_t ch
     p.num = (int)n;
     p.chunks = (int)chunks;
     p.scale = a.scale;
-    p.max_norm = a.max_norm;
-    p.eps = a.eps;
+    p.max_norm = stage == 2 ? INFINITY : a.max_norm;  // the norm alone
+    p.eps = stage == 2 ? 0.0f : a.eps;
     p.write_norm = last;
     int end = 0;
     for (size_t i = 0; i < n; i++) {
@@ -405,7 +454,7 @@ size_t clip_scratch_bytes(const hc_clip_grads_t& a) {
             return cudaSuccess;
         }) != cudaSuccess)
         return 0;
-    return parts * sizeof(double);
+    return parts * sizeof(SquareSum);
 }
 
 cudaError_t launch_clip(const hc_clip_grads_t& a, bool apply, cudaStream_t stream) {
