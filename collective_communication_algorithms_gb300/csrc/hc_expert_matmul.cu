@@ -200,6 +200,111 @@ __global__ void __launch_bounds__(kPThreads) plain_product_kernel(const PlainPar
     }
 }
 
+// The 16 bytes that begin s (even) bytes behind the first of two vectors.
+__device__ __forceinline__ uint4 bytes_from(const uint4& u, const uint4& v, int s) {
+    uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+    if (s & 8)
+#pragma unroll
+        for (int i = 0; i < 6; i++) w[i] = w[i + 2];
+    if (s & 4)
+#pragma unroll
+        for (int i = 0; i < 5; i++) w[i] = w[i + 1];
+    const int bits = (s & 2) * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                      __funnelshift_r(w[3], w[4], bits));
+}
+
+// ---------------------------------------------------------------------------
+// bf16 products of few rows (of all groups together), the weight summed along
+// its rows
+//
+// Bound by the bytes of the weights that have rows: a warp takes a row of the
+// weight, in aligned vectors of 16 bytes wherever it begins, and multiplies it
+// by up to four of the group's rows, which lie in shared memory.  One token
+// through two experts of 4096 x 1024: 16.8 MB.
+// ---------------------------------------------------------------------------
+constexpr size_t kFewRows = 16, kFewDim = 8192;
+constexpr int kFewThreads = 256, kFewAtOnce = 4, kFewBatch = 4;
+
+struct FewParams {
+    const Bf16* x;
+    const Bf16* w;
+    void* out;
+    const int32_t* offsets;
+    int64_t rows, x_stride, w_stride, w_expert, out_stride;
+    int E, N, K;
+};
+
+template <class TO>
+__global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ int bound[kMaxExperts + 1], before[kMaxExperts + 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    grid_wait();
+    grid_release();
+    if (warp == 0) read_groups(p.offsets, p.E, p.rows, 1 << 30, bound, before);  // before: groups with rows
+    __syncthreads();
+    if ((int)blockIdx.y >= before[p.E]) return;
+    const int e = group_of(before, p.E, blockIdx.y), o = blockIdx.x * (kFewThreads / 32) + warp;
+    const int vectors = (p.K + 7) / 8;
+    const uintptr_t from = (uintptr_t)(p.w + e * p.w_expert + min(o, p.N - 1) * p.w_stride), end = from + 2 * (uintptr_t)p.K;
+    const uintptr_t base = from & ~(uintptr_t)15;
+    const int shift = (int)(from & 15);
+    Bf16* xs = (Bf16*)smem;  // kFewAtOnce rows of whole vectors
+    for (int r0 = bound[e]; r0 < bound[e + 1]; r0 += kFewAtOnce) {
+        const int n = min(kFewAtOnce, bound[e + 1] - r0);
+        uint4 u[kFewBatch], v[kFewBatch];
+        const auto load = [&](int c0) {
+#pragma unroll
+            for (int k = 0; k < kFewBatch; k++) {
+                const uintptr_t a = base + 16 * (uintptr_t)(c0 + 32 * k);
+                u[k] = v[k] = make_uint4(0, 0, 0, 0);
+                if (a < end) u[k] = *(const uint4*)a;
+                if (shift && a + 16 < end) v[k] = *(const uint4*)(a + 16);
+            }
+        };
+        load(lane);
+        __syncthreads();  // the rows before have been read
+        for (int r = 0; r < kFewAtOnce; r++)
+            for (int c = threadIdx.x; c < vectors * 8; c += kFewThreads)
+                xs[r * vectors * 8 + c] = r < n && c < p.K ? p.x[(int64_t)(r0 + r) * p.x_stride + c] : Bf16{0};
+        __syncthreads();
+        float acc[kFewAtOnce];
+#pragma unroll
+        for (int r = 0; r < kFewAtOnce; r++) acc[r] = 0.0f;
+        for (int c0 = lane; c0 < vectors; c0 += 32 * kFewBatch) {
+            if (c0 != lane) load(c0);
+#pragma unroll
+            for (int k = 0; k < kFewBatch; k++) {
+                const int c = c0 + 32 * k;
+                if (c >= vectors) continue;
+                float w[8];
+                unpack(bytes_from(u[k], v[k], shift), w);
+                if (c * 8 + 8 > p.K)  // behind the row lies another's
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        if (c * 8 + i >= p.K) w[i] = 0.0f;
+#pragma unroll
+                for (int r = 0; r < kFewAtOnce; r++) {
+                    float y[8];
+                    unpack(((const uint4*)xs)[r * vectors + c], y);
+#pragma unroll
+                    for (int i = 0; i < 8; i++) acc[r] = fmaf(w[i], y[i], acc[r]);
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kFewAtOnce; r++) acc[r] = warp_sum(acc[r]);
+        if (lane == 0 && o < p.N)
+#pragma unroll
+            for (int r = 0; r < kFewAtOnce; r++)
+                if (r < n) put((TO*)p.out + (int64_t)(r0 + r) * p.out_stride + o, acc[r]);
+    }
+}
+
+// Whether the first two products take that kernel.
+bool few_rows(size_t rows, size_t K, bool along) { return along && rows <= kFewRows && K <= kFewDim; }
+
 // ---------------------------------------------------------------------------
 // bf16 products on the tensor cores
 //
@@ -329,7 +434,8 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
     }
     if (warp == 2) tmem_alloc<G>(&bar.tmem, 2 * T);
     grid_wait();
-    grid_release();
+    // no early release: the next kernel's blocks would take up registers beside
+    // this one's and wait there
     if (warp == 3) read_groups(p.offsets, p.E, p.rows, T, bound, tile);
     tensor_fence_before();
     __syncthreads();
@@ -343,6 +449,19 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
     const int64_t tiles = (ROWS ? (int64_t)tile[p.E] : (int64_t)((p.M + T - 1) / T) * p.E) * across;
     const int64_t step = gridDim.x / G;
     const auto expired = [&] { atomicExch(p.err, (int)HC_ERR_TIMEOUT); };
+    // A whole warp's wait: one lane polls, and the warp is together again
+    // afterwards, as elections and loads from tensor memory need it, with one
+    // answer for all.
+    const auto warp_wait = [&](auto wait) {
+        bool ok = true;
+        if (lane == 0) {
+            ok = wait();
+            if (!ok) expired();
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
+        __syncwarp();  // what the lane has seen, all have
+        return ok;
+    };
 
     if (warp == 0 && lane == 0) {  // copies
         Ring at;
@@ -396,18 +515,24 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
                 }
             }
         }
-        // a block does not leave while copies into its shared memory are under
-        // way: the first block waits for those of both (the other leaves after it)
-        for (int s = 0; s < issued; s++) {
-            if (raw_used >> s & 1) {
-                mbar_wait_quick(&bar.raw[s], (raw_phase >> s & 1) ^ 1, kWaitLimitNs);
-            } else if (rank == 0) {
-                if (p.hold) mbar_arrive(&bar.full[s]);
-                mbar_wait_quick(&bar.full[s], turns >> s & 1, kWaitLimitNs);
+        // A block does not leave while copies into its shared memory are under
+        // way, nor before the last arrivals on its barriers: those of finished
+        // products come by themselves, from the first block to both, and one that
+        // came late would find the next block's barriers in this one's place.
+        for (int s = 0; ok && s < issued; s++)
+            if (!(ok = mbar_wait_quick(&bar.empty[s], turns >> s & 1, p.wait_ns))) expired();
+        if (!ok) {  // the first block waits for the copies of both
+            for (int s = 0; s < issued; s++) {
+                if (raw_used >> s & 1) {
+                    mbar_wait_quick(&bar.raw[s], (raw_phase >> s & 1) ^ 1, kWaitLimitNs);
+                } else if (rank == 0) {
+                    if (p.hold) mbar_arrive(&bar.full[s]);
+                    mbar_wait_quick(&bar.full[s], turns >> s & 1, kWaitLimitNs);
+                }
             }
+            if (G > 1)  // and either for some time beyond any copy's or arrival's
+                for (const unsigned long long t0 = global_ns(); global_ns() - t0 < kTestWaitLimitNs;) {}
         }
-        if (G > 1 && !ok)  // and if either has given up, some time beyond any copy's
-            for (const unsigned long long t0 = global_ns(); global_ns() - t0 < kTestWaitLimitNs;) {}
     } else if (warp == 1 && rank == 0) {  // products
         // 16 steps of the sum further on, in units of a descriptor's address
         constexpr bool AK = ROWS && WK, BK = ROWS;  // summed along rows in shared memory
@@ -422,11 +547,11 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
             const TensorTile t = tensor_tile<ROWS, T>(p, bound, tile, i, across);
             if (!t.K) continue;
             const uint32_t set = n & 1, sums = tmem + set * T, shape = product_shape(!AK, !BK, T, t.n());
-            if (!(ok = first_wait<G>(&bar.sums_empty[set], ((n >> 1) & 1) ^ 1, p.wait_ns))) break;
+            if (!(ok = warp_wait([&] { return first_wait<G>(&bar.sums_empty[set], ((n >> 1) & 1) ^ 1, p.wait_ns); }))) break;
             tensor_fence_after();
             for (int k0 = 0; k0 < t.K; k0 += kTK, at.next()) {
                 const int s = at.s;
-                if (!(ok = mbar_wait_quick(&bar.full[s], at.turn, p.wait_ns))) break;
+                if (!(ok = warp_wait([&] { return mbar_wait_quick(&bar.full[s], at.turn, p.wait_ns); }))) break;
                 tensor_fence_after();
                 const uint64_t a = a0 + (uint32_t)(s * (kTStageBytes >> 4)), b = b0 + (uint32_t)(s * (kTStageBytes >> 4));
                 if (elected()) {
@@ -446,10 +571,9 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
             __syncwarp();
             n++;
         }
-        if (!ok && lane == 0) expired();
         if (elected()) products_arrive<G>(&bar.drain, false);  // tensor memory is freed after the last products
         __syncwarp();
-        mbar_wait_quick(&bar.drain, 0, kWaitLimitNs);
+        if (lane == 0) mbar_wait_quick(&bar.drain, 0, kWaitLimitNs);
     } else if (!ROWS && warp == 3) {  // zeros behind the last row of a group
         Ring at;
         uint32_t phase = 0, zeroed = 0;
@@ -460,10 +584,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
             if (!rest) continue;
             const int s = at.s;
             at.next();
-            if (!mbar_wait_quick(&bar.raw[s], phase >> s & 1, p.wait_ns)) {
-                if (lane == 0) expired();
-                break;
-            }
+            if (!warp_wait([&] { return mbar_wait_quick(&bar.raw[s], phase >> s & 1, p.wait_ns); })) break;
             phase ^= 1u << s;
             const int zeros = (16 - rest % 16) % 16 * 8;  // rows that a product reads, 16 bytes each
             for (int j = lane; j < zeros * (kTStageBytes / 8192); j += 32)  // in all boxes
@@ -474,12 +595,8 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
                 if (lane == 0) first_arrive<G>(&bar.zeroed);
             } else {
                 if (G > 1) {
-                    if (!first_wait<G>(&bar.zeroed, zeroed & 1, p.wait_ns)) {
-                        if (lane == 0) expired();
-                        break;
-                    }
+                    if (!warp_wait([&] { return first_wait<G>(&bar.zeroed, zeroed & 1, p.wait_ns); })) break;
                     zeroed++;
-                    __syncwarp();
                 }
                 if (lane == 0) mbar_arrive(&bar.full[s]);
             }
@@ -503,25 +620,23 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
             const auto rows_left = [&](int c, int j) { return (ROWS ? t.nlen - c : t.mlen - m) - j * V - r0; };
             const auto place = [&](int c, int j) { return out + (ROWS ? (int64_t)(c + j * V) * p.out_stride : (int64_t)(j * V) * p.out_stride + c); };
             const bool add = !ROWS && p.accumulate;
-            // 16-byte accesses of whole steps of columns, without a branch within a
-            // lane's rows: those would keep loads from overlapping
-            const bool fast = p.out_vec && (ROWS ? t.mlen - m >= 32 : t.nlen % 32 == 0);
+            const auto cols_left = [&](int c) { return ROWS ? t.mlen - m : t.nlen - c; };
+            // 16-byte accesses, of which a lane makes all or none at its columns:
+            // branches about parts of them would keep loads from overlapping
+            const bool fast = p.out_vec && (ROWS ? t.mlen : t.nlen) % V == 0;
             constexpr int AHEAD = ROWS ? 1 : 4;  // steps of 32 columns that what is added to is loaded ahead
             uint4 old[AHEAD][N];
             const auto fetch = [&](int c, uint4 (&v)[N]) {
 #pragma unroll
                 for (int j = 0; j < N; j++)
-                    if (rows_left(c, j) > 0) v[j] = *(const uint4*)place(c, j);
+                    if (rows_left(c, j) > 0 && at < cols_left(c)) v[j] = *(const uint4*)place(c, j);
             };
             if (add && fast)
 #pragma unroll
                 for (int h = 0; h < AHEAD; h++)
                     if (h * 32 < t.nlen) fetch(h * 32, old[h]);
             if (t.K) {
-                if (!mbar_wait_quick(&bar.sums_full[set], (n >> 1) & 1, p.wait_ns)) {
-                    if (lane == 0) expired();
-                    break;
-                }
+                if (!warp_wait([&] { return mbar_wait_quick(&bar.sums_full[set], (n >> 1) & 1, p.wait_ns); })) break;
                 tensor_fence_after();
                 n++;
             }
@@ -556,15 +671,21 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
                     }
                     __syncwarp();
                     if (!fast) {  // element by element: a lane has a column
-                        const int rows = (ROWS ? t.nlen - c : t.mlen - m), cols = (ROWS ? t.mlen - m : t.nlen - c);
-                        if (lane < cols) {
-                            TO* to = place(c, 0) - r0 * p.out_stride - at + lane;
-#pragma unroll 8
-                            for (int r = 0; r < min(rows, 32); r++) {
-                                const float x = *(const float*)(mine + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
-                                put(to + r * p.out_stride, add ? x + to_f32(to[r * p.out_stride]) : x);
+                        const int rows = min(32, ROWS ? t.nlen - c : t.mlen - m);
+                        TO* to = place(c, 0) - r0 * p.out_stride - at + lane;
+                        if (lane < cols_left(c))
+#pragma unroll
+                            for (int r0 = 0; r0 < 32; r0 += 16) {
+                                float y[16];
+#pragma unroll
+                                for (int r = 0; r < 16; r++) y[r] = add && r0 + r < rows ? to_f32(to[(r0 + r) * p.out_stride]) : 0.0f;
+#pragma unroll
+                                for (int r = 0; r < 16; r++) {
+                                    const float x = *(const float*)(mine + (r0 + r) * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+                                    if (r0 + r < rows) put(to + (r0 + r) * p.out_stride, x + y[r]);
+                                }
                             }
-                        }
+                        __syncwarp();
                         continue;
                     }
 #pragma unroll
@@ -585,7 +706,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
 #pragma unroll
                             for (int g = 0; g < V; g++) x[g] += y[g];
                         }
-                        if (rows_left(c, j) > 0) *(uint4*)place(c, j) = pack(x);
+                        if (rows_left(c, j) > 0 && at < cols_left(c)) *(uint4*)place(c, j) = pack(x);
                     }
                     if (add && fast && c + 32 * AHEAD < t.nlen) fetch(c + 32 * AHEAD, old[h]);
                 }
@@ -627,28 +748,21 @@ cudaError_t launch_plain(const PlainParams& p, hc_dtype_t out, cudaStream_t stre
 // operands that tiled copies cannot take (pointers or strides that are not
 // whole 16 bytes) are copied row by row into scratch first
 // ---------------------------------------------------------------------------
-struct PackParams {
+struct PackJob {
     const Bf16* from;
     Bf16* to;
     int64_t rows, per;          // rows in all, rows of one expert
     int64_t stride, expert;     // of `from`
     int cols, pitch;            // pitch: of `to`
+    int weights;                // experts without rows are left out
+};
+constexpr int kPackJobs = 3;
+struct PackParams {
+    PackJob job[kPackJobs];
+    const int32_t* offsets;
+    int jobs;
 };
 constexpr int kPackThreads = 256;
-
-// The 16 bytes that begin s (even) bytes behind the first of two vectors.
-__device__ __forceinline__ uint4 bytes_from(const uint4& u, const uint4& v, int s) {
-    uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-    if (s & 8)
-#pragma unroll
-        for (int i = 0; i < 6; i++) w[i] = w[i + 2];
-    if (s & 4)
-#pragma unroll
-        for (int i = 0; i < 5; i++) w[i] = w[i + 1];
-    const int bits = (s & 2) * 8;
-    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
-                      __funnelshift_r(w[3], w[4], bits));
-}
 
 // A warp takes a row, a lane eight elements: the aligned vectors that hold
 // them (none without a byte of the row), shifted into place.  What a row's last
@@ -656,26 +770,32 @@ __device__ __forceinline__ uint4 bytes_from(const uint4& u, const uint4& v, int 
 __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackParams p) {
     grid_wait();
     grid_release();
-    const int lane = threadIdx.x & 31, vectors = p.pitch / 8;
-    for (int64_t r = (int64_t)blockIdx.x * (kPackThreads / 32) + threadIdx.x / 32; r < p.rows;
-         r += (int64_t)gridDim.x * (kPackThreads / 32)) {
-        const int64_t e = r / p.per;
-        const uintptr_t from = (uintptr_t)(p.from + e * p.expert + (r - e * p.per) * p.stride);
-        const uintptr_t end = from + 2 * (uintptr_t)p.cols, base = from & ~(uintptr_t)15;
-        const int s = (int)(from & 15);
-        uint4* to = (uint4*)(p.to + r * p.pitch);
-        for (int c0 = lane; c0 < vectors; c0 += 128) {
-            uint4 u[4], v[4];
+    const int lane = threadIdx.x & 31;
+    const int64_t first = (int64_t)blockIdx.x * (kPackThreads / 32) + threadIdx.x / 32, step = (int64_t)gridDim.x * (kPackThreads / 32);
+    for (int j = 0; j < p.jobs; j++) {
+        const PackJob& q = p.job[j];
+        const int vectors = q.pitch / 8;
+        for (int64_t r = first; r < q.rows; r += step) {
+            const int64_t e = r / q.per;
+            // offsets that do not rise give no rows either, whatever is before them
+            if (q.weights && p.offsets[e + 1] <= p.offsets[e]) continue;
+            const uintptr_t from = (uintptr_t)(q.from + e * q.expert + (r - e * q.per) * q.stride);
+            const uintptr_t end = from + 2 * (uintptr_t)q.cols, base = from & ~(uintptr_t)15;
+            const int s = (int)(from & 15);
+            uint4* to = (uint4*)(q.to + r * q.pitch);
+            for (int c0 = lane; c0 < vectors; c0 += 128) {
+                uint4 u[4], v[4];
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-                const uintptr_t a = base + 16 * (uintptr_t)(c0 + 32 * k);
-                u[k] = v[k] = make_uint4(0, 0, 0, 0);
-                if (a < end) u[k] = *(const uint4*)a;
-                if (s && a + 16 < end) v[k] = *(const uint4*)(a + 16);
+                for (int k = 0; k < 4; k++) {
+                    const uintptr_t a = base + 16 * (uintptr_t)(c0 + 32 * k);
+                    u[k] = v[k] = make_uint4(0, 0, 0, 0);
+                    if (a < end) u[k] = *(const uint4*)a;
+                    if (s && a + 16 < end) v[k] = *(const uint4*)(a + 16);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    if (c0 + 32 * k < vectors) to[c0 + 32 * k] = bytes_from(u[k], v[k], s);
             }
-#pragma unroll
-            for (int k = 0; k < 4; k++)
-                if (c0 + 32 * k < vectors) to[c0 + 32 * k] = bytes_from(u[k], v[k], s);
         }
     }
 }
@@ -684,28 +804,39 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackParams p) 
 struct Operand {
     const void* p;
     int64_t experts, rows, cols, stride, expert;
+    bool weights;
     bool aligned() const { return (uintptr_t)p % 16 == 0 && stride % 8 == 0 && expert % 8 == 0; }
     int64_t pitch() const { return (cols + 7) / 8 * 8; }
     size_t packed_bytes() const { return (size_t)(experts * rows * pitch() * 2 + 255) / 256 * 256; }
 };
 
-cudaError_t pack(Operand& x, unsigned char*& scratch, cudaStream_t stream, int sms) {
-    if (x.aligned()) return cudaSuccess;
-    PackParams p;
-    p.from = (const Bf16*)x.p;
-    p.to = (Bf16*)scratch;
-    p.rows = x.experts * x.rows;
-    p.per = x.rows;
-    p.stride = x.stride;
-    p.expert = x.expert;
-    p.cols = (int)x.cols;
-    p.pitch = (int)x.pitch();
-    scratch += x.packed_bytes();
-    x.p = p.to;
-    x.stride = p.pitch;
-    x.expert = x.rows * p.pitch;
-    if (!p.rows) return cudaSuccess;
-    const int64_t blocks = std::min<int64_t>((p.rows + 7) / 8, (int64_t)sms * 8);
+// Copies those of the operands that need it into scratch, and points them there.
+cudaError_t pack(Operand* const* list, int n, const int32_t* offsets, void* scratch, cudaStream_t stream, int sms) {
+    PackParams p = {};
+    p.offsets = offsets;
+    unsigned char* at = (unsigned char*)scratch;
+    int64_t most = 0;
+    for (int i = 0; i < n; i++) {
+        Operand& x = *list[i];
+        if (x.aligned()) continue;
+        PackJob& q = p.job[p.jobs++];
+        q.from = (const Bf16*)x.p;
+        q.to = (Bf16*)at;
+        q.rows = x.experts * x.rows;
+        q.per = x.rows;
+        q.stride = x.stride;
+        q.expert = x.expert;
+        q.cols = (int)x.cols;
+        q.pitch = (int)x.pitch();
+        q.weights = x.weights;
+        at += x.packed_bytes();
+        most = std::max(most, q.rows);
+        x.p = q.to;
+        x.stride = q.pitch;
+        x.expert = x.rows * q.pitch;
+    }
+    if (!most) return cudaSuccess;
+    const int64_t blocks = std::min<int64_t>((most + kPackThreads / 32 - 1) / (kPackThreads / 32), (int64_t)sms * 8);
     void* args[] = {&p};
     return launch_op((const void*)pack_kernel, dim3((unsigned)blocks), dim3(kPackThreads), args, 0, stream);
 }
@@ -768,18 +899,18 @@ cudaError_t launch_tensor(TensorParams& p, const Operand& a, const Operand& b, h
 
 Operand rows_operand(const void* p, size_t rows, size_t cols, size_t stride) {
     // a single row has no next one: any stride will do
-    return Operand{p, 1, (int64_t)rows, (int64_t)cols, rows > 1 ? (int64_t)stride : ((int64_t)cols + 7) / 8 * 8, 0};
+    return Operand{p, 1, (int64_t)rows, (int64_t)cols, rows > 1 ? (int64_t)stride : ((int64_t)cols + 7) / 8 * 8, 0, false};
 }
 Operand weight_operand(const void* p, size_t experts, size_t in, size_t out, hc_weight_layout_t layout, size_t stride, size_t expert) {
     const bool out_in = layout == HC_WEIGHT_OUT_IN;
-    return Operand{p, (int64_t)experts, (int64_t)(out_in ? out : in), (int64_t)(out_in ? in : out), (int64_t)stride, (int64_t)expert};
+    return Operand{p, (int64_t)experts, (int64_t)(out_in ? out : in), (int64_t)(out_in ? in : out), (int64_t)stride, (int64_t)expert, true};
 }
 size_t packed(const Operand& x) { return x.aligned() ? 0 : x.packed_bytes(); }
 
 // The first two products: rows of `a` times the weight, which is summed along
 // its own rows (along) or across them.
-cudaError_t rows_product(Operand a, Operand w, bool along, void* out, size_t out_stride, size_t N, hc_dtype_t in, hc_dtype_t to,
-                         const int32_t* offsets, unsigned char*& scratch, cudaStream_t stream, int sms) {
+cudaError_t rows_product(const Operand& a, const Operand& w, bool along, void* out, size_t out_stride, size_t N, hc_dtype_t in,
+                         hc_dtype_t to, const int32_t* offsets, cudaStream_t stream, int sms) {
     if (in == HC_FLOAT32) {
         PlainParams p = {};
         p.a = a.p;
@@ -798,9 +929,27 @@ cudaError_t rows_product(Operand a, Operand w, bool along, void* out, size_t out
         p.b_vec = whole(w.p, (size_t)w.stride, (size_t)w.expert, 4);
         return along ? launch_plain<true, true>(p, to, stream, sms) : launch_plain<true, false>(p, to, stream, sms);
     }
-    cudaError_t e = pack(a, scratch, stream, sms);
-    if (e == cudaSuccess) e = pack(w, scratch, stream, sms);
-    if (e != cudaSuccess) return e;
+    if (few_rows((size_t)a.rows, (size_t)a.cols, along)) {
+        FewParams p;
+        p.x = (const Bf16*)a.p;
+        p.w = (const Bf16*)w.p;
+        p.out = out;
+        p.offsets = offsets;
+        p.rows = a.rows;
+        p.x_stride = a.stride;
+        p.w_stride = w.stride;
+        p.w_expert = w.expert;
+        p.out_stride = (int64_t)out_stride;
+        p.E = (int)w.experts;
+        p.N = (int)N;
+        p.K = (int)a.cols;
+        void* args[] = {&p};
+        const dim3 grid((unsigned)((N + kFewThreads / 32 - 1) / (kFewThreads / 32)), (unsigned)std::min<int64_t>(w.experts, a.rows));
+        const void* fn = to == HC_BFLOAT16 ? (const void*)few_rows_kernel<Bf16> : (const void*)few_rows_kernel<float>;
+        const int smem = kFewAtOnce * (int)a.pitch() * 2;
+        if (!allow_smem((void*)fn, smem)) return cudaErrorInvalidValue;
+        return launch_op(fn, grid, dim3(kFewThreads), args, smem, stream);
+    }
     TensorParams p;
     p.out = out;
     p.offsets = offsets;
@@ -819,7 +968,7 @@ cudaError_t rows_product(Operand a, Operand w, bool along, void* out, size_t out
 }  // namespace
 
 size_t expert_matmul_scratch(const hc_expert_matmul_t& a) {
-    if (a.dtype != HC_BFLOAT16 || !a.rows) return 0;
+    if (a.dtype != HC_BFLOAT16 || !a.rows || few_rows(a.rows, a.in_dim, a.weight_layout == HC_WEIGHT_OUT_IN)) return 0;
     return packed(rows_operand(a.x, a.rows, a.in_dim, a.x_stride)) +
            packed(weight_operand(a.weight, a.experts, a.in_dim, a.out_dim, a.weight_layout, a.weight_stride, a.expert_stride));
 }
@@ -827,36 +976,42 @@ size_t expert_matmul_scratch(const hc_expert_matmul_t& a) {
 size_t expert_matmul_grad_scratch(const hc_expert_matmul_grad_t& a) {
     if (a.dtype != HC_BFLOAT16 || !a.rows) return 0;
     size_t n = packed(rows_operand(a.grad_out, a.rows, a.out_dim, a.grad_out_stride));
-    if (a.grad_x)
+    if (a.grad_x && !few_rows(a.rows, a.out_dim, a.weight_layout == HC_WEIGHT_IN_OUT))
         n += packed(weight_operand(a.weight, a.experts, a.in_dim, a.out_dim, a.weight_layout, a.weight_stride, a.expert_stride));
     if (a.grad_weight) n += packed(rows_operand(a.x, a.rows, a.in_dim, a.x_stride));
     return n;
 }
 
 cudaError_t launch_expert_matmul(const hc_expert_matmul_t& a, cudaStream_t stream, int sms) {
-    unsigned char* scratch = (unsigned char*)a.scratch;
-    return rows_product(rows_operand(a.x, a.rows, a.in_dim, a.x_stride),
-                        weight_operand(a.weight, a.experts, a.in_dim, a.out_dim, a.weight_layout, a.weight_stride, a.expert_stride),
-                        a.weight_layout == HC_WEIGHT_OUT_IN, a.out, a.out_stride, a.out_dim, a.dtype, a.out_dtype, a.offsets,
-                        scratch, stream, sms);
+    Operand x = rows_operand(a.x, a.rows, a.in_dim, a.x_stride);
+    Operand w = weight_operand(a.weight, a.experts, a.in_dim, a.out_dim, a.weight_layout, a.weight_stride, a.expert_stride);
+    if (a.dtype == HC_BFLOAT16 && !few_rows(a.rows, a.in_dim, a.weight_layout == HC_WEIGHT_OUT_IN)) {
+        Operand* const list[] = {&x, &w};
+        const cudaError_t e = pack(list, 2, a.offsets, a.scratch, stream, sms);
+        if (e != cudaSuccess) return e;
+    }
+    return rows_product(x, w, a.weight_layout == HC_WEIGHT_OUT_IN, a.out, a.out_stride, a.out_dim, a.dtype, a.out_dtype, a.offsets,
+                        stream, sms);
 }
 
 cudaError_t launch_expert_matmul_grad(const hc_expert_matmul_grad_t& a, cudaStream_t stream, int sms) {
-    unsigned char* scratch = (unsigned char*)a.scratch;
     const bool out_in = a.weight_layout == HC_WEIGHT_OUT_IN;
     Operand go = rows_operand(a.grad_out, a.rows, a.out_dim, a.grad_out_stride);
-    if (a.dtype == HC_BFLOAT16 && a.rows) {  // once for both products
-        const cudaError_t e = pack(go, scratch, stream, sms);
+    Operand x = rows_operand(a.x, a.rows, a.in_dim, a.x_stride);
+    Operand w = weight_operand(a.weight, a.experts, a.in_dim, a.out_dim, a.weight_layout, a.weight_stride, a.expert_stride);
+    if (a.dtype == HC_BFLOAT16 && a.rows) {
+        Operand* list[kPackJobs] = {&go};
+        int n = 1;
+        if (a.grad_x && !few_rows(a.rows, a.out_dim, !out_in)) list[n++] = &w;
+        if (a.grad_weight) list[n++] = &x;
+        const cudaError_t e = pack(list, n, a.offsets, a.scratch, stream, sms);
         if (e != cudaSuccess) return e;
     }
     if (a.grad_x && a.rows) {
-        const cudaError_t e =
-            rows_product(go, weight_operand(a.weight, a.experts, a.in_dim, a.out_dim, a.weight_layout, a.weight_stride, a.expert_stride),
-                         !out_in, a.grad_x, a.grad_x_stride, a.in_dim, a.dtype, a.dtype, a.offsets, scratch, stream, sms);
+        const cudaError_t e = rows_product(go, w, !out_in, a.grad_x, a.grad_x_stride, a.in_dim, a.dtype, a.dtype, a.offsets, stream, sms);
         if (e != cudaSuccess) return e;
     }
     if (!a.grad_weight) return cudaSuccess;
-    Operand x = rows_operand(a.x, a.rows, a.in_dim, a.x_stride);
     const size_t M = out_in ? a.out_dim : a.in_dim, N = out_in ? a.in_dim : a.out_dim;
     if (a.dtype == HC_FLOAT32) {
         const Operand &m = out_in ? go : x, &n = out_in ? x : go;
@@ -878,11 +1033,7 @@ cudaError_t launch_expert_matmul_grad(const hc_expert_matmul_grad_t& a, cudaStre
         p.accumulate = a.accumulate;
         return launch_plain<false, false>(p, a.grad_weight_dtype, stream, sms);
     }
-    if (a.rows) {
-        const cudaError_t e = pack(x, scratch, stream, sms);
-        if (e != cudaSuccess) return e;
-    } else {
-        // no row is read, but a copy's description wants an address and a stride
+    if (!a.rows) {  // no row is read, but a copy's description wants an address and a stride
         go.p = x.p = (const void*)((uintptr_t)a.grad_weight / 16 * 16);
         go.stride = go.pitch();
         x.stride = x.pitch();

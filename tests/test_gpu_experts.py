@@ -80,6 +80,8 @@ SIZES = [  # rows, experts, in, out
     (1, 1, 8, 8), (1, 3, 64, 40), (2, 8, 1024, 512), (5, 2, 1, 1), (16, 4, 72, 264), (33, 3, 17, 9), (130, 2, 128, 256),
     (257, 5, 200, 136), (300, 40, 64, 64), (1000, 7, 129, 383), (1025, 16, 512, 264), (4099, 3, 264, 520), (37, 1024, 24, 16),
     (600, 4, 1032, 2056),
+    # tiles that two blocks share, in all three products
+    (5006, 16, 193, 2003), (20011, 5, 1040, 776),
 ]
 KINDS = ["even", "skewed", "last", "none"]
 
@@ -291,6 +293,31 @@ def test_gradients_against_differences():
         got = float((o["grad_" + name].to(D) * d)[inside if name == "x" else slice(None)].sum())
         size = float((o["grad_" + name].to(D).abs() * d.abs())[inside if name == "x" else slice(None)].sum())
         assert abs(got - slope) <= (outer + rows) * 2.0 ** -23 * size + 1e-9 * abs(slope)
+
+
+@pytest.mark.parametrize("inner,outer", [(1001, 2003), (1000, 2000)])
+def test_many_calls_one_after_the_other(inner, outer):
+    """Blocks follow one another on an SM thousands of times, without a wait
+    that gives up and with the same bits."""
+    from collective_communication_algorithms_gb300 import _binding as B
+    g = gen(outer)
+    rows, experts = 5006, 16
+    offsets, _ = groups("even", experts, rows)
+    x, w = normal(g, rows, inner, dtype=BF16), normal(g, experts, outer, inner, dtype=BF16)
+    go = normal(g, rows, outer, dtype=BF16)
+    a = hc.bind_expert_matmul(x, w, offsets)
+    b = hc.bind_expert_matmul_grad(go, offsets, x=x, weight=w)
+    a()
+    b()
+    first = [v.clone() for c in (a, b) for v in c.outputs.values()]
+    for _ in range(20):
+        for _ in range(150):
+            a()
+        for _ in range(50):
+            b()
+        torch.cuda.synchronize()
+        assert B.hc_device_status() == 0
+    assert all(torch.equal(u, v) for u, v in zip(first, [v for c in (a, b) for v in c.outputs.values()]))
 
 
 # ------------------------------------------------------------------ combine
