@@ -225,6 +225,7 @@ __device__ __forceinline__ uint4 bytes_from(const uint4& u, const uint4& v, int 
 // ---------------------------------------------------------------------------
 constexpr size_t kFewRows = 16, kFewDim = 8192;
 constexpr int kFewThreads = 256, kFewAtOnce = 4, kFewBatch = 4;
+constexpr int kFewEach = 4, kFewBlock = kFewThreads / 32 * kFewEach;  // weight rows of a warp, of a block
 
 struct FewParams {
     const Bf16* x;
@@ -245,60 +246,69 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
     if (warp == 0) read_groups(p.offsets, p.E, p.rows, 1 << 30, bound, before);  // before: groups with rows
     __syncthreads();
     if ((int)blockIdx.y >= before[p.E]) return;
-    const int e = group_of(before, p.E, blockIdx.y), o = blockIdx.x * (kFewThreads / 32) + warp;
-    const int vectors = (p.K + 7) / 8;
-    const uintptr_t from = (uintptr_t)(p.w + e * p.w_expert + min(o, p.N - 1) * p.w_stride), end = from + 2 * (uintptr_t)p.K;
-    const uintptr_t base = from & ~(uintptr_t)15;
-    const int shift = (int)(from & 15);
+    const int e = group_of(before, p.E, blockIdx.y), o0 = blockIdx.x * kFewBlock + warp * kFewEach;
+    const int each = max(0, min(kFewEach, p.N - o0));  // weight rows of this warp
+    const int vectors = (p.K + 7) / 8, batches = (vectors + 32 * kFewBatch - 1) / (32 * kFewBatch);
+    const Bf16* w0 = p.w + e * p.w_expert + o0 * p.w_stride;
     Bf16* xs = (Bf16*)smem;  // kFewAtOnce rows of whole vectors
     for (int r0 = bound[e]; r0 < bound[e + 1]; r0 += kFewAtOnce) {
         const int n = min(kFewAtOnce, bound[e + 1] - r0);
-        uint4 u[kFewBatch], v[kFewBatch];
-        const auto load = [&](int c0) {
+        // batch i of the warp's rows: the vectors that hold it, one batch ahead
+        uint4 u[2][kFewBatch], v[2][kFewBatch];
+        const auto load = [&](int i, uint4 (&a)[kFewBatch], uint4 (&b)[kFewBatch]) {
+            const uintptr_t from = (uintptr_t)(w0 + (i / batches) * p.w_stride), end = from + 2 * (uintptr_t)p.K;
+            const uintptr_t at = (from & ~(uintptr_t)15) + 16 * (uintptr_t)(i % batches * 32 * kFewBatch + lane);
 #pragma unroll
             for (int k = 0; k < kFewBatch; k++) {
-                const uintptr_t a = base + 16 * (uintptr_t)(c0 + 32 * k);
-                u[k] = v[k] = make_uint4(0, 0, 0, 0);
-                if (a < end) u[k] = *(const uint4*)a;
-                if (shift && a + 16 < end) v[k] = *(const uint4*)(a + 16);
+                a[k] = b[k] = make_uint4(0, 0, 0, 0);
+                if (i < each * batches && at + 512 * k < end) a[k] = *(const uint4*)(at + 512 * k);
+                if ((from & 15) && i < each * batches && at + 512 * k + 16 < end) b[k] = *(const uint4*)(at + 512 * k + 16);
             }
         };
-        load(lane);
+        load(0, u[0], v[0]);
         __syncthreads();  // the rows before have been read
         for (int r = 0; r < kFewAtOnce; r++)
+#pragma unroll 4
             for (int c = threadIdx.x; c < vectors * 8; c += kFewThreads)
                 xs[r * vectors * 8 + c] = r < n && c < p.K ? p.x[(int64_t)(r0 + r) * p.x_stride + c] : Bf16{0};
         __syncthreads();
-        float acc[kFewAtOnce];
+        float acc[kFewAtOnce] = {};
+        for (int i0 = 0; i0 < each * batches; i0 += 2)
 #pragma unroll
-        for (int r = 0; r < kFewAtOnce; r++) acc[r] = 0.0f;
-        for (int c0 = lane; c0 < vectors; c0 += 32 * kFewBatch) {
-            if (c0 != lane) load(c0);
+            for (int h = 0; h < 2; h++) {
+                const int i = i0 + h;
+                if (i >= each * batches) break;
+                load(i + 1, u[h ^ 1], v[h ^ 1]);
+                const int f = i / batches, c0 = (i - f * batches) * 32 * kFewBatch + lane;
+                const int shift = (int)((uintptr_t)(w0 + f * p.w_stride) & 15);
 #pragma unroll
-            for (int k = 0; k < kFewBatch; k++) {
-                const int c = c0 + 32 * k;
-                if (c >= vectors) continue;
-                float w[8];
-                unpack(bytes_from(u[k], v[k], shift), w);
-                if (c * 8 + 8 > p.K)  // behind the row lies another's
+                for (int k = 0; k < kFewBatch; k++) {
+                    const int c = c0 + 32 * k;
+                    if (c >= vectors) continue;
+                    float w[8];
+                    unpack(bytes_from(u[h][k], v[h][k], shift), w);
+                    if (c * 8 + 8 > p.K)  // behind the row lies another's
 #pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        if (c * 8 + i >= p.K) w[i] = 0.0f;
+                        for (int j = 0; j < 8; j++)
+                            if (c * 8 + j >= p.K) w[j] = 0.0f;
 #pragma unroll
-                for (int r = 0; r < kFewAtOnce; r++) {
-                    float y[8];
-                    unpack(((const uint4*)xs)[r * vectors + c], y);
+                    for (int r = 0; r < kFewAtOnce; r++) {
+                        if (r >= n) break;
+                        float y[8];
+                        unpack(((const uint4*)xs)[r * vectors + c], y);
 #pragma unroll
-                    for (int i = 0; i < 8; i++) acc[r] = fmaf(w[i], y[i], acc[r]);
+                        for (int j = 0; j < 8; j++) acc[r] = fmaf(w[j], y[j], acc[r]);
+                    }
+                }
+                if (i + 1 == (f + 1) * batches) {  // the row's last
+#pragma unroll
+                    for (int r = 0; r < kFewAtOnce; r++) {
+                        const float sum = warp_sum(acc[r]);
+                        if (lane == 0 && r < n) put((TO*)p.out + (int64_t)(r0 + r) * p.out_stride + o0 + f, sum);
+                        acc[r] = 0.0f;
+                    }
                 }
             }
-        }
-#pragma unroll
-        for (int r = 0; r < kFewAtOnce; r++) acc[r] = warp_sum(acc[r]);
-        if (lane == 0 && o < p.N)
-#pragma unroll
-            for (int r = 0; r < kFewAtOnce; r++)
-                if (r < n) put((TO*)p.out + (int64_t)(r0 + r) * p.out_stride + o, acc[r]);
     }
 }
 
@@ -344,7 +354,7 @@ struct TensorParams {
 
 struct TensorBarriers {
     uint64_t full[kTStages], empty[kTStages], raw[kTStages];  // raw: landed, to be overwritten in part
-    uint64_t zeroed;  // by the other block
+    uint64_t zeroed[kTStages];  // by the other block, which may be stages ahead
     uint64_t sums_full[2], sums_empty[2], drain;
     uint32_t tmem;
 };
@@ -421,12 +431,12 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
             mbar_init(&bar.full[s], 1 + p.hold);
             mbar_init(&bar.empty[s], 1);
             mbar_init(&bar.raw[s], 1);
+            mbar_init(&bar.zeroed[s], 1);
         }
         for (int s = 0; s < 2; s++) {
             mbar_init(&bar.sums_full[s], 1);
             mbar_init(&bar.sums_empty[s], 4 * G);
         }
-        mbar_init(&bar.zeroed, 1);
         mbar_init(&bar.drain, 1);
         mbar_init_fence();
         prefetch_map(&p.a);
@@ -576,7 +586,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
         if (lane == 0) mbar_wait_quick(&bar.drain, 0, kWaitLimitNs);
     } else if (!ROWS && warp == 3) {  // zeros behind the last row of a group
         Ring at;
-        uint32_t phase = 0, zeroed = 0;
+        uint32_t phase = 0;  // of each stage's turns with such rows
         for (int64_t i = blockIdx.x / G; i < tiles; i += step) {
             const TensorTile t = tensor_tile<ROWS, T>(p, bound, tile, i, across);
             const int rest = t.K % kTK;
@@ -584,20 +594,18 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
             if (!rest) continue;
             const int s = at.s;
             at.next();
-            if (!warp_wait([&] { return mbar_wait_quick(&bar.raw[s], phase >> s & 1, p.wait_ns); })) break;
+            const uint32_t turn = phase >> s & 1;
             phase ^= 1u << s;
+            if (!warp_wait([&] { return mbar_wait_quick(&bar.raw[s], turn, p.wait_ns); })) break;
             const int zeros = (16 - rest % 16) % 16 * 8;  // rows that a product reads, 16 bytes each
             for (int j = lane; j < zeros * (kTStageBytes / 8192); j += 32)  // in all boxes
                 *(uint4*)(stages + s * kTStageBytes + j / zeros * 8192 + rest * 128 + j % zeros * 16) = make_uint4(0, 0, 0, 0);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (rank > 0) {
-                if (lane == 0) first_arrive<G>(&bar.zeroed);
+                if (lane == 0) first_arrive<G>(&bar.zeroed[s]);
             } else {
-                if (G > 1) {
-                    if (!warp_wait([&] { return first_wait<G>(&bar.zeroed, zeroed & 1, p.wait_ns); })) break;
-                    zeroed++;
-                }
+                if (G > 1 && !warp_wait([&] { return first_wait<G>(&bar.zeroed[s], turn, p.wait_ns); })) break;
                 if (lane == 0) mbar_arrive(&bar.full[s]);
             }
         }
@@ -944,7 +952,7 @@ cudaError_t rows_product(const Operand& a, const Operand& w, bool along, void* o
         p.N = (int)N;
         p.K = (int)a.cols;
         void* args[] = {&p};
-        const dim3 grid((unsigned)((N + kFewThreads / 32 - 1) / (kFewThreads / 32)), (unsigned)std::min<int64_t>(w.experts, a.rows));
+        const dim3 grid((unsigned)((N + kFewBlock - 1) / kFewBlock), (unsigned)std::min<int64_t>(w.experts, a.rows));
         const void* fn = to == HC_BFLOAT16 ? (const void*)few_rows_kernel<Bf16> : (const void*)few_rows_kernel<float>;
         const int smem = kFewAtOnce * (int)a.pitch() * 2;
         if (!allow_smem((void*)fn, smem)) return cudaErrorInvalidValue;

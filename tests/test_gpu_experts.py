@@ -295,13 +295,13 @@ def test_gradients_against_differences():
         assert abs(got - slope) <= (outer + rows) * 2.0 ** -23 * size + 1e-9 * abs(slope)
 
 
-@pytest.mark.parametrize("inner,outer", [(1001, 2003), (1000, 2000)])
-def test_many_calls_one_after_the_other(inner, outer):
+@pytest.mark.parametrize("rows,experts,inner,outer", [(5006, 16, 1001, 2003), (5006, 16, 1000, 2000), (2003, 64, 520, 1040),
+                                                      (20000, 88, 440, 944)])
+def test_many_calls_one_after_the_other(rows, experts, inner, outer):
     """Blocks follow one another on an SM thousands of times, without a wait
     that gives up and with the same bits."""
     from collective_communication_algorithms_gb300 import _binding as B
     g = gen(outer)
-    rows, experts = 5006, 16
     offsets, _ = groups("even", experts, rows)
     x, w = normal(g, rows, inner, dtype=BF16), normal(g, experts, outer, inner, dtype=BF16)
     go = normal(g, rows, outer, dtype=BF16)
