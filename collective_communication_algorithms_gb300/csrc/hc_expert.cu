@@ -125,18 +125,30 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanPara
     if (!SINGLE) {  // a warp takes an expert's counts of all blocks, four a lane
         static_assert(kPlanMaxBlocks == 128, "four counts a lane");
         const int b = lane * 4, me = blockIdx.x;
-#pragma unroll 4
-        for (int e = warp; e < E; e += kPlanWarps) {
-            int4 c = b < p.blocks ? *(const int4*)&p.counts[e * kPlanMaxBlocks + b] : make_int4(0, 0, 0, 0);
-            if (b + 1 >= p.blocks) c.y = 0;
-            if (b + 2 >= p.blocks) c.z = 0;
-            if (b + 3 >= p.blocks) c.w = 0;
-            const int all = __reduce_add_sync(0xFFFFFFFFu, c.x + c.y + c.z + c.w);
-            const int mine = __reduce_add_sync(
-                0xFFFFFFFFu, (b < me ? c.x : 0) + (b + 1 < me ? c.y : 0) + (b + 2 < me ? c.z : 0) + (b + 3 < me ? c.w : 0));
-            if (lane == 0) {
-                total[e] = all;
-                before[e] = mine;
+        constexpr int AT_ONCE = 8;  // experts whose counts are under way together
+        for (int e0 = warp; e0 < E; e0 += kPlanWarps * AT_ONCE) {
+            int4 some[AT_ONCE];
+#pragma unroll
+            for (int k = 0; k < AT_ONCE; k++) {
+                const int e = e0 + k * kPlanWarps;
+                some[k] = make_int4(0, 0, 0, 0);
+                if (e < E && b < p.blocks) some[k] = *(const int4*)&p.counts[e * kPlanMaxBlocks + b];
+            }
+#pragma unroll
+            for (int k = 0; k < AT_ONCE; k++) {
+                const int e = e0 + k * kPlanWarps;
+                if (e >= E) break;
+                int4 c = some[k];
+                if (b + 1 >= p.blocks) c.y = 0;
+                if (b + 2 >= p.blocks) c.z = 0;
+                if (b + 3 >= p.blocks) c.w = 0;
+                const int all = __reduce_add_sync(0xFFFFFFFFu, c.x + c.y + c.z + c.w);
+                const int mine = __reduce_add_sync(
+                    0xFFFFFFFFu, (b < me ? c.x : 0) + (b + 1 < me ? c.y : 0) + (b + 2 < me ? c.z : 0) + (b + 3 < me ? c.w : 0));
+                if (lane == 0) {
+                    total[e] = all;
+                    before[e] = mine;
+                }
             }
         }
     }

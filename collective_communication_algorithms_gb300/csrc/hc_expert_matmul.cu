@@ -214,6 +214,26 @@ __device__ __forceinline__ uint4 bytes_from(const uint4& u, const uint4& v, int 
                       __funnelshift_r(w[3], w[4], bits));
 }
 
+// Elements 8 c .. 8 c + 7 of a row of `cols` that begins anywhere, from the
+// aligned vectors that hold them (none without a byte of the row); zeros behind
+// the row's end.
+__device__ __forceinline__ uint4 row_vector(const Bf16* row, int c, int cols) {
+    const uintptr_t from = (uintptr_t)row, end = from + 2 * (uintptr_t)cols, at = (from & ~(uintptr_t)15) + 16 * (uintptr_t)c;
+    const int s = (int)(from & 15);
+    uint4 u = make_uint4(0, 0, 0, 0), v = u;
+    if (at < end) u = *(const uint4*)at;
+    if (s && at + 16 < end) v = *(const uint4*)(at + 16);
+    uint4 w = bytes_from(u, v, s);
+    const int left = cols - 8 * c;
+    if (left < 8) {
+        uint32_t* x = &w.x;
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (2 * i + 2 > left) x[i] = 2 * i + 1 > left ? 0u : x[i] & 0xFFFFu;
+    }
+    return w;
+}
+
 // ---------------------------------------------------------------------------
 // bf16 products of few rows (of all groups together), the weight summed along
 // its rows
@@ -223,7 +243,7 @@ __device__ __forceinline__ uint4 bytes_from(const uint4& u, const uint4& v, int 
 // by up to four of the group's rows, which lie in shared memory.  One token
 // through two experts of 4096 x 1024: 16.8 MB.
 // ---------------------------------------------------------------------------
-constexpr size_t kFewRows = 16, kFewDim = 8192;
+constexpr int64_t kFewRows = 16, kFewDim = 8192;
 constexpr int kFewThreads = 256, kFewAtOnce = 4, kFewBatch = 4;
 constexpr int kFewEach = 4, kFewBlock = kFewThreads / 32 * kFewEach;  // weight rows of a warp, of a block
 
@@ -267,10 +287,10 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
         };
         load(0, u[0], v[0]);
         __syncthreads();  // the rows before have been read
-        for (int r = 0; r < kFewAtOnce; r++)
-#pragma unroll 4
-            for (int c = threadIdx.x; c < vectors * 8; c += kFewThreads)
-                xs[r * vectors * 8 + c] = r < n && c < p.K ? p.x[(int64_t)(r0 + r) * p.x_stride + c] : Bf16{0};
+        for (int j = threadIdx.x; j < n * vectors; j += kFewThreads) {
+            const int r = j / vectors, c = j - r * vectors;
+            ((uint4*)xs)[j] = row_vector(p.x + (int64_t)(r0 + r) * p.x_stride, c, p.K);
+        }
         __syncthreads();
         float acc[kFewAtOnce] = {};
         for (int i0 = 0; i0 < each * batches; i0 += 2)
@@ -287,7 +307,7 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
                     if (c >= vectors) continue;
                     float w[8];
                     unpack(bytes_from(u[h][k], v[h][k], shift), w);
-                    if (c * 8 + 8 > p.K)  // behind the row lies another's
+                    if (c * 8 + 8 > p.K)  // behind the row lies another's, of any value
 #pragma unroll
                         for (int j = 0; j < 8; j++)
                             if (c * 8 + j >= p.K) w[j] = 0.0f;
@@ -311,9 +331,6 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
             }
     }
 }
-
-// Whether the first two products take that kernel.
-bool few_rows(size_t rows, size_t K, bool along) { return along && rows <= kFewRows && K <= kFewDim; }
 
 // ---------------------------------------------------------------------------
 // bf16 products on the tensor cores
@@ -768,31 +785,32 @@ constexpr int kPackJobs = 3;
 struct PackParams {
     PackJob job[kPackJobs];
     const int32_t* offsets;
-    int jobs;
+    int jobs, experts;
 };
 constexpr int kPackThreads = 256;
 
-// A warp takes a row, a lane eight elements: the aligned vectors that hold
-// them (none without a byte of the row), shifted into place.  What a row's last
-// vector holds behind the row is not read by anyone.
+// A warp takes a row, a lane eight elements.
 __global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackParams p) {
+    __shared__ bool used[kMaxExperts];
     grid_wait();
     grid_release();
+    // offsets that do not rise give no rows, whatever is before them
+    for (int e = threadIdx.x; e < p.experts; e += kPackThreads) used[e] = p.offsets[e + 1] > p.offsets[e];
+    __syncthreads();
     const int lane = threadIdx.x & 31;
-    const int64_t first = (int64_t)blockIdx.x * (kPackThreads / 32) + threadIdx.x / 32, step = (int64_t)gridDim.x * (kPackThreads / 32);
+    const int first = blockIdx.x * (kPackThreads / 32) + threadIdx.x / 32, step = gridDim.x * (kPackThreads / 32);
     for (int j = 0; j < p.jobs; j++) {
         const PackJob& q = p.job[j];
         const int vectors = q.pitch / 8;
         for (int64_t r = first; r < q.rows; r += step) {
             const int64_t e = r / q.per;
-            // offsets that do not rise give no rows either, whatever is before them
-            if (q.weights && p.offsets[e + 1] <= p.offsets[e]) continue;
+            if (q.weights && !used[e]) continue;
             const uintptr_t from = (uintptr_t)(q.from + e * q.expert + (r - e * q.per) * q.stride);
             const uintptr_t end = from + 2 * (uintptr_t)q.cols, base = from & ~(uintptr_t)15;
             const int s = (int)(from & 15);
             uint4* to = (uint4*)(q.to + r * q.pitch);
             for (int c0 = lane; c0 < vectors; c0 += 128) {
-                uint4 u[4], v[4];
+                uint4 u[4], v[4];  // as in row_vector, but nobody reads what lies behind a row
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
                     const uintptr_t a = base + 16 * (uintptr_t)(c0 + 32 * k);
@@ -818,10 +836,18 @@ struct Operand {
     size_t packed_bytes() const { return (size_t)(experts * rows * pitch() * 2 + 255) / 256 * 256; }
 };
 
+// Whether the first two products take the kernel for few rows: where tiles
+// would first need a copy of the weights (1 token through 2 of 8 experts of
+// 4096 x 1024, aligned: 8.1 us against 7.2 in tiles; of 4095 x 1023: 8 against 12).
+bool few_rows(const Operand& a, const Operand& w, bool along) {
+    return along && !(a.aligned() && w.aligned()) && a.rows <= kFewRows && a.cols <= kFewDim;
+}
+
 // Copies those of the operands that need it into scratch, and points them there.
-cudaError_t pack(Operand* const* list, int n, const int32_t* offsets, void* scratch, cudaStream_t stream, int sms) {
+cudaError_t pack(Operand* const* list, int n, const int32_t* offsets, size_t experts, void* scratch, cudaStream_t stream, int sms) {
     PackParams p = {};
     p.offsets = offsets;
+    p.experts = (int)experts;
     unsigned char* at = (unsigned char*)scratch;
     int64_t most = 0;
     for (int i = 0; i < n; i++) {
@@ -937,7 +963,7 @@ cudaError_t rows_product(const Operand& a, const Operand& w, bool along, void* o
         p.b_vec = whole(w.p, (size_t)w.stride, (size_t)w.expert, 4);
         return along ? launch_plain<true, true>(p, to, stream, sms) : launch_plain<true, false>(p, to, stream, sms);
     }
-    if (few_rows((size_t)a.rows, (size_t)a.cols, along)) {
+    if (few_rows(a, w, along)) {
         FewParams p;
         p.x = (const Bf16*)a.p;
         p.w = (const Bf16*)w.p;
@@ -976,16 +1002,19 @@ cudaError_t rows_product(const Operand& a, const Operand& w, bool along, void* o
 }  // namespace
 
 size_t expert_matmul_scratch(const hc_expert_matmul_t& a) {
-    if (a.dtype != HC_BFLOAT16 || !a.rows || few_rows(a.rows, a.in_dim, a.weight_layout == HC_WEIGHT_OUT_IN)) return 0;
-    return packed(rows_operand(a.x, a.rows, a.in_dim, a.x_stride)) +
-           packed(weight_operand(a.weight, a.experts, a.in_dim, a.out_dim, a.weight_layout, a.weight_stride, a.expert_stride));
+    if (a.dtype != HC_BFLOAT16 || !a.rows) return 0;
+    const Operand x = rows_operand(a.x, a.rows, a.in_dim, a.x_stride);
+    const Operand w = weight_operand(a.weight, a.experts, a.in_dim, a.out_dim, a.weight_layout, a.weight_stride, a.expert_stride);
+    return few_rows(x, w, a.weight_layout == HC_WEIGHT_OUT_IN) ? 0 : packed(x) + packed(w);
 }
 
 size_t expert_matmul_grad_scratch(const hc_expert_matmul_grad_t& a) {
     if (a.dtype != HC_BFLOAT16 || !a.rows) return 0;
-    size_t n = packed(rows_operand(a.grad_out, a.rows, a.out_dim, a.grad_out_stride));
-    if (a.grad_x && !few_rows(a.rows, a.out_dim, a.weight_layout == HC_WEIGHT_IN_OUT))
-        n += packed(weight_operand(a.weight, a.experts, a.in_dim, a.out_dim, a.weight_layout, a.weight_stride, a.expert_stride));
+    const Operand go = rows_operand(a.grad_out, a.rows, a.out_dim, a.grad_out_stride);
+    const Operand w = weight_operand(a.weight, a.experts, a.in_dim, a.out_dim, a.weight_layout, a.weight_stride, a.expert_stride);
+    const bool few = a.grad_x && few_rows(go, w, a.weight_layout == HC_WEIGHT_IN_OUT);
+    size_t n = few && !a.grad_weight ? 0 : packed(go);
+    if (a.grad_x && !few) n += packed(w);
     if (a.grad_weight) n += packed(rows_operand(a.x, a.rows, a.in_dim, a.x_stride));
     return n;
 }
@@ -993,9 +1022,9 @@ size_t expert_matmul_grad_scratch(const hc_expert_matmul_grad_t& a) {
 cudaError_t launch_expert_matmul(const hc_expert_matmul_t& a, cudaStream_t stream, int sms) {
     Operand x = rows_operand(a.x, a.rows, a.in_dim, a.x_stride);
     Operand w = weight_operand(a.weight, a.experts, a.in_dim, a.out_dim, a.weight_layout, a.weight_stride, a.expert_stride);
-    if (a.dtype == HC_BFLOAT16 && !few_rows(a.rows, a.in_dim, a.weight_layout == HC_WEIGHT_OUT_IN)) {
+    if (a.dtype == HC_BFLOAT16 && !few_rows(x, w, a.weight_layout == HC_WEIGHT_OUT_IN)) {
         Operand* const list[] = {&x, &w};
-        const cudaError_t e = pack(list, 2, a.offsets, a.scratch, stream, sms);
+        const cudaError_t e = pack(list, 2, a.offsets, a.experts, a.scratch, stream, sms);
         if (e != cudaSuccess) return e;
     }
     return rows_product(x, w, a.weight_layout == HC_WEIGHT_OUT_IN, a.out, a.out_stride, a.out_dim, a.dtype, a.out_dtype, a.offsets,
@@ -1007,16 +1036,20 @@ cudaError_t launch_expert_matmul_grad(const hc_expert_matmul_grad_t& a, cudaStre
     Operand go = rows_operand(a.grad_out, a.rows, a.out_dim, a.grad_out_stride);
     Operand x = rows_operand(a.x, a.rows, a.in_dim, a.x_stride);
     Operand w = weight_operand(a.weight, a.experts, a.in_dim, a.out_dim, a.weight_layout, a.weight_stride, a.expert_stride);
+    const Operand given = go;
+    const bool few = a.dtype == HC_BFLOAT16 && a.grad_x && few_rows(go, w, !out_in);
     if (a.dtype == HC_BFLOAT16 && a.rows) {
-        Operand* list[kPackJobs] = {&go};
-        int n = 1;
-        if (a.grad_x && !few_rows(a.rows, a.out_dim, !out_in)) list[n++] = &w;
+        Operand* list[kPackJobs];
+        int n = 0;
+        if (!few || a.grad_weight) list[n++] = &go;
+        if (a.grad_x && !few) list[n++] = &w;
         if (a.grad_weight) list[n++] = &x;
-        const cudaError_t e = pack(list, n, a.offsets, a.scratch, stream, sms);
+        const cudaError_t e = pack(list, n, a.offsets, a.experts, a.scratch, stream, sms);
         if (e != cudaSuccess) return e;
     }
     if (a.grad_x && a.rows) {
-        const cudaError_t e = rows_product(go, w, !out_in, a.grad_x, a.grad_x_stride, a.in_dim, a.dtype, a.dtype, a.offsets, stream, sms);
+        const cudaError_t e =
+            rows_product(few ? given : go, w, !out_in, a.grad_x, a.grad_x_stride, a.in_dim, a.dtype, a.dtype, a.offsets, stream, sms);
         if (e != cudaSuccess) return e;
     }
     if (!a.grad_weight) return cudaSuccess;

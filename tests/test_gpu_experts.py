@@ -320,6 +320,45 @@ def test_many_calls_one_after_the_other(rows, experts, inner, outer):
     assert all(torch.equal(u, v) for u, v in zip(first, [v for c in (a, b) for v in c.outputs.values()]))
 
 
+@pytest.mark.parametrize("rows,experts,inner,outer", [(100, 3, 72, 136), (5006, 16, 264, 2000), (2003, 64, 520, 1040)])
+def test_expired_wait_reports_timeout_then_recovers(rows, experts, inner, outer):
+    """hc_test_expire_waits: the first wait on the copies gives up after 1 ms,
+    although they land; the call ends, writes nowhere else, reports, and the
+    next one is right."""
+    import time
+    from collective_communication_algorithms_gb300 import _binding as B
+    g = gen(rows)
+    offsets, cuts = groups("even", experts, rows)
+    x, w = normal(g, rows, inner, dtype=BF16), normal(g, experts, outer, inner, dtype=BF16)
+    go = normal(g, rows, outer, dtype=BF16)
+    out, intact = guarded(rows, outer, BF16)
+    gx, intact_x = guarded(rows, inner, BF16)
+    flat, intact_w = guarded(experts * outer, inner, F32)
+    a = hc.bind_expert_matmul(x, w, offsets, out=out)
+    b = hc.bind_expert_matmul_grad(go, offsets, x=x, weight=w, grad_x=gx, grad_weight=flat.view(experts, outer, inner))
+    for call in (a, b):
+        call()
+        torch.cuda.synchronize()
+        want = [v.clone() for v in call.outputs.values()]
+        assert B.hc_device_status() == 0
+        B.hc_test_expire_waits(True)
+        try:
+            t0 = time.perf_counter()
+            call()
+            torch.cuda.synchronize()
+            elapsed = time.perf_counter() - t0
+        finally:
+            B.hc_test_expire_waits(False)
+        assert elapsed < 1.0, elapsed
+        assert B.hc_device_status(clear=True) == 6
+        assert B.hc_device_status() == 0
+        assert intact() and intact_x() and intact_w()
+        call()
+        torch.cuda.synchronize()
+        assert B.hc_device_status() == 0
+        assert all(torch.equal(u, v) for u, v in zip(want, call.outputs.values()))
+
+
 # ------------------------------------------------------------------ combine
 def combine(y, slots, w):
     here = (slots >= 0) & (slots < y.shape[0])
