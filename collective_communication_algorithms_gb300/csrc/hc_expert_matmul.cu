@@ -88,20 +88,52 @@ struct PlainParams {
     int accumulate;
 };
 
-constexpr int kPK = 16, kPThreads = 256, kPPad = 4;
+constexpr int kPThreads = 256, kPEach = 8, kPPad = 4;
 
-// L elements at p, of which n (any value) are in range.
-template <int L>
-__device__ __forceinline__ void load_l(const float* p, int n, bool vec, float (&v)[L]) {
-    if (vec && n >= L) {
+// One operand's T x PK elements of a step, kPEach of them a thread's: in pieces
+// of four where rows lie on whole 16 bytes, else one by one, neighbours in a
+// row going to neighbouring threads.  ALONG: k runs along the operand's rows.
+template <bool ALONG, int T, int PK>
+__device__ __forceinline__ void load_step(const float* p, int64_t stride, int k0, int K, int len, bool vec, float (&v)[kPEach]) {
+    const int tid = threadIdx.x;
+    if (vec) {
+        constexpr int PER = (ALONG ? PK : T) / kPEach;  // threads of a row
+        const int row = tid / PER + (ALONG ? 0 : k0), col = tid % PER * kPEach + (ALONG ? k0 : 0);
+        const int n = row < (ALONG ? len : K) ? (ALONG ? K : len) - col : 0;
+        const float* at = p + row * stride + col;
+        if (n >= kPEach) {
 #pragma unroll
-        for (int i = 0; i < L; i += 4) {
-            const float4 w = *(const float4*)(p + i);
-            v[i] = w.x; v[i + 1] = w.y; v[i + 2] = w.z; v[i + 3] = w.w;
+            for (int i = 0; i < kPEach; i += 4) {
+                const float4 w = *(const float4*)(at + i);
+                v[i] = w.x; v[i + 1] = w.y; v[i + 2] = w.z; v[i + 3] = w.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPEach; i++) v[i] = i < n ? at[i] : 0.0f;
         }
     } else {
+        constexpr int PER = ALONG ? PK : T / kPEach;
 #pragma unroll
-        for (int i = 0; i < L; i++) v[i] = i < n ? p[i] : 0.0f;
+        for (int i = 0; i < kPEach; i++) {
+            const int row = ALONG ? tid / PER + kPThreads / PER * i : k0 + tid / PER;
+            const int col = ALONG ? k0 + tid % PER : tid % PER + PER * i;
+            v[i] = row < (ALONG ? len : K) && col < (ALONG ? K : len) ? p[row * stride + col] : 0.0f;
+        }
+    }
+}
+// Keeps them as [k][row or column of the sums].
+template <bool ALONG, int T, int PK>
+__device__ __forceinline__ void keep_step(float (&to)[PK][T + kPPad], bool vec, const float (&v)[kPEach]) {
+    const int tid = threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < kPEach; i++) {
+        if (vec) {
+            constexpr int PER = (ALONG ? PK : T) / kPEach;
+            to[ALONG ? tid % PER * kPEach + i : tid / PER][ALONG ? tid / PER : tid % PER * kPEach + i] = v[i];
+        } else {
+            constexpr int PER = ALONG ? PK : T / kPEach;
+            to[ALONG ? tid % PER : tid / PER][ALONG ? tid / PER + kPThreads / PER * i : tid % PER + PER * i] = v[i];
+        }
     }
 }
 
@@ -110,8 +142,8 @@ __device__ __forceinline__ void load_l(const float* p, int n, bool vec, float (&
 // T x T sums a block, L x L a thread, in pieces of four.
 template <class TO, bool ROWS, bool BK, int T>
 __global__ void __launch_bounds__(kPThreads) plain_product_kernel(const PlainParams p) {
-    constexpr int L = T / 16;
-    __shared__ __align__(16) float as[kPK][T + kPPad], bs[kPK][T + kPPad];
+    constexpr int L = T / 16, PK = kPThreads * kPEach / T;  // steps of 16 or 32 of the sum
+    __shared__ __align__(16) float as[2][PK][T + kPPad], bs[2][PK][T + kPPad];
     __shared__ int bound[kMaxExperts + 1], tile[kMaxExperts + 1];
     const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
     grid_wait();
@@ -144,57 +176,64 @@ __global__ void __launch_bounds__(kPThreads) plain_product_kernel(const PlainPar
         const float* a = (const float*)p.a + first * p.a_stride + m0;
         const float* b = (const float*)p.b + (ROWS ? e * p.b_expert + (BK ? (int64_t)n0 * p.b_stride : n0)
                                                    : first * p.b_stride + n0);
-        // places of this thread's L elements: along k (row, k) or along m (k, column)
-        const int kr = tid / (16 / L), kc = (tid % (16 / L)) * L, mr = tid / 16, mc = (tid % 16) * L;
-        float av[L], bv[L], acc[L][L];
+        float av[kPEach], bv[kPEach];
+        Pair acc[L][L / 2];  // two columns each
 #pragma unroll
         for (int x = 0; x < L; x++)
 #pragma unroll
-            for (int y = 0; y < L; y++) acc[x][y] = 0.0f;
+            for (int y = 0; y < L / 2; y++) acc[x][y] = Pair(0.0f, 0.0f);
         auto fetch = [&](int k0) {
-            if (ROWS) load_l<L>(a + kr * p.a_stride + k0 + kc, kr < mlen ? K - k0 - kc : 0, p.a_vec, av);
-            else load_l<L>(a + (int64_t)(k0 + mr) * p.a_stride + mc, k0 + mr < K ? mlen - mc : 0, p.a_vec, av);
-            if (BK) load_l<L>(b + kr * p.b_stride + k0 + kc, kr < nlen ? K - k0 - kc : 0, p.b_vec, bv);
-            else load_l<L>(b + (int64_t)(k0 + mr) * p.b_stride + mc, k0 + mr < K ? nlen - mc : 0, p.b_vec, bv);
+            load_step<ROWS, T, PK>(a, p.a_stride, k0, K, mlen, p.a_vec, av);
+            load_step<BK, T, PK>(b, p.b_stride, k0, K, nlen, p.b_vec, bv);
         };
-        if (K) fetch(0);
-        for (int k0 = 0; k0 < K; k0 += kPK) {
-            __syncthreads();
+        auto keep = [&](int h) {
+            keep_step<ROWS, T, PK>(as[h], p.a_vec, av);
+            keep_step<BK, T, PK>(bs[h], p.b_vec, bv);
+        };
+        __syncthreads();  // the tile before has been read
+        if (K) {
+            fetch(0);
+            keep(0);
+        }
+        __syncthreads();
+        int h = 0;
+        for (int k0 = 0; k0 < K; k0 += PK, h ^= 1) {
+            if (k0 + PK < K) fetch(k0 + PK);
 #pragma unroll
-            for (int j = 0; j < L; j++) {
-                if (ROWS) as[kc + j][kr] = av[j];
-                else as[mr][mc + j] = av[j];
-                if (BK) bs[kc + j][kr] = bv[j];
-                else bs[mr][mc + j] = bv[j];
-            }
-            __syncthreads();
-            if (k0 + kPK < K) fetch(k0 + kPK);
+            for (int k = 0; k < PK; k++) {
+                float x[L];
+                Pair y[L / 2];
 #pragma unroll
-            for (int k = 0; k < kPK; k++) {
-                float x[L], y[L];
-#pragma unroll
-                for (int h = 0; h < L / 4; h++) {
-                    const float4 u = *(const float4*)&as[k][h * 64 + ty * 4], w = *(const float4*)&bs[k][h * 64 + tx * 4];
-                    x[4 * h] = u.x; x[4 * h + 1] = u.y; x[4 * h + 2] = u.z; x[4 * h + 3] = u.w;
-                    y[4 * h] = w.x; y[4 * h + 1] = w.y; y[4 * h + 2] = w.z; y[4 * h + 3] = w.w;
+                for (int g = 0; g < L / 4; g++) {
+                    const float4 u = *(const float4*)&as[h][k][g * 64 + ty * 4];
+                    const ulonglong2 w = *(const ulonglong2*)&bs[h][k][g * 64 + tx * 4];
+                    x[4 * g] = u.x; x[4 * g + 1] = u.y; x[4 * g + 2] = u.z; x[4 * g + 3] = u.w;
+                    y[2 * g].v = w.x; y[2 * g + 1].v = w.y;
                 }
 #pragma unroll
-                for (int q = 0; q < L; q++)
+                for (int q = 0; q < L; q++) {
+                    const Pair xx(x[q], x[q]);
 #pragma unroll
-                    for (int r = 0; r < L; r++) acc[q][r] = fmaf(x[q], y[r], acc[q][r]);
+                    for (int r = 0; r < L / 2; r++) acc[q][r] = fma_pair(xx, y[r], acc[q][r]);
+                }
             }
+            if (k0 + PK < K) keep(h ^ 1);
+            __syncthreads();
         }
         TO* out = (TO*)p.out + (ROWS ? first * p.out_stride : e * p.out_expert + (int64_t)m0 * p.out_stride) + n0;
 #pragma unroll
         for (int q = 0; q < L; q++) {
             const int row = (q / 4) * 64 + ty * 4 + q % 4;
             if (row >= mlen) continue;
+            float sums[L];
+#pragma unroll
+            for (int r = 0; r < L / 2; r++) acc[q][r].get(sums[2 * r], sums[2 * r + 1]);
 #pragma unroll
             for (int r = 0; r < L; r++) {
                 const int col = (r / 4) * 64 + tx * 4 + r % 4;
                 if (col >= nlen) continue;
                 TO* at = out + row * p.out_stride + col;
-                put(at, (!ROWS && p.accumulate ? to_f32(*at) : 0.0f) + acc[q][r]);
+                put(at, (!ROWS && p.accumulate ? to_f32(*at) : 0.0f) + sums[r]);
             }
         }
     }
@@ -759,7 +798,7 @@ cudaError_t launch_plain(PlainParams p, cudaStream_t stream, int sms) {
     };
     // tiles of 128 (half the loads a product) while there are two for every SM, of 64 for fewer
     const bool large = tiles(128) >= 2 * (int64_t)sms;
-    const int64_t grid = std::min<int64_t>(tiles(large ? 128 : 64), (int64_t)sms * (large ? 2 : 4));
+    const int64_t grid = std::min<int64_t>(tiles(large ? 128 : 64), (int64_t)sms * (large ? 2 : 3));
     void* args[] = {&p};
     const void* fn = large ? (const void*)plain_product_kernel<TO, ROWS, BK, 128> : (const void*)plain_product_kernel<TO, ROWS, BK, 64>;
     return launch_op(fn, dim3((unsigned)grid), dim3(kPThreads), args, 0, stream);
