@@ -19,8 +19,6 @@ namespace {
 // groups: bound[e] .. bound[e + 1] are the rows of expert e, tile[e] the tiles
 // of rows before it
 // ---------------------------------------------------------------------------
-
-
 // By one warp: offsets clamped to [0, rows] and made non-decreasing, and the
 // sums of ceil(rows of a group / tile_rows).
 __device__ __forceinline__ void read_groups(const int32_t* offsets, int E, int64_t rows, int tile_rows, int* bound,
@@ -86,6 +84,7 @@ struct PlainParams {
     int E, M, N, K;           // M: weights' gradient's rows; K: of the first two products
     int a_vec, b_vec;         // whole 16 bytes
     int accumulate;
+    int splits;               // blocks of a tile
 };
 
 constexpr int kPThreads = 256, kPEach = 8, kPPad = 4;
@@ -139,8 +138,19 @@ __device__ __forceinline__ void keep_step(float (&to)[PK][T + kPPad], bool vec, 
 
 // ROWS: the first two products, whose sums run along a's rows; b is summed
 // along its rows (BK) or across them.
-// T x T sums a block, L x L a thread, in pieces of four.
-template <class TO, bool ROWS, bool BK, int T>
+__device__ __forceinline__ float load_remote(const float* local, unsigned rank) {
+    float v;
+    asm volatile("{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %1, %2;\n ld.shared::cluster.f32 %0, [r];\n}\n"
+                 : "=f"(v)
+                 : "r"(smem_addr(local)), "r"(rank)
+                 : "memory");
+    return v;
+}
+
+// T x T sums a block, L x L a thread, in pieces of four.  SPLIT: the blocks of a
+// cluster share a tile, each with a run of the sum's steps; every block then
+// adds up its part of the tile's rows over the blocks, in their order.
+template <class TO, bool ROWS, bool BK, int T, bool SPLIT>
 __global__ void __launch_bounds__(kPThreads) plain_product_kernel(const PlainParams p) {
     constexpr int L = T / 16, PK = kPThreads * kPEach / T;  // steps of 16 or 32 of the sum
     __shared__ __align__(16) float as[2][PK][T + kPPad], bs[2][PK][T + kPPad];
@@ -153,7 +163,8 @@ __global__ void __launch_bounds__(kPThreads) plain_product_kernel(const PlainPar
     __syncthreads();
     const int nt = (p.N + T - 1) / T;
     const int64_t mt = ROWS ? tile[p.E] : (int64_t)((p.M + T - 1) / T) * p.E;
-    for (int64_t i = blockIdx.x; i < mt * nt; i += gridDim.x) {
+    const int splits = SPLIT ? p.splits : 1, rank = SPLIT ? (int)blockIdx.x % splits : 0;
+    for (int64_t i = blockIdx.x / splits; i < mt * nt; i += gridDim.x / splits) {
         const int m = (int)(i / nt), n0 = (int)(i % nt) * T;
         int e, m0, mlen, K;
         int64_t first;  // ROWS: the tile's first row; else the group's
@@ -176,6 +187,8 @@ __global__ void __launch_bounds__(kPThreads) plain_product_kernel(const PlainPar
         const float* a = (const float*)p.a + first * p.a_stride + m0;
         const float* b = (const float*)p.b + (ROWS ? e * p.b_expert + (BK ? (int64_t)n0 * p.b_stride : n0)
                                                    : first * p.b_stride + n0);
+        const int run = ((K + PK - 1) / PK + splits - 1) / splits * PK, begin = rank * run;
+        K = min(K, begin + run);  // this block's steps end there
         float av[kPEach], bv[kPEach];
         Pair acc[L][L / 2];  // two columns each
 #pragma unroll
@@ -191,13 +204,13 @@ __global__ void __launch_bounds__(kPThreads) plain_product_kernel(const PlainPar
             keep_step<BK, T, PK>(bs[h], p.b_vec, bv);
         };
         __syncthreads();  // the tile before has been read
-        if (K) {
-            fetch(0);
+        if (begin < K) {
+            fetch(begin);
             keep(0);
         }
         __syncthreads();
         int h = 0;
-        for (int k0 = 0; k0 < K; k0 += PK, h ^= 1) {
+        for (int k0 = begin; k0 < K; k0 += PK, h ^= 1) {
             if (k0 + PK < K) fetch(k0 + PK);
 #pragma unroll
             for (int k = 0; k < PK; k++) {
@@ -221,6 +234,31 @@ __global__ void __launch_bounds__(kPThreads) plain_product_kernel(const PlainPar
             __syncthreads();
         }
         TO* out = (TO*)p.out + (ROWS ? first * p.out_stride : e * p.out_expert + (int64_t)m0 * p.out_stride) + n0;
+        if constexpr (SPLIT) {
+            static_assert(T * (T + kPPad) <= 2 * PK * (T + kPPad), "the sums take the place of one operand");
+            float(*part)[T + kPPad] = (float(*)[T + kPPad]) & as[0][0][0];
+#pragma unroll
+            for (int q = 0; q < L; q++)
+#pragma unroll
+                for (int r = 0; r < L / 2; r++) {
+                    float2 v;
+                    acc[q][r].get(v.x, v.y);
+                    *(float2*)&part[(q / 4) * 64 + ty * 4 + q % 4][(r / 2) * 64 + tx * 4 + r % 2 * 2] = v;
+                }
+            cluster_arrive();
+            cluster_wait();
+            for (int j = tid; j < T / splits * T; j += kPThreads) {
+                const int row = j / T * splits + rank, col = j % T;
+                if (row >= mlen || col >= nlen) continue;
+                float sum = 0.0f;
+                for (int q = 0; q < splits; q++) sum += load_remote(&part[row][col], q);
+                TO* at = out + row * p.out_stride + col;
+                put(at, (!ROWS && p.accumulate ? to_f32(*at) : 0.0f) + sum);
+            }
+            cluster_arrive();  // all have read before the next tile, or the end
+            cluster_wait();
+            continue;
+        }
 #pragma unroll
         for (int q = 0; q < L; q++) {
             const int row = (q / 4) * 64 + ty * 4 + q % 4;
@@ -798,10 +836,18 @@ cudaError_t launch_plain(PlainParams p, cudaStream_t stream, int sms) {
     };
     // tiles of 128 (half the loads a product) while there are two for every SM, of 64 for fewer
     const bool large = tiles(128) >= 2 * (int64_t)sms;
-    const int64_t grid = std::min<int64_t>(tiles(large ? 128 : 64), (int64_t)sms * (large ? 2 : 3));
+    // less than one for every SM: their sums are split among blocks, each of
+    // which keeps eight steps or more (26 rows an expert, 96 x 3843: 51 us, by
+    // single blocks 173)
+    const int64_t steps = (ROWS ? p.K : p.rows / p.E) / 32;
+    p.splits = 1;
+    while (!large && p.splits < kMaxCluster && tiles(64) * p.splits <= sms && steps >= p.splits * 16) p.splits *= 2;
+    const int64_t grid = std::min<int64_t>(tiles(large ? 128 : 64) * p.splits, (int64_t)sms * (large || p.splits > 1 ? 2 : 3) / p.splits * p.splits);
     void* args[] = {&p};
-    const void* fn = large ? (const void*)plain_product_kernel<TO, ROWS, BK, 128> : (const void*)plain_product_kernel<TO, ROWS, BK, 64>;
-    return launch_op(fn, dim3((unsigned)grid), dim3(kPThreads), args, 0, stream);
+    const void* fn = large          ? (const void*)plain_product_kernel<TO, ROWS, BK, 128, false>
+                     : p.splits > 1 ? (const void*)plain_product_kernel<TO, ROWS, BK, 64, true>
+                                    : (const void*)plain_product_kernel<TO, ROWS, BK, 64, false>;
+    return launch_op(fn, dim3((unsigned)grid), dim3(kPThreads), args, 0, stream, p.splits);
 }
 template <bool ROWS, bool BK>
 cudaError_t launch_plain(const PlainParams& p, hc_dtype_t out, cudaStream_t stream, int sms) {

@@ -320,9 +320,10 @@ hc_status_t hc_graph_destroy(hc_graph_t graph);
  * Training operators
  * ------------------
  * The operators of a training step on either side of its collectives: the
- * embedding lookup, the norms and the gate at a block's boundary and the
- * distillation loss, each with its gradient.  They leave the gradients in
- * the caller's buffers, ready for hc_allreduce / hc_reduce_scatter.
+ * embedding lookup, the norms and the gate at a block's boundary, the
+ * distillation loss and an expert layer, each with its gradient, and the
+ * clipping of the reduced gradients.  They leave the gradients in the caller's
+ * buffers, ready for hc_allreduce / hc_reduce_scatter.
  *
  * Conventions shared by these entry points (the pages have no counterpart)
  *  - One GPU's tensors; asynchronous on `stream`, capturable into a CUDA
@@ -616,7 +617,9 @@ size_t hc_expert_plan_scratch_bytes(const hc_expert_plan_t* args);
  *  experts at most 1024, rows at most 2^30, in_dim and out_dim at most 65536
  *  (HC_ERR_UNSUPPORTED).
  *  scratch   : bf16 operands whose pointers or strides are not whole 16 bytes
- *              are copied into it first; 0 bytes are needed when all are.
+ *              are copied into it first (weights: of experts with rows); 0
+ *              bytes are needed when all are.  *_scratch_bytes looks at the
+ *              pointers' alignment.
  */
 typedef enum { HC_WEIGHT_OUT_IN = 0, HC_WEIGHT_IN_OUT = 1 } hc_weight_layout_t;
 typedef struct {
@@ -818,9 +821,9 @@ hc_status_t hc_select_algo(hc_coll_t coll, int P, int ranks_per_server, size_t c
  * Device-side status of the kernels that wait on shared-memory barriers (the
  * TMA-staged kernels: fused AllReduce / ReduceScatter, the step kernel's
  * launches of wide reduces and broadcasts, the block norm and its gradient
- * for rows of more than 256 columns, and the distillation loss).  Each such
- * wait gives up after about 2 s; the kernel then records HC_ERR_TIMEOUT here
- * and returns instead of hanging.
+ * for rows of more than 256 columns, the distillation loss, and the expert
+ * layer's bf16 products).  Each such wait gives up after about 2 s; the kernel
+ * then records HC_ERR_TIMEOUT here and returns instead of hanging.
  * Returns HC_OK, HC_ERR_TIMEOUT, or HC_ERR_CUDA if the flag cannot be read.
  * Synchronises with the current device (it copies the flag to the host);
  * clear != 0 resets the flag.

@@ -82,6 +82,10 @@ SIZES = [  # rows, experts, in, out
     (600, 4, 1032, 2056),
     # tiles that two blocks share, in all three products
     (5006, 16, 193, 2003), (20011, 5, 1040, 776),
+    # few rows of weights that no tiled copy takes
+    (13, 5, 1003, 37), (16, 40, 515, 129), (3, 2, 8193, 9),
+    # sums of few tiles that several blocks share
+    (40, 3, 3843, 70), (30, 2, 96, 2500), (3000, 1, 65, 40),
 ]
 KINDS = ["even", "skewed", "last", "none"]
 
