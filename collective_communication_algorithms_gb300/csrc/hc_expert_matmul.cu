@@ -257,21 +257,21 @@ __global__ void __launch_bounds__(kPThreads) plain_product_kernel(const PlainPar
             }
             cluster_arrive();  // all have read before the next tile, or the end
             cluster_wait();
-            continue;
-        }
+        } else {
 #pragma unroll
-        for (int q = 0; q < L; q++) {
-            const int row = (q / 4) * 64 + ty * 4 + q % 4;
-            if (row >= mlen) continue;
-            float sums[L];
+            for (int q = 0; q < L; q++) {
+                const int row = (q / 4) * 64 + ty * 4 + q % 4;
+                if (row >= mlen) continue;
+                float sums[L];
 #pragma unroll
-            for (int r = 0; r < L / 2; r++) acc[q][r].get(sums[2 * r], sums[2 * r + 1]);
+                for (int r = 0; r < L / 2; r++) acc[q][r].get(sums[2 * r], sums[2 * r + 1]);
 #pragma unroll
-            for (int r = 0; r < L; r++) {
-                const int col = (r / 4) * 64 + tx * 4 + r % 4;
-                if (col >= nlen) continue;
-                TO* at = out + row * p.out_stride + col;
-                put(at, (!ROWS && p.accumulate ? to_f32(*at) : 0.0f) + sums[r]);
+                for (int r = 0; r < L; r++) {
+                    const int col = (r / 4) * 64 + tx * 4 + r % 4;
+                    if (col >= nlen) continue;
+                    TO* at = out + row * p.out_stride + col;
+                    put(at, (!ROWS && p.accumulate ? to_f32(*at) : 0.0f) + sums[r]);
+                }
             }
         }
     }
@@ -310,7 +310,6 @@ __device__ __forceinline__ uint4 row_vector(const Bf16* row, int c, int cols) {
     }
     return w;
 }
-
 // ---------------------------------------------------------------------------
 // bf16 products of few rows (of all groups together), the weight summed along
 // its rows
@@ -430,9 +429,20 @@ __global__ void __launch_bounds__(kFewThreads) few_rows_kernel(const FewParams p
 // group's last are overwritten with zeros in shared memory, by a warp of their
 // own, before the products may start.
 // ---------------------------------------------------------------------------
-constexpr int kTM = 128, kTK = 64, kTThreads = 256, kTStages = 6;  // kTM: of one block, of both operands
+constexpr int kTM = 128, kTK = 64, kTStages = 6;  // kTM: of one block, of both operands
 constexpr int kTOperandBytes = kTM * kTK * 2, kTStageBytes = 2 * kTOperandBytes;
 constexpr int kTStagingBytes = 4 * 32 * 128;
+// The tensor cores cut off where they add to a sum: after n steps of 16 it is
+// short by about n 2^-26 of itself (2.1e-6 for 2048 rows, measured; 9e-6 for
+// 8192).  binary32 gradients of the weights, which are summed along as many
+// rows as a group has, are therefore taken out every 512 rows and added up,
+// rounded, in registers (4.7e-7 at any length, for 476 us instead of 412 at 32768
+// rows of 16, 2048 x 4096).  bf16 results lose nothing that they could show.
+constexpr int kTSegment = 512;
+template <bool ROWS, class TO>
+constexpr bool kTLong = !ROWS && sizeof(TO) == 4;
+template <bool LONG>
+constexpr int kTThreadsOf = LONG ? 384 : 256;
 
 struct TensorParams {
     CUtensorMap a, b;
@@ -509,10 +519,95 @@ __device__ __forceinline__ TensorTile tensor_tile(const TensorParams& p, const i
     return t;
 }
 
+// The binary32 weight gradients' way out, by eight warps: each has a half of the
+// columns of 32 rows in registers, adds the segments up as they come, and
+// brings the total through shared memory to the output, 16 columns at a time.
+// What the output holds is added by L2 (a rounded addition to each element, one
+// in a call, so the order is fixed all the same): 590 us where waiting for old
+// values took 675 (32768 rows of 16, 2048 x 4096).
+template <int G, int T, class Wait>
+__device__ __forceinline__ void long_sums_to_output(const TensorParams& p, const int* bound, unsigned char* staging, uint64_t* sums_full,
+                                                    uint64_t* sums_empty, uint32_t tmem, int64_t tiles, int across, int rank,
+                                                    Wait warp_wait) {
+    constexpr int W = T / 2;  // columns of a warp
+    const int warp = (threadIdx.x >> 5) - 4, lane = threadIdx.x & 31, q = warp & 3, c0 = (warp >> 2) * W;
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + c0;
+    unsigned char* mine = staging + warp * 2048;
+    const int r0 = lane / 4, at = lane % 4 * 4, m = rank * kTM + q * 32;
+    uint32_t n = 0;
+    for (int64_t i = blockIdx.x / G; i < tiles; i += gridDim.x / G) {
+        const TensorTile t = tensor_tile<false, T>(p, bound, nullptr, i, across);
+        if (!t.K && p.accumulate) continue;
+        const int cols = t.nlen - c0, rows = t.mlen - m;  // of this warp
+        float* out = (float*)p.out + t.e * p.out_expert + (int64_t)(t.m0 + m + r0) * p.out_stride + t.n0 + c0 + at;
+        const bool fast = p.out_vec && t.nlen % 4 == 0, add = p.accumulate;
+        float sum[W];
+#pragma unroll
+        for (int j = 0; j < W; j++) sum[j] = 0.0f;
+        bool ok = true;
+        for (int k = 0; k < t.K; k += kTSegment, n++) {
+            const uint32_t set = n & 1;
+            if (!(ok = warp_wait([&] { return mbar_wait_quick(&sums_full[set], (n >> 1) & 1, p.wait_ns); }))) break;
+            tensor_fence_after();
+#pragma unroll
+            for (int c = 0; c < W; c += 16)
+                if (c < cols) {
+                    uint32_t v[16];
+                    tmem_load16(lanes + set * T + c, v);
+                    tmem_load_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; j++) sum[c + j] += __uint_as_float(v[j]);
+                }
+            tensor_fence_before();
+            __syncwarp();
+            if (lane == 0) first_arrive<G>(&sums_empty[set]);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < W; c += 16) {
+            if (c >= cols) break;
+            __syncwarp();  // the step before has been read
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                *(float4*)(mine + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+                    make_float4(sum[c + 4 * j], sum[c + 4 * j + 1], sum[c + 4 * j + 2], sum[c + 4 * j + 3]);
+            __syncwarp();
+            if (fast) {
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int r = j * 8 + r0;
+                    const float4 x = *(const float4*)(mine + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+                    float* to = out + (int64_t)(j * 8) * p.out_stride + c;
+                    if (r >= rows || c + at >= cols) continue;
+                    if (add)
+                        asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w)
+                                     : "memory");
+                    else
+                        *(float4*)to = x;
+                }
+            } else {  // element by element: a lane has a column of every other row
+                float* to = out - (int64_t)r0 * p.out_stride - at + (lane >> 4) * p.out_stride + (lane & 15) + c;
+                if (c + (lane & 15) < cols)
+#pragma unroll
+                    for (int r = 0; r < 16; r++) {
+                        const int row = 2 * r + (lane >> 4);
+                        const float x = *(const float*)(mine + row * 64 + ((((lane >> 2) & 3) ^ ((row >> 1) & 3)) << 4) + (lane & 3) * 4);
+                        if (row >= rows) continue;
+                        if (add) asm volatile("red.global.add.f32 [%0], %1;" ::"l"(to + 2 * r * p.out_stride), "f"(x) : "memory");
+                        else to[2 * r * p.out_stride] = x;
+                    }
+                __syncwarp();
+            }
+        }
+    }
+}
+
 // ROWS: the first two products; WK: their weight is summed along its rows.
 template <bool ROWS, bool WK, int G, class TO>
-__global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __grid_constant__ TensorParams p) {
+__global__ void __launch_bounds__(kTThreadsOf<kTLong<ROWS, TO>>, 1) tensor_product_kernel(const __grid_constant__ TensorParams p) {
     constexpr int T = kTM * G;
+    constexpr bool LONG = kTLong<ROWS, TO>;
+    constexpr int SEGMENT = LONG ? kTSegment : 1 << 30;  // steps of a sum taken out at once
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int bound[kMaxExperts + 1], tile[kMaxExperts + 1];
     unsigned char* stages = smem + (1024 - (smem_addr(smem) & 1023)) % 1024;
@@ -529,7 +624,7 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
         }
         for (int s = 0; s < 2; s++) {
             mbar_init(&bar.sums_full[s], 1);
-            mbar_init(&bar.sums_empty[s], 4 * G);
+            mbar_init(&bar.sums_empty[s], (LONG ? 8 : 4) * G);
         }
         mbar_init(&bar.drain, 1);
         mbar_init_fence();
@@ -579,6 +674,11 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
             const int am = t.m0 + rank * kTM, half = t.n() / G, bn = (ROWS ? (int)t.first : t.n0) + rank * half;
             const int boxes = (half + 63) / 64;  // of 64 n
             const unsigned bytes = kTOperandBytes + boxes * 8192;
+            // what the sums of this block will be added to is brought into L2
+            // meanwhile, eight rows a step (all that are left with the last)
+            int row = 0;
+            const int rows = LONG && p.accumulate && p.out_vec && t.nlen % 4 == 0 ? min(kTM, t.mlen - rank * kTM) : 0;
+            const uintptr_t old = (uintptr_t)((TO*)p.out + t.e * p.out_expert + (int64_t)am * p.out_stride + t.n0);
             for (int k0 = 0; k0 < t.K; k0 += kTK, at.next()) {
                 const int s = at.s;
                 if (!mbar_wait_quick(&bar.empty[s], at.turn ^ 1, p.wait_ns)) {
@@ -617,6 +717,11 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
                     if (ROWS) tile_g2s<G>(b + j * 8192, &p.b, k0, bn + 64 * j, to);
                     else tile_g2s<G>(b + j * 8192, &p.b, bn + 64 * j, (int)t.first + k0, to);
                 }
+                if constexpr (LONG)
+                    for (const int upto = k0 + kTK < t.K ? min(rows, row + 8) : rows; row < upto; row++)
+                        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(old + (uintptr_t)(row * p.out_stride) * sizeof(TO)),
+                                     "r"((unsigned)(t.nlen * sizeof(TO)))
+                                     : "memory");
             }
         }
         // A block does not leave while copies into its shared memory are under
@@ -650,30 +755,33 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
         for (int64_t i = blockIdx.x / G; ok && i < tiles; i += step) {
             const TensorTile t = tensor_tile<ROWS, T>(p, bound, tile, i, across);
             if (!t.K) continue;
-            const uint32_t set = n & 1, sums = tmem + set * T, shape = product_shape(!AK, !BK, T, t.n());
-            if (!(ok = warp_wait([&] { return first_wait<G>(&bar.sums_empty[set], ((n >> 1) & 1) ^ 1, p.wait_ns); }))) break;
-            tensor_fence_after();
+            const uint32_t shape = product_shape(!AK, !BK, T, t.n());
             for (int k0 = 0; k0 < t.K; k0 += kTK, at.next()) {
+                const uint32_t set = n & 1, sums = tmem + set * T;
+                const int k = k0 % SEGMENT;
+                if (!k) {
+                    if (!(ok = warp_wait([&] { return first_wait<G>(&bar.sums_empty[set], ((n >> 1) & 1) ^ 1, p.wait_ns); }))) break;
+                    tensor_fence_after();
+                }
                 const int s = at.s;
                 if (!(ok = warp_wait([&] { return mbar_wait_quick(&bar.full[s], at.turn, p.wait_ns); }))) break;
                 tensor_fence_after();
                 const uint64_t a = a0 + (uint32_t)(s * (kTStageBytes >> 4)), b = b0 + (uint32_t)(s * (kTStageBytes >> 4));
+                const bool last = k + kTK == SEGMENT || k0 + kTK >= t.K;
                 if (elected()) {
                     if (t.K - k0 >= kTK) {
 #pragma unroll
-                        for (int j = 0; j < kTK / 16; j++) product16<G>(sums, a + j * a_on, b + j * b_on, shape, k0 > 0 || j > 0);
+                        for (int j = 0; j < kTK / 16; j++) product16<G>(sums, a + j * a_on, b + j * b_on, shape, k > 0 || j > 0);
                     } else {
                         for (int j = 0; j < (t.K - k0 + 15) / 16; j++)
-                            product16<G>(sums, a + j * a_on, b + j * b_on, shape, k0 > 0 || j > 0);
+                            product16<G>(sums, a + j * a_on, b + j * b_on, shape, k > 0 || j > 0);
                     }
                     products_arrive<G>(&bar.empty[s]);
+                    if (last) products_arrive<G>(&bar.sums_full[set]);
                 }
                 __syncwarp();
+                n += last;
             }
-            if (!ok) break;
-            if (elected()) products_arrive<G>(&bar.sums_full[set]);
-            __syncwarp();
-            n++;
         }
         if (elected()) products_arrive<G>(&bar.drain, false);  // tensor memory is freed after the last products
         __syncwarp();
@@ -703,6 +811,8 @@ __global__ void __launch_bounds__(kTThreads, 1) tensor_product_kernel(const __gr
                 if (lane == 0) mbar_arrive(&bar.full[s]);
             }
         }
+    } else if constexpr (LONG) {
+        if (warp >= 4) long_sums_to_output<G, T>(p, bound, staging, bar.sums_full, bar.sums_empty, tmem, tiles, across, rank, warp_wait);
     } else if (warp >= 4) {  // sums to the output
         constexpr int V = 16 / (int)sizeof(TO), PER = 32 / V, N = 32 / V;  // elements of a lane, lanes and steps of 32 columns
         const int q = warp - 4;
@@ -1004,7 +1114,7 @@ cudaError_t launch_tensor(TensorParams& p, const Operand& a, const Operand& b, c
     const int64_t mt = ROWS ? p.rows / T + std::min<int64_t>(p.E, p.rows) + 1 : (int64_t)((p.M + T - 1) / T) * p.E;
     void* args[] = {&p};
     const int64_t grid = std::min<int64_t>(mt * nt, sms / G) * G;
-    return launch_op(fn, dim3((unsigned)grid), dim3(kTThreads), args, kTSmem, stream, G);
+    return launch_op(fn, dim3((unsigned)grid), dim3(kTThreadsOf<kTLong<ROWS, TO>>), args, kTSmem, stream, G);
 }
 template <bool ROWS, bool WK>
 cudaError_t launch_tensor(TensorParams& p, const Operand& a, const Operand& b, hc_dtype_t out, cudaStream_t stream, int sms) {
