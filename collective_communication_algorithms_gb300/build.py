@@ -55,6 +55,7 @@ def build(force: bool = False) -> str:
     deps = [os.path.join(CSRC, s) for s in SOURCES]
     deps += [os.path.join(CSRC, "hc_internal.h"), os.path.join(CSRC, "hc_device.cuh"),
              os.path.join(CSRC, "hc_ops.h"), os.path.join(CSRC, "hc_ops.cuh"),
+             os.path.join(CSRC, "hc_tensor.cuh"),
              os.path.join(ROOT, "include", "hc.h")]
     if not force and not _stale(LIB, deps):
         return LIB
