@@ -646,8 +646,9 @@ size_t hc_expert_matmul_scratch_bytes(const hc_expert_matmul_t* args);
  *               read for grad_x, x only for grad_weight.
  *  accumulate : 1: added to what grad_weight holds (in binary32, rounded
  *               once; bf16 operands, binary32 gradients: one addition to each
- *               element in L2, where subnormal values count as 0); experts without rows are then left alone.  0: their
- *               gradients are written as zeros.
+ *               element in L2, where subnormal values count as 0); experts
+ *               without rows are then left alone.  0: their gradients are
+ *               written as zeros.
  * Sums of bf16 products along rows are rounded every 512 rows (binary32
  * gradients of the weights); other sums of bf16 products lose up to 2^-29 of
  * their terms' magnitudes for each term in the tensor cores, which cut off.
