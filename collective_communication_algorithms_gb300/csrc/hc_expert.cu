@@ -433,13 +433,15 @@ cudaError_t launch_expert_plan(const hc_expert_plan_t& a, cudaStream_t stream) {
     p.blocks = s.blocks;
     void* args[] = {&p};
     const int smem = (kPlanWarps + (s.blocks > 1 ? 2 : 0)) * p.E * (int)sizeof(int32_t);
+    const void* fn = s.blocks > 1 ? (const void*)plan_place_kernel<false> : (const void*)plan_place_kernel<true>;
+    // asked for at any size: what a block has without asking, 48 KiB, counts
+    // the kernel's own variables too
+    if (!allow_smem((void*)fn, smem)) return cudaErrorInvalidValue;
     if (s.blocks > 1) {
         const cudaError_t e = launch_op((const void*)plan_count_kernel, dim3((unsigned)s.blocks), dim3(kPlanThreads), args,
                                         p.E * sizeof(int32_t), stream);
         if (e != cudaSuccess) return e;
     }
-    const void* fn = s.blocks > 1 ? (const void*)plan_place_kernel<false> : (const void*)plan_place_kernel<true>;
-    if (smem > 48 * 1024 && !allow_smem((void*)fn, smem)) return cudaErrorInvalidValue;
     return launch_op(fn, dim3((unsigned)s.blocks), dim3(kPlanThreads), args, smem, stream);
 }
 
