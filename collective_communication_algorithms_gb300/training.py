@@ -354,6 +354,28 @@ def bind_distill_grad(logits, teacher_logits, teacher_ids, stats, row_weight=Non
                  (logits, teacher_logits, teacher_ids, row_weight, stats, grad), logits)
 
 
+def _dense(name, t, device):
+    """A CUDA tensor whose elements fill one piece of memory, in any order of
+    its dimensions."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+    if not t.is_contiguous():
+        at = 1
+        for stride, size in sorted((t.stride(d), t.shape[d]) for d in range(t.dim()) if t.shape[d] > 1):
+            if stride != at:
+                raise ValueError("%s must be dense (strides %s of shape %s)" % (name, t.stride(), tuple(t.shape)))
+            at *= size
+    return t
+
+
+def _alike(a, b):
+    """Whether two dense tensors of one shape hold their elements in one order."""
+    return a.stride() == b.stride() or not a.numel() or all(
+        x == y or n == 1 for x, y, n in zip(a.stride(), b.stride(), a.shape))
+
+
 def _clip(name, grads, out, norm, factor, scratch, stream, **kw):
     import torch
     grads = list(grads)
@@ -366,10 +388,14 @@ def _clip(name, grads, out, norm, factor, scratch, stream, **kw):
             raise ValueError("%d outputs for %d gradients" % (len(out), len(grads)))
     table = (B.hc_grad_t * len(grads))()
     for i, g in enumerate(grads):
-        _check("grads[%d]" % i, g, g.shape, device=first.device, contiguous=True)
+        _dense("grads[%d]" % i, g, first.device)
         table[i].in_, table[i].count, table[i].in_dtype = g.data_ptr(), g.numel(), B.DTYPES[_dtype(g)]
         if out is not None:
-            o = _check("out[%d]" % i, out[i], g.shape, device=first.device, contiguous=True)
+            o = _dense("out[%d]" % i, out[i], first.device)
+            if o.shape != g.shape:
+                raise ValueError("out[%d] has shape %s, not %s" % (i, tuple(o.shape), tuple(g.shape)))
+            if not _alike(o, g):
+                raise ValueError("out[%d] is laid out in strides %s, not in %s" % (i, o.stride(), g.stride()))
             table[i].out, table[i].out_dtype = o.data_ptr(), B.DTYPES[_dtype(o)]
     norm = _new(first, (1,), torch.float32) if norm is None else norm
     _check("norm", norm, (1,), torch.float32, first.device, contiguous=True)
@@ -387,10 +413,11 @@ def _clip(name, grads, out, norm, factor, scratch, stream, **kw):
 @_on_stream
 def bind_clip_grads(grads, max_norm, out=None, norm=None, factor=None, scale=1.0, eps=1e-6, scratch=None, *,
                     stream=None):
-    """The gradients (a sequence of contiguous tensors, bf16 and fp32 mixed as
-    they come) times scale * min(1, max_norm / (norm + eps)), where norm =
-    |scale| * the root of the sum of all their squares: in place, or into the
-    tensors of `out` (of either type)."""
+    """The gradients (a sequence of dense tensors, bf16 and fp32 mixed as they
+    come) times scale * min(1, max_norm / (norm + eps)), where norm = |scale| *
+    the root of the sum of all their squares: in place, or into the tensors of
+    `out` (of either type, laid out as the gradients are).  Dense: the elements
+    fill one piece of memory, in any order of the dimensions."""
     return _clip("hc_clip_grads", grads, out, norm, factor, scratch, stream, scale=scale, max_norm=max_norm, eps=eps)
 
 
