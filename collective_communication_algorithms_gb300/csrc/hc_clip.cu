@@ -245,7 +245,8 @@ __device__ __forceinline__ Factor factor_of(const P& p) {
         const float norm = __fsqrt_rn(__fadd_rn(q.hi, q.lo)), scaled = norm * fabsf(p.scale), limit = p.max_norm;
         // all that follows lies well inside binary32's range
         const auto middling = [](float v) { return v > 1e-18f && v < 1e18f; };
-        if (q.wide == 0.0 && middling(scaled) && middling(fabsf(p.scale)) && (middling(limit) || isinf(limit))) {
+        if (q.wide == 0.0 && middling(scaled) && middling(scaled + p.eps) && middling(fabsf(p.scale)) &&
+            (middling(limit) || isinf(limit))) {
             f.norm = scaled;
             f.factor = fminf(1.0f, __fdiv_rn(limit, scaled + p.eps)) * p.scale;
         } else {
