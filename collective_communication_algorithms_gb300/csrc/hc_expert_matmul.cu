@@ -461,6 +461,7 @@ struct TensorBarriers {
     uint64_t zeroed[kTStages];  // by the other block, which may be stages ahead
     uint64_t sums_full[2], sums_empty[2], drain;
     uint32_t tmem;
+    volatile uint32_t copied;  // stages whose copies this block has begun
 };
 constexpr int kTSmem = 1024 + kTStages * kTStageBytes + kTStagingBytes + (int)sizeof(TensorBarriers) + 8;
 
@@ -628,6 +629,7 @@ __global__ void __launch_bounds__(kTThreadsOf<kTLong<ROWS, TO>>, 1) tensor_produ
             mbar_init(&bar.sums_empty[s], (LONG ? 8 : 4) * G);
         }
         mbar_init(&bar.drain, 1);
+        bar.copied = 0;
         mbar_init_fence();
         prefetch_map(&p.a);
         prefetch_map(&p.b);
@@ -651,11 +653,18 @@ __global__ void __launch_bounds__(kTThreadsOf<kTLong<ROWS, TO>>, 1) tensor_produ
     const auto expired = [&] { atomicExch(p.err, (int)HC_ERR_TIMEOUT); };
     // A whole warp's wait: one lane polls, and the warp is together again
     // afterwards, as elections and loads from tensor memory need it, with one
-    // answer for all.
+    // answer for all.  What is waited for may lie any number of stages ahead (a
+    // tile's sums, the next group with a remainder), so the wait only gives up
+    // when the block's copies have stood still for as long; they stop by
+    // themselves once the ring is full.
     const auto warp_wait = [&](auto wait) {
         bool ok = true;
         if (lane == 0) {
-            ok = wait();
+            uint32_t before;
+            do {
+                before = bar.copied;
+                ok = wait();
+            } while (!ok && bar.copied != before);
             if (!ok) expired();
         }
         ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
@@ -666,6 +675,7 @@ __global__ void __launch_bounds__(kTThreadsOf<kTLong<ROWS, TO>>, 1) tensor_produ
     if (warp == 0 && lane == 0) {  // copies
         Ring at;
         int issued = 0;           // stages that hold copies, at most all
+        uint32_t copied = 0;
         uint32_t turns = 0;       // the parity of each stage's last turn
         uint32_t raw_used = 0;    // stages whose last copies went to raw
         uint32_t raw_phase = 0;
@@ -713,6 +723,7 @@ __global__ void __launch_bounds__(kTThreadsOf<kTLong<ROWS, TO>>, 1) tensor_produ
                     if (ROWS) tile_g2s<G>(b + j * 8192, &p.b, k0, bn + 64 * j, to);
                     else tile_g2s<G>(b + j * 8192, &p.b, bn + 64 * j, (int)t.first + k0, to);
                 }
+                bar.copied = ++copied;
             }
         }
         // A block does not leave while copies into its shared memory are under
