@@ -612,8 +612,9 @@ size_t hc_expert_plan_scratch_bytes(const hc_expert_plan_t* args);
  * Rows in no group are not read, and are left as they were in out.  Offsets
  * are clamped to [0, rows] and to non-decreasing order.
  *  dtype     : x and weight; out_dtype: out.  Products of bf16 values are
- *              exact and are summed in binary32 by the tensor cores; binary32
- *              values are multiplied and summed in binary32 (no TF32).
+ *              exact and are summed in binary32 by the tensor cores (how
+ *              exactly: hc_expert_matmul_grad below); binary32 values are
+ *              multiplied and summed in binary32 (no TF32).
  *  experts at most 1024, rows at most 2^30, in_dim and out_dim at most 65536
  *  (HC_ERR_UNSUPPORTED).
  *  scratch   : bf16 operands whose pointers or strides are not whole 16 bytes
@@ -649,9 +650,10 @@ size_t hc_expert_matmul_scratch_bytes(const hc_expert_matmul_t* args);
  *               element in L2, where subnormal values count as 0); experts
  *               without rows are then left alone.  0: their gradients are
  *               written as zeros.
- * Sums of bf16 products along rows are rounded every 512 rows (binary32
- * gradients of the weights); other sums of bf16 products lose up to 2^-29 of
- * their terms' magnitudes for each term in the tensor cores, which cut off.
+ * The tensor cores, which sum the products of bf16 values (here and in
+ * hc_expert_matmul), cut off where they add, up to 2^-25 of the sum so far for
+ * each term.  Sums for binary32 results are therefore taken out every 512 terms
+ * and added up, rounded: terms of one sign end short by at most 1e-5 of their sum.
  */
 typedef struct {
     size_t struct_size;
