@@ -439,12 +439,16 @@ constexpr int kTStagingBytes = 4 * 32 * 128;
 // that is half of its end on average, n / 16 2^-24 for the sums).  Measured, bf16
 // values of [0.5, 1): 3.2e-5 after 8192, 3.8e-4 after 65536 terms.
 // LONG: sums are taken out every kTSegment steps and added up, rounded, in
-// registers: at most 9.5e-6 of a segment at any length.  binary32 results of
-// long sums are made so (weight gradients: 476 us instead of 412 at 32768 rows of
-// 16, 2048 x 4096; forward product: 369 instead of 348 at 4096 -> 2048).
-constexpr int kTSegment = 512;
-template <bool ROWS, class TO>
-constexpr bool kTLong = sizeof(TO) == 4;
+// registers, so that no length costs more than a segment does: 9.5e-6 of it for
+// binary32 results, 1.5e-4 for bf16 ones, whose own rounding is up to 2e-3.
+// binary32 results are always made so (476 us instead of 412 for weight gradients
+// of 32768 rows of 16, 2048 x 4096; 369 instead of 348 for the forward product of
+// as many, 4096 -> 2048), bf16 ones from sums of more than kTPlain terms (353 us
+// either way for those weight gradients, but with plain sums four warps are
+// enough).
+template <class TO>
+constexpr int kTSegment = sizeof(TO) == 4 ? 512 : 8192;
+constexpr int64_t kTPlain = 16384;
 template <bool LONG>
 constexpr int kTThreadsOf = LONG ? 384 : 256;
 
@@ -529,11 +533,11 @@ __device__ __forceinline__ TensorTile tensor_tile(const TensorParams& p, const i
 // forward product a column of sums is a row of the output, which the 32 lanes
 // store as it is; the weights' gradient goes through shared memory, 16 columns at
 // a time.
-// What the output holds is added by L2 (a rounded addition to each element, one
-// in a call, so the order is fixed all the same): 478 us where waiting for old
+// What a binary32 output holds is added by L2 (a rounded addition to each
+// element, one in a call, so the order is fixed all the same): 478 us where waiting for old
 // values took 675, and bringing them into L2 beforehand 590 (32768 rows of 16,
 // 2048 x 4096; 462 without adding).
-template <bool ROWS, int G, int T, class Wait>
+template <bool ROWS, int G, int T, class TO, class Wait>
 __device__ __forceinline__ void long_sums_to_output(const TensorParams& p, const int* bound, const int* tile, unsigned char* staging,
                                                     uint64_t* sums_full, uint64_t* sums_empty, uint32_t tmem, int64_t tiles, int across,
                                                     int rank, Wait warp_wait) {
@@ -551,7 +555,7 @@ __device__ __forceinline__ void long_sums_to_output(const TensorParams& p, const
 #pragma unroll
         for (int j = 0; j < W; j++) sum[j] = 0.0f;
         bool ok = true;
-        for (int k = 0; k < t.K; k += kTSegment, n++) {
+        for (int k = 0; k < t.K; k += kTSegment<TO>, n++) {
             const uint32_t set = n & 1;
             if (!(ok = warp_wait([&] { return mbar_wait_quick(&sums_full[set], (n >> 1) & 1, p.wait_ns); }))) break;
             tensor_fence_after();
@@ -570,17 +574,17 @@ __device__ __forceinline__ void long_sums_to_output(const TensorParams& p, const
         }
         if (!ok) break;
         if constexpr (ROWS) {
-            float* to = (float*)p.out + (t.first + c0) * p.out_stride + t.m0 + m + lane;
+            TO* to = (TO*)p.out + (t.first + c0) * p.out_stride + t.m0 + m + lane;
 #pragma unroll
             for (int c = 0; c < W; c += 16) {
                 if (c >= cols) break;
 #pragma unroll
                 for (int j = 0; j < 16; j++)
-                    if (c + j < cols && lane < rows) to[(c + j) * p.out_stride] = sum[c + j];
+                    if (c + j < cols && lane < rows) put(to + (c + j) * p.out_stride, sum[c + j]);
             }
             continue;
         }
-        float* out = (float*)p.out + t.e * p.out_expert + (int64_t)(t.m0 + m + r0) * p.out_stride + t.n0 + c0 + at;
+        TO* out = (TO*)p.out + t.e * p.out_expert + (int64_t)(t.m0 + m + r0) * p.out_stride + t.n0 + c0 + at;
         const bool fast = p.out_vec && t.nlen % 4 == 0, add = p.accumulate;
 #pragma unroll
         for (int c = 0; c < W; c += 16) {
@@ -592,28 +596,43 @@ __device__ __forceinline__ void long_sums_to_output(const TensorParams& p, const
                     make_float4(sum[c + 4 * j], sum[c + 4 * j + 1], sum[c + 4 * j + 2], sum[c + 4 * j + 3]);
             __syncwarp();
             if (fast) {
+                uint2 old[4];  // bf16: what is added to
+                if constexpr (sizeof(TO) == 2)
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        if (add && j * 8 + r0 < rows && c + at < cols) old[j] = *(const uint2*)(out + (int64_t)(j * 8) * p.out_stride + c);
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     const int r = j * 8 + r0;
-                    const float4 x = *(const float4*)(mine + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
-                    float* to = out + (int64_t)(j * 8) * p.out_stride + c;
+                    float4 x = *(const float4*)(mine + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+                    TO* to = out + (int64_t)(j * 8) * p.out_stride + c;
                     if (r >= rows || c + at >= cols) continue;
-                    if (add)
+                    if constexpr (sizeof(TO) == 2) {
+                        if (add) {
+                            x.x += bf_lo(old[j].x);
+                            x.y += bf_hi(old[j].x);
+                            x.z += bf_lo(old[j].y);
+                            x.w += bf_hi(old[j].y);
+                        }
+                        *(uint2*)to = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+                    } else if (add)
                         asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w)
                                      : "memory");
                     else
                         *(float4*)to = x;
                 }
             } else {  // element by element: a lane has a column of every other row
-                float* to = out - (int64_t)r0 * p.out_stride - at + (lane >> 4) * p.out_stride + (lane & 15) + c;
+                TO* to = out - (int64_t)r0 * p.out_stride - at + (lane >> 4) * p.out_stride + (lane & 15) + c;
                 if (c + (lane & 15) < cols)
 #pragma unroll
                     for (int r = 0; r < 16; r++) {
                         const int row = 2 * r + (lane >> 4);
                         const float x = *(const float*)(mine + row * 64 + ((((lane >> 2) & 3) ^ ((row >> 1) & 3)) << 4) + (lane & 3) * 4);
                         if (row >= rows) continue;
-                        if (add) asm volatile("red.global.add.f32 [%0], %1;" ::"l"(to + 2 * r * p.out_stride), "f"(x) : "memory");
-                        else to[2 * r * p.out_stride] = x;
+                        TO* one = to + 2 * r * p.out_stride;
+                        if constexpr (sizeof(TO) == 2) put(one, add ? to_f32(*one) + x : x);
+                        else if (add) asm volatile("red.global.add.f32 [%0], %1;" ::"l"(one), "f"(x) : "memory");
+                        else *one = x;
                     }
                 __syncwarp();
             }
@@ -622,11 +641,10 @@ __device__ __forceinline__ void long_sums_to_output(const TensorParams& p, const
 }
 
 // ROWS: the first two products; WK: their weight is summed along its rows.
-template <bool ROWS, bool WK, int G, class TO>
-__global__ void __launch_bounds__(kTThreadsOf<kTLong<ROWS, TO>>, 1) tensor_product_kernel(const __grid_constant__ TensorParams p) {
+template <bool ROWS, bool WK, int G, class TO, bool LONG>
+__global__ void __launch_bounds__(kTThreadsOf<LONG>, 1) tensor_product_kernel(const __grid_constant__ TensorParams p) {
     constexpr int T = kTM * G;
-    constexpr bool LONG = kTLong<ROWS, TO>;
-    constexpr int SEGMENT = LONG ? kTSegment : 1 << 30;  // steps of a sum taken out at once
+    constexpr int SEGMENT = LONG ? kTSegment<TO> : 1 << 30;  // steps of a sum taken out at once
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int bound[kMaxExperts + 1], tile[kMaxExperts + 1];
     unsigned char* stages = smem + (1024 - (smem_addr(smem) & 1023)) % 1024;
@@ -832,7 +850,7 @@ __global__ void __launch_bounds__(kTThreadsOf<kTLong<ROWS, TO>>, 1) tensor_produ
         }
     } else if constexpr (LONG) {
         if (warp >= 4)
-            long_sums_to_output<ROWS, G, T>(p, bound, tile, staging, bar.sums_full, bar.sums_empty, tmem, tiles, across, rank, warp_wait);
+            long_sums_to_output<ROWS, G, T, TO>(p, bound, tile, staging, bar.sums_full, bar.sums_empty, tmem, tiles, across, rank, warp_wait);
     } else if (warp >= 4) {  // sums to the output
         constexpr int V = 16 / (int)sizeof(TO), PER = 32 / V, N = 32 / V;  // elements of a lane, lanes and steps of 32 columns
         const int q = warp - 4;
@@ -1118,7 +1136,7 @@ cudaError_t describe(CUtensorMap* map, const Operand& x, int box_rows, bool expe
                : cudaErrorInvalidValue;
 }
 
-template <bool ROWS, bool WK, int G, class TO>
+template <bool ROWS, bool WK, int G, class TO, bool LONG>
 cudaError_t launch_tensor(TensorParams& p, const Operand& a, const Operand& b, cudaStream_t stream, int sms) {
     constexpr int T = kTM * G;
     cudaError_t e = describe(&p.a, a, ROWS && WK ? kTM : 64, ROWS);
@@ -1128,22 +1146,27 @@ cudaError_t launch_tensor(TensorParams& p, const Operand& a, const Operand& b, c
     if (!p.err) return cudaErrorInvalidValue;
     p.hold = expiring_waits() ? 1 : 0;
     p.wait_ns = p.hold ? kTestWaitLimitNs : kWaitLimitNs;
-    const void* fn = (const void*)tensor_product_kernel<ROWS, WK, G, TO>;
+    const void* fn = (const void*)tensor_product_kernel<ROWS, WK, G, TO, LONG>;
     if (!allow_smem((void*)fn, kTSmem)) return cudaErrorInvalidValue;
     const int64_t nt = (p.N + T - 1) / T;
     const int64_t mt = ROWS ? p.rows / T + std::min<int64_t>(p.E, p.rows) + 1 : (int64_t)((p.M + T - 1) / T) * p.E;
     void* args[] = {&p};
     const int64_t grid = std::min<int64_t>(mt * nt, sms / G) * G;
-    return launch_op(fn, dim3((unsigned)grid), dim3(kTThreadsOf<kTLong<ROWS, TO>>), args, kTSmem, stream, G);
+    return launch_op(fn, dim3((unsigned)grid), dim3(kTThreadsOf<LONG>), args, kTSmem, stream, G);
 }
 template <bool ROWS, bool WK>
 cudaError_t launch_tensor(TensorParams& p, const Operand& a, const Operand& b, hc_dtype_t out, cudaStream_t stream, int sms) {
     // Two blocks a tile, unless that leaves pairs of SMs without one.
     const int64_t mt = ROWS ? (p.rows + 255) / 256 : (int64_t)((p.M + 255) / 256) * p.E;
     const bool two = mt * ((p.N + 255) / 256) >= sms / 2;
-    if (out == HC_BFLOAT16)
-        return two ? launch_tensor<ROWS, WK, 2, Bf16>(p, a, b, stream, sms) : launch_tensor<ROWS, WK, 1, Bf16>(p, a, b, stream, sms);
-    return two ? launch_tensor<ROWS, WK, 2, float>(p, a, b, stream, sms) : launch_tensor<ROWS, WK, 1, float>(p, a, b, stream, sms);
+    if (out == HC_FLOAT32)
+        return two ? launch_tensor<ROWS, WK, 2, float, true>(p, a, b, stream, sms)
+                   : launch_tensor<ROWS, WK, 1, float, true>(p, a, b, stream, sms);
+    if ((ROWS ? p.K : p.rows) > kTPlain)  // a group's rows are the device's to know: all of them at most
+        return two ? launch_tensor<ROWS, WK, 2, Bf16, true>(p, a, b, stream, sms)
+                   : launch_tensor<ROWS, WK, 1, Bf16, true>(p, a, b, stream, sms);
+    return two ? launch_tensor<ROWS, WK, 2, Bf16, false>(p, a, b, stream, sms)
+               : launch_tensor<ROWS, WK, 1, Bf16, false>(p, a, b, stream, sms);
 }
 
 Operand rows_operand(const void* p, size_t rows, size_t cols, size_t stride) {

@@ -18,7 +18,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import collective_communication_algorithms_gb300 as hc  # noqa: E402
-from training_util import D  # noqa: E402
+from training_util import D, half_ulp  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -131,3 +131,57 @@ def test_long_products_in_binary32(inner, rows, outer, layout):
         want = torch.cat([x[cuts[e]:cuts[e + 1]].to(D) @ part.to(D).t() for part in w[e].split(256)], dim=1)
         off = (out[cuts[e]:cuts[e + 1]].to(D) - want).abs() / want
         assert float(off.max()) <= short(inner, 512), float(off.max())
+
+
+@pytest.mark.parametrize("inner,outer", [(24, 40), (33, 17), (264, 520)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_weight_gradients_in_bf16_of_a_million_rows(inner, outer, accumulate):
+    """Segments of 8192 rows, and the rounding to bf16, which is 12 times as much."""
+    g = gen(inner)
+    cuts, offsets = cut_at([(1 << 20) + 77, 1000])
+    x, go = upper(g, cuts[-1], inner), upper(g, cuts[-1], outer)
+    gw = upper(g, 2, outer, inner)
+    want = weight_gradient(go, x, cuts) + (gw.to(D) if accumulate else 0.0)
+    hc.expert_matmul_grad(go, offsets, x=x, grad_weight=gw, accumulate=accumulate)
+    off = ((gw.to(D) - want).abs() - half_ulp(want, BF16)) / want
+    assert float(off.max()) <= short((1 << 20) + 77, 8192), float(off.max())
+
+
+@pytest.mark.parametrize("inner", [16384, 16385, 65536])
+@pytest.mark.parametrize("rows,outer", [(100, 24), (3000, 2003)])
+@pytest.mark.parametrize("layout", ["out_in", "in_out"])
+def test_long_products_in_bf16(inner, rows, outer, layout):
+    """Sums of more than 16384 terms are taken out too."""
+    g = gen(inner)
+    cuts, offsets = cut_at([rows // 3, 0, rows - rows // 3])
+    x = upper(g, rows, inner)
+    w = upper(g, 3, outer, inner)
+    if layout == "in_out":
+        w = w.transpose(1, 2).contiguous().transpose(1, 2)
+    out = hc.expert_matmul(x, w, offsets)["out"]
+    for e in (0, 2):
+        want = torch.cat([x[cuts[e]:cuts[e + 1]].to(D) @ part.to(D).t() for part in w[e].split(256)], dim=1)
+        off = ((out[cuts[e]:cuts[e + 1]].to(D) - want).abs() - half_ulp(want, BF16)) / want
+        assert float(off.max()) <= short(inner, 16384 if inner <= 16384 else 8192), float(off.max())
+
+
+@pytest.mark.parametrize("inner,outer", [(40, 24), (129, 136), (264, 520)])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("layout", ["out_in", "in_out"])
+def test_weight_gradients_of_whole_numbers_over_many_rows(inner, outer, accumulate, layout):
+    """Groups around a bf16 segment, and a strided, unaligned gradient whose
+    surroundings stay as they are."""
+    g = gen(outer)
+    counts = [8191, 0, 8192, 8193, 16385, 1, 63, 64]
+    cuts, offsets = cut_at(counts)
+    x, go = whole(g, cuts[-1], inner), whole(g, cuts[-1], outer)
+    a, b = (outer, inner) if layout == "out_in" else (inner, outer)
+    store = torch.full((len(counts) * (a * (b + 3) + 5) + 7,), -7.0, dtype=BF16, device="cuda")
+    gw = store[1:].as_strided((len(counts), a, b), (a * (b + 3) + 5, b + 3, 1))
+    gw.copy_(whole(g, len(counts), a, b))
+    gw = gw if layout == "out_in" else gw.transpose(1, 2)
+    want = weight_gradient(go, x, cuts) + (gw.to(D) if accumulate else 0.0)
+    hc.expert_matmul_grad(go, offsets, x=x, grad_weight=gw, accumulate=accumulate)
+    assert torch.equal(gw, want.to(F32).to(BF16))
+    gw.fill_(-7.0)
+    assert bool((store == -7.0).all())
