@@ -185,3 +185,29 @@ def test_weight_gradients_of_whole_numbers_over_many_rows(inner, outer, accumula
     assert torch.equal(gw, want.to(F32).to(BF16))
     gw.fill_(-7.0)
     assert bool((store == -7.0).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_whole_numbers_behind_two_gib(dtype):
+    """Every output of rows whose offsets in elements pass 2^31, to the bit."""
+    inner, rows = 32768, 70001
+    if torch.cuda.mem_get_info()[0] < 12 * rows * inner * 2:
+        pytest.skip("needs %d GB" % (12 * rows * inner * 2 >> 30))
+    g = gen(12)
+    cuts, offsets = cut_at([rows - 35, 0, 33])  # the last two rows are in no group
+    x = torch.zeros(rows, inner, dtype=dtype, device="cuda")
+    x[-200:] = whole(g, 200, inner).to(dtype)
+    x[:100] = whole(g, 100, inner).to(dtype)
+    w, go = whole(g, 3, 24, inner).to(dtype), whole(g, rows, 24).to(dtype)
+    out = hc.expert_matmul(x, w, offsets)["out"]
+    gw = torch.empty(3, 24, inner, device="cuda")
+    o = hc.expert_matmul_grad(go, offsets, x=x, weight=w, grad_weight=gw)
+    for e in range(3):
+        a, b = cuts[e], cuts[e + 1]
+        for c in range(a, b, 8192):
+            d = min(b, c + 8192)
+            assert torch.equal(out[c:d], (x[c:d].to(D) @ w[e].to(D).t()).to(F32).to(dtype))
+            assert torch.equal(o["grad_x"][c:d], (go[c:d].to(D) @ w[e].to(D)).to(F32).to(dtype))
+        near = torch.tensor([r for r in range(a, b) if r < 100 or r >= rows - 200], dtype=torch.long, device="cuda")  # others are 0
+        assert torch.equal(gw[e], (go[near].to(D).t() @ x[near].to(D)).to(F32))
+    assert bool((out[-2:] == 0).all()) and bool((o["grad_x"][-2:] == 0).all())
