@@ -564,7 +564,6 @@ __device__ __forceinline__ void long_sums_to_output(const TensorParams& p, const
                 if (c < cols) {
                     uint32_t v[16];
                     tmem_load16(lanes + set * T + c, v);
-                    tmem_load_wait();
 #pragma unroll
                     for (int j = 0; j < 16; j++) sum[c + j] += __uint_as_float(v[j]);
                 }
@@ -899,7 +898,6 @@ __global__ void __launch_bounds__(kTThreadsOf<LONG>, 1) tensor_product_kernel(co
                     if (t.K) {
                         __syncwarp();
                         tmem_load32(lanes + set * T + c, v);
-                        tmem_load_wait();
                         if (c + 32 >= t.nlen) {
                             tensor_fence_before();
                             __syncwarp();
