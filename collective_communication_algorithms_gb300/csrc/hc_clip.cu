@@ -4,10 +4,11 @@
 //   norm = |scale| sqrt(sum g^2),  out = scale min(1, max_norm / (norm + eps)) g
 //
 // Bound by bytes: every gradient is read for the norm, read again for the
-// product, and written.  Two kernels: the first leaves one partial sum a block, the second adds those up in every block (in the same order, so
-// all get the same factor) and scales.  A block has the same run of the
-// tensors in both and goes through it forwards, then backwards, so that what
-// it read last still comes from L2.
+// product, and written.  Two kernels: the first leaves one partial sum a block,
+// the second adds those up in every block (in the same order, so all get the same
+// factor) and scales.  A block has the same run of the tensors in both and goes
+// through it forwards, then backwards, so that what it read last still comes from
+// L2.
 //
 // The tensors' table travels in the kernel's parameters (up to 32 KB), so a
 // call needs no copy to the device and can be captured; longer lists take
@@ -100,11 +101,6 @@ __device__ __forceinline__ void store_one(uintptr_t p, bool bf, uint64_t i, floa
     else ((float*)p)[i] = v;
 }
 
-template <bool BF>
-__device__ __forceinline__ void words_of(const uint4& w, float (&v)[BF ? 8 : 4]) {
-    unpack(w, v);
-}
-
 // The squares of up to kClipBatch vectors held in registers.
 template <bool BF>
 __device__ __forceinline__ void add_vectors(SquareSum& q, const uint4 (&w)[kClipBatch]) {
@@ -112,7 +108,7 @@ __device__ __forceinline__ void add_vectors(SquareSum& q, const uint4 (&w)[kClip
 #pragma unroll
     for (int i = 0; i < kClipBatch; i++) {
         float v[BF ? 8 : 4];
-        words_of<BF>(w[i], v);
+        unpack(w[i], v);
 #pragma unroll
         for (int j = 0; j < (BF ? 8 : 4); j += 4) {
             a = fmaf(v[j], v[j], a);
@@ -137,7 +133,7 @@ __device__ __forceinline__ void add_vectors(SquareSum& q, const uint4 (&w)[kClip
         for (int k = 1; k < kClipBatch; k++)
             if (k == i) x = w[k];
         float v[BF ? 8 : 4];
-        words_of<BF>(x, v);
+        unpack(x, v);
 #pragma unroll
         for (int j = 0; j < (BF ? 8 : 4); j++) q.wide = fma((double)v[j], (double)v[j], q.wide);
     }

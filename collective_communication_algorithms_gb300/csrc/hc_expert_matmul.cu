@@ -136,8 +136,6 @@ __device__ __forceinline__ void keep_step(float (&to)[PK][T + kPPad], bool vec, 
     }
 }
 
-// ROWS: the first two products, whose sums run along a's rows; b is summed
-// along its rows (BK) or across them.
 __device__ __forceinline__ float load_remote(const float* local, unsigned rank) {
     float v;
     asm volatile("{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %1, %2;\n ld.shared::cluster.f32 %0, [r];\n}\n"
@@ -147,6 +145,8 @@ __device__ __forceinline__ float load_remote(const float* local, unsigned rank) 
     return v;
 }
 
+// ROWS: the first two products, whose sums run along a's rows; b is summed
+// along its rows (BK) or across them.
 // T x T sums a block, L x L a thread, in pieces of four.  SPLIT: the blocks of a
 // cluster share a tile, each with a run of the sum's steps; every block then
 // adds up its part of the tile's rows over the blocks, in their order.

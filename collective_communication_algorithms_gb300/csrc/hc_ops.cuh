@@ -1,6 +1,7 @@
 // hc_ops.cuh -- device-side building blocks of the training operators
-// (hc_embedding.cu, hc_block_norm.cu, hc_distill.cu): element access in
-// binary32, reductions over the threads of a row, programmatic launches.
+// (hc_embedding.cu, hc_block_norm.cu, hc_distill.cu, hc_clip.cu, hc_expert.cu,
+// hc_expert_matmul.cu): element access in binary32, reductions over the threads
+// of a row, programmatic launches.
 // Internal; not installed.
 #pragma once
 

@@ -162,7 +162,7 @@ __device__ __forceinline__ bool first_wait(uint64_t* m, unsigned parity, unsigne
 
 // ---------------------------------------------------------------------------
 // tiled copies; x counts elements along the innermost direction and is a
-// multiple of 64 (128 bytes) in every use
+// multiple of 16 (32 bytes) in every use
 // ---------------------------------------------------------------------------
 // G = 2: the barrier may be the cluster's first block's (first_blocks).
 template <int G>

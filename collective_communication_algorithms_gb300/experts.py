@@ -100,7 +100,9 @@ def bind_expert_matmul_grad(grad_out, offsets, x=None, weight=None, grad_x=None,
     """grad_x[r] = weight[e]^T @ grad_out[r], if weight is given, and
     grad_weight[e] (+)= the sum of grad_out[r] x[r]^T over e's rows, if x is
     (in grad_weight_dtype, x's type; grad_weight's layout is then its own, and
-    has to be weight's if that is given too)."""
+    has to be weight's if that is given too).  What is added to a fp32
+    grad_weight of bf16 operands counts as 0 where it is subnormal, as does
+    what it holds."""
     rows, outer = grad_out.shape
     experts = offsets.shape[0] - 1
     _check("grad_out", grad_out, (rows, outer))

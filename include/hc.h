@@ -536,7 +536,7 @@ hc_status_t hc_distill_grad(const hc_distill_t* args, hc_stream_t stream);
  *             in place; else out may be exactly `in` if the types are alike.
  *             Outputs may overlap neither each other nor another input
  *             (HC_ERR_INVALID_ARG): a tensor that is listed twice is refused
- *             in hc_clip_grads, and counts twice in hc_grad_norm.
+ *             where it is clipped in place, and counts twice elsewhere.
  *  norm     : one binary32; factor: one binary32, NULL: not kept.
  *  max_norm : above 0; infinity: no limit.  eps at least 0.
  * Tensors clipped in place are left alone when factor is exactly 1.  A NaN
@@ -609,12 +609,15 @@ size_t hc_expert_plan_scratch_bytes(const hc_expert_plan_t* args);
  *   out[r] = weight[e] x[r]      for offsets[e] <= r < offsets[e + 1]
  * weight is experts x out_dim x in_dim (weight_layout HC_WEIGHT_OUT_IN) or
  * experts x in_dim x out_dim (HC_WEIGHT_IN_OUT).
- * Rows in no group are not read, and are left as they were in out.  Offsets
- * are clamped to [0, rows] and to non-decreasing order.
+ * Rows in no group have no influence on results, whatever they hold, and are
+ * left as they were in out; some are read, with the rows of a group before them
+ * or where operands are copied.  Offsets are clamped to [0, rows] and to
+ * non-decreasing order.
  *  dtype     : x and weight; out_dtype: out.  Products of bf16 values are
  *              exact and are summed in binary32 by the tensor cores (how
  *              exactly: hc_expert_matmul_grad below); binary32 values are
- *              multiplied and summed in binary32 (no TF32).
+ *              multiplied and summed in binary32 (no TF32), a rounding
+ *              for each term.
  *  experts at most 1024, rows at most 2^30, in_dim and out_dim at most 65536
  *  (HC_ERR_UNSUPPORTED).
  *  scratch   : bf16 operands whose pointers or strides are not whole 16 bytes
@@ -833,8 +836,9 @@ hc_status_t hc_select_algo(hc_coll_t coll, int P, int ranks_per_server, size_t c
  * TMA-staged kernels: fused AllReduce / ReduceScatter, the step kernel's
  * launches of wide reduces and broadcasts, the block norm and its gradient
  * for rows of more than 256 columns, the distillation loss, and the expert
- * layer's bf16 products).  Each such wait gives up after about 2 s; the kernel
- * then records HC_ERR_TIMEOUT here and returns instead of hanging.
+ * layer's bf16 products).  Each such wait gives up after about 2 s (in the expert
+ * layer's products: after its block's copies have stood still for as long); the
+ * kernel then records HC_ERR_TIMEOUT here and returns instead of hanging.
  * Returns HC_OK, HC_ERR_TIMEOUT, or HC_ERR_CUDA if the flag cannot be read.
  * Synchronises with the current device (it copies the flag to the host);
  * clear != 0 resets the flag.
