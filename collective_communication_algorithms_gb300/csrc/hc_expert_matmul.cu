@@ -694,11 +694,12 @@ __global__ void __launch_bounds__(kTThreadsOf<LONG>, 1) tensor_product_kernel(co
     const auto warp_wait = [&](auto wait) {
         bool ok = true;
         if (lane == 0) {
-            uint32_t before;
-            do {
-                before = bar.copied;
+            ok = wait();
+            for (bool on = true; !ok && on;) {
+                const uint32_t before = bar.copied;
                 ok = wait();
-            } while (!ok && bar.copied != before);
+                on = bar.copied != before;
+            }
             if (!ok) expired();
         }
         ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
