@@ -442,8 +442,8 @@ constexpr int kTStagingBytes = 4 * 32 * 128;
 // registers, so that no length costs more than a segment does: 9.5e-6 of it for
 // binary32 results, 1.5e-4 for bf16 ones, whose own rounding is up to 2e-3.
 // binary32 results are always made so (476 us instead of 412 for weight gradients
-// of 32768 rows of 16, 2048 x 4096; 369 instead of 348 for the forward product of
-// as many, 4096 -> 2048), bf16 ones from sums of more than kTPlain terms (353 us
+// of 32768 rows of 16, 2048 x 4096; 369 to 408 instead of 348 for the forward
+// product of as many, 4096 -> 2048), bf16 ones from sums of more than kTPlain terms (353 us
 // either way for those weight gradients, but with plain sums four warps are
 // enough).
 template <class TO>
