@@ -9,8 +9,9 @@ Metric: effective algbw = n * b / t (bytes of one rank's vector per second of
 one call), GB/s.  The inputs (512 MiB) and outputs (512 MiB) are larger than
 the 129 MB L2, so no flush is needed between calls.
 
-Prints one JSON line (rank 0).  Other workloads (--workload) print the same
-line for the other configurations.
+Prints one JSON line (rank 0) on stdout, and the other configurations as one
+more on stderr.  Other workloads (--workload) print the same line for the other
+configurations.
 
   python bench.py [--gpus N] [--steps K] [--warmup W] [--workload NAME] [--impl reference]
 """
@@ -143,7 +144,7 @@ def parse_args():
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-e2e", action="store_true")
     ap.add_argument("--no-configs", action="store_true",
-                    help="skip the other configurations (the `configs` array of the line)")
+                    help="skip the other configurations (the `configs` array on stderr)")
     ap.add_argument("--sweep", choices=["small", "select", "hostlink", "hbm"], default=None,
                     help="small: RHD AllReduce latency sweep (P x n), eager vs graph mode; "
                          "select: cost-model selector against measured times; "
@@ -729,9 +730,15 @@ def run_ours(args, w):
         "e2e": e2e,
         "gpu_launches": args.steps * launches,
         "clocks": clocks,
-        "configs": configs,
-        "configs_clocks": configs_clocks,
     }
+    emit(line, configs, configs_clocks)
+
+
+def emit(line, configs=None, configs_clocks=None):
+    """The other configurations, some 15 KB, on stderr; then the line alone on
+    stdout, where it is read from the end of a log that may be cut."""
+    if configs is not None:
+        print(json.dumps({"configs": configs, "configs_clocks": configs_clocks}), file=sys.stderr, flush=True)
     print(json.dumps(line), flush=True)
 
 
