@@ -21,29 +21,47 @@ def _zeros(like, shape, dtype):
     return torch.zeros(shape, dtype=dtype, device=like.device)
 
 
-def _experts_weight(name, w, shape, dtype, device):
-    """(pointer, layout, row stride, expert stride) of experts x out x in
-    weights, stored so or as the transposed view of experts x in x out."""
+def _check_weight(name, w, shape, dtype, device):
     if not w.is_cuda or w.device != device:
         raise ValueError("%s must be on %s" % (name, device))
     if tuple(w.shape) != tuple(shape):
         raise ValueError("%s has shape %s, not %s" % (name, tuple(w.shape), tuple(shape)))
     if dtype is not None and w.dtype != dtype:
         raise TypeError("%s is %s, not %s" % (name, w.dtype, dtype))
-    experts, out, inner = shape
-    if inner == 1 or w.stride(2) == 1:
-        layout, rows, cols, stride = "out_in", out, inner, w.stride(1)
-    elif out == 1 or w.stride(1) == 1:
-        layout, rows, cols, stride = "in_out", inner, out, w.stride(2)
-    else:
-        raise ValueError("%s must have unit stride along its inputs or its outputs" % name)
+
+
+def _rows_of(w, layout):
+    """(rows, columns, row stride, column stride) of an expert's weight in a layout."""
+    row, col = (1, 2) if layout == "out_in" else (2, 1)
+    return w.shape[row], w.shape[col], w.stride(row), w.stride(col)
+
+
+def _layout(**weights):
+    """The layout that all of these have: experts x out x in ("out_in"), or the
+    transposed view of experts x in x out ("in_out").  With one input or one
+    output a weight may have both."""
+    able = {}
+    for name, w in weights.items():
+        able[name] = [k for k in B.LAYOUTS for rows, cols, stride, unit in [_rows_of(w, k)]
+                      if (cols == 1 or unit == 1) and (rows == 1 or stride >= cols)]
+        if not able[name]:
+            raise ValueError("%s must have unit stride along its inputs or its outputs, and rows that do not overlap" % name)
+    common = [k for k in B.LAYOUTS if all(k in v for v in able.values())]
+    if not common:
+        raise ValueError("grad_weight must be laid out as weight is (%s)" % able["weight"][0])
+    return common[0]
+
+
+def _experts_weight(name, w, layout):
+    """(pointer, row stride, expert stride) of weights in a layout that they have."""
+    rows, cols, stride, _ = _rows_of(w, layout)
     if rows == 1:
         stride = cols
     extent = (rows - 1) * stride + cols
-    step = w.stride(0) if experts > 1 else extent
-    if stride < cols or step < extent:
-        raise ValueError("%s: rows and experts must not overlap" % name)
-    return w.data_ptr(), layout, stride, step
+    step = w.stride(0) if w.shape[0] > 1 else extent
+    if step < extent:
+        raise ValueError("%s: experts must not overlap" % name)
+    return w.data_ptr(), stride, step
 
 
 def _offsets(offsets, experts, device):
@@ -82,7 +100,9 @@ def bind_expert_matmul(x, weight, offsets, out=None, out_dtype=None, scratch=Non
     rows, inner = x.shape
     experts, outer = weight.shape[0], weight.shape[1]
     _check("x", x, (rows, inner))
-    wp, layout, ws, es = _experts_weight("weight", weight, (experts, outer, inner), x.dtype, x.device)
+    _check_weight("weight", weight, (experts, outer, inner), x.dtype, x.device)
+    layout = _layout(weight=weight)
+    wp, ws, es = _experts_weight("weight", weight, layout)
     out = _zeros(x, (rows, outer), out_dtype or x.dtype) if out is None else out
     _check("out", out, (rows, outer), out_dtype, x.device)
     (xp, xs), (op, os_) = _matrix(x), _matrix(out)
@@ -109,9 +129,17 @@ def bind_expert_matmul_grad(grad_out, offsets, x=None, weight=None, grad_x=None,
     if x is None and weight is None:
         raise ValueError("weight (for grad_x) or x (for grad_weight) is needed")
     inner = x.shape[1] if x is not None else weight.shape[2]
-    device, kw, outputs, layout = grad_out.device, {}, {}, None
+    device, kw, outputs, shape = grad_out.device, {}, {}, (experts, outer, inner)
+    given = {}
     if weight is not None:
-        wp, layout, ws, es = _experts_weight("weight", weight, (experts, outer, inner), grad_out.dtype, device)
+        _check_weight("weight", weight, shape, grad_out.dtype, device)
+        given["weight"] = weight
+    if x is not None and grad_weight is not None:
+        _check_weight("grad_weight", grad_weight, shape, grad_weight_dtype, device)
+        given["grad_weight"] = grad_weight
+    layout = _layout(**given) if given else "out_in"
+    if weight is not None:
+        wp, ws, es = _experts_weight("weight", weight, layout)
         grad_x = _zeros(grad_out, (rows, inner), grad_out.dtype) if grad_x is None else grad_x
         _check("grad_x", grad_x, (rows, inner), grad_out.dtype, device)
         gp, gs = _matrix(grad_x)
@@ -124,14 +152,10 @@ def bind_expert_matmul_grad(grad_out, offsets, x=None, weight=None, grad_x=None,
         if grad_weight is None:
             if accumulate:
                 raise ValueError("accumulate needs grad_weight")
-            grad_weight = _new(x, (experts, outer, inner) if layout != "in_out" else (experts, inner, outer),
-                               grad_weight_dtype or x.dtype)
+            grad_weight = _new(x, shape if layout == "out_in" else (experts, inner, outer), grad_weight_dtype or x.dtype)
             if layout == "in_out":
                 grad_weight = grad_weight.transpose(1, 2)
-        gp, own, gs, ge = _experts_weight("grad_weight", grad_weight, (experts, outer, inner), grad_weight_dtype, device)
-        if layout is not None and layout != own:
-            raise ValueError("grad_weight must be laid out as weight is (%s)" % layout)
-        layout = own
+        gp, gs, ge = _experts_weight("grad_weight", grad_weight, layout)
         xp, xs = _matrix(x)
         kw.update(x=xp, x_stride=xs, grad_weight=gp, grad_weight_stride=gs, grad_expert_stride=ge,
                   grad_weight_dtype=_dtype(grad_weight))
